@@ -224,6 +224,94 @@ int nvfp4_mm(const uint8_t* codes_a, const uint8_t* scales_a, const uint8_t* cod
              void* out, int out_dtype, cudaStream_t stream);
 
 /*
+ * Operators a model served from NVFP4 weights runs next to the product above.
+ * Their weights are frozen: no gradient is taken.
+ */
+
+/* quantized output of nvfp4_rmsnorm:
+ *   FMT_NVFP4  the layouts above: e2m1 codes [M,K/2], one E4M3 byte per 16
+ *   FMT_MXFP8  8-bit block scaling (OCP microscaling: E4M3 elements, E8M0
+ *              scales): codes [M,K] E4M3, scales [M,ceil(K/32)], byte b standing
+ *              for 2^(b - 127); a row's last group holds 16 elements when
+ *              K % 32 == 16 */
+enum nvfp4_format { NVFP4_FMT_NVFP4 = 0, NVFP4_FMT_MXFP8 = 1 };
+
+/*
+ * nvfp4_rmsnorm -- the residual stream's addition, the root-mean-square norm
+ * and the quantization of its output, in one pass.  Per row, in fp32:
+ *   h = x (+ hidden);  hidden_out = h rounded to dtype
+ *   y = (h * (1 / sqrt(sum(h^2) / K + eps))) * weight
+ *   out = y rounded to dtype (when out != NULL); codes, scales = y quantized:
+ *   FMT_NVFP4  as nvfp4_quantize of y as an F32 tensor, 1x16 blocks, RTN, with
+ *              gamax_mode NONE, TENSOR_GIVEN, ROW (max |y| of the row, written
+ *              to gamax[r]) or ROW_GIVEN
+ *   FMT_MXFP8  per group: e = the least integer >= -127 with max|y| <= 448 * 2^e
+ *              (NaN dropped; at most 120), byte e + 127, codes E4M3(y * 2^-e)
+ *              nearest-even, an infinity to +-448, NaN to 0x7F
+ * Arguments
+ *   x            device [M,K], dtype F32 or BF16;  hidden: NULL or [M,K] of dtype
+ *   weight       NULL (ones) or device [K], weight_dtype F32 or BF16
+ *   eps          >= 0, finite
+ *   hidden_out   [M,K] of dtype, required with hidden and refused without; may be
+ *                hidden itself (updated in place)
+ *   out          NULL or [M,K] of dtype
+ *   codes/scales the outputs of `format`; both NULL when only out or hidden_out
+ *                is wanted
+ * A sum of squares past fp32's range gives y = 0 for finite elements, as the
+ * fp32 formula does.  EINVAL on bad shapes (K % 16), enums, pointers or eps,
+ * gamax_mode TENSOR (the maximum over all rows is not known in one pass), a
+ * gamax_mode with FMT_MXFP8, a bound outside (0, 448].
+ */
+int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int dtype, const void* weight,
+                  int weight_dtype, float eps, void* hidden_out, void* out, int format, int gamax_mode,
+                  float* gamax, float scale_bound, uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* activations of nvfp4_mv: F32 and BF16 as nvfp4_dtype, or E4M3 codes with
+ * E8M0 scales (FMT_MXFP8 above) */
+enum nvfp4_x_type { NVFP4_X_F32 = 0, NVFP4_X_BF16 = 1, NVFP4_X_MXFP8 = 2 };
+
+/*
+ * nvfp4_mv -- the product of a few tokens with an NVFP4 weight:
+ *   out[m,n] = S_dec(n) * sum_k x[m,k] * (q[n,k] * dec(s[n,k/16]))
+ *   x        device [M,K] of x_type;  x_scales: [M,ceil(K/32)] with MXFP8, else NULL
+ *   codes, scales   [N,K/2], [N,K/16]: a rowwise 1x16 output of nvfp4_quantize
+ *   gamax    NULL with gamax_mode NONE; 1 fp32 (TENSOR_GIVEN) or N (ROW_GIVEN)
+ *   out      device [M,N], F32 or BF16 (RNE)
+ * q * dec(s) is exact in f16.  x enters as f16 after a power-of-two scaling per
+ * token and K-slice: an F32 x as the sum of two f16 (22 bits), BF16 and MXFP8 x
+ * exactly, except that what lies 2^39 below the slice's largest magnitude is
+ * lost.  Sums are fp32 in a fixed order (the same bits on every run).
+ * EINVAL: M outside [0, 16] (larger M: nvfp4_mm, nvfp4_grouped_mm), N < 0, K < 0,
+ * K % 16, N or K >= 2^31, N * K too large, bad enums, pointers or bound.
+ */
+int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* codes, const uint8_t* scales,
+             int64_t M, int64_t N, int64_t K, int gamax_mode, const float* gamax, float scale_bound, void* out,
+             int out_dtype, cudaStream_t stream);
+
+/*
+ * nvfp4_grouped_mm -- matrix products grouped by expert, ragged, on the
+ * block-scaled FP4 tensor cores: for e in [0, E) and rows r in
+ * [offsets[e], offsets[e+1])
+ *   out[r,:] = (A[r,:] B[e]^T) * S_dec(A, r) * S_dec(B, e)
+ *   codes_a, scales_a   [T,K/2], [T,K/16] row-major: a rowwise 1x16 output of
+ *                nvfp4_quantize or nvfp4_rmsnorm, rows sorted by expert
+ *   offsets      device int64 [E+1], non-decreasing in [0, T] (values outside are
+ *                clamped to it; a group that ends before it starts is empty)
+ *   codes_b      [E,N,K/2];  scales_b: each expert's scale bytes in the
+ *                nvfp4_scales_to_mma layout, [E, 128*ceil(N/128), K/16]
+ *   gamax_a      by gamax_a_mode: NULL (NONE), 1 fp32 (TENSOR_GIVEN) or T (ROW_GIVEN)
+ *   gamax_b      NULL, or E fp32 (one per expert)
+ *   out          [T,N], F32 or BF16; rows in no group are not written
+ * Products are exact and accumulate in fp32.  EINVAL: a negative size, K % 64,
+ * E * N, T or K >= 2^31, bad enums, pointers or bound.  A CTA that stops waiting
+ * for its tensor-core work writes NaN to its tile of out.
+ */
+int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int64_t* offsets,
+                     const uint8_t* codes_b, const uint8_t* scales_b, int64_t E, int64_t T, int64_t N, int64_t K,
+                     int gamax_a_mode, const float* gamax_a, const float* gamax_b, float scale_bound, void* out,
+                     int out_dtype, cudaStream_t stream);
+
+/*
  * nvfp4_probe_divide -- diagnostic.  out[i] = a[i] / b[i] computed by the
  * device routine the plain quantizer uses for "every element is divided by the
  * decoded scale" [fp4-train, Method] (its stochastic-rounding form, which must

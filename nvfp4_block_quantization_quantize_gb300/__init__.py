@@ -11,6 +11,8 @@ Functions (same names as the C ABI):
   nvfp4_dequantize(codes, scales, M, K, ...) -> tensor
   nvfp4_qdq(x, ...)        -> dict(out[, codes, scales][, gamax])
   nvfp4_amax(x, ...)       -> tensor
+  nvfp4_mm, nvfp4_mv, nvfp4_grouped_mm: products with NVFP4 weights
+  nvfp4_rmsnorm(x, ...)    -> dict(codes, scales[, hidden][, out][, gamax])
 Calls on CUDA tensors stay on their device.  Calls on CPU tensors (the
 host-buffer path) stage their inputs on the current CUDA device and copy the
 results back (into the caller's host tensors when given, else into new pinned
@@ -38,6 +40,8 @@ BLOCK_1X16, BLOCK_16X16 = 0, 1
 RTN, SR, RTN_STD = 0, 1, 2
 GAMAX_NONE, GAMAX_TENSOR, GAMAX_ROW, GAMAX_TENSOR_GIVEN, GAMAX_ROW_GIVEN = 0, 1, 2, 3, 4
 ERR_NONE, ERR_MAE, ERR_MSE = 0, 1, 2
+FMT_NVFP4, FMT_MXFP8 = 0, 1
+X_F32, X_BF16, X_MXFP8 = 0, 1, 2
 OK, EINVAL, ECUDA = 0, 1, 2
 
 _NAMES = {
@@ -47,6 +51,7 @@ _NAMES = {
                    "tensor_given": GAMAX_TENSOR_GIVEN, "row_given": GAMAX_ROW_GIVEN},
     "err_mode": {"none": ERR_NONE, "mae": ERR_MAE, "mse": ERR_MSE},
     "dtype": {"f32": F32, "bf16": BF16},
+    "format": {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8},
 }
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_dequantize", "nvfp4_qdq", "nvfp4_amax",
@@ -100,6 +105,12 @@ def load_library(path: str | None = None):
         lib.nvfp4_scales_to_mma.argtypes = [P, i64, i64, P, P]
         lib.nvfp4_mm.restype = i32
         lib.nvfp4_mm.argtypes = [P, P, P, P, i64, i64, i64, P, P, f32, P, i32, P]
+        lib.nvfp4_rmsnorm.restype = i32
+        lib.nvfp4_rmsnorm.argtypes = [P, P, i64, i64, i32, P, i32, f32, P, P, i32, i32, P, f32, P, P, P]
+        lib.nvfp4_mv.restype = i32
+        lib.nvfp4_mv.argtypes = [P, P, i32, P, P, i64, i64, i64, i32, P, f32, P, i32, P]
+        lib.nvfp4_grouped_mm.restype = i32
+        lib.nvfp4_grouped_mm.argtypes = [P, P, P, P, P, i64, i64, i64, i64, i32, P, P, f32, P, i32, P]
         lib.nvfp4_last_error.restype = ctypes.c_char_p
         lib.nvfp4_last_error.argtypes = []
         lib.nvfp4_abi_version.restype = i32
@@ -860,6 +871,196 @@ def _check_mm_args(codes_a, scales_a, codes_b, scales_b, M, N, K, gamax_a, gamax
         _check_dev(out, "out", torch.float32 if odt == F32 else torch.bfloat16, M * N if ok else 0, dev,
                    at_least=True)
     return dev
+
+
+# ---- serving operators ------------------------------------------------------------------------
+# Calls on device tensors only.  They are short (a few microseconds of GPU
+# time for single tokens), so their host side is kept short too: pointers go
+# to ctypes as plain integers, the device is switched only when it is not the
+# current one, and a call on a given stream runs wholly on it (copies and
+# allocations too).
+def _given_stream(stream, dev):
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    if int(stream) == 0:
+        return torch.cuda.stream(torch.cuda.default_stream(dev))
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev))
+
+
+def _launch(lib, fn, dev, *args):
+    """fn(*args, current stream of dev), its status checked."""
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != OK:
+        _check(lib, rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda_2d(t, name, call):
+    if not torch.is_tensor(t) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{call}: {name} must be a 2-D CUDA tensor")
+    return t.device
+
+
+def _bytes_like(t, dtypes):
+    """t viewed as uint8 when its dtype is one of the one-byte dtypes."""
+    return t.view(torch.uint8) if torch.is_tensor(t) and t.dtype in dtypes else t
+
+
+def _rows_gamax(gamax, rows, dev, name):
+    """(mode, tensor) of a global amax with one value or one per row."""
+    if gamax is None:
+        return GAMAX_NONE, None
+    if gamax.numel() == 1:
+        return GAMAX_TENSOR_GIVEN, _check_dev(gamax, name, torch.float32, 1, dev)
+    return GAMAX_ROW_GIVEN, _check_dev(gamax, name, torch.float32, rows, dev)
+
+
+def nvfp4_rmsnorm(x: torch.Tensor, weight=None, *, hidden=None, hidden_out=None, eps: float = 1e-6,
+                  format="mxfp8", gamax_mode="none", gamax=None, scale_bound: float = 448.0,
+                  want_codes: bool = True, want_out: bool = False, out=None, codes=None, scales=None,
+                  stream=None) -> dict:
+    """h = x + hidden, its root-mean-square norm times weight, quantized, in one
+    pass (see nvfp4.h): dict(codes, scales[, hidden][, out][, gamax]).
+
+    x, hidden: [M, K] float32 or bfloat16 alike; weight: [K] of either.  "mxfp8"
+    gives E4M3 codes [M, K] and E8M0 scales [M, ceil(K/32)], "nvfp4" what
+    nvfp4_quantize gives (gamax_mode "none", "tensor_given", "row",
+    "row_given"), all uint8.  "hidden" is h rounded to x's dtype: a new tensor,
+    or hidden_out (which may be hidden: in place).  "out" (want_out, or a given
+    out) is the norm itself in x's dtype; want_codes=False leaves the codes out."""
+    lib = load_library()
+    dev = _cuda_2d(x, "x", "nvfp4_rmsnorm")
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_rmsnorm(x, weight, hidden=hidden, hidden_out=hidden_out, eps=eps, format=format,
+                                 gamax_mode=gamax_mode, gamax=gamax, scale_bound=scale_bound,
+                                 want_codes=want_codes, want_out=want_out, out=out, codes=codes, scales=scales)
+    M, K = x.shape
+    dt, fmt, gm = _x_dtype(x), _enum("format", format), _enum("gamax_mode", gamax_mode)
+    xd = x.contiguous()
+    wdt = dt
+    if weight is not None:
+        wdt = _x_dtype(weight)
+        weight = _check_dev(weight.contiguous(), "weight", weight.dtype, K, dev)
+    res = {}
+    if hidden is not None:
+        if hidden_out is not hidden:
+            hidden = hidden.contiguous()
+        _check_dev(hidden, "hidden", x.dtype, M * K, dev)
+        res["hidden"] = torch.empty((M, K), dtype=x.dtype, device=dev) if hidden_out is None else \
+            _check_dev(hidden_out, "hidden_out", x.dtype, M * K, dev)
+    elif hidden_out is not None:
+        raise ValueError("nvfp4: hidden_out goes with hidden")
+    if want_out or out is not None:
+        res["out"] = torch.empty((M, K), dtype=x.dtype, device=dev) if out is None else \
+            _check_dev(out, "out", x.dtype, M * K, dev)
+    if want_codes:
+        mx = fmt == FMT_MXFP8
+        cols, groups = (K, -(-K // 32)) if mx else (K // 2, K // 16)
+        res["codes"] = torch.empty((M, cols), dtype=torch.uint8, device=dev) if codes is None else \
+            _check_dev(codes, "codes", torch.uint8, M * cols, dev)
+        res["scales"] = torch.empty((M, groups), dtype=torch.uint8, device=dev) if scales is None else \
+            _check_dev(scales, "scales", torch.uint8, M * groups, dev)
+    g = None
+    if gm != GAMAX_NONE:
+        g = _gamax_buffer(gm, gamax, M, dev)
+        res["gamax"] = g
+    _launch(lib, lib.nvfp4_rmsnorm, dev, xd.data_ptr(), _addr(hidden), M, K, dt, _addr(weight), wdt, eps,
+            _addr(res.get("hidden")), _addr(res.get("out")), fmt, gm, _addr(g), scale_bound,
+            _addr(res.get("codes")), _addr(res.get("scales")))
+    return res
+
+
+def nvfp4_mv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, x_scales=None, gamax=None,
+             scale_bound: float = 448.0, out_dtype="bf16", out=None, stream=None) -> torch.Tensor:
+    """x @ W^T for at most 16 rows of x and an NVFP4 weight (see nvfp4.h).
+
+    codes [N, K/2], scales [N, K/16]: nvfp4_quantize's rowwise 1x16 output, gamax
+    its global amax (one value or N).  x [M, K]: float32, bfloat16, or E4M3 codes
+    (uint8 or float8_e4m3fn) with x_scales [M, ceil(K/32)] E8M0 (uint8 or
+    float8_e8m0fnu), as nvfp4_rmsnorm leaves them.  Returns [M, N]."""
+    lib = load_library()
+    dev = _cuda_2d(x, "x", "nvfp4_mv")
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_mv(x, codes, scales, x_scales=x_scales, gamax=gamax, scale_bound=scale_bound,
+                            out_dtype=out_dtype, out=out)
+    M, K = x.shape
+    _cuda_2d(codes, "codes", "nvfp4_mv")
+    N = codes.shape[0]
+    if x_scales is None:
+        xt = _x_dtype(x)                        # X_F32, X_BF16 are the dtypes' values
+        xd = x.contiguous()
+    else:
+        xt = X_MXFP8
+        x, x_scales = _bytes_like(x, (torch.float8_e4m3fn,)), _bytes_like(x_scales, (torch.float8_e8m0fnu,))
+        xd = _check_dev(x.contiguous(), "x", torch.uint8, M * K, dev)
+        x_scales = _check_dev(x_scales.contiguous(), "x_scales", torch.uint8, M * -(-K // 32), dev)
+    _check_dev(codes, "codes", torch.uint8, N * K // 2, dev)
+    _check_dev(scales, "scales", torch.uint8, N * K // 16, dev)
+    gm, g = _rows_gamax(gamax, N, dev, "gamax")
+    odt = _enum("dtype", out_dtype)
+    tdt = torch.float32 if odt == F32 else torch.bfloat16
+    o = torch.empty((M, N), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, M * N, dev)
+    _launch(lib, lib.nvfp4_mv, dev, xd.data_ptr(), _addr(x_scales), xt, codes.data_ptr(), scales.data_ptr(), M, N, K,
+            gm, _addr(g), scale_bound, o.data_ptr(), odt)
+    return o
+
+
+def nvfp4_grouped_scales_to_mma(scales: torch.Tensor) -> torch.Tensor:
+    """Scale bytes [E, rows, cols] of E weights, each in nvfp4_scales_to_mma's
+    layout: [E, 128*ceil(rows/128), 4*ceil(cols/4)] (once per model)."""
+    if not torch.is_tensor(scales) or not scales.is_cuda or scales.dim() != 3 or scales.dtype != torch.uint8:
+        raise ValueError("nvfp4_grouped_scales_to_mma: scales must be a CUDA uint8 [E, rows, cols] tensor")
+    E, rows, cols = scales.shape
+    o = torch.empty((E, -(-rows // 128) * 128, -(-cols // 4) * 4), dtype=torch.uint8, device=scales.device)
+    for e in range(E):
+        nvfp4_scales_to_mma(scales[e], out=o[e])
+    return o
+
+
+def nvfp4_grouped_mm(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: torch.Tensor, codes_b: torch.Tensor,
+                     scales_b: torch.Tensor, *, gamax_a=None, gamax_b=None, scale_bound: float = 448.0,
+                     out_dtype="bf16", out=None, stream=None) -> torch.Tensor:
+    """Rows offsets[e] .. offsets[e+1] of A times expert e's weight transposed, for
+    every expert, on the FP4 tensor cores (see nvfp4.h).
+
+    codes_a [T, K/2], scales_a [T, K/16]: rowwise 1x16 NVFP4, rows sorted by
+    expert; gamax_a: their amax, one value or T.  offsets: int64 [E+1] on the
+    device (never read on the host).  codes_b [E, N, K/2], scales_b in
+    nvfp4_grouped_scales_to_mma's layout, gamax_b one amax per expert.  Returns
+    [T, N]; rows in no group are not written.  K a multiple of 64."""
+    lib = load_library()
+    dev = _cuda_2d(codes_a, "codes_a", "nvfp4_grouped_mm")
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_grouped_mm(codes_a, scales_a, offsets, codes_b, scales_b, gamax_a=gamax_a,
+                                    gamax_b=gamax_b, scale_bound=scale_bound, out_dtype=out_dtype, out=out)
+    if not torch.is_tensor(codes_b) or codes_b.dim() != 3:
+        raise ValueError("nvfp4_grouped_mm: codes_b must be [E, N, K/2]")
+    T, K = codes_a.shape[0], codes_a.shape[1] * 2
+    E, N = codes_b.shape[0], codes_b.shape[1]
+    ca = _check_dev(codes_a.contiguous(), "codes_a", torch.uint8, T * K // 2, dev)
+    sa = _check_dev(scales_a.contiguous(), "scales_a", torch.uint8, T * K // 16, dev)
+    _check_dev(offsets, "offsets", torch.int64, E + 1, dev)
+    _check_dev(codes_b, "codes_b", torch.uint8, E * N * K // 2, dev)
+    _check_dev(scales_b, "scales_b", torch.uint8, E * (-(-N // 128) * 128) * (-(-K // 64) * 4), dev)
+    gm, ga = _rows_gamax(gamax_a, T, dev, "gamax_a")
+    if gamax_b is not None:
+        _check_dev(gamax_b, "gamax_b", torch.float32, E, dev)
+    odt = _enum("dtype", out_dtype)
+    tdt = torch.float32 if odt == F32 else torch.bfloat16
+    o = torch.empty((T, N), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, T * N, dev)
+    _launch(lib, lib.nvfp4_grouped_mm, dev, ca.data_ptr(), sa.data_ptr(), offsets.data_ptr(), codes_b.data_ptr(),
+            scales_b.data_ptr(), E, T, N, K, gm, _addr(ga), _addr(gamax_b), scale_bound, o.data_ptr(), odt)
+    return o
 
 
 def nvfp4_global_scales(gamax: torch.Tensor, scale_bound: float = 448.0, stream=None):

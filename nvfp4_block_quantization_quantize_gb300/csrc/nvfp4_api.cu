@@ -245,6 +245,124 @@ int nvfp4_global_scales(const float* gamax, int64_t n, float scale_bound, float*
     return NVFP4_OK;
 }
 
+int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int dtype, const void* weight,
+                  int weight_dtype, float eps, void* hidden_out, void* out, int format, int gamax_mode,
+                  float* gamax, float scale_bound, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    int rc = check_shape(M, K);
+    if (rc) return rc;
+    if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad dtype %d", dtype);
+    if (weight_dtype != NVFP4_F32 && weight_dtype != NVFP4_BF16)
+        return fail(NVFP4_EINVAL, "bad weight_dtype %d", weight_dtype);
+    if (!(eps >= 0.0f && eps <= 3.4028234663852886e+38f)) return fail(NVFP4_EINVAL, "eps must be >= 0 and finite");
+    if (format != NVFP4_FMT_NVFP4 && format != NVFP4_FMT_MXFP8) return fail(NVFP4_EINVAL, "bad format %d", format);
+    if (gamax_mode < NVFP4_GAMAX_NONE || gamax_mode > NVFP4_GAMAX_ROW_GIVEN)
+        return fail(NVFP4_EINVAL, "bad gamax_mode %d", gamax_mode);
+    if (gamax_mode == NVFP4_GAMAX_TENSOR)
+        return fail(NVFP4_EINVAL, "the norm quantizes in one pass: give the tensor amax, or use a per-row one");
+    if (format == NVFP4_FMT_MXFP8 && gamax_mode != NVFP4_GAMAX_NONE)
+        return fail(NVFP4_EINVAL, "NVFP4_FMT_MXFP8 has no global scale");
+    if (!(scale_bound > 0.0f && scale_bound <= 448.0f)) return fail(NVFP4_EINVAL, "scale_bound must be in (0, 448]");
+    if ((codes == nullptr) != (scales == nullptr)) return fail(NVFP4_EINVAL, "give both codes and scales, or neither");
+    const bool any = M > 0 && K > 0;
+    if (any && !codes && gamax_mode != NVFP4_GAMAX_NONE)
+        return fail(NVFP4_EINVAL, "a gamax_mode needs codes and scales");
+    if (any && !codes && !out && !hidden_out) return fail(NVFP4_EINVAL, "no output is given");
+    if ((hidden == nullptr) != (hidden_out == nullptr))
+        return fail(NVFP4_EINVAL, "give both hidden and hidden_out, or neither");
+    if ((rc = check_ptr(x, "x", any))) return rc;
+    if ((rc = check_ptr(hidden, "hidden", false))) return rc;
+    if ((rc = check_ptr(weight, "weight", false))) return rc;
+    if ((rc = check_ptr(hidden_out, "hidden_out", false))) return rc;
+    if ((rc = check_ptr(out, "out", false))) return rc;
+    if ((rc = check_ptr(codes, "codes", false))) return rc;
+    if ((rc = check_ptr(scales, "scales", false))) return rc;
+    if ((rc = check_ptr(gamax, "gamax", gamax_mode != NVFP4_GAMAX_NONE && M > 0, 4))) return rc;
+    if (M == 0) return NVFP4_OK;
+    if (K == 0) {                               // an empty row's amax is +0
+        if (gamax_mode != NVFP4_GAMAX_ROW) return NVFP4_OK;
+        const int err = static_cast<int>(cudaMemsetAsync(gamax, 0, static_cast<size_t>(M) * 4, stream));
+        return err ? cuda_fail(err, "norm zero fill") : NVFP4_OK;
+    }
+    const nvfp4::NormArgs a{x, hidden, M, K, dtype, weight, weight_dtype, eps, hidden_out, out, format, gamax_mode,
+                            gamax, scale_bound, codes, scales};
+    const int err = nvfp4::launch_rmsnorm(a, stream);
+    if (err) return cuda_fail(err, "norm launch");
+    return NVFP4_OK;
+}
+
+int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* codes, const uint8_t* scales,
+             int64_t M, int64_t N, int64_t K, int gamax_mode, const float* gamax, float scale_bound, void* out,
+             int out_dtype, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    if (M < 0 || N < 0 || K < 0) return fail(NVFP4_EINVAL, "M, N and K must be >= 0");
+    if (M > 16) return fail(NVFP4_EINVAL, "nvfp4_mv takes at most 16 rows of x (got %lld)", (long long)M);
+    if (K % 16) return fail(NVFP4_EINVAL, "K must be a multiple of 16 (got %lld)", (long long)K);
+    if (N >= (int64_t{1} << 31) || K >= (int64_t{1} << 31)) return fail(NVFP4_EINVAL, "N and K must be below 2^31");
+    if (x_type < NVFP4_X_F32 || x_type > NVFP4_X_MXFP8) return fail(NVFP4_EINVAL, "bad x_type %d", x_type);
+    if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
+    if (gamax_mode != NVFP4_GAMAX_NONE && gamax_mode != NVFP4_GAMAX_TENSOR_GIVEN &&
+        gamax_mode != NVFP4_GAMAX_ROW_GIVEN)
+        return fail(NVFP4_EINVAL, "gamax_mode must be NONE, TENSOR_GIVEN or ROW_GIVEN (got %d)", gamax_mode);
+    if (!(scale_bound > 0.0f && scale_bound <= 448.0f)) return fail(NVFP4_EINVAL, "scale_bound must be in (0, 448]");
+    if ((x_type == NVFP4_X_MXFP8) != (x_scales != nullptr) && M > 0 && K > 0)
+        return fail(NVFP4_EINVAL, "x_scales go with an MXFP8 x");
+    const bool any = M > 0 && N > 0;
+    const bool anyk = any && K > 0;
+    int rc;
+    if ((rc = check_ptr(x, "x", anyk))) return rc;
+    if ((rc = check_ptr(x_scales, "x_scales", false))) return rc;
+    if ((rc = check_ptr(codes, "codes", anyk))) return rc;
+    if ((rc = check_ptr(scales, "scales", anyk))) return rc;
+    if ((rc = check_ptr(gamax, "gamax", any && gamax_mode != NVFP4_GAMAX_NONE, 4))) return rc;
+    if ((rc = check_ptr(out, "out", any))) return rc;
+    if (!any) return NVFP4_OK;
+    if (K == 0) {
+        const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(N) * (out_dtype == NVFP4_F32 ? 4 : 2);
+        const int err = static_cast<int>(cudaMemsetAsync(out, 0, bytes, stream));
+        return err ? cuda_fail(err, "mv zero fill") : NVFP4_OK;
+    }
+    const nvfp4::MvArgs a{x, x_scales, x_type, codes, scales, static_cast<int>(M), static_cast<int>(N),
+                          static_cast<int>(K), gamax_mode, gamax, scale_bound, out, out_dtype};
+    const int err = nvfp4::launch_mv(a, stream);
+    if (err) return cuda_fail(err, "mv launch");
+    return NVFP4_OK;
+}
+
+int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int64_t* offsets,
+                     const uint8_t* codes_b, const uint8_t* scales_b, int64_t E, int64_t T, int64_t N, int64_t K,
+                     int gamax_a_mode, const float* gamax_a, const float* gamax_b, float scale_bound, void* out,
+                     int out_dtype, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    constexpr int64_t kMax = int64_t{1} << 31;
+    if (E < 0 || T < 0 || N < 0 || K < 0) return fail(NVFP4_EINVAL, "E, T, N and K must be >= 0");
+    if (K % 64) return fail(NVFP4_EINVAL, "nvfp4_grouped_mm needs K %% 64 == 0 (got %lld)", (long long)K);
+    if (E >= kMax || T >= kMax || N >= kMax || K >= kMax || (N > 0 && E > (kMax - 1) / N))
+        return fail(NVFP4_EINVAL, "E * N, T and K must be below 2^31");
+    if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
+    if (gamax_a_mode != NVFP4_GAMAX_NONE && gamax_a_mode != NVFP4_GAMAX_TENSOR_GIVEN &&
+        gamax_a_mode != NVFP4_GAMAX_ROW_GIVEN)
+        return fail(NVFP4_EINVAL, "gamax_a_mode must be NONE, TENSOR_GIVEN or ROW_GIVEN (got %d)", gamax_a_mode);
+    if (!(scale_bound > 0.0f && scale_bound <= 448.0f)) return fail(NVFP4_EINVAL, "scale_bound must be in (0, 448]");
+    const bool any = E > 0 && T > 0 && N > 0;
+    const bool anyk = any && K > 0;
+    int rc;
+    if ((rc = check_ptr(codes_a, "codes_a", anyk))) return rc;
+    if ((rc = check_ptr(scales_a, "scales_a", anyk))) return rc;
+    if ((rc = check_ptr(offsets, "offsets", any, 8))) return rc;
+    if ((rc = check_ptr(codes_b, "codes_b", anyk))) return rc;
+    if ((rc = check_ptr(scales_b, "scales_b", anyk))) return rc;
+    if ((rc = check_ptr(gamax_a, "gamax_a", any && gamax_a_mode != NVFP4_GAMAX_NONE, 4))) return rc;
+    if ((rc = check_ptr(gamax_b, "gamax_b", false, 4))) return rc;
+    if ((rc = check_ptr(out, "out", any))) return rc;
+    if (!any) return NVFP4_OK;
+    const nvfp4::GroupedArgs a{codes_a, scales_a, offsets, codes_b, scales_b, E, T, N, K, gamax_a_mode, gamax_a,
+                               gamax_b, scale_bound, out, out_dtype};
+    const int err = nvfp4::launch_grouped_mm(a, stream);
+    if (err) return cuda_fail(err, "grouped mm launch");
+    return NVFP4_OK;
+}
+
 int nvfp4_probe_divide(const float* a, const float* b, float* out, int64_t n, cudaStream_t stream) {
     g_msg[0] = '\0';
     if (n < 0) return fail(NVFP4_EINVAL, "n must be >= 0");

@@ -68,6 +68,52 @@ struct DequantArgs {
     int out_dtype;
 };
 
+struct NormArgs {
+    const void* x;
+    const void* hidden;       // null = nothing to add
+    int64_t M, K;
+    int dtype;
+    const void* weight;       // null = ones
+    int weight_dtype;
+    float eps;
+    void* hidden_out;         // null without hidden; may be hidden
+    void* out;                // null = not wanted
+    int format, gamax_mode;
+    float* gamax;
+    float bound;
+    uint8_t* codes;           // null = not wanted
+    uint8_t* scales;
+};
+
+struct MvArgs {
+    const void* x;
+    const uint8_t* x_scales;
+    int x_type;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int M, N, K;
+    int gamax_mode;           // NONE, TENSOR_GIVEN or ROW_GIVEN
+    const float* gamax;
+    float bound;
+    void* out;
+    int out_dtype;
+};
+
+struct GroupedArgs {
+    const uint8_t* codes_a;
+    const uint8_t* scales_a;
+    const int64_t* offsets;
+    const uint8_t* codes_b;
+    const uint8_t* scales_b;
+    int64_t E, T, N, K;
+    int gamax_a_mode;         // NONE, TENSOR_GIVEN or ROW_GIVEN
+    const float* gamax_a;
+    const float* gamax_b;     // null = none
+    float bound;
+    void* out;
+    int out_dtype;
+};
+
 // launchers (each returns cudaGetLastError() after its launches)
 int launch_quantize_rows(const QuantArgs& a, void* stream);    // rowwise output only
 int launch_quantize_tiles(const QuantArgs& a, void* stream);   // rowwise + columnwise
@@ -76,6 +122,9 @@ int launch_scales_mma(const uint8_t* in, int64_t rows, int64_t cols, uint8_t* ou
 int launch_mm(const uint8_t* A, const uint8_t* SA, const uint8_t* B, const uint8_t* SB, int64_t M, int64_t N,
               int64_t K, const float* gamax_a, const float* gamax_b, float bound, void* out, int out_dtype,
               void* stream);
+int launch_rmsnorm(const NormArgs& a, void* stream);
+int launch_mv(const MvArgs& a, void* stream);
+int launch_grouped_mm(const GroupedArgs& a, void* stream);
 int launch_amax(const void* x, int64_t M, int64_t K, int dtype, const float* residual, int mode,
                 float* out, void* stream);
 int launch_probe_divide(const float* a, const float* b, float* out, int64_t n, void* stream);
