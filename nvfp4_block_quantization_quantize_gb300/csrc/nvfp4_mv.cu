@@ -7,19 +7,25 @@
 // shared memory), the warp-level MMA takes them straight from registers.
 //   - A weight decodes exactly to f16: q * dec(s) has at most 6 significant bits
 //     and lies in [2^-10, 2688].
-//   - x is scaled per token and K-slice by a power of two to at most 2^15 and
-//     held in shared memory as f16 (an fp32 x as hi + lo, 22 bits), in the order
-//     the MMA's B fragments are read.
+//   - x is scaled per token and warp by a power of two to at most 2^15 and held
+//     in shared memory as f16 (an fp32 x as hi + lo, 22 bits), in the order the
+//     MMA's B fragments are read.
 //   - m16n8k16: 16 weight rows times 8 tokens.  The order of k inside a product
 //     is free as long as A and B agree, so lane (g, t) of a warp takes whole
 //     blocks: 16 * VB consecutive weights of rows g and g + 8, one 8 * VB-byte
-//     load and VB scale bytes a row, for 4 * VB products.
-//   - A chain of products starts from zero every 64 * VB columns and is added to
-//     an fp32 sum, so the tensor core's own accumulation stays short.
-// A CTA has W warps of 16 rows each over one slice of K (8 chunks of 64 * VB);
-// each warp issues all the slice's loads at once.  The CTAs of a cluster take the
-// slices of the same rows in turn and add their partial sums through distributed
-// shared memory in rank order: no workspace, no atomics, the same bits each run.
+//     load and VB scale bytes a row, for 4 * VB products (a chunk: 64 * VB columns).
+//   - A chain of products starts from zero every two blocks and is added to an
+//     fp32 sum, so the tensor core's own accumulation stays short.
+// A CTA has 8 warps: WK parts of its columns times WR groups of 16 weight rows.  Its x
+// is staged once; then each warp walks down row tiles with kAhead chunks of weights in
+// flight (registers; the loads run on across tiles).  Per tile the WK warps of a row
+// group add their sums through shared memory.  Where the columns are too many for one
+// CTA, or the rows too few for all SMs, the CTAs of a cluster split the columns and
+// their sums meet through distributed shared memory at the end: no workspace, no
+// atomics, every sum in a fixed order.
+//
+// VB is 4 where rows of codes are whole 32-byte sectors (K % 64 == 0, codes 32-byte
+// aligned): one 256-bit and one 32-bit load per row and 256 columns.  Otherwise 1.
 #include <cooperative_groups.h>
 
 #include "nvfp4_block.cuh"
@@ -29,8 +35,32 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMvChunks = 8;                              // chunks of 64 * VB columns per slice
+constexpr int kMvWarps = 8;
 constexpr int kMvMaxCluster = 8;
+constexpr int kMvMaxTiles = 16;                           // row tiles per cluster with sums kept to the end
+
+template <int VB>
+constexpr int kAhead = VB == 4 ? 3 : 8;                   // chunks of weights in flight per warp
+template <int VB>
+constexpr int kStep = 4 / VB;                             // chunks in the 256 columns a warp stages at once
+constexpr int kMvCtas = 2;                                // CTAs an SM holds
+constexpr int kMvMaxX = 72 * 1024;                        // x's share of a CTA's shared memory
+
+// how the work is cut, chosen by the host
+struct MvPlan {
+    int S;                    // CTAs of a cluster (parts of the columns)
+    int WK;                   // warps a CTA splits its columns among; the others take further rows
+    int tiles;                // tiles of 16 * (8 / WK) rows per cluster
+    int cpw;                  // chunks per warp and round, a multiple of kStep
+    int rounds;               // rounds of S * WK * cpw chunks over K
+};
+
+// bytes of a token's part of x (n chunks): its cells, and half a bank row more so
+// that two tokens' fragment reads do not meet in a bank
+template <int XT, int VB>
+__host__ __device__ constexpr int x_stride(int n) {
+    return n * 128 * VB * (XT == NVFP4_X_F32 ? 2 : 1) + 64;
+}
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -40,303 +70,450 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// a code byte's two weights, scaled (s holds the block's scale twice)
-__device__ __forceinline__ uint32_t weight2(uint32_t w, int byte, uint32_t s) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(e2m1_decode_byte(w, byte)), "r"(s));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// a word's eight weights, scaled, as four f16 pairs (s holds the block's scale twice)
+__device__ __forceinline__ void weights8(uint32_t w, uint32_t s, uint32_t* h) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = mul_f16x2(h[i], s);
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t bytes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bytes)));
+    return h;
 }
 
 // VB scale bytes -> f16 pairs, each holding one scale twice
 template <int VB>
 __device__ __forceinline__ void scale_pairs(uint32_t bytes, uint32_t* s) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bytes)));
-    s[0] = __byte_perm(h, h, 0x1010);
-    if (VB == 2) s[VB - 1] = __byte_perm(h, h, 0x3232);
-}
-
-// VB blocks' codes (8 bytes each) streamed past L1, and their scale bytes
-template <int VB>
-__device__ __forceinline__ void load_blocks(const uint8_t* codes, const uint8_t* scales, int64_t blk, bool in,
-                                            uint32_t* w, uint32_t& s) {
 #pragma unroll
-    for (int i = 0; i < 2 * VB; ++i) w[i] = 0;
-    s = 0;
-    if (!in) return;
-    if (VB == 2) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2 * VB - 2]), "=r"(w[2 * VB - 1])
-                     : "l"(codes + blk * 8));
-        s = __ldg(reinterpret_cast<const uint16_t*>(scales + blk));
-    } else {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1])
-                     : "l"(codes + blk * 8));
-        s = __ldg(scales + blk);
+    for (int i = 0; i < VB; i += 2) {
+        const uint32_t h = e4m3_pair(bytes >> (8 * i));
+        s[i] = __byte_perm(h, h, 0x1010);
+        if (VB > 1) s[(i + 1) % VB] = __byte_perm(h, h, 0x3232);
     }
 }
 
-// 8 elements of x as fp32; columns past K are zero
+// VB blocks' codes (8 bytes each), streamed past L1, and their scale bytes
+template <int VB>
+__device__ __forceinline__ void load_blocks(const uint8_t* codes, const uint8_t* scales, uint32_t* w, uint32_t& s) {
+    if constexpr (VB == 4) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(codes));
+        s = __ldg(reinterpret_cast<const uint32_t*>(scales));
+    } else {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(codes));
+        s = __ldg(scales);
+    }
+}
+
+// ---- staging of x -----------------------------------------------------------------------------
+// The n chunks of columns from k0 of one part, every token: first copied as they are
+// into the token's part of shared memory (MXFP8 into its second half), then converted
+// in place, 256 columns at a time, to cells of 16 bytes: cell (chunk, j, part, t) holds
+// the 8 f16 values of columns chunk * 64 VB + t * 16 VB + 8 j, part 0 being hi and 1 lo.
+// The part's WR warps take the tokens in turn.
 template <int XT>
-__device__ __forceinline__ void load_x8(const MvArgs& a, int64_t m, int k, float* v) {
+constexpr int kXSize = XT == NVFP4_X_F32 ? 4 : XT == NVFP4_X_BF16 ? 2 : 1;
+
+template <int XT, int VB>
+__device__ __forceinline__ int raw_offset(int n) {
+    return XT == NVFP4_X_MXFP8 ? n * 64 * VB : 0;
+}
+
+template <int XT, int VB>
+__device__ __forceinline__ void copy_x(const MvArgs& a, uint8_t* xs, int64_t k0, int n, int wr, int WR, int lane) {
+    const int64_t left = a.K - k0;
+    const int cols = static_cast<int>(left < n * 64 * VB ? (left > 0 ? left : 0) : n * 64 * VB);
+    const uint8_t* src = static_cast<const uint8_t*>(a.x) + k0 * kXSize<XT>;
+    for (int m = wr; m < a.M; m += WR) {
+        uint8_t* dst = xs + m * x_stride<XT, VB>(n) + raw_offset<XT, VB>(n);
+        const uint8_t* row = src + static_cast<int64_t>(m) * a.K * kXSize<XT>;
+        for (int i = lane; i < cols * kXSize<XT> / 16; i += 32) cp_async16(dst + 16 * i, row + 16 * i);
+    }
+    cp_async_commit();
+}
+
+// 2^e as a float, e >= -149
+__device__ __forceinline__ float power_of_two(int e) {
+    return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
+}
+
+// 8 columns as four f16 pairs: the raw ones at r scaled by f (MXFP8: f already an f16 pair's bits)
+template <int XT, int P>
+__device__ __forceinline__ void convert8(const uint8_t* r, uint32_t f, uint32_t (*h)[4]) {
+    if (XT == NVFP4_X_MXFP8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (k >= a.K) return;                       // K % 16 == 0: a piece of 8 is whole or absent
-    const int64_t e = m * a.K + k;
+        for (int q = 0; q < 4; ++q) h[0][q] = mul_f16x2(e4m3_pair((q < 2 ? u.x : u.y) >> (16 * (q & 1))), f);
+        return;
+    }
+    float v[8];
     if (XT == NVFP4_X_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + e);
-        const float4 u = __ldg(p), w = __ldg(p + 1);
+        const float4* p = reinterpret_cast<const float4*>(r);
+        const float4 u = p[0], w = p[1];
         v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w, v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
-    } else if (XT == NVFP4_X_BF16) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + e));
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(r);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int q = 0; q < 4; ++q) {
+            v[2 * q] = __uint_as_float(w[q] << 16);
+            v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
         }
-    } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + e));
-        const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            e4m3_decode2(w[i >> 1] >> (16 * (i & 1)), w[i >> 1] >> (16 * (i & 1) + 8), v[2 * i], v[2 * i + 1]);
-    }
-}
-
-// One token's slice of x (columns k0 .. k0 + 512 * VB - 1) to shared memory by
-// one warp: cell (chunk, j, part, token, t) of 16 bytes holds the 8 f16 values of
-// columns chunk * 64 VB + t * 16 VB + 8 j of token's part (hi or lo).  Returns the
-// exponent the token's sums are to be scaled by.
-template <int XT, int VB>
-__device__ __forceinline__ int stage_x(const MvArgs& a, uint4* xs, int Mp, int m, int k0, int lane) {
-    constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
-    constexpr int N8 = 2 * VB;                            // pieces of 8 columns per lane: 512 VB / 8 / 32
-    float v[N8][8];
-    int ex;
-#pragma unroll
-    for (int i = 0; i < N8; ++i) load_x8<XT>(a, m, k0 + (lane + 32 * i) * 8, v[i]);
-    if (XT == NVFP4_X_MXFP8) {
-        // value = e4m3 * 2^(b - 127); scaled by 2^(6 - top) with top the largest b: at most 448 * 64
-        const int groups = (a.K + 31) / 32;
-        int b[N8], top = 0;
-#pragma unroll
-        for (int i = 0; i < N8; ++i) {
-            const int k = k0 + (lane + 32 * i) * 8;
-            b[i] = k < a.K ? a.x_scales[static_cast<int64_t>(m) * groups + k / 32] : 0;
-            if (b[i] != 255) top = max(top, b[i]);
-        }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-#pragma unroll
-        for (int i = 0; i < N8; ++i) {
-            const int f = 127 + 6 + b[i] - top;           // the factor's exponent field
-            const float s = b[i] == 255 ? __int_as_float(0x7FC00000) : f > 0 ? __int_as_float(f << 23) : 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = mul_rn(v[i][q], s);
-        }
-        ex = top - 127 - 6;
-    } else {
-        float mx = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N8; ++i)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mx = max_nd(mx, fabsf(v[i][q]));
-        // exponent of the maximum, at least -112 so that 2^(14 - e) is a float
-        const int e = max(static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)) >> 23) - 127, -112);
-        const float s = __int_as_float((127 + 14 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < N8; ++i)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = mul_rn(v[i][q], s);
-        ex = e - 14;
     }
 #pragma unroll
-    for (int i = 0; i < N8; ++i) {
-        const int piece = lane + 32 * i;                  // columns 8 * piece of the slice
-        const int chunk = piece / (8 * VB), t = piece / (2 * VB) % 4, j = piece % (2 * VB);
-        uint4* cell = xs + (((chunk * 2 * VB + j) * P) * Mp + m) * 4 + t;
+    for (int q = 0; q < 4; ++q) {
+        float x0 = mul_rn(v[2 * q], __uint_as_float(f)), x1 = mul_rn(v[2 * q + 1], __uint_as_float(f));
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const __half2 h = __floats2half2_rn(v[i][2 * q], v[i][2 * q + 1]);
-                w[q] = *reinterpret_cast<const uint32_t*>(&h);
-                if (P == 2 && p == 0) {
-                    // what hi leaves; an infinite hi (an infinity of x) leaves nothing
-                    const float2 f = __half22float2(h);
-                    v[i][2 * q] = isinf(f.x) ? 0.0f : sub_rn(v[i][2 * q], f.x);
-                    v[i][2 * q + 1] = isinf(f.y) ? 0.0f : sub_rn(v[i][2 * q + 1], f.y);
-                }
-            }
-            cell[p * Mp * 4] = make_uint4(w[0], w[1], w[2], w[3]);
+            const __half2 o = __floats2half2_rn(x0, x1);
+            h[p][q] = *reinterpret_cast<const uint32_t*>(&o);
+            // what hi leaves; an infinite hi (an infinity of x) leaves nothing
+            const float2 b = __half22float2(o);
+            x0 = isinf(b.x) ? 0.0f : sub_rn(x0, b.x);
+            x1 = isinf(b.y) ? 0.0f : sub_rn(x1, b.y);
         }
     }
-    return ex;
 }
 
-// grid.x = cluster size * row blocks; a cluster's CTAs share W * 16 rows.
-// Mp: M rounded up to a power of two (a lane group past it reads another token's
-// values, and its columns are not stored).
-template <int XT, int NT, int VB>
-__global__ void __launch_bounds__(256) k_mv(const MvArgs a, int Mp) {
-    extern __shared__ uint4 xs[];
-    constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
-    constexpr int kSlice = kMvChunks * 64 * VB;
-    __shared__ float part[8 * 16 * 16];                   // [token][row]: W * 16 rows of at most 16 tokens
-    __shared__ int ex[16];
-    pdl_wait();
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int S = cluster.num_blocks(), rank = cluster.block_rank();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int R = W * 16;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / S) * R;
-    const int64_t r = row0 + warp * 16 + g;
-    const int64_t bpr = a.K / 16;
-    const int slices = (a.K + kSlice - 1) / kSlice;
-    float tot[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[n][i] = 0.0f;
+// largest magnitude (its bits) of 8 raw columns, NaN dropped
+template <int XT>
+__device__ __forceinline__ uint32_t top8(const uint8_t* r) {
+    if (XT == NVFP4_X_F32) {
+        const float4* p = reinterpret_cast<const float4*>(r);
+        const float4 u = p[0], w = p[1];
+        const float m0 = max_nd(max_nd(fabsf(u.x), fabsf(u.y)), max_nd(fabsf(u.z), fabsf(u.w)));
+        const float m1 = max_nd(max_nd(fabsf(w.x), fabsf(w.y)), max_nd(fabsf(w.z), fabsf(w.w)));
+        return __float_as_uint(max_nd(max_nd(m0, m1), 0.0f));
+    }
+    const uint4 u = *reinterpret_cast<const uint4*>(r);
+    uint32_t p = absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y);
+    p = absmax_bf16x2(absmax_bf16x2(p, u.z), u.w);
+    return max(p << 16, p & 0xFFFF0000u);
+}
 
-    for (int sl = rank; sl < slices; sl += S) {
-        const int k0 = sl * kSlice;
-        uint32_t w[kMvChunks][2][2 * VB], sc[kMvChunks][2];
-#pragma unroll
-        for (int c = 0; c < kMvChunks; ++c) {
-            const int64_t blk = k0 / 16 + (c * 4 + t) * VB;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                load_blocks<VB>(a.codes, a.scales, (r + 8 * h) * bpr + blk, r + 8 * h < a.N && blk < bpr, w[c][h],
-                                sc[c][h]);
+// Converts the copied columns of tokens wr, wr + WR, ..; up[m]: what that token's sums are to
+// be multiplied by.  sb: the tokens' E8M0 bytes of these columns, sb_stride apart.
+template <int XT, int VB>
+__device__ __forceinline__ void convert_x(const MvArgs& a, uint8_t* xs, float* up, const uint8_t* sb, int sb_stride,
+                                          int64_t k0, int n, int wr, int WR, int lane) {
+    constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
+    constexpr int kPiece = 8 * kXSize<XT>;                // bytes of 8 raw columns
+    const int steps = n / kStep<VB>;
+    const int64_t left = a.K - k0;
+    const int pieces = static_cast<int>(left < steps * 256 ? (left > 0 ? left : 0) : steps * 256) / 8;
+    for (int m = wr; m < a.M; m += WR) {
+        uint8_t* cells = xs + m * x_stride<XT, VB>(n);
+        const uint8_t* raw = cells + raw_offset<XT, VB>(n);
+        uint32_t top = 0;
+        if (XT == NVFP4_X_MXFP8) {
+            for (int i = lane; i * 4 < pieces; i += 32) {
+                const uint32_t b = sb[m * sb_stride + i];
+                top = max(top, b == 255 ? 0u : b);
+            }
+        } else {
+            for (int i = lane; i < pieces; i += 32) top = max(top, top8<XT>(raw + kPiece * i));
         }
-        __syncthreads();                                  // the previous slice's x is no longer read
-        for (int m = warp; m < a.M; m += W) {
-            const int e = stage_x<XT, VB>(a, xs, Mp, m, k0, lane);
-            if (lane == 0) ex[m] = e;
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        // scaled to at most 2^15: x by 2^(14 - e), e its exponent (at least -112, so that this is a
+        // float); an E4M3 element by 2^(b - top + 6)
+        const int e = XT == NVFP4_X_MXFP8 ? static_cast<int>(top) - 127 - 6
+                                          : max(static_cast<int>(top >> 23) - 127, -112) - 14;
+        if (lane == 0) up[m] = power_of_two(e);
+        const float down = XT == NVFP4_X_MXFP8 ? 0.0f : power_of_two(-e);
+#pragma unroll 2
+        for (int s = 0; s < steps; ++s) {
+            const int i = s * 32 + lane;                  // piece of 8 columns
+            uint32_t f = __float_as_uint(down);
+            if (XT == NVFP4_X_MXFP8) {
+                const int b = i < pieces ? sb[m * sb_stride + i / 4] : 0;
+                const __half2 f2 = __float2half2_rn(b == 255 ? __int_as_float(0x7FC00000)
+                                                             : power_of_two(max(b - static_cast<int>(top) + 6, -149)));
+                f = *reinterpret_cast<const uint32_t*>(&f2);
+            }
+            uint32_t h[P][4];
+            convert8<XT, P>(raw + kPiece * i, f, h);
+            __syncwarp();                                 // all of the step is read
+            const int j = i % (2 * VB), t = i / (2 * VB) % 4, chunk = i / (8 * VB);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<uint4*>(cells + (((chunk * 2 * VB + j) * P + p) * 4 + t) * 16) =
+                    i < pieces ? make_uint4(h[p][0], h[p][1], h[p][2], h[p][3]) : make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void store_out(const MvArgs& a, int m, int64_t n, float v) {
+    if (a.gamax_mode != NVFP4_GAMAX_NONE) {
+        float enc, dec;
+        global_scales(a.gamax[a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? n : 0], a.bound, enc, dec);
+        v = mul_rn(v, dec);
+    }
+    const int64_t o = static_cast<int64_t>(m) * a.N + n;
+    if (a.out_dtype == NVFP4_F32) static_cast<float*>(a.out)[o] = v;
+    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+}
+
+template <int NT>
+constexpr int kMvRow = 8 * NT * 16;                       // floats of a warp's tile of sums
+
+// Dynamic shared memory: x [WK][M][x_stride(cpw)]; an MXFP8 x's scale bytes [WK][M][2 VB cpw];
+// then the sums kept to the end [tiles][WR][M][16] when the columns are split.  Lane groups
+// past the last token read its values, and their columns are not stored.  Rows past N and
+// blocks past K read the last ones again: such rows are not stored, such blocks meet zeros of x.
+template <int XT, int NT, int VB>
+__global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, const MvPlan p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
+    __shared__ float red[2][kMvWarps][kMvRow<NT>];        // [token][row] of each warp, two tiles in turn
+    __shared__ float up[kMvWarps][16];                    // of each part of the columns
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = p.S > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int WR = kMvWarps / p.WK, wk = warp % p.WK, wr = warp / p.WK;
+    const int g = lane >> 2, t = lane & 3;
+    const int bpr = a.K / 16;
+    const int all_chunks = (bpr + 4 * VB - 1) / (4 * VB);
+    const int tile0 = static_cast<int>(blockIdx.x / p.S) * p.tiles;
+    const int ntiles = min(p.tiles, (a.N + 16 * WR - 1) / (16 * WR) - tile0);
+    const int stride = x_stride<XT, VB>(p.cpw);
+    const int sb_stride = XT == NVFP4_X_MXFP8 ? 2 * VB * p.cpw : 0;
+    uint8_t* xs = smem + static_cast<size_t>(wk) * a.M * stride;
+    uint8_t* sb = smem + static_cast<size_t>(p.WK) * a.M * stride + wk * a.M * sb_stride;
+    float* kept = reinterpret_cast<float*>(smem + static_cast<size_t>(p.WK) * a.M * (stride + sb_stride));
+    const uint8_t* frag[NT];                              // this lane's fragments of its tokens
+#pragma unroll
+    for (int q = 0; q < NT; ++q) frag[q] = xs + min(q * 8 + g, a.M - 1) * stride + t * 16;
+    const bool keep = p.S > 1 || p.rounds > 1;
+    int turn = 0;                                         // of red, over all tiles and rounds
+    pdl_trigger();                                        // the next kernel waits for this one's end itself
+    pdl_wait();
+
+    for (int round = 0; round < p.rounds; ++round) {
+        const int chunk0 = ((round * p.S + rank) * p.WK + wk) * p.cpw;
+        const int n = min(max(all_chunks - chunk0, 0), p.cpw);          // this warp's chunks
+        const int total = ntiles * n;
+        const int64_t k0 = static_cast<int64_t>(chunk0) * 64 * VB;
+        if (round) __syncthreads();                       // the previous round's x is no longer read
+        copy_x<XT, VB>(a, xs, k0, p.cpw, wr, WR, lane);
+        if (XT == NVFP4_X_MXFP8) {
+            const int64_t groups = (static_cast<int64_t>(a.K) + 31) / 32, first = k0 / 32;
+            for (int i = lane; i < sb_stride * a.M; i += 32) {
+                const int m = i / sb_stride;
+                const int64_t q = first + i % sb_stride;
+                if (m % WR == wr) sb[i] = q < groups ? __ldg(a.x_scales + m * groups + q) : 0;
+            }
+        }
+        // loads run kAhead chunks ahead of the products, on into the next tiles
+        uint32_t w[kAhead<VB>][2][2 * VB], sc[kAhead<VB>][2];
+        int lt = 0, lc = 0;
+        int64_t r0, r1;                                   // first blocks of rows g and g + 8 of tile lt
+        auto rows = [&] {
+            const int row = ((tile0 + lt) * WR + wr) * 16 + g;
+            r0 = static_cast<int64_t>(min(row, a.N - 1)) * bpr;
+            r1 = static_cast<int64_t>(min(row + 8, a.N - 1)) * bpr;
+        };
+        rows();
+        auto load = [&](int u) {
+            if (lt >= ntiles || n == 0) return;
+            const int blk = min(((chunk0 + lc) * 4 + t) * VB, bpr - VB);
+            load_blocks<VB>(a.codes + (r0 + blk) * 8, a.scales + (r0 + blk), w[u][0], sc[u][0]);
+            load_blocks<VB>(a.codes + (r1 + blk) * 8, a.scales + (r1 + blk), w[u][1], sc[u][1]);
+            if (++lc == n) {
+                lc = 0;
+                ++lt;
+                rows();
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead<VB>; ++u) load(u);
+        cp_async_wait<0>();
+        __syncwarp();
+        convert_x<XT, VB>(a, xs, up[wk], sb, sb_stride, k0, p.cpw, wr, WR, lane);
         __syncthreads();
         float acc[NT][4];
+        int c = 0, tile = 0;
+        auto clear = [&](float (*f)[4]) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) f[q][i] = 0.0f;
+        };
+        // a row group's sums of a tile, added in the order of its WK warps by the threads of (token, row)
+        auto end_tile = [&] {
+            float* r = red[turn][warp];
 #pragma unroll
-        for (int c = 0; c < kMvChunks; ++c) {
-            if (k0 + c * 64 * VB >= a.K) break;
-            uint32_t s[2][VB];
-            scale_pairs<VB>(sc[c][0], s[0]);
-            scale_pairs<VB>(sc[c][1], s[1]);
-            float d[NT][4];
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < 4; ++i) {
+                    const int m = q * 8 + 2 * t + (i & 1);
+                    if (m < a.M) r[m * 16 + g + 8 * (i >> 1)] = mul_rn(acc[q][i], up[wk][m]);
+                }
+            // by number, one barrier a row group: its warps come here from different steps of the loop below
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * p.WK) : "memory");
+            for (int i = wk * 32 + lane; i < a.M * 16; i += 32 * p.WK) {
+                float v = 0.0f;
+                for (int q = 0; q < p.WK; ++q) v = add_rn(v, red[turn][wr * p.WK + q][i]);
+                if (keep) {
+                    float* k = kept + (tile * WR + wr) * a.M * 16 + i;
+                    *k = round ? add_rn(*k, v) : v;
+                } else {
+                    const int64_t row = static_cast<int64_t>((tile0 + tile) * WR + wr) * 16 + (i & 15);
+                    if (row < a.N) store_out(a, i >> 4, row, v);
+                }
+            }
+            clear(acc);
+            c = 0;
+            ++tile;
+            turn ^= 1;
+        };
+        clear(acc);
+        for (int i0 = 0; i0 < total; i0 += kAhead<VB>) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+            for (int u = 0; u < kAhead<VB>; ++u) {
+                if (i0 + u >= total) break;
+                uint32_t s[2][VB];
+                scale_pairs<VB>(sc[u][0], s[0]);
+                scale_pairs<VB>(sc[u][1], s[1]);
+                const int at = c * (128 * VB * P);
+                float d[NT][4];
+                clear(d);
 #pragma unroll
-            for (int j = 0; j < 2 * VB; ++j) {            // word j of each row: two products
-                uint32_t A[2][4];
+                for (int j = 0; j < 2 * VB; ++j) {        // word j of each row: two products
+                    uint32_t A[2][4];
+                    weights8(w[u][0][j], s[0][j / 2], A[0]);
+                    weights8(w[u][1][j], s[1][j / 2], A[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) A[h][i] = weight2(w[c][h][j], i, s[h][j / 2]);
+                        for (int h = 0; h < P; ++h) {
+                            const uint4 b = *reinterpret_cast<const uint4*>(frag[q] + at + (j * P + h) * 64);
+                            mma_f16(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
+                            mma_f16(d[q], A[0][2], A[1][2], A[0][3], A[1][3], b.z, b.w);
+                        }
+                    if (j % 4 == 3 || j == 2 * VB - 1) {  // the chain's end
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                        for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const int tok = (n * 8 + g) & (Mp - 1);
-                        const uint4 b = xs[(((c * 2 * VB + j) * P + p) * Mp + tok) * 4 + t];
-                        mma_f16(d[n], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
-                        mma_f16(d[n], A[0][2], A[1][2], A[0][3], A[1][3], b.z, b.w);
+                            for (int i = 0; i < 4; ++i) acc[q][i] = add_rn(acc[q][i], d[q][i]);
+                        clear(d);
                     }
+                }
+                load(u);
+                if (++c == n) end_tile();
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = add_rn(acc[n][i], d[n][i]);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = n * 8 + 2 * t + (i & 1);
-                if (m < a.M) tot[n][i] = add_rn(tot[n][i], ldexpf(acc[n][i], ex[m]));
+        while (tile < ntiles) end_tile();                 // a warp with no columns takes part with zeros
+    }
+    if (keep) {
+        // the parts of the columns, added in rank order
+        if (p.S > 1) cluster.sync();
+        else __syncthreads();
+        for (int i = rank * blockDim.x + tid; i < ntiles * WR * a.M * 16; i += p.S * blockDim.x) {
+            const int64_t row = (static_cast<int64_t>(tile0) * WR + i / (a.M * 16)) * 16 + (i & 15);
+            if (row >= a.N) continue;
+            float v = kept[i];
+            if (p.S > 1) {
+                v = 0.0f;
+                for (int q = 0; q < p.S; ++q) v = add_rn(v, *cluster.map_shared_rank(kept + i, q));
             }
-    }
-    // the cluster's partial sums, added in rank order
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = n * 8 + 2 * t + (i & 1);
-            if (m < a.M) part[m * R + warp * 16 + g + 8 * (i >> 1)] = tot[n][i];
+            store_out(a, i / 16 % a.M, row, v);
         }
-    cluster.sync();
-    for (int i = rank * blockDim.x + tid; i < a.M * R; i += S * blockDim.x) {
-        const int m = i / R;
-        const int64_t n = row0 + i % R;
-        if (n >= a.N) continue;
-        float v = 0.0f;
-        for (int q = 0; q < S; ++q) v = add_rn(v, *cluster.map_shared_rank(part + i, q));
-        if (a.gamax_mode != NVFP4_GAMAX_NONE) {
-            float enc, dec;
-            global_scales(a.gamax[a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? n : 0], a.bound, enc, dec);
-            v = mul_rn(v, dec);
-        }
-        const int64_t o = static_cast<int64_t>(m) * a.N + n;
-        if (a.out_dtype == NVFP4_F32) static_cast<float*>(a.out)[o] = v;
-        else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+        if (p.S > 1) cluster.sync();                      // kept is read by the whole cluster
     }
-    cluster.sync();                                       // part is read by the whole cluster
-    pdl_trigger();
+}
+
+// The cut whose longest row of CTAs takes the least time, in the time of a warp's chunk of
+// 256 columns: S parts of the columns over a cluster and WK over a CTA's warps (what does
+// not fit a CTA's shared memory takes more rounds), the row tiles spread over the clusters
+// that run at once.  A tile's end costs about half a chunk, a cluster's two barriers about
+// two, staging about one per 2 KB of a CTA's x.
+template <int XT, int VB>
+MvPlan plan_mv(const MvArgs& a) {
+    const int64_t chunks = (static_cast<int64_t>(a.K) + 64 * VB - 1) / (64 * VB);
+    const int64_t rows = (static_cast<int64_t>(a.N) + 15) / 16;
+    MvPlan best = {};
+    double least = -1.0;
+    for (int S = 1; S <= kMvMaxCluster; ++S)
+        for (int WK = 1; WK <= kMvWarps; WK *= 2) {
+            if (S * WK > 1 && static_cast<int64_t>(S * WK - 1) >= chunks) continue;      // a part without columns
+            const int most = ((kMvMaxX / (WK * a.M) - 64) / (x_stride<XT, VB>(1) - 64)) / kStep<VB> * kStep<VB>;
+            if (most < 1) continue;
+            const int WR = kMvWarps / WK;
+            int64_t cpw = (chunks + S * WK - 1) / (S * WK);
+            const int64_t rounds = (cpw + most - 1) / most;
+            cpw = ((cpw + rounds - 1) / rounds + kStep<VB> - 1) / kStep<VB> * kStep<VB>;
+            const int64_t row_tiles = (rows + WR - 1) / WR;
+            const int64_t clusters = static_cast<int64_t>(kMvCtas) * sm_count() / S;
+            int64_t tiles = (row_tiles + clusters - 1) / clusters;
+            if ((S > 1 || rounds > 1) && tiles * WR > kMvMaxTiles) tiles = kMvMaxTiles / WR;
+            const int64_t waves = ((row_tiles + tiles - 1) / tiles + clusters - 1) / clusters;
+            const double chunk = VB / 4.0;
+            const double stage = static_cast<double>(rounds) * WK * a.M * x_stride<XT, VB>(static_cast<int>(cpw)) / 2048;
+            const double time = waves * (tiles * rounds * (cpw * chunk + 0.5) + stage / kMvWarps + (S > 1 ? 2 : 0));
+            if (least < 0 || time < least) {
+                least = time;
+                best = MvPlan{S, WK, static_cast<int>(tiles), static_cast<int>(cpw), static_cast<int>(rounds)};
+            }
+        }
+    return best;
 }
 
 template <int XT, int NT, int VB>
 cudaError_t launch_mv_t(const MvArgs& a, cudaStream_t s) {
-    constexpr int kSlice = kMvChunks * 64 * VB;
-    constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
-    int Mp = 1;
-    while (Mp < a.M) Mp *= 2;
-    const size_t smem = static_cast<size_t>(Mp) * kSlice * 2 * P;
-    const int slices = (a.K + kSlice - 1) / kSlice;
-    // the fewest rounds of at most kMvMaxCluster slices, in equal parts
-    const int rounds = (slices + kMvMaxCluster - 1) / kMvMaxCluster;
-    const int S = (slices + rounds - 1) / rounds;
-    // whole 8-warp CTAs when they fill the SMs, else fewer warps each
-    int W = 8;
-    while (W > 1 && (static_cast<int64_t>(a.N) + 16 * W - 1) / (16 * W) * S < 2 * sm_count()) W /= 2;
-    const int64_t blocks = (static_cast<int64_t>(a.N) + 16 * W - 1) / (16 * W) * S;
+    const MvPlan p = plan_mv<XT, VB>(a);
+    const int64_t WR = kMvWarps / p.WK;
+    const int64_t blocks = ((static_cast<int64_t>(a.N) + 16 * WR - 1) / (16 * WR) + p.tiles - 1) / p.tiles * p.S;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const size_t sb = XT == NVFP4_X_MXFP8 ? 2 * VB * p.cpw : 0;
+    const size_t smem = static_cast<size_t>(p.WK) * a.M * (x_stride<XT, VB>(p.cpw) + sb) +
+                        (p.S > 1 || p.rounds > 1 ? p.tiles * WR * a.M * 64 : 0);
     static thread_local int configured_dev = -1;         // the attribute is per device
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_dev != dev) {
         const cudaError_t e = cudaFuncSetAttribute(k_mv<XT, NT, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   16 * kSlice * 2 * P);
+                                                   kMvMaxX + kMvMaxX / 32 + kMvMaxTiles * 16 * 64);
         if (e != cudaSuccess) return e;
         configured_dev = dev;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(32 * W);
+    cfg.blockDim = dim3(32 * kMvWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.x = p.S;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_mv<XT, NT, VB>, a, Mp);
+    cfg.numAttrs = p.S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_mv<XT, NT, VB>, a, p);
 }
 
 template <int XT>
 cudaError_t launch_mv_x(const MvArgs& a, cudaStream_t s) {
-    if (a.K % 32 == 0) return a.M <= 8 ? launch_mv_t<XT, 1, 2>(a, s) : launch_mv_t<XT, 2, 2>(a, s);
+    if (a.K % 64 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 32 == 0)
+        return a.M <= 8 ? launch_mv_t<XT, 1, 4>(a, s) : launch_mv_t<XT, 2, 4>(a, s);
     return a.M <= 8 ? launch_mv_t<XT, 1, 1>(a, s) : launch_mv_t<XT, 2, 1>(a, s);
 }
 
