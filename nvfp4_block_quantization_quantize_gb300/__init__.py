@@ -60,6 +60,7 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_dequantize", "nvfp4_qdq", "nvfp4_amax",
 
 _lock = threading.Lock()
 _lib = None
+_call = None                                    # the short path of the serving operators (csrc/nvfp4_call.cpp)
 
 
 class NVFP4Error(RuntimeError):
@@ -72,7 +73,7 @@ class NVFP4Error(RuntimeError):
 
 def load_library(path: str | None = None):
     """Load the C library (no CUDA call is made).  Raises if it is not built."""
-    global _lib
+    global _lib, _call
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -116,7 +117,9 @@ def load_library(path: str | None = None):
         lib.nvfp4_abi_version.restype = i32
         lib.nvfp4_abi_version.argtypes = []
         if path is None:
-            _lib = lib
+            from . import _nvfp4_call
+            _nvfp4_call.bind(*[ctypes.cast(f, P).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm)])
+            _lib, _call = lib, _nvfp4_call
         return lib
 
 
@@ -874,11 +877,10 @@ def _check_mm_args(codes_a, scales_a, codes_b, scales_b, M, N, K, gamax_a, gamax
 
 
 # ---- serving operators ------------------------------------------------------------------------
-# Calls on device tensors only.  They are short (a few microseconds of GPU
-# time for single tokens), so their host side is kept short too: pointers go
-# to ctypes as plain integers, the device is switched only when it is not the
-# current one, and a call on a given stream runs wholly on it (copies and
-# allocations too).
+# Calls on device tensors only.  A well-formed call goes through the short path
+# (csrc/nvfp4_call.cpp); it returns None for any other, which is then checked,
+# made contiguous or refused here.  A call on a given stream runs wholly on it
+# (copies and allocations too).
 def _given_stream(stream, dev):
     if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
@@ -935,7 +937,11 @@ def nvfp4_rmsnorm(x: torch.Tensor, weight=None, *, hidden=None, hidden_out=None,
     "row_given"), all uint8.  "hidden" is h rounded to x's dtype: a new tensor,
     or hidden_out (which may be hidden: in place).  "out" (want_out, or a given
     out) is the norm itself in x's dtype; want_codes=False leaves the codes out."""
-    lib = load_library()
+    lib = _lib or load_library()
+    if stream is None and gamax_mode == "none" and want_codes and scale_bound == 448.0:
+        res = _call.rmsnorm(x, weight, hidden, hidden_out, eps, format, want_out, out, codes, scales)
+        if res is not None:
+            return res
     dev = _cuda_2d(x, "x", "nvfp4_rmsnorm")
     if stream is not None:
         with _given_stream(stream, dev):
@@ -986,7 +992,11 @@ def nvfp4_mv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, x_sc
     its global amax (one value or N).  x [M, K]: float32, bfloat16, or E4M3 codes
     (uint8 or float8_e4m3fn) with x_scales [M, ceil(K/32)] E8M0 (uint8 or
     float8_e8m0fnu), as nvfp4_rmsnorm leaves them.  Returns [M, N]."""
-    lib = load_library()
+    lib = _lib or load_library()
+    if stream is None:
+        o = _call.mv(x, codes, scales, x_scales, gamax, scale_bound, out_dtype, out)
+        if o is not None:
+            return o
     dev = _cuda_2d(x, "x", "nvfp4_mv")
     if stream is not None:
         with _given_stream(stream, dev):
@@ -1037,7 +1047,12 @@ def nvfp4_grouped_mm(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: tor
     device (never read on the host).  codes_b [E, N, K/2], scales_b in
     nvfp4_grouped_scales_to_mma's layout, gamax_b one amax per expert.  Returns
     [T, N]; rows in no group are not written.  K a multiple of 64."""
-    lib = load_library()
+    lib = _lib or load_library()
+    if stream is None:
+        o = _call.grouped_mm(codes_a, scales_a, offsets, codes_b, scales_b, gamax_a, gamax_b, scale_bound, out_dtype,
+                             out)
+        if o is not None:
+            return o
     dev = _cuda_2d(codes_a, "codes_a", "nvfp4_grouped_mm")
     if stream is not None:
         with _given_stream(stream, dev):

@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel with ``-gencode
 arch=compute_103a,code=sm_103a`` (GB300 only), then one shared library is
-linked with the static CUDA runtime.  The fp32 steps the method pins must
+linked with the static CUDA runtime.  Beside them g++ compiles
+``_nvfp4_call.so``, the binding's short path for the serving operators (CPython
+and torch headers; it holds no arithmetic).  The fp32 steps the method pins must
 round exactly as written, so the build keeps IEEE division / square root,
 does not flush subnormals and does not contract multiply-adds.
 """
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libnvfp4_gb300.so")
+CALL_PATH = os.path.join(PKG, "_nvfp4_call.so")
 SOURCES = ["nvfp4_rows.cu", "nvfp4_tiles.cu", "nvfp4_aux.cu", "nvfp4_mm.cu", "nvfp4_norm.cu", "nvfp4_mv.cu",
            "nvfp4_grouped.cu", "nvfp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,6 +35,19 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is needed to build libnvfp4_gb300.so")
+
+
+def _call_command(out: str) -> list[str]:
+    import sysconfig
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    libs = ["torch_python", "torch_cuda", "torch_cpu", "c10_cuda", "c10"]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
+            os.path.join(CSRC, "nvfp4_call.cpp"), "-o", out, "-L" + os.path.join(t, "lib"), *["-l" + n for n in libs],
+            "-Wl,-rpath," + os.path.join(t, "lib")]
 
 
 def _deps():
@@ -53,9 +69,9 @@ def source_digest() -> str:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALL_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALL_PATH))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -74,8 +90,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_call():
+        tmp = CALL_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run(_call_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on nvfp4_call.cpp:\n{r.stderr}")
+        return tmp
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        call = ex.submit(compile_call)
         results = list(ex.map(compile_one, SOURCES))
+        os.replace(call.result(), CALL_PATH)
     if verbose or ptxas_info:
         for obj, log in results:
             sys.stderr.write(log)
