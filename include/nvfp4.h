@@ -302,14 +302,18 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
  *   gamax_a      by gamax_a_mode: NULL (NONE), 1 fp32 (TENSOR_GIVEN) or T (ROW_GIVEN)
  *   gamax_b      NULL, or E fp32 (one per expert)
  *   out          [T,N], F32 or BF16; rows in no group are not written
+ *   workspace    device memory of nvfp4_grouped_mm_workspace(E, T, N, K) bytes (NULL when
+ *                that is 0), written and read by this call alone
  * Products are exact and accumulate in fp32.  EINVAL: a negative size, K % 64,
- * E * N, T or K >= 2^31, bad enums, pointers or bound.  A CTA that stops waiting
- * for its tensor-core work writes NaN to its tile of out.
+ * E * N, T or K >= 2^31, bad enums, pointers or bound, a workspace that is too
+ * small.  A CTA that stops waiting for its tensor-core work writes NaN to its tile
+ * of out.
  */
+int64_t nvfp4_grouped_mm_workspace(int64_t E, int64_t T, int64_t N, int64_t K);
 int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int64_t* offsets,
                      const uint8_t* codes_b, const uint8_t* scales_b, int64_t E, int64_t T, int64_t N, int64_t K,
                      int gamax_a_mode, const float* gamax_a, const float* gamax_b, float scale_bound, void* out,
-                     int out_dtype, cudaStream_t stream);
+                     int out_dtype, uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * nvfp4_probe_divide -- diagnostic.  out[i] = a[i] / b[i] computed by the

@@ -111,14 +111,17 @@ def load_library(path: str | None = None):
         lib.nvfp4_mv.restype = i32
         lib.nvfp4_mv.argtypes = [P, P, i32, P, P, i64, i64, i64, i32, P, f32, P, i32, P]
         lib.nvfp4_grouped_mm.restype = i32
-        lib.nvfp4_grouped_mm.argtypes = [P, P, P, P, P, i64, i64, i64, i64, i32, P, P, f32, P, i32, P]
+        lib.nvfp4_grouped_mm.argtypes = [P, P, P, P, P, i64, i64, i64, i64, i32, P, P, f32, P, i32, P, i64, P]
+        lib.nvfp4_grouped_mm_workspace.restype = i64
+        lib.nvfp4_grouped_mm_workspace.argtypes = [i64, i64, i64, i64]
         lib.nvfp4_last_error.restype = ctypes.c_char_p
         lib.nvfp4_last_error.argtypes = []
         lib.nvfp4_abi_version.restype = i32
         lib.nvfp4_abi_version.argtypes = []
         if path is None:
             from . import _nvfp4_call
-            _nvfp4_call.bind(*[ctypes.cast(f, P).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm)])
+            _nvfp4_call.bind(*[ctypes.cast(f, P).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm,
+                                                                     lib.nvfp4_grouped_mm_workspace)])
             _lib, _call = lib, _nvfp4_call
         return lib
 
@@ -1073,8 +1076,11 @@ def nvfp4_grouped_mm(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: tor
     odt = _enum("dtype", out_dtype)
     tdt = torch.float32 if odt == F32 else torch.bfloat16
     o = torch.empty((T, N), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, T * N, dev)
+    need = lib.nvfp4_grouped_mm_workspace(E, T, N, K)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _launch(lib, lib.nvfp4_grouped_mm, dev, ca.data_ptr(), sa.data_ptr(), offsets.data_ptr(), codes_b.data_ptr(),
-            scales_b.data_ptr(), E, T, N, K, gm, _addr(ga), _addr(gamax_b), scale_bound, o.data_ptr(), odt)
+            scales_b.data_ptr(), E, T, N, K, gm, _addr(ga), _addr(gamax_b), scale_bound, o.data_ptr(), odt, _addr(ws),
+            need)
     return o
 
 

@@ -329,10 +329,18 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
     return NVFP4_OK;
 }
 
+int64_t nvfp4_grouped_mm_workspace(int64_t E, int64_t T, int64_t N, int64_t K) {
+    constexpr int64_t kMax = int64_t{1} << 31;
+    if (E <= 0 || T <= 0 || N <= 0 || K <= 0 || E >= kMax || T >= kMax || N >= kMax || K >= kMax) return 0;
+    nvfp4::GroupedArgs a = {};
+    a.E = E, a.T = T, a.N = N, a.K = K;
+    return nvfp4::grouped_workspace(a);
+}
+
 int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int64_t* offsets,
                      const uint8_t* codes_b, const uint8_t* scales_b, int64_t E, int64_t T, int64_t N, int64_t K,
                      int gamax_a_mode, const float* gamax_a, const float* gamax_b, float scale_bound, void* out,
-                     int out_dtype, cudaStream_t stream) {
+                     int out_dtype, uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream) {
     g_msg[0] = '\0';
     constexpr int64_t kMax = int64_t{1} << 31;
     if (E < 0 || T < 0 || N < 0 || K < 0) return fail(NVFP4_EINVAL, "E, T, N and K must be >= 0");
@@ -357,7 +365,11 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
     if ((rc = check_ptr(out, "out", any))) return rc;
     if (!any) return NVFP4_OK;
     const nvfp4::GroupedArgs a{codes_a, scales_a, offsets, codes_b, scales_b, E, T, N, K, gamax_a_mode, gamax_a,
-                               gamax_b, scale_bound, out, out_dtype};
+                               gamax_b, scale_bound, out, out_dtype, workspace};
+    const int64_t need = nvfp4::grouped_workspace(a);
+    if (workspace_bytes < need)
+        return fail(NVFP4_EINVAL, "the workspace needs %lld bytes (got %lld)", (long long)need, (long long)workspace_bytes);
+    if ((rc = check_ptr(workspace, "workspace", need > 0))) return rc;
     const int err = nvfp4::launch_grouped_mm(a, stream);
     if (err) return cuda_fail(err, "grouped mm launch");
     return NVFP4_OK;

@@ -25,6 +25,7 @@ namespace {
 decltype(&nvfp4_rmsnorm) f_rmsnorm = nullptr;
 decltype(&nvfp4_mv) f_mv = nullptr;
 decltype(&nvfp4_grouped_mm) f_grouped_mm = nullptr;
+decltype(&nvfp4_grouped_mm_workspace) f_grouped_ws = nullptr;
 
 PyObject* none() { Py_RETURN_NONE; }
 
@@ -79,6 +80,22 @@ at::Tensor empty(int64_t rows, int64_t cols, at::ScalarType type, int dev) {
                                   std::nullopt);
 }
 
+// Outputs up to this many bytes together share one allocation (an allocation costs
+// about 2 us on the Grace host between other work; larger ones are kept apart so that
+// one output does not hold the others' memory).
+constexpr int64_t kShared = 1 << 20;
+
+// a contiguous tensor of `base`'s storage from byte `at` on, which moves past it (to a multiple of 256)
+at::Tensor part(const at::Tensor& base, int64_t* at, int64_t rows, int64_t cols, at::ScalarType type) {
+    const int64_t size = static_cast<int64_t>(c10::elementSize(type));
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(*at / size);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({rows, cols});
+    *at += (rows * cols * size + 255) / 256 * 256;
+    return t;
+}
+
 // the global amax of `rows` rows: one value or one per row
 bool rows_gamax(PyObject* o, int64_t rows, int dev, int* mode, const at::Tensor** t) {
     *t = nullptr;
@@ -90,12 +107,15 @@ bool rows_gamax(PyObject* o, int64_t rows, int dev, int* mode, const at::Tensor*
     return (*t)->numel() == 1 || (*t)->numel() == rows;
 }
 
-// the output [rows, cols]: the given tensor, or a new one
-bool output(PyObject* o, int64_t rows, int64_t cols, at::ScalarType type, int dev, at::Tensor* t) {
+// the output [rows, cols]: the given tensor, or a new one (a part of `shared` when that is defined)
+bool output(PyObject* o, int64_t rows, int64_t cols, at::ScalarType type, int dev, at::Tensor* t,
+            const at::Tensor* shared = nullptr, int64_t* at = nullptr) {
     if (given(o)) {
         const at::Tensor* g = tensor(o, dev, type, rows * cols);
         if (!g) return false;
         *t = *g;
+    } else if (shared && shared->defined()) {
+        *t = part(*shared, at, rows, cols, type);
     } else {
         *t = empty(rows, cols, type, dev);
     }
@@ -180,11 +200,15 @@ PyObject* grouped_mm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (odt < 0 || !rows_gamax(v[5], T, dev, &mode, &ga) ||
             !output(v[9], T, N, odt == NVFP4_F32 ? at::kFloat : at::kBFloat16, dev, &out))
             return none();
+        const int64_t need = f_grouped_ws(E, T, N, K);
+        at::Tensor ws;                                    // free for the stream's next work once this call is enqueued
+        if (need > 0) ws = empty(1, need, at::kByte, dev);
         const int rc = f_grouped_mm(
             static_cast<const uint8_t*>(ca->data_ptr()), static_cast<const uint8_t*>(sa->data_ptr()),
             static_cast<const int64_t*>(off->data_ptr()), static_cast<const uint8_t*>(cb->data_ptr()),
             static_cast<const uint8_t*>(sb->data_ptr()), E, T, N, K, mode, static_cast<const float*>(data(ga)),
             static_cast<const float*>(data(gb)), bound, out.data_ptr(), odt,
+            need > 0 ? static_cast<uint8_t*>(ws.data_ptr()) : nullptr, need,
             c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
         return rc == NVFP4_OK ? wrap(v[9], out) : none();
     });
@@ -214,18 +238,18 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
             w = tensor(v[1], dev);
             if (!w || w->numel() != K || (wdt = dtype_of(*w)) < 0) return none();
         }
-        at::Tensor hidden_out, out, codes, scales;
-        if (given(v[2])) {
-            hidden = tensor(v[2], dev, x->scalar_type(), M * K);
-            if (!hidden || !output(v[3], M, K, x->scalar_type(), dev, &hidden_out)) return none();
-        } else if (given(v[3])) {
-            return none();
-        }
-        const bool want_out = given(v[7]) || v[6] == Py_True;
-        if (want_out && !output(v[7], M, K, x->scalar_type(), dev, &out)) return none();
-        const bool mx = fmt == NVFP4_FMT_MXFP8;
-        if (!output(v[8], M, mx ? K : K / 2, at::kByte, dev, &codes) ||
-            !output(v[9], M, mx ? (K + 31) / 32 : K / 16, at::kByte, dev, &scales))
+        at::Tensor hidden_out, out, codes, scales, shared;
+        if (given(v[2]) ? !(hidden = tensor(v[2], dev, x->scalar_type(), M * K)) : given(v[3])) return none();
+        const bool want_out = given(v[7]) || v[6] == Py_True, mx = fmt == NVFP4_FMT_MXFP8;
+        const int64_t cols = mx ? K : K / 2, groups = mx ? (K + 31) / 32 : K / 16;
+        const int64_t full = M * K * static_cast<int64_t>(x->element_size());
+        const int64_t bytes = (hidden ? full : 0) + (want_out ? full : 0) + M * (cols + groups) + 4 * 256;
+        int64_t at = 0;
+        if (bytes <= kShared) shared = empty(1, bytes, at::kByte, dev);
+        if ((hidden && !output(v[3], M, K, x->scalar_type(), dev, &hidden_out, &shared, &at)) ||
+            (want_out && !output(v[7], M, K, x->scalar_type(), dev, &out, &shared, &at)) ||
+            !output(v[8], M, cols, at::kByte, dev, &codes, &shared, &at) ||
+            !output(v[9], M, groups, at::kByte, dev, &scales, &shared, &at))
             return none();
         const int rc = f_rmsnorm(
             x->data_ptr(), data(hidden), M, K, dt, data(w), wdt, eps, hidden ? hidden_out.data_ptr() : nullptr,
@@ -244,13 +268,14 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
-// bind(rmsnorm, mv, grouped_mm): the addresses of the C ABI's functions in the loaded library
+// bind(rmsnorm, mv, grouped_mm, grouped_mm_workspace): the addresses of the C ABI's functions in the loaded library
 PyObject* bind(PyObject*, PyObject* args) {
-    unsigned long long a, b, c;
-    if (!PyArg_ParseTuple(args, "KKK", &a, &b, &c)) return nullptr;
+    unsigned long long a, b, c, d;
+    if (!PyArg_ParseTuple(args, "KKKK", &a, &b, &c, &d)) return nullptr;
     f_rmsnorm = reinterpret_cast<decltype(f_rmsnorm)>(static_cast<uintptr_t>(a));
     f_mv = reinterpret_cast<decltype(f_mv)>(static_cast<uintptr_t>(b));
     f_grouped_mm = reinterpret_cast<decltype(f_grouped_mm)>(static_cast<uintptr_t>(c));
+    f_grouped_ws = reinterpret_cast<decltype(f_grouped_ws)>(static_cast<uintptr_t>(d));
     Py_RETURN_NONE;
 }
 

@@ -51,36 +51,41 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// token tile `slot` of the groups: its expert, first row and row count (0: none)
-__device__ __forceinline__ void find_tile(const GroupedArgs& a, int64_t slot, int BT, int& expert, int64_t& row,
-                                          int& rows) {
+// rows [lo, hi) of expert e, the offsets clamped to [0, T]
+__device__ __forceinline__ void group_rows(const GroupedArgs& a, int e, int& lo, int& hi) {
+    const long long* off = reinterpret_cast<const long long*>(a.offsets) + e;
+    const long long T = a.T;
+    lo = static_cast<int>(min(max(__ldg(off), 0LL), T));
+    hi = max(static_cast<int>(min(max(__ldg(off + 1), 0LL), T)), lo);
+}
+
+// Token tile `slot` of the groups: its expert, first row and row count (0: past the
+// last).  A whole warp calls it; T < 2^31, so 32 bits do.
+__device__ __forceinline__ void find_tile(const GroupedArgs& a, int slot, int BT, int& expert, int& row, int& rows) {
     const int lane = threadIdx.x & 31;
     expert = 0;
     row = 0;
     rows = 0;
-    int64_t before = 0;                                   // tiles of the experts seen so far
-    for (int64_t e0 = 0; e0 < a.E; e0 += 32) {
-        const int64_t e = e0 + lane;
-        int64_t lo = 0, n = 0;
-        if (e < a.E) {
-            lo = min(max(a.offsets[e], int64_t{0}), a.T);
-            n = max(min(max(a.offsets[e + 1], int64_t{0}), a.T) - lo, int64_t{0});
-        }
-        const int64_t tiles = (n + BT - 1) / BT;
-        int64_t upto = tiles;                             // inclusive scan over the lanes
+    int before = 0;                                       // tiles of the experts seen so far
+    for (int e0 = 0; e0 < static_cast<int>(a.E); e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < a.E) group_rows(a, e, lo, hi);
+        const int n = hi - lo;
+        const int tiles = (n + BT - 1) / BT;
+        int upto = tiles;                                 // inclusive scan over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += u;
         }
         const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + upto > slot);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            const int64_t first = before + __shfl_sync(0xFFFFFFFFu, upto - tiles, l);
-            const int64_t at = (slot - first) * BT;
-            expert = static_cast<int>(e0 + l);
+            const int at = (slot - before - __shfl_sync(0xFFFFFFFFu, upto - tiles, l)) * BT;
+            expert = e0 + l;
             row = __shfl_sync(0xFFFFFFFFu, lo, l) + at;
-            rows = static_cast<int>(min(__shfl_sync(0xFFFFFFFFu, n, l) - at, static_cast<int64_t>(BT)));
+            rows = min(__shfl_sync(0xFFFFFFFFu, n, l) - at, BT);
             return;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -88,10 +93,10 @@ __device__ __forceinline__ void find_tile(const GroupedArgs& a, int64_t slot, in
 }
 
 // the 16 scale bytes of token row `row` from step k0 on (zeros past its last step)
-__device__ __forceinline__ uint4 token_scales(const GroupedArgs& a, int64_t row, int k0, int ksteps) {
+__device__ __forceinline__ uint4 token_scales(const GroupedArgs& a, int row, int k0, int ksteps) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (k0 >= ksteps) return v;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.scales_a) + row * ksteps + k0;   // 4 bytes a step
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.scales_a) + static_cast<int64_t>(row) * ksteps + k0;
     if (ksteps % 4 == 0) return __ldg(reinterpret_cast<const uint4*>(p));
     v.x = __ldg(p);
     if (k0 + 1 < ksteps) v.y = __ldg(p + 1);
@@ -112,10 +117,10 @@ __global__ void __launch_bounds__(kGmThreads)
     __shared__ int timed_out;
     __shared__ float alpha[BT];
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);               // the same for the whole warp, and known to be
     pdl_wait();
-    int expert, rows;
-    int64_t row0;
+    int expert, row0, rows;
     find_tile(a, blockIdx.x % tiles, BT, expert, row0, rows);
     if (rows == 0) return;                                // the same for the whole CTA
     const int ntile = static_cast<int>(blockIdx.x) / tiles;
@@ -165,15 +170,15 @@ __global__ void __launch_bounds__(kGmThreads)
             uint8_t* slot = smem + s * G::kSlot;
             mbar_expect_tx(&full[s], static_cast<uint32_t>(G::kSlotW + G::kSlotT + nk * 512));
             tma_2d(slot, &mapW, k0 * 32, wrow, &full[s]);
-            tma_2d(slot + G::kSlotW, &mapT, k0 * 32, static_cast<int>(row0), &full[s]);
+            tma_2d(slot + G::kSlotW, &mapT, k0 * 32, row0, &full[s]);
             bulk_copy(slot + G::kSlotW + G::kSlotT, sfw + static_cast<int64_t>(k0) * 512, nk * 512, &full[s]);
         }
-    } else if (tid == 32) {
-        // ---- products ----
-        const uint32_t idesc = instr_desc(kGmRows, BT);
+    } else if (warp == 1) {
+        // ---- products (the whole warp issues, one lane's predicate guards) ----
+        const uint32_t idesc = instr_desc(kGmRows, BT), el = elect_one();
         for (int t = 0; t < nstages; ++t) {
             const int s = t % G::kStages;
-            if (timed_out || !mbar_wait(&full[s], static_cast<uint32_t>((t / G::kStages) & 1))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], static_cast<uint32_t>((t / G::kStages) & 1)))) {
                 timed_out = 1;
                 break;
             }
@@ -188,18 +193,15 @@ __global__ void __launch_bounds__(kGmThreads)
             for (int kk = 0; kk < kGmStageK; ++kk) {
                 if (kk >= nk) break;
                 const uint32_t c = c0 + kk * G::kSfCols;
-                asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(c), "l"(dsw + kk * 32));
+                copy_scales_warp<1>(el, c, dsw + kk * 32);
 #pragma unroll
                 for (int j = 0; j < G::kSfbTiles; ++j)
-                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(c + 4 + 4 * j),
-                                 "l"(dst + (kk * G::kSfbTiles + j) * 32));
-                mma_f4(tmem, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, t + kk > 0 ? 1u : 0u);
+                    copy_scales_warp<1>(el, c + 4 + 4 * j, dst + (kk * G::kSfbTiles + j) * 32);
+                mma_f4_warp<1>(el, tmem, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, t + kk > 0 ? 1u : 0u);
             }
-            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                smem_addr(&empty[s])));
+            commit_warp<1>(el, &empty[s]);
         }
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_addr(&accb)));
+        commit_warp<1>(el, &accb);
     } else if (warp >= 4 && warp < 4 + G::kSfWarps) {
         // ---- the tokens' scales: rows i and, of 256-token tiles, i + 128 ----
         const int i = tid - 128;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kGmThreads)
                 // no stage at all (K == 0): the accumulator was never written
                 const float acc = nstages ? __uint_as_float(v[i]) : 0.0f;
                 const float f = bad ? __int_as_float(0x7FC00000) : mul_rn(acc, alpha[c0 + i]);
-                const int64_t o = (row0 + c0 + i) * a.N + n;
+                const int64_t o = static_cast<int64_t>(row0 + c0 + i) * a.N + n;
                 if (ODT == NVFP4_F32) static_cast<float*>(a.out)[o] = f;
                 else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f);
             }
@@ -272,6 +274,389 @@ __global__ void __launch_bounds__(kGmThreads)
     __syncthreads();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmem));
+}
+
+// ---- many tokens an expert: pairs of SMs -------------------------------------------------------
+// The same product with tcgen05 .cta_group::2: the two CTAs of a cluster share a tile of 256
+// weight rows (128 each, and their accumulator lanes) times up to 192 tokens (each CTA
+// stages half of them), so a CTA loads 28 KB of codes per 256 columns for 128 x 192 outputs
+// instead of 32 KB for 128 x 128: a 128 x 128 tile wants about 140 bytes a clock per SM
+// from L2 at the FP4 rate, more than it gives.  Two accumulators (2 x 192 of 512
+// tensor-memory columns) let the stores of one tile overlap the products of the next;
+// one persistent CTA per SM walks the tiles, token tiles fastest.
+//   warp 0       TMA of the CTA's own half of a stage, all of it signalling the first
+//                CTA's barrier (a thread's own release to the other CTA would cost
+//                about 0.9 us a stage, measured, against 0.2 us of products)
+//   warp 1       in the first CTA: scale copies and MMAs for both
+//   warps 2-9    accumulator to global memory
+// The tokens' scales are laid out for the tiles by a kernel before (k_token_scales, into
+// the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
+// group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
+// unfinished tiles become NaN.
+#ifndef PAIRMEAN
+#define PAIRMEAN 64
+#endif
+constexpr int kPairMean = PAIRMEAN;
+constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
+constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
+constexpr int kGpBT = 192;
+constexpr int kGpStages = 6;
+constexpr int kGpSlotW = 128 * 128, kGpSlotT = kGpBT / 2 * 128;
+constexpr int kGpSlotSfw = kGmStageK * 512, kGpSlotSft = kGmStageK * 1024;
+constexpr int kGpSlot = kGpSlotW + kGpSlotT + kGpSlotSfw + kGpSlotSft;       // 34 KB
+constexpr int kGpTurn = 32 * 64;                          // bytes a store warp turns at once: 32 tokens x 32 rows of bf16
+constexpr int kGpSmem = kGpStages * kGpSlot + kGpStoreWarps * kGpTurn + 1024;
+constexpr int kGpGroups = 256;                            // experts whose places are kept in shared memory
+constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages of 4 steps of 4 + 8 columns
+
+// token tiles of 192 rows, at most: all full ones, and one partial one a group
+int64_t pair_slots(const GroupedArgs& a) { return a.T / kGpBT + (a.E < a.T ? a.E : a.T); }
+
+// The token tiles' scales in the tensor cores' layout: tile (slot, step, half) of 512
+// bytes at (slot * ksteps + step) * 2 + half, word (r % 32) * 4 + r / 32 of it row r's
+// four bytes of the step.  One CTA a slot; a thread takes row tid, so that a row's
+// bytes are read by one thread, 16 at a time.
+__global__ void __launch_bounds__(256) k_token_scales(const GroupedArgs a, uint32_t* out) {
+    pdl_trigger();                                        // the product waits for this kernel's end itself
+    pdl_wait();
+    int expert, row0, rows;
+    find_tile(a, blockIdx.x, kGpBT, expert, row0, rows);
+    const int ksteps = static_cast<int>(a.K / 64), i = threadIdx.x;
+    if (rows == 0 || i >= (rows + 31) / 32 * 32) return;  // what the product copies but no stored column uses stays
+    for (int k0 = blockIdx.y * 8; k0 < min(ksteps, static_cast<int>(blockIdx.y + 1) * 8); k0 += 4) {
+        const uint4 v = i < rows ? token_scales(a, row0 + i, k0, ksteps) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t* o = out + ((static_cast<int64_t>(blockIdx.x) * ksteps + k0) * 2 + i / 128) * 128 + (i % 32) * 4 + i % 128 / 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k0 + k < ksteps) o[k * 256] = w[k];
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// mbar_wait for arrivals from the other CTA of the pair
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+    for (long it = 0; it < kWaitLimit; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
+// TMA into this CTA's shared memory, signalling the barrier at cluster address bar (of either CTA)
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <int ODT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
+    k_grouped_pair(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapT,
+                   const __grid_constant__ CUtensorMap mapSW, const __grid_constant__ CUtensorMap mapST,
+                   const GroupedArgs a, unsigned slots, unsigned all_tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t full[kGpStages], empty[kGpStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int timed_out;
+    __shared__ __align__(16) float alpha[2][kGpBT];
+    __shared__ int tiles_to[kGpGroups], first_row[kGpGroups], end_row[kGpGroups];     // of each expert
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);               // the same for the whole warp, and known to be
+    const int rank = static_cast<int>(blockIdx.x & 1);
+    const unsigned pairs = gridDim.x / 2;
+    const int ksteps = static_cast<int>(a.K / 64);
+    const int nstages = (ksteps + kGmStageK - 1) / kGmStageK;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    if (tid == 32) {
+        for (int i = 0; i < kGpStages; ++i) {
+            mbar_init(&full[i]);                          // used in the first CTA: both CTAs' transactions
+            mbar_init(&empty[i]);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i]);
+            mbar_init(&acc_empty[i], 2 * kGpStoreWarps);  // of both CTAs
+        }
+        timed_out = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const uint32_t tmem = tmem_base;
+    pdl_trigger();                                        // the next kernel waits for this one's end itself
+    pdl_wait();
+
+    // the experts' rows, and the token tiles up to each: what find_tile makes of the offsets, once
+    const bool few = a.E <= kGpGroups;
+    if (few) {
+        for (int e = tid; e < a.E; e += kGpThreads) group_rows(a, e, first_row[e], end_row[e]);
+        __syncthreads();
+        if (warp == 0) {
+            int before = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const int e = e0 + lane;
+                int upto = e < a.E ? (end_row[e] - first_row[e] + kGpBT - 1) / kGpBT : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += u;
+                }
+                if (e < a.E) tiles_to[e] = before + upto;
+                before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            }
+        }
+        __syncthreads();
+    }
+    auto find = [&](int slot, int& expert, int& row0, int& rows) {
+        if (!few) return find_tile(a, slot, kGpBT, expert, row0, rows);
+        expert = row0 = rows = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, e0 + lane < a.E && tiles_to[e0 + lane] > slot);
+            if (!hit) continue;
+            expert = e0 + __ffs(hit) - 1;
+            row0 = first_row[expert] + (slot - (expert ? tiles_to[expert - 1] : 0)) * kGpBT;
+            rows = min(end_row[expert] - row0, kGpBT);
+            return;
+        }
+    };
+    int st = 0, it = 0;                                   // stages and (non-empty) tiles so far
+    // one pass over the pair's tiles, the same in every role
+    auto each_tile = [&](auto body) {
+        for (unsigned tile = blockIdx.x / 2; tile < all_tiles; tile += pairs) {
+            const int slot = static_cast<int>(tile % slots);
+            int expert, row0, rows;
+            find(slot, expert, row0, rows);
+            // the same in all lanes; the reduction lets the compiler know
+            rows = __reduce_max_sync(0xFFFFFFFFu, rows);
+            if (rows == 0) continue;
+            const int N = (rows + 31) / 32 * 32;
+            if (!body(static_cast<int>(tile / slots), slot, expert, row0, rows, N)) return;
+            ++it;
+        }
+    };
+    if (warp == 0) {
+        const int sf_tiles = static_cast<int>((a.N + 127) / 128);
+        each_tile([&](int ntile, int slot, int expert, int row0, int, int N) {
+            const int n0 = ntile * 256 + rank * 128;
+            const int wrow = expert * static_cast<int>(a.N) + n0, trow = row0 + rank * (N / 2);
+            // a pair's second half past N has no scale tile of its own: any one will do
+            const int sfw = (expert * sf_tiles + min(n0 / 128, sf_tiles - 1)) * ksteps, sft = slot * ksteps * 2;
+            for (int t = 0; t < nstages; ++t, ++st) {
+                const int s = st % kGpStages;
+                if (st >= kGpStages && !mbar_wait_cluster(&empty[s], static_cast<uint32_t>((st / kGpStages - 1) & 1))) {
+                    timed_out = 1;
+                    return false;
+                }
+                if (lane == 0) {
+                    const int k0 = t * kGmStageK;
+                    uint8_t* dst = smem + s * kGpSlot;
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * kGpSlot);
+                    tma_2d_pair(dst, &mapW, k0 * 32, wrow, bar);
+                    tma_2d_pair(dst + kGpSlotW, &mapT, k0 * 32, trow, bar);
+                    tma_2d_pair(dst + kGpSlotW + kGpSlotT, &mapSW, 0, sfw + k0, bar);
+                    tma_2d_pair(dst + kGpSlotW + kGpSlotT + kGpSlotSfw, &mapST, 0, sft + 2 * k0, bar);
+                }
+                __syncwarp();
+            }
+            return true;
+        });
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t el = elect_one();
+        each_tile([&](int, int, int, int, int, int N) {
+            const uint32_t idesc = instr_desc(256, N);
+            const int buf = it & 1;
+            if (it >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[buf], static_cast<uint32_t>((it / 2 - 1) & 1)))) {
+                timed_out = 1;
+                return false;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;");
+            const uint32_t d = tmem + buf * kGpBT;
+            for (int t = 0; t < nstages; ++t, ++st) {
+                const int s = st % kGpStages;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&full[s], static_cast<uint32_t>((st / kGpStages) & 1)))) {
+                    timed_out = 1;
+                    return false;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;");
+                const uint32_t slot = smem_addr(smem) + s * kGpSlot, sf = slot + kGpSlotW + kGpSlotT;
+                const uint64_t dw = smem_desc(slot, 16, 1024, 2), dt = smem_desc(slot + kGpSlotW, 16, 1024, 2);
+                const uint64_t dsw = smem_desc(sf, 0, 128), dst = smem_desc(sf + kGpSlotSfw, 0, 128);
+                // Two stages' columns in turn: the copies of a stage follow the products of the stage
+                // before the last in the tensor pipe, which takes copies and products in issue order.
+                const uint32_t c0 = tmem + kGpColSf + static_cast<uint32_t>(st & 1) * 48;
+                const int nk = min(ksteps - t * kGmStageK, kGmStageK);
+#pragma unroll
+                for (int kk = 0; kk < kGmStageK; ++kk) {
+                    if (kk >= nk) break;
+                    const uint32_t c = c0 + kk * 12;
+                    copy_scales_warp<2>(el, c, dsw + kk * 32);
+                    copy_scales_warp<2>(el, c + 4, dst + kk * 64);
+                    if (N > 128) copy_scales_warp<2>(el, c + 8, dst + kk * 64 + 32);
+                    mma_f4_warp<2>(el, d, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, t + kk > 0 ? 1u : 0u);
+                }
+                commit_warp<2>(el, &empty[s]);
+            }
+            commit_warp<2>(el, &acc_full[buf]);
+            return true;
+        });
+    } else if (warp >= 2) {
+        // a quarter of the accumulator's lanes, and columns 96 * part up to 96 more
+        constexpr int kCols = kGpBT / (kGpStoreWarps / 4);
+        const int quad = warp & 3, part = (warp - 2) / 4;
+        const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(part * kCols);
+        const bool wide = a.N % 8 == 0;
+        uint8_t* turn = smem + kGpStages * kGpSlot + (warp - 2) * kGpTurn;
+        each_tile([&](int ntile, int, int expert, int row0, int rows, int) {
+            const int buf = it & 1;
+            for (int i = tid - 64; i < kGpBT; i += 32 * kGpStoreWarps) {
+                float enc, da = 1.0f, db = 1.0f;
+                if (i < rows && a.gamax_a_mode != NVFP4_GAMAX_NONE)
+                    global_scales(a.gamax_a[a.gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? row0 + i : 0], a.bound, enc, da);
+                if (a.gamax_b) global_scales(a.gamax_b[expert], a.bound, enc, db);
+                alpha[buf][i] = mul_rn(da, db);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kGpStoreWarps) : "memory");
+            if (!timed_out && !mbar_wait_cluster(&acc_full[buf], static_cast<uint32_t>((it / 2) & 1))) timed_out = 1;
+            __syncwarp();
+            const bool bad = timed_out != 0;
+            asm volatile("tcgen05.fence::after_thread_sync;");
+            // all of the warp's columns first, so that the accumulator is free before anything is stored
+            uint32_t v[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32)
+                if (part * kCols + c < rows)
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                        : "=r"(v[c]), "=r"(v[c + 1]), "=r"(v[c + 2]), "=r"(v[c + 3]), "=r"(v[c + 4]), "=r"(v[c + 5]),
+                          "=r"(v[c + 6]), "=r"(v[c + 7]), "=r"(v[c + 8]), "=r"(v[c + 9]), "=r"(v[c + 10]), "=r"(v[c + 11]),
+                          "=r"(v[c + 12]), "=r"(v[c + 13]), "=r"(v[c + 14]), "=r"(v[c + 15]), "=r"(v[c + 16]),
+                          "=r"(v[c + 17]), "=r"(v[c + 18]), "=r"(v[c + 19]), "=r"(v[c + 20]), "=r"(v[c + 21]),
+                          "=r"(v[c + 22]), "=r"(v[c + 23]), "=r"(v[c + 24]), "=r"(v[c + 25]), "=r"(v[c + 26]),
+                          "=r"(v[c + 27]), "=r"(v[c + 28]), "=r"(v[c + 29]), "=r"(v[c + 30]), "=r"(v[c + 31])
+                        : "r"(from + buf * kGpBT + static_cast<uint32_t>(c)));
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;");
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&acc_empty[buf]);
+                else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+            }
+            const int64_t nw = static_cast<int64_t>(ntile) * 256 + rank * 128 + 32 * quad;     // the warp's first row
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) {
+                const int col = part * kCols + c;
+                if (col >= rows) break;
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 al = *reinterpret_cast<const float4*>(&alpha[buf][col + i]);
+                    f[i] = mul_rn(__uint_as_float(v[c + i]), al.x);
+                    f[i + 1] = mul_rn(__uint_as_float(v[c + i + 1]), al.y);
+                    f[i + 2] = mul_rn(__uint_as_float(v[c + i + 2]), al.z);
+                    f[i + 3] = mul_rn(__uint_as_float(v[c + i + 3]), al.w);
+                }
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __int_as_float(0x7FC00000);
+                }
+                if (ODT == NVFP4_BF16 && wide) {
+                    // a lane has one weight row of 32 tokens: turned in shared memory, four lanes store a
+                    // token's 32 rows (64 bytes) at 16 bytes each
+                    __syncwarp();                         // the last turn is read
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        *reinterpret_cast<__nv_bfloat16*>(turn + i * 64 + lane * 2) = __float2bfloat16_rn(f[i]);
+                    __syncwarp();
+                    const int64_t n = nw + (lane & 3) * 8;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        const int token = col + i + lane / 4;
+                        const uint4 o = *reinterpret_cast<const uint4*>(turn + (i + lane / 4) * 64 + (lane & 3) * 16);
+                        if (token < rows && n < a.N)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                      static_cast<int64_t>(row0 + token) * a.N + n) = o;
+                    }
+                } else if (nw + lane < a.N) {
+                    int64_t o = static_cast<int64_t>(row0 + col) * a.N + nw + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i, o += a.N) {
+                        if (col + i >= rows) break;
+                        if (ODT == NVFP4_F32) static_cast<float*>(a.out)[o] = f[i];
+                        else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f[i]);
+                    }
+                }
+            }
+            return true;
+        });
+    }
+    // neither CTA leaves while the other may still read its shared memory or arrive at its barriers
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int ODT>
+cudaError_t launch_pair(const GroupedArgs& a, cudaStream_t s) {
+    const int64_t slots = pair_slots(a), ksteps = a.K / 64;
+    const int64_t tiles = slots * ((a.N + 255) / 256);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    CUtensorMap mapW = {}, mapT = {}, mapSW = {}, mapST = {};
+    if (!encode_codes_map(&mapW, a.codes_b, a.E * a.N, a.K, 128) ||
+        !encode_codes_map(&mapT, a.codes_a, a.T, a.K, kGpBT / 2) ||
+        !encode_scales_map(&mapSW, a.scales_b, a.E * ((a.N + 127) / 128) * ksteps, kGmStageK) ||
+        !encode_scales_map(&mapST, a.workspace, slots * ksteps * 2, 2 * kGmStageK))
+        return cudaErrorInvalidValue;
+    static thread_local int configured_dev = -1;         // the attribute and the pairs are per device
+    static thread_local int pairs_at_once = 0;            // an odd SM of a GPC has no partner
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        cudaError_t e = cudaFuncSetAttribute(k_grouped_pair<ODT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGpSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / 2 * 2));
+        cfg.blockDim = dim3(kGpThreads);
+        cfg.dynamicSmemBytes = kGpSmem;
+        if ((e = cudaOccupancyMaxActiveClusters(&pairs_at_once, k_grouped_pair<ODT>, &cfg)) != cudaSuccess) return e;
+        if (pairs_at_once < 1) return cudaErrorInvalidConfiguration;
+        configured_dev = dev;
+    }
+    const cudaError_t e = launch_pdl(k_token_scales, dim3(static_cast<unsigned>(slots), static_cast<unsigned>((ksteps + 7) / 8)),
+                                     dim3(256), 0, s, a, reinterpret_cast<uint32_t*>(a.workspace));
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = tiles < pairs_at_once ? tiles : pairs_at_once;
+    return launch_pdl(k_grouped_pair<ODT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGpThreads), kGpSmem, s, mapW,
+                      mapT, mapSW, mapST, a, static_cast<unsigned>(slots), static_cast<unsigned>(tiles));
 }
 
 template <int BT, int ODT>
@@ -305,8 +690,19 @@ cudaError_t launch_grouped_o(const GroupedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// whether the call takes pairs of SMs (and a workspace)
+static bool takes_pairs(const GroupedArgs& a) {
+    return a.K > 0 && a.N > 128 && a.E > 0 && (a.T + a.E - 1) / a.E >= kPairMean && a.K / 64 <= 8 * 65535;
+}
+
+int64_t grouped_workspace(const GroupedArgs& a) {
+    return takes_pairs(a) ? pair_slots(a) * (a.K / 64) * 1024 : 0;
+}
+
 int launch_grouped_mm(const GroupedArgs& a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (takes_pairs(a))
+        return static_cast<int>(a.out_dtype == NVFP4_F32 ? launch_pair<NVFP4_F32>(a, s) : launch_pair<NVFP4_BF16>(a, s));
     // tokens a tile: about twice the mean group, so that most groups are one tile
     const int64_t mean = (a.T + a.E - 1) / a.E;
     if (mean <= 8) return static_cast<int>(launch_grouped_o<16>(a, s));

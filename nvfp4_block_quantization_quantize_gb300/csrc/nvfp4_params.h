@@ -112,6 +112,7 @@ struct GroupedArgs {
     float bound;
     void* out;
     int out_dtype;
+    uint8_t* workspace;       // grouped_workspace() bytes
 };
 
 // launchers (each returns cudaGetLastError() after its launches)
@@ -124,6 +125,7 @@ int launch_mm(const uint8_t* A, const uint8_t* SA, const uint8_t* B, const uint8
               void* stream);
 int launch_rmsnorm(const NormArgs& a, void* stream);
 int launch_mv(const MvArgs& a, void* stream);
+int64_t grouped_workspace(const GroupedArgs& a);   // of E, T, N, K alone
 int launch_grouped_mm(const GroupedArgs& a, void* stream);
 int launch_amax(const void* x, int64_t M, int64_t K, int dtype, const float* residual, int mode,
                 float* out, void* stream);

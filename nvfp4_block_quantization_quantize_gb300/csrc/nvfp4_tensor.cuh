@@ -101,22 +101,105 @@ __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t da, uint64_t db, uin
         "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc));
 }
 
-// 2D map of a [rows, K/2]-byte code matrix, boxes of box_rows x 128 bytes, 128-byte swizzle
-inline bool encode_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows) {
+// ---- issue by a whole warp ---------------------------------------------------------------------
+// The forms above are issued by one thread under a branch; the compiler then moves
+// each operand to a uniform register per instruction, and issuing costs about 45
+// clocks an instruction (measured: 128 x 128 x 64 products with two scale copies
+// each take 134 clocks apart instead of 92).  Here the whole warp comes along with
+// the same operands and one elected lane's predicate guards the instruction.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+// CG: CTAs of the product (1, or the 2 SMs of a pair: M up to 256)
+template <int CG>
+__device__ __forceinline__ void mma_f4_warp(uint32_t el, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(el));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(el));
+}
+
+// a 512-byte scale tile to four tensor-memory columns
+template <int CG>
+__device__ __forceinline__ void copy_scales_warp(uint32_t el, uint32_t col, uint64_t desc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(col), "l"(desc), "r"(el));
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(col), "l"(desc), "r"(el));
+}
+
+// arrive on bar (with CG == 2 in both CTAs of the pair) when the products issued so far are done
+template <int CG>
+__device__ __forceinline__ void commit_warp(uint32_t el, uint64_t* bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+            "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+                smem_addr(bar)),
+            "r"(el), "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&encode), 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return false;
+        PFN_cuTensorMapEncodeTiled_v12000 f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&f), 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = f;
     }
+    return encode;
+}
+
+// 2D map of a [rows, K/2]-byte code matrix, boxes of box_rows x 128 bytes, 128-byte swizzle
+inline bool encode_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
     const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2D map of `tiles` 512-byte scale tiles, boxes of box_tiles of them
+inline bool encode_scales_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles, int box_tiles) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_tiles)};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(scales), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

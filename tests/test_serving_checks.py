@@ -92,8 +92,8 @@ def test_mv_rejects(lib, case):
 
 
 def grouped(lib, ca=A16, sa=A16, off=A16, cb=A16, sb=A16, E=4, T=8, N=32, K=64, gm=0, ga=None, gb=None, bound=448.0,
-            out=A16, odt=1):
-    return lib.nvfp4_grouped_mm(ca, sa, off, cb, sb, E, T, N, K, gm, ga, gb, bound, out, odt, None)
+            out=A16, odt=1, ws=None, ws_bytes=0):
+    return lib.nvfp4_grouped_mm(ca, sa, off, cb, sb, E, T, N, K, gm, ga, gb, bound, out, odt, ws, ws_bytes, None)
 
 
 GROUPED_BAD = {
@@ -112,6 +112,9 @@ GROUPED_BAD = {
     "offsets misaligned": dict(off=A4),
     "codes_b misaligned": dict(cb=A8),
     "out NULL": dict(out=None),
+    "workspace too small": dict(E=1, T=4096, N=1024, K=1024, ws=A16, ws_bytes=64),
+    "workspace NULL": dict(E=1, T=4096, N=1024, K=1024, ws_bytes=1 << 30),
+    "workspace misaligned": dict(E=1, T=4096, N=1024, K=1024, ws=A8, ws_bytes=1 << 30),
 }
 
 
