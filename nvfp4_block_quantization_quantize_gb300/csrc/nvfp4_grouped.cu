@@ -293,10 +293,6 @@ __global__ void __launch_bounds__(kGmThreads)
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
-#ifndef PAIRMEAN
-#define PAIRMEAN 64
-#endif
-constexpr int kPairMean = PAIRMEAN;
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;
@@ -690,9 +686,18 @@ cudaError_t launch_grouped_o(const GroupedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// whether the call takes pairs of SMs (and a workspace)
+// Whether the call takes pairs of SMs (and a workspace): where their waves are fewer than
+// 3/2 of the single SMs' ones, on the tiles to be expected (a half-filled one a group).  A
+// wave of pairs takes about 2/3 of the time of a wave of 128 x 128 tiles, two CTAs an SM
+// (measured over 13 shapes; e.g. K 4096, us pairs / single: 8 experts 1024 x 4096 27 / 30, 1
+// expert 1024 x 14336 39 / 49, 32 experts 4096 x 4096 69 / 81, but 8 experts 512 x 4096 25 / 21).
 static bool takes_pairs(const GroupedArgs& a) {
-    return a.K > 0 && a.N > 128 && a.E > 0 && (a.T + a.E - 1) / a.E >= kPairMean && a.K / 64 <= 8 * 65535;
+    constexpr int64_t kSms = 152;
+    if (a.K <= 0 || a.E <= 0 || a.T < 33 * a.E || a.K / 64 > 8 * 65535) return false;
+    const int64_t pair_tiles = ((2 * a.T + kGpBT - 1) / kGpBT + a.E) / 2 * ((a.N + 255) / 256);
+    const int64_t tiles = ((2 * a.T + 127) / 128 + a.E) / 2 * ((a.N + 127) / 128);
+    const int64_t pair_waves = (pair_tiles + kSms / 2 - 1) / (kSms / 2), waves = (tiles + 2 * kSms - 1) / (2 * kSms);
+    return a.N > 128 && 2 * pair_waves <= 3 * waves;
 }
 
 int64_t grouped_workspace(const GroupedArgs& a) {

@@ -355,6 +355,49 @@ def test_grouped_exact(name, N, K):
     assert np.array_equal(to_np(y).astype(np.float64), ref)
 
 
+PAIRS = {                                                 # many tokens an expert: pairs of SMs
+    "ragged": (4, [0, 1000, 1000, 1033, 2500], 4096, 320),
+    "rows off the tiles": (3, [0, 191, 900, 1733], 6008, 192),
+    "N not of 8": (2, [0, 769, 1600], 6001, 64),
+    "one expert": (1, [0, 1536], 6144, 448),
+    "second half past N": (2, [0, 1000, 2000], 4224, 128),
+    "many stages": (1, [0, 200], 20000, 2112),
+    "over 256 experts": (300, list(range(0, 300 * 40, 40)) + [12000], 256, 64),
+}
+
+
+@pytest.mark.parametrize("name", sorted(PAIRS))
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_grouped_pairs_exact(name, out_dtype):
+    E, offsets, N, K = PAIRS[name]
+    T = offsets[-1]
+    assert nv.load_library().nvfp4_grouped_mm_workspace(E, T, N, K) > 0
+    rng = np.random.default_rng(E + N + K)
+    ca, sa, cb, sb = grouped_inputs(rng, E, T, N, K)
+    sa = (0x38 + 8 * rng.integers(-1, 2, sa.shape)).astype(np.uint8)
+    sb = (0x38 + 8 * rng.integers(-1, 2, sb.shape)).astype(np.uint8)
+    y = to_np(grouped_gpu(ca, sa, offsets, cb, sb, out_dtype=out_dtype).float())
+    ref, mag = grouped_reference(ca, sa, cb, sb, offsets, K)
+    assert mag.max() < 2 ** 20
+    want = ref.astype(np.float32)
+    assert np.array_equal(y, want if out_dtype == "f32" else bf16_round(want))
+
+
+def test_grouped_pairs_scales_and_rows_in_no_group():
+    rng = np.random.default_rng(15)
+    E, offsets, N, K, T = 3, [5, 905, 905, 2105], 4104, 320, 2200
+    assert nv.load_library().nvfp4_grouped_mm_workspace(E, T, N, K) > 0
+    ca, sa, cb, sb = grouped_inputs(rng, E, T, N, K)
+    sa[:5] = sa[2105:] = 0x7F
+    ga, gb = rng.uniform(0.1, 9.0, T).astype(np.float32), rng.uniform(0.1, 9.0, E).astype(np.float32)
+    buf = torch.full((T, N), 5.0, device="cuda")
+    y = to_np(grouped_gpu(ca, sa, offsets, cb, sb, out_dtype="f32", out=buf, gamax_a=to_dev(ga), gamax_b=to_dev(gb)))
+    sa[:5] = sa[2105:] = 0x38
+    ref, mag = grouped_reference(ca[5:2105], sa[5:2105], cb, sb, [0, 900, 900, 2100], K, ga[5:2105], gb)
+    assert (y[:5] == 5).all() and (y[2105:] == 5).all()
+    assert (np.abs(y[5:2105] - ref) <= mag * (K / 64 + 4) * 2.0 ** -22).all()
+
+
 @pytest.mark.parametrize("a_mode", ["none", "tensor", "row"])
 @pytest.mark.parametrize("b_amax", [False, True])
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16"])

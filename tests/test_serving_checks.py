@@ -112,9 +112,9 @@ GROUPED_BAD = {
     "offsets misaligned": dict(off=A4),
     "codes_b misaligned": dict(cb=A8),
     "out NULL": dict(out=None),
-    "workspace too small": dict(E=1, T=4096, N=1024, K=1024, ws=A16, ws_bytes=64),
-    "workspace NULL": dict(E=1, T=4096, N=1024, K=1024, ws_bytes=1 << 30),
-    "workspace misaligned": dict(E=1, T=4096, N=1024, K=1024, ws=A8, ws_bytes=1 << 30),
+    "workspace too small": dict(E=8, T=8192, N=14336, K=4096, ws=A16, ws_bytes=64),
+    "workspace NULL": dict(E=8, T=8192, N=14336, K=4096, ws_bytes=1 << 40),
+    "workspace misaligned": dict(E=8, T=8192, N=14336, K=4096, ws=A8, ws_bytes=1 << 40),
 }
 
 
@@ -122,6 +122,13 @@ GROUPED_BAD = {
 def test_grouped_rejects(lib, case):
     assert grouped(lib, **GROUPED_BAD[case]) == 1
     assert lib.nvfp4_last_error() != b""
+
+
+def test_workspace_is_asked_for_by_the_sizes(lib):
+    assert lib.nvfp4_grouped_mm_workspace(64, 64, 2048, 4096) == 0
+    assert lib.nvfp4_grouped_mm_workspace(8, 8192, 14336, 4096) == (8192 // 192 + 8) * 64 * 1024
+    for bad in ((0, 1, 1, 64), (1, -1, 1, 64), (1 << 31, 1, 1, 64)):
+        assert lib.nvfp4_grouped_mm_workspace(*bad) == 0
 
 
 def test_empty_calls_are_valid(lib):
