@@ -14,8 +14,8 @@
 //     is free as long as A and B agree, so lane (g, t) of a warp takes whole
 //     blocks: 16 * VB consecutive weights of rows g and g + 8, one 8 * VB-byte
 //     load and VB scale bytes a row, for 4 * VB products (a chunk: 64 * VB columns).
-//   - A chain of products starts from zero every two blocks and is added to an
-//     fp32 sum, so the tensor core's own accumulation stays short.
+//   - A chain of at most 16 products starts from zero and is added to an fp32 sum,
+//     so the tensor core's own accumulation stays short.
 // A CTA has 8 warps: WK parts of its columns times WR groups of 16 weight rows.  Its x
 // is staged once; then each warp walks down row tiles with kAhead chunks of weights in
 // flight (registers; the loads run on across tiles).  Per tile the WK warps of a row
@@ -40,7 +40,7 @@ constexpr int kMvMaxCluster = 8;
 constexpr int kMvMaxTiles = 16;                           // row tiles per cluster with sums kept to the end
 
 template <int VB>
-constexpr int kAhead = VB == 4 ? 3 : 8;                   // chunks of weights in flight per warp
+constexpr int kAhead = VB == 4 ? 2 : 4;                   // chunks of weights in flight per warp
 template <int VB>
 constexpr int kStep = 4 / VB;                             // chunks in the 256 columns a warp stages at once
 constexpr int kMvCtas = 2;                                // CTAs an SM holds
@@ -68,6 +68,15 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the first product of a chain: c = a b
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -111,7 +120,7 @@ __device__ __forceinline__ void scale_pairs(uint32_t bytes, uint32_t* s) {
 template <int VB>
 __device__ __forceinline__ void load_blocks(const uint8_t* codes, const uint8_t* scales, uint32_t* w, uint32_t& s) {
     if constexpr (VB == 4) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                      : "l"(codes));
         s = __ldg(reinterpret_cast<const uint32_t*>(scales));
@@ -146,6 +155,12 @@ __device__ __forceinline__ void copy_x(const MvArgs& a, uint8_t* xs, int64_t k0,
         for (int i = lane; i < cols * kXSize<XT> / 16; i += 32) cp_async16(dst + 16 * i, row + 16 * i);
     }
     cp_async_commit();
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
 }
 
 // 2^e as a float, e >= -149
@@ -259,12 +274,16 @@ __device__ __forceinline__ void convert_x(const MvArgs& a, uint8_t* xs, float* u
     }
 }
 
-__device__ __forceinline__ void store_out(const MvArgs& a, int m, int64_t n, float v) {
-    if (a.gamax_mode != NVFP4_GAMAX_NONE) {
-        float enc, dec;
+// decode scale of weight row n (any n without a per-row amax)
+__device__ __forceinline__ float decode(const MvArgs& a, int64_t n) {
+    float enc, dec = 1.0f;
+    if (a.gamax_mode != NVFP4_GAMAX_NONE)
         global_scales(a.gamax[a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? n : 0], a.bound, enc, dec);
-        v = mul_rn(v, dec);
-    }
+    return dec;
+}
+
+__device__ __forceinline__ void store_out(const MvArgs& a, int m, int64_t n, float v, float dec) {
+    v = mul_rn(v, dec);
     const int64_t o = static_cast<int64_t>(m) * a.N + n;
     if (a.out_dtype == NVFP4_F32) static_cast<float*>(a.out)[o] = v;
     else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
@@ -281,6 +300,7 @@ template <int XT, int NT, int VB>
 __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, const MvPlan p) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
+    constexpr int kChain = VB == 1 ? 2 : 8 / P;           // words of a row whose products form a chain: at most 16
     __shared__ float red[2][kMvWarps][kMvRow<NT>];        // [token][row] of each warp, two tiles in turn
     __shared__ float up[kMvWarps][16];                    // of each part of the columns
     const cg::cluster_group cluster = cg::this_cluster();
@@ -314,27 +334,38 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
         copy_x<XT, VB>(a, xs, k0, p.cpw, wr, WR, lane);
         if (XT == NVFP4_X_MXFP8) {
             const int64_t groups = (static_cast<int64_t>(a.K) + 31) / 32, first = k0 / 32;
-            for (int i = lane; i < sb_stride * a.M; i += 32) {
-                const int m = i / sb_stride;
-                const int64_t q = first + i % sb_stride;
-                if (m % WR == wr) sb[i] = q < groups ? __ldg(a.x_scales + m * groups + q) : 0;
+            for (int m = wr; m < a.M; m += WR) {
+                const uint8_t* src = a.x_scales + m * groups + first;
+                uint8_t* dst = sb + m * sb_stride;
+                if (groups % 4 == 0) {                    // whole words, with x's copies
+                    for (int i = 4 * lane; i < sb_stride; i += 128)
+                        if (first + i < groups) cp_async4(dst + i, src + i);
+                } else {
+                    for (int i = lane; i < sb_stride; i += 32)
+                        if (first + i < groups) dst[i] = __ldg(src + i);
+                }
             }
+            cp_async_commit();
         }
         // loads run kAhead chunks ahead of the products, on into the next tiles
         uint32_t w[kAhead<VB>][2][2 * VB], sc[kAhead<VB>][2];
+        // (pointers to the lane's blocks of rows g and g + 8 in the warp's first chunk, and bytes from there)
         int lt = 0, lc = 0;
-        int64_t r0, r1;                                   // first blocks of rows g and g + 8 of tile lt
+        const uint8_t *c0, *c1, *s0, *s1;
+        const int first_blk = (chunk0 * 4 + t) * VB, most_blk = bpr - VB - first_blk;
         auto rows = [&] {
             const int row = ((tile0 + lt) * WR + wr) * 16 + g;
-            r0 = static_cast<int64_t>(min(row, a.N - 1)) * bpr;
-            r1 = static_cast<int64_t>(min(row + 8, a.N - 1)) * bpr;
+            const int64_t r0 = static_cast<int64_t>(min(row, a.N - 1)) * bpr + first_blk;
+            const int64_t r1 = static_cast<int64_t>(min(row + 8, a.N - 1)) * bpr + first_blk;
+            s0 = a.scales + r0, s1 = a.scales + r1;
+            c0 = a.codes + r0 * 8, c1 = a.codes + r1 * 8;
         };
         rows();
         auto load = [&](int u) {
             if (lt >= ntiles || n == 0) return;
-            const int blk = min(((chunk0 + lc) * 4 + t) * VB, bpr - VB);
-            load_blocks<VB>(a.codes + (r0 + blk) * 8, a.scales + (r0 + blk), w[u][0], sc[u][0]);
-            load_blocks<VB>(a.codes + (r1 + blk) * 8, a.scales + (r1 + blk), w[u][1], sc[u][1]);
+            const int blk = min(lc * 4 * VB, most_blk);
+            load_blocks<VB>(c0 + blk * 8, s0 + blk, w[u][0], sc[u][0]);
+            load_blocks<VB>(c1 + blk * 8, s1 + blk, w[u][1], sc[u][1]);
             if (++lc == n) {
                 lc = 0;
                 ++lt;
@@ -347,6 +378,9 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
         __syncwarp();
         convert_x<XT, VB>(a, xs, up[wk], sb, sb_stride, k0, p.cpw, wr, WR, lane);
         __syncthreads();
+        // without a per-row amax the decode scale is known here; with one, its row's is fetched ahead
+        const bool per_row = a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN;
+        const float dec_all = per_row || keep ? 1.0f : decode(a, 0);
         float acc[NT][4];
         int c = 0, tile = 0;
         auto clear = [&](float (*f)[4]) {
@@ -355,7 +389,8 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[q][i] = 0.0f;
         };
-        // a row group's sums of a tile, added in the order of its WK warps by the threads of (token, row)
+        // A row group's sums of a tile, added in the order of its WK warps by the threads of (token, row);
+        // the warps take turns at being the first of those (few tokens need one warp only).
         auto end_tile = [&] {
             float* r = red[turn][warp];
 #pragma unroll
@@ -365,17 +400,21 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
                     const int m = q * 8 + 2 * t + (i & 1);
                     if (m < a.M) r[m * 16 + g + 8 * (i >> 1)] = mul_rn(acc[q][i], up[wk][m]);
                 }
+            const int from = ((wk + tile) & (p.WK - 1)) * 32 + lane;
+            const int64_t row = static_cast<int64_t>((tile0 + tile) * WR + wr) * 16 + (lane & 15);
+            const float dec = per_row && !keep && from < a.M * 16 && row < a.N ? decode(a, row) : dec_all;
             // by number, one barrier a row group: its warps come here from different steps of the loop below
             asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * p.WK) : "memory");
-            for (int i = wk * 32 + lane; i < a.M * 16; i += 32 * p.WK) {
+            for (int i = from; i < a.M * 16; i += 32 * p.WK) {
                 float v = 0.0f;
-                for (int q = 0; q < p.WK; ++q) v = add_rn(v, red[turn][wr * p.WK + q][i]);
+#pragma unroll
+                for (int q = 0; q < kMvWarps; ++q)
+                    if (q < p.WK) v = add_rn(v, red[turn][wr * p.WK + q][i]);
                 if (keep) {
                     float* k = kept + (tile * WR + wr) * a.M * 16 + i;
                     *k = round ? add_rn(*k, v) : v;
-                } else {
-                    const int64_t row = static_cast<int64_t>((tile0 + tile) * WR + wr) * 16 + (i & 15);
-                    if (row < a.N) store_out(a, i >> 4, row, v);
+                } else if (row < a.N) {
+                    store_out(a, i >> 4, row, v, dec);
                 }
             }
             clear(acc);
@@ -393,7 +432,6 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
                 scale_pairs<VB>(sc[u][1], s[1]);
                 const int at = c * (128 * VB * P);
                 float d[NT][4];
-                clear(d);
 #pragma unroll
                 for (int j = 0; j < 2 * VB; ++j) {        // word j of each row: two products
                     uint32_t A[2][4];
@@ -404,16 +442,17 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
 #pragma unroll
                         for (int h = 0; h < P; ++h) {
                             const uint4 b = *reinterpret_cast<const uint4*>(frag[q] + at + (j * P + h) * 64);
-                            mma_f16(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
+                            if (j % kChain == 0 && h == 0)
+                                mma_f16_first(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
+                            else
+                                mma_f16(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
                             mma_f16(d[q], A[0][2], A[1][2], A[0][3], A[1][3], b.z, b.w);
                         }
-                    if (j % 4 == 3 || j == 2 * VB - 1) {  // the chain's end
+                    if (j % kChain == kChain - 1)         // the chain's end
 #pragma unroll
                         for (int q = 0; q < NT; ++q)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) acc[q][i] = add_rn(acc[q][i], d[q][i]);
-                        clear(d);
-                    }
                 }
                 load(u);
                 if (++c == n) end_tile();
@@ -422,18 +461,24 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
         while (tile < ntiles) end_tile();                 // a warp with no columns takes part with zeros
     }
     if (keep) {
-        // the parts of the columns, added in rank order
+        // the parts of the columns, added in rank order (read from the CTAs that have them: sending them to
+        // the one that adds them up, with one barrier less, took 2 us longer)
         if (p.S > 1) cluster.sync();
         else __syncthreads();
         for (int i = rank * blockDim.x + tid; i < ntiles * WR * a.M * 16; i += p.S * blockDim.x) {
             const int64_t row = (static_cast<int64_t>(tile0) * WR + i / (a.M * 16)) * 16 + (i & 15);
             if (row >= a.N) continue;
+            const float dec = decode(a, row);
             float v = kept[i];
             if (p.S > 1) {
-                v = 0.0f;
-                for (int q = 0; q < p.S; ++q) v = add_rn(v, *cluster.map_shared_rank(kept + i, q));
+                float part[kMvMaxCluster];                // loaded together: a remote load takes long
+#pragma unroll
+                for (int q = 0; q < kMvMaxCluster; ++q) part[q] = q < p.S ? *cluster.map_shared_rank(kept + i, q) : 0.0f;
+                v = part[0];
+#pragma unroll
+                for (int q = 1; q < kMvMaxCluster; ++q) v = q < p.S ? add_rn(v, part[q]) : v;
             }
-            store_out(a, i / 16 % a.M, row, v);
+            store_out(a, i / 16 % a.M, row, v, dec);
         }
         if (p.S > 1) cluster.sync();                      // kept is read by the whole cluster
     }
