@@ -15,27 +15,101 @@ namespace {
 
 constexpr int kNormMaxThreads = 1024;
 
-// 16 elements of memory this kernel may also write (the hidden state in place):
-// a plain load, not the read-only path
+// 32 bytes of memory.  W: the address is 32-byte aligned (one 256-bit access: a warp's
+// 16-element blocks of bf16 are then one contiguous piece).  RO: through the read-only
+// path; the hidden state, which this kernel may write in place, is not.
+template <bool W, bool RO>
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+    if constexpr (W) {
+        if constexpr (RO)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                         : "l"(p));
+        else
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                         : "l"(p)
+                         : "memory");
+    } else {
+        const uint4* q = static_cast<const uint4*>(p);
+        const uint4 a = RO ? __ldg(q) : q[0], b = RO ? __ldg(q + 1) : q[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+
+template <bool W>
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+    if constexpr (W)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        uint4* q = static_cast<uint4*>(p);
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// 16 elements from element elem0, as they are (8 words of bf16, 16 of fp32)
 template <int DT>
-__device__ __forceinline__ void load16_rw(const void* base, int64_t elem0, float* y) {
-    if (DT == NVFP4_BF16) lds16<DT>(static_cast<const uint16_t*>(base) + elem0, y);
-    else lds16<DT>(static_cast<const float*>(base) + elem0, y);
+constexpr int kWords = DT == NVFP4_BF16 ? 8 : 16;
+
+template <int DT, bool W, bool RO>
+__device__ __forceinline__ void load_raw(const void* base, int64_t elem0, uint32_t* w) {
+    const uint8_t* p = static_cast<const uint8_t*>(base) + elem0 * (DT == NVFP4_BF16 ? 2 : 4);
+    load32<W, RO>(p, w);
+    if (DT == NVFP4_F32) load32<W, RO>(p + 32, w + kWords<DT> - 8);
 }
 
 template <int DT>
+__device__ __forceinline__ void widen(const uint32_t* w, float* y) {
+#pragma unroll
+    for (int i = 0; i < kWords<DT>; ++i) {
+        if (DT == NVFP4_BF16) {
+            y[2 * i] = __uint_as_float(w[i] << 16);
+            y[(2 * i + 1) % 16] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            y[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+template <int DT, bool W>
 __device__ __forceinline__ void store16(void* base, int64_t elem0, const float* y) {
-    if (DT == NVFP4_BF16) store16_bf16(static_cast<uint16_t*>(base), elem0, y);
-    else store16_f32(static_cast<float*>(base), elem0, y);
+    uint8_t* p = static_cast<uint8_t*>(base) + elem0 * (DT == NVFP4_BF16 ? 2 : 4);
+    uint32_t w[kWords<DT>];
+#pragma unroll
+    for (int i = 0; i < kWords<DT>; ++i) {
+        if (DT == NVFP4_BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[(2 * i + 1) % 16]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            w[i] = __float_as_uint(y[i]);
+        }
+    }
+    store32<W>(p, w);
+    if (DT == NVFP4_F32) store32<W>(p + 32, w + kWords<DT> - 8);
 }
 
-// h = x + hidden of the 16 elements from elem0
+// x (+ hidden) of 16 elements as loaded
 template <int DT>
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t elem0, float* h) {
-    load16<DT>(a.x, elem0, h);
+struct Raw {
+    uint32_t x[kWords<DT>], r[kWords<DT>];
+};
+
+template <int DT, bool W>
+__device__ __forceinline__ void load_block(const NormArgs& a, int64_t elem0, Raw<DT>& raw) {
+    load_raw<DT, W, true>(a.x, elem0, raw.x);
+    if (a.hidden) load_raw<DT, W, false>(a.hidden, elem0, raw.r);
+}
+
+// h = x + hidden
+template <int DT>
+__device__ __forceinline__ void sum_block(const NormArgs& a, const Raw<DT>& raw, float* h) {
+    widen<DT>(raw.x, h);
     if (a.hidden) {
         float r[16];
-        load16_rw<DT>(a.hidden, elem0, r);
+        widen<DT>(raw.r, r);
         add16(h, r);
     }
 }
@@ -120,127 +194,142 @@ __device__ __forceinline__ void quantize16(const NormArgs& a, int64_t row, int64
     }
 }
 
-// blockDim (threads per row, rows per CTA); C blocks of 16 per thread held in
-// registers, or C == 0 with the row read twice
-template <int DT, int C, int FMT>
-__global__ void __launch_bounds__(kNormMaxThreads) k_rmsnorm(const NormArgs a) {
-    __shared__ float ssum[32], smax[32];
+// blockDim (threads per row, rows per CTA).  C == 1: a thread holds its block of 16 in
+// registers; the CTA walks down the rows, the next row's loads under way while the present
+// one is reduced and stored.  C == 0: a thread walks along a row, which is read a second
+// time.  W: every row starts on 32 bytes.  MAXT: rows of at most 512 threads have the
+// registers to hold the next row in fp32 too, as one CTA an SM (4096 x 7168: 32 us, two
+// CTAs that spill 38 us, without the next row 56 us); bf16 is held to 64, for three and more
+// (16384 x 4096 with hidden: 73 us; with 104 registers and fewer CTAs 77 us).
+template <int DT, int C, int FMT, bool W, int MAXT>
+__global__ void __launch_bounds__(MAXT, DT == NVFP4_BF16 && MAXT == 512 ? 2 : 1) k_rmsnorm(const NormArgs a) {
+    __shared__ float ssum[2][32], smax[2][32];
+    pdl_trigger();                                        // the next kernel waits for this one's end itself
     pdl_wait();
     const int64_t bpr = a.K / 16;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const bool in = row < a.M;
     const int64_t T = blockDim.x;
+    const int64_t hop = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     // threads of a pair stay together: every thread makes the same number of steps
-    const int64_t steps = C ? C : (bpr + T - 1) / T;
-    float h[C ? C : 1][16];
-    float sum = 0.0f;
-    auto load = [&](int64_t c, float* v) {
+    const int64_t steps = C ? 1 : (bpr + T - 1) / T;
+        constexpr bool kAhead = C == 1 && (DT == NVFP4_BF16 || MAXT == 512);     // fp32 of 1024 threads would spill
+    Raw<DT> raw;
+    auto load = [&](int64_t r, int64_t c) {
         const int64_t blk = threadIdx.x + c * T;
-        if (in && blk < bpr) load_h<DT>(a, (row * bpr + blk) * 16, v);
+        if (r < a.M && blk < bpr) load_block<DT, W>(a, (r * bpr + blk) * 16, raw);
+    };
+    auto value = [&](int64_t r, int64_t c, float* h) {
+        if (r < a.M && threadIdx.x + c * T < bpr) sum_block<DT>(a, raw, h);
         else
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 16; ++i) h[i] = 0.0f;
     };
-    auto square = [&](const float* v) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s = __fmaf_rn(v[i], v[i], s);
-        sum = add_rn(sum, s);
-    };
-    if constexpr (C) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) load(c, h[c]);
-#pragma unroll
-        for (int c = 0; c < C; ++c) square(h[c]);
-    } else {
+    if (kAhead) load(row, 0);
+    int turn = 0;                                         // of the reductions' slots
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y; first < a.M; first += hop, row += hop, turn ^= 1) {
+        const bool in = row < a.M;
+        float h[16], sum = 0.0f;
         for (int64_t c = 0; c < steps; ++c) {
-            load(c, h[0]);
-            square(h[0]);
-        }
-    }
-    const float mean = div_rn(row_reduce<false>(sum, ssum), static_cast<float>(a.K));
-    const float rstd = div_rn(1.0f, __fsqrt_rn(add_rn(mean, a.eps)));
-    GScale g{0.0f, 1.0f, 1.0f};
-    if (FMT == NVFP4_FMT_NVFP4 && a.codes && a.gamax_mode != NVFP4_GAMAX_NONE) {
-        if (a.gamax_mode == NVFP4_GAMAX_ROW) {
-            float m = 0.0f;
-            auto rowmax = [&](int64_t c, const float* v) {
-                const int64_t blk = threadIdx.x + c * T;
-                if (!in || blk >= bpr) return;
-                float y[16];
-                normed(a, blk * 16, rstd, v, y);
-                m = max_nd(m, absmax16(y));
-            };
-            if constexpr (C) {
+            if (!kAhead) load(row, c);
+            value(row, c, h);
+            float s = 0.0f;
 #pragma unroll
-                for (int c = 0; c < C; ++c) rowmax(c, h[c]);
-            } else {
+            for (int i = 0; i < 16; ++i) s = __fmaf_rn(h[i], h[i], s);
+            sum = add_rn(sum, s);
+        }
+        if (kAhead) load(row + hop, 0);
+        const float mean = div_rn(row_reduce<false>(sum, ssum[turn]), static_cast<float>(a.K));
+        const float rstd = div_rn(1.0f, __fsqrt_rn(add_rn(mean, a.eps)));
+        GScale g{0.0f, 1.0f, 1.0f};
+        if (FMT == NVFP4_FMT_NVFP4 && a.codes && a.gamax_mode != NVFP4_GAMAX_NONE) {
+            if (a.gamax_mode == NVFP4_GAMAX_ROW) {
+                float m = 0.0f;
                 for (int64_t c = 0; c < steps; ++c) {
-                    load(c, h[0]);
-                    rowmax(c, h[0]);
+                    const int64_t blk = threadIdx.x + c * T;
+                    if (!C) {
+                        load(row, c);
+                        value(row, c, h);
+                    }
+                    if (!in || blk >= bpr) continue;
+                    float y[16];
+                    normed(a, blk * 16, rstd, h, y);
+                    m = max_nd(m, absmax16(y));
                 }
+                g.A = row_reduce<true>(m, smax[turn]);
+                if (in && threadIdx.x == 0) a.gamax[row] = g.A;
+            } else if (in) {
+                g.A = a.gamax[a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? row : 0];
             }
-            g.A = row_reduce<true>(m, smax);
-            if (in && threadIdx.x == 0) a.gamax[row] = g.A;
-        } else if (in) {
-            g.A = a.gamax[a.gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? row : 0];
+            global_scales(g.A, a.bound, g.Senc, g.Sdec);
         }
-        global_scales(g.A, a.bound, g.Senc, g.Sdec);
-    }
-    auto finish = [&](int64_t c, const float* v) {
-        const int64_t blk = threadIdx.x + c * T;
-        const bool live = in && blk < bpr;
-        float y[16];
-        if (live) {
-            if (a.hidden_out) store16<DT>(a.hidden_out, (row * bpr + blk) * 16, v);
-            normed(a, blk * 16, rstd, v, y);
-            if (a.out) store16<DT>(a.out, (row * bpr + blk) * 16, y);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-        }
-        if (a.codes) quantize16<FMT>(a, row, blk, bpr, live, g, y);
-    };
-    if constexpr (C) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) finish(c, h[c]);
-    } else {
         for (int64_t c = 0; c < steps; ++c) {
-            load(c, h[0]);
-            finish(c, h[0]);
+            const int64_t blk = threadIdx.x + c * T;
+            if (!C) {
+                load(row, c);
+                value(row, c, h);
+            }
+            const bool live = in && blk < bpr;
+            float y[16];
+            if (live) {
+                if (a.hidden_out) store16<DT, W>(a.hidden_out, (row * bpr + blk) * 16, h);
+                normed(a, blk * 16, rstd, h, y);
+                if (a.out) store16<DT, W>(a.out, (row * bpr + blk) * 16, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+            }
+            if (a.codes) quantize16<FMT>(a, row, blk, bpr, live, g, y);
         }
     }
-    pdl_trigger();
+}
+
+template <int DT, int FMT, bool W>
+cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s) {
+    const int64_t bpr = a.K / 16;
+    const bool whole = bpr <= kNormMaxThreads;
+    const int T = whole ? static_cast<int>((bpr + 31) / 32 * 32) : kNormMaxThreads;
+    const int rows = T >= 256 ? 1 : 256 / T;
+    auto* kernel = T * rows <= 512 ? k_rmsnorm<DT, 1, FMT, W, 512>
+                   : whole         ? k_rmsnorm<DT, 1, FMT, W, kNormMaxThreads>
+                                   : k_rmsnorm<DT, 0, FMT, W, kNormMaxThreads>;
+    // as many CTAs as run at once, found once per device, variant and CTA size (8 of 32 .. 256 threads a
+    // row have 256 a CTA; above, one size each)
+    static thread_local int dev_of = -1, at_once[2][33];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev_of != dev) {
+        for (auto& v : at_once)
+            for (int& n : v) n = 0;
+        dev_of = dev;
+    }
+    int& n = at_once[whole][T * rows / 32];
+    if (n == 0) {
+        int per_sm = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, T * rows, 0);
+        if (e != cudaSuccess) return e;
+        n = (per_sm < 1 ? 1 : per_sm) * sm_count();
+    }
+    const int64_t blocks = (a.M + rows - 1) / rows;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < n ? blocks : n)), dim3(T, rows), 0, s, a);
 }
 
 template <int DT, int FMT>
-cudaError_t launch_c(const NormArgs& a, int C, dim3 grid, dim3 block, cudaStream_t s) {
-    switch (C) {
-        case 1: return launch_pdl(k_rmsnorm<DT, 1, FMT>, grid, block, 0, s, a);
-        case 2: return launch_pdl(k_rmsnorm<DT, 2, FMT>, grid, block, 0, s, a);
-        default: return launch_pdl(k_rmsnorm<DT, 0, FMT>, grid, block, 0, s, a);
-    }
+cudaError_t launch_norm_w(const NormArgs& a, cudaStream_t s) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.hidden) |
+                           reinterpret_cast<uintptr_t>(a.hidden_out) | reinterpret_cast<uintptr_t>(a.out);
+    return bits % 32 == 0 ? launch_norm_t<DT, FMT, true>(a, s) : launch_norm_t<DT, FMT, false>(a, s);
 }
 
 }  // namespace
 
 int launch_rmsnorm(const NormArgs& a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t bpr = a.K / 16;
-    const int C = bpr <= kNormMaxThreads ? 1 : bpr <= 2 * kNormMaxThreads ? 2 : 0;
-    int T = kNormMaxThreads;
-    if (C) T = static_cast<int>(((bpr + C - 1) / C + 31) / 32 * 32);
-    const int rows = T >= 256 ? 1 : 256 / T;
-    const int64_t blocks = (a.M + rows - 1) / rows;
-    if (blocks > 0x7FFFFFFF) return static_cast<int>(cudaErrorInvalidConfiguration);
-    const dim3 grid(static_cast<unsigned>(blocks)), block(static_cast<unsigned>(T), static_cast<unsigned>(rows));
-    const bool bf = a.dtype == NVFP4_BF16, mx = a.format == NVFP4_FMT_MXFP8;
-    cudaError_t e;
-    if (bf) e = mx ? launch_c<NVFP4_BF16, NVFP4_FMT_MXFP8>(a, C, grid, block, s)
-                   : launch_c<NVFP4_BF16, NVFP4_FMT_NVFP4>(a, C, grid, block, s);
-    else e = mx ? launch_c<NVFP4_F32, NVFP4_FMT_MXFP8>(a, C, grid, block, s)
-                : launch_c<NVFP4_F32, NVFP4_FMT_NVFP4>(a, C, grid, block, s);
-    return static_cast<int>(e);
+    const bool mx = a.format == NVFP4_FMT_MXFP8;
+    if (a.dtype == NVFP4_BF16)
+        return static_cast<int>(mx ? launch_norm_w<NVFP4_BF16, NVFP4_FMT_MXFP8>(a, s)
+                                   : launch_norm_w<NVFP4_BF16, NVFP4_FMT_NVFP4>(a, s));
+    return static_cast<int>(mx ? launch_norm_w<NVFP4_F32, NVFP4_FMT_MXFP8>(a, s)
+                               : launch_norm_w<NVFP4_F32, NVFP4_FMT_NVFP4>(a, s));
 }
 
 }  // namespace nvfp4
