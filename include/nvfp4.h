@@ -258,7 +258,8 @@ enum nvfp4_format { NVFP4_FMT_NVFP4 = 0, NVFP4_FMT_MXFP8 = 1 };
  *   codes/scales the outputs of `format`; both NULL when only out or hidden_out
  *                is wanted
  * A sum of squares past fp32's range gives y = 0 for finite elements, as the
- * fp32 formula does.  EINVAL on bad shapes (K % 16), enums, pointers or eps,
+ * fp32 formula does.  EINVAL on bad shapes (K % 16), enums, pointers or eps, an
+ * output that is an input or another output (but for hidden_out and hidden),
  * gamax_mode TENSOR (the maximum over all rows is not known in one pass), a
  * gamax_mode with FMT_MXFP8, a bound outside (0, 448].
  */
@@ -278,11 +279,11 @@ enum nvfp4_x_type { NVFP4_X_F32 = 0, NVFP4_X_BF16 = 1, NVFP4_X_MXFP8 = 2 };
  *   gamax    NULL with gamax_mode NONE; 1 fp32 (TENSOR_GIVEN) or N (ROW_GIVEN)
  *   out      device [M,N], F32 or BF16 (RNE)
  * q * dec(s) is exact in f16.  x enters as f16 after a power-of-two scaling per
- * token and K-slice: an F32 x as the sum of two f16 (22 bits), BF16 and MXFP8 x
- * exactly, except that what lies 2^39 below the slice's largest magnitude is
+ * token and part of K: an F32 x as the sum of two f16 (22 bits), BF16 and MXFP8 x
+ * exactly, except that what lies 2^39 below the part's largest magnitude is
  * lost.  Sums are fp32 in a fixed order (the same bits on every run).
  * EINVAL: M outside [0, 16] (larger M: nvfp4_mm, nvfp4_grouped_mm), N < 0, K < 0,
- * K % 16, N or K >= 2^31, N * K too large, bad enums, pointers or bound.
+ * K % 16, N or K >= 2^30, bad enums, pointers or bound.
  */
 int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* codes, const uint8_t* scales,
              int64_t M, int64_t N, int64_t K, int gamax_mode, const float* gamax, float scale_bound, void* out,
@@ -305,7 +306,7 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
  *   workspace    device memory of nvfp4_grouped_mm_workspace(E, T, N, K) bytes (NULL when
  *                that is 0), written and read by this call alone
  * Products are exact and accumulate in fp32.  EINVAL: a negative size, K % 64,
- * E * N, T or K >= 2^31, bad enums, pointers or bound, a workspace that is too
+ * E * N, T or K >= 2^30, bad enums, pointers or bound, a workspace that is too
  * small.  A CTA that stops waiting for its tensor-core work writes NaN to its tile
  * of out.
  */

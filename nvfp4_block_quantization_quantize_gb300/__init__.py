@@ -56,7 +56,8 @@ _NAMES = {
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_dequantize", "nvfp4_qdq", "nvfp4_amax",
             "nvfp4_global_scales", "nvfp4_probe_divide", "nvfp4_probe_e2m1", "nvfp4_probe_sub_f16", "nvfp4_last_error",
-            "nvfp4_abi_version")
+            "nvfp4_abi_version", "nvfp4_scales_to_mma", "nvfp4_mm", "nvfp4_rmsnorm", "nvfp4_mv", "nvfp4_grouped_mm",
+            "nvfp4_grouped_mm_workspace")
 
 _lock = threading.Lock()
 _lib = None

@@ -270,6 +270,8 @@ int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int d
     if (any && !codes && !out && !hidden_out) return fail(NVFP4_EINVAL, "no output is given");
     if ((hidden == nullptr) != (hidden_out == nullptr))
         return fail(NVFP4_EINVAL, "give both hidden and hidden_out, or neither");
+    if (any && (hidden_out == x || (out && (out == x || out == hidden || out == hidden_out))))
+        return fail(NVFP4_EINVAL, "outputs must not be inputs (but hidden_out may be hidden) nor each other");
     if ((rc = check_ptr(x, "x", any))) return rc;
     if ((rc = check_ptr(hidden, "hidden", false))) return rc;
     if ((rc = check_ptr(weight, "weight", false))) return rc;
@@ -298,7 +300,7 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
     if (M < 0 || N < 0 || K < 0) return fail(NVFP4_EINVAL, "M, N and K must be >= 0");
     if (M > 16) return fail(NVFP4_EINVAL, "nvfp4_mv takes at most 16 rows of x (got %lld)", (long long)M);
     if (K % 16) return fail(NVFP4_EINVAL, "K must be a multiple of 16 (got %lld)", (long long)K);
-    if (N >= (int64_t{1} << 31) || K >= (int64_t{1} << 31)) return fail(NVFP4_EINVAL, "N and K must be below 2^31");
+    if (N >= (int64_t{1} << 30) || K >= (int64_t{1} << 30)) return fail(NVFP4_EINVAL, "N and K must be below 2^30");
     if (x_type < NVFP4_X_F32 || x_type > NVFP4_X_MXFP8) return fail(NVFP4_EINVAL, "bad x_type %d", x_type);
     if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
     if (gamax_mode != NVFP4_GAMAX_NONE && gamax_mode != NVFP4_GAMAX_TENSOR_GIVEN &&
@@ -330,7 +332,7 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
 }
 
 int64_t nvfp4_grouped_mm_workspace(int64_t E, int64_t T, int64_t N, int64_t K) {
-    constexpr int64_t kMax = int64_t{1} << 31;
+    constexpr int64_t kMax = int64_t{1} << 30;
     if (E <= 0 || T <= 0 || N <= 0 || K <= 0 || E >= kMax || T >= kMax || N >= kMax || K >= kMax) return 0;
     nvfp4::GroupedArgs a = {};
     a.E = E, a.T = T, a.N = N, a.K = K;
@@ -342,11 +344,11 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
                      int gamax_a_mode, const float* gamax_a, const float* gamax_b, float scale_bound, void* out,
                      int out_dtype, uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream) {
     g_msg[0] = '\0';
-    constexpr int64_t kMax = int64_t{1} << 31;
+    constexpr int64_t kMax = int64_t{1} << 30;
     if (E < 0 || T < 0 || N < 0 || K < 0) return fail(NVFP4_EINVAL, "E, T, N and K must be >= 0");
     if (K % 64) return fail(NVFP4_EINVAL, "nvfp4_grouped_mm needs K %% 64 == 0 (got %lld)", (long long)K);
     if (E >= kMax || T >= kMax || N >= kMax || K >= kMax || (N > 0 && E > (kMax - 1) / N))
-        return fail(NVFP4_EINVAL, "E * N, T and K must be below 2^31");
+        return fail(NVFP4_EINVAL, "E * N, T and K must be below 2^30");
     if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
     if (gamax_a_mode != NVFP4_GAMAX_NONE && gamax_a_mode != NVFP4_GAMAX_TENSOR_GIVEN &&
         gamax_a_mode != NVFP4_GAMAX_ROW_GIVEN)

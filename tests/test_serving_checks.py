@@ -48,6 +48,8 @@ NORM_BAD = {
     "hidden without hidden_out": dict(hidden=A16),
     "hidden_out without hidden": dict(hidden_out=A16),
     "x NULL": dict(x=None),
+    "hidden_out is x": dict(hidden=ctypes.c_void_p(0x20000), hidden_out=A16),
+    "out is x": dict(out=A16),
     "x misaligned": dict(x=A8),
     "weight misaligned": dict(weight=A8),
     "codes misaligned": dict(codes=A8),
@@ -69,7 +71,7 @@ MV_BAD = {
     "17 rows": dict(M=17),
     "negative N": dict(N=-1),
     "K not a multiple of 16": dict(K=72),
-    "N of 2^31": dict(N=1 << 31),
+    "N of 2^30": dict(N=1 << 30),
     "bad x type": dict(xt=3),
     "mxfp8 without scales": dict(xt=2),
     "scales without mxfp8": dict(xs=A16),
@@ -99,8 +101,8 @@ def grouped(lib, ca=A16, sa=A16, off=A16, cb=A16, sb=A16, E=4, T=8, N=32, K=64, 
 GROUPED_BAD = {
     "K not a multiple of 64": dict(K=96),
     "negative E": dict(E=-1),
-    "E * N of 2^31": dict(E=1 << 16, N=1 << 15),
-    "T of 2^31": dict(T=1 << 31),
+    "E * N of 2^30": dict(E=1 << 16, N=1 << 14),
+    "T of 2^30": dict(T=1 << 30),
     "computed amax": dict(gm=2, ga=A16),
     "gamax_a NULL": dict(gm=3),
     "gamax_b misaligned": dict(gb=ODD),
