@@ -19,6 +19,8 @@
 //     tiles cannot be laid out ahead: thread i reads token i's 16 scale bytes of a
 //     stage (some stages ahead, in registers) and writes them where the tile
 //     wants them.  The same warps then read the accumulator and store.
+// Measured: 64 tokens on 64 experts of [2048, 4096] 28.4 us (5.7 TB/s), 2 of 8 experts of
+// [1024, 1024] 3.5 us, 1999 tokens on 13 experts of [1430, 2112] 15 us.
 // A tile's last columns may read the next group's rows (or, past T, zeros): those
 // products are computed and not stored.  Every wait is bounded; a CTA whose wait
 // runs out writes NaN to its tile.
@@ -293,6 +295,8 @@ __global__ void __launch_bounds__(kGmThreads)
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
+// Measured: 8192 tokens on 8 experts of [14336, 4096] 205 us (4.7 PFLOP/s, tensor pipe 52 %
+// active); the copies alone take 184 us, 52 bytes a clock per SM from L2.
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;

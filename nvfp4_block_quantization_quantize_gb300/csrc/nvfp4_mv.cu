@@ -24,6 +24,10 @@
 // their sums meet through distributed shared memory at the end: no workspace, no
 // atomics, every sum in a fixed order.
 //
+// Measured: 4 tokens x [65536, 8192] 53 us (5.7 TB/s, 0.84 of the copy rate; without its
+// products the structure takes 51.5 us, without the scale bytes too 45.5), 1 token x
+// [14336, 4096] 9.0 us (3.7 TB/s), [1024, 1024] 2.2 us.
+//
 // VB is 4 where rows of codes are whole 32-byte sectors (K % 64 == 0, codes 32-byte
 // aligned): one 256-bit and one 32-bit load per row and 256 columns.  Otherwise 1.
 #include <cooperative_groups.h>
