@@ -18,7 +18,8 @@
 //   - warps 4-7: the tokens' scales.  Groups start at any row, so their 128 x 4
 //     tiles cannot be laid out ahead: thread i reads token i's 16 scale bytes of a
 //     stage (some stages ahead, in registers) and writes them where the tile
-//     wants them.  The same warps then read the accumulator and store.
+//     wants them;
+//   - warps 2 and 3: the tokens' decode scales.  All warps then store the accumulator.
 // Measured: 64 tokens on 64 experts of [2048, 4096] 28.4 us (5.7 TB/s), 2 of 8 experts of
 // [1024, 1024] 3.5 us, 1999 tokens on 13 experts of [1430, 2112] 15 us.
 // A tile's last columns may read the next group's rows (or, past T, zeros): those
@@ -107,6 +108,65 @@ __device__ __forceinline__ uint4 token_scales(const GroupedArgs& a, int row, int
     return v;
 }
 
+// 32 accumulator columns of this warp's 32 lanes, from the warp's tensor-memory address
+__device__ __forceinline__ void load_columns(uint32_t from, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(from));
+}
+
+// Scales and stores them: token col + i of the tile (of `rows`, the first at row0 of out) for
+// weight row nw + lane.  alpha: the tile's decode scales (readable up to col + 31).  bad: NaN
+// instead.  bf16 rows that start on 16 bytes are turned in shared memory (2 KB at turn), so
+// that four lanes store a token's 32 rows at 16 bytes each; else a lane stores its own row.
+constexpr int kTurn = 32 * 64;
+
+template <int ODT>
+__device__ __forceinline__ void store_columns(const GroupedArgs& a, const uint32_t* v, const float* alpha, int col,
+                                              int rows, int row0, int64_t nw, bool bad, uint8_t* turn, int lane) {
+    float f[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const float4 al = *reinterpret_cast<const float4*>(alpha + col + i);
+        f[i] = mul_rn(__uint_as_float(v[i]), al.x);
+        f[i + 1] = mul_rn(__uint_as_float(v[i + 1]), al.y);
+        f[i + 2] = mul_rn(__uint_as_float(v[i + 2]), al.z);
+        f[i + 3] = mul_rn(__uint_as_float(v[i + 3]), al.w);
+    }
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = __int_as_float(0x7FC00000);
+    }
+    if (ODT == NVFP4_BF16 && a.N % 8 == 0) {
+        __syncwarp();                                     // the last turn is read
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<__nv_bfloat16*>(turn + i * 64 + lane * 2) = __float2bfloat16_rn(f[i]);
+        __syncwarp();
+        const int64_t n = nw + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            const int token = col + i + lane / 4;
+            const uint4 o = *reinterpret_cast<const uint4*>(turn + (i + lane / 4) * 64 + (lane & 3) * 16);
+            if (token < rows && n < a.N)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(row0 + token) * a.N + n) = o;
+        }
+    } else if (nw + lane < a.N) {
+        int64_t o = static_cast<int64_t>(row0 + col) * a.N + nw + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, o += a.N) {
+            if (col + i >= rows) break;
+            if (ODT == NVFP4_F32) static_cast<float*>(a.out)[o] = f[i];
+            else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f[i]);
+        }
+    }
+}
+
 template <int BT, int ODT>
 __global__ void __launch_bounds__(kGmThreads)
     k_grouped(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapT,
@@ -117,26 +177,18 @@ __global__ void __launch_bounds__(kGmThreads)
     __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], accb;
     __shared__ uint32_t tmem_base;
     __shared__ int timed_out;
-    __shared__ float alpha[BT];
+    __shared__ __align__(16) float alpha[BT < 32 ? 32 : BT];
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);               // the same for the whole warp, and known to be
-    pdl_wait();
-    int expert, row0, rows;
-    find_tile(a, blockIdx.x % tiles, BT, expert, row0, rows);
-    if (rows == 0) return;                                // the same for the whole CTA
-    const int ntile = static_cast<int>(blockIdx.x) / tiles;
-    const int n0 = ntile * kGmRows;
-    const int ksteps = static_cast<int>(a.K / 64);
-    const int nstages = (ksteps + kGmStageK - 1) / kGmStageK;
-
+    // what needs no input, while the kernel before may still run
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&tmem_base)),
                      "r"(G::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid == 0) {
+    if (tid == 32) {
         for (int i = 0; i < G::kStages; ++i) {
             mbar_init(&full[i], 1 + G::kSfWarps);         // the TMA's transactions and the scale warps
             mbar_init(&empty[i]);
@@ -144,14 +196,18 @@ __global__ void __launch_bounds__(kGmThreads)
         mbar_init(&accb);
         timed_out = 0;
         asm volatile("fence.mbarrier_init.release.cluster;");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mapW)));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mapT)));
     }
-    for (int i = tid; i < rows; i += kGmThreads) {
-        float enc, da = 1.0f, db = 1.0f;
-        if (a.gamax_a_mode != NVFP4_GAMAX_NONE)
-            global_scales(a.gamax_a[a.gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? row0 + i : 0], a.bound, enc, da);
-        if (a.gamax_b) global_scales(a.gamax_b[expert], a.bound, enc, db);
-        alpha[i] = mul_rn(da, db);
-    }
+    pdl_trigger();                                        // the next kernel waits for this one's end itself
+    pdl_wait();
+    int expert, row0, rows;
+    find_tile(a, blockIdx.x % tiles, BT, expert, row0, rows);
+    const int ntile = static_cast<int>(blockIdx.x) / tiles;
+    const int n0 = ntile * kGmRows;
+    const int ksteps = static_cast<int>(a.K / 64);
+    // a tile past the last takes part in the barriers alone
+    const int nstages = rows == 0 ? 0 : (ksteps + kGmStageK - 1) / kGmStageK;
     asm volatile("tcgen05.fence::before_thread_sync;");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;");
@@ -204,6 +260,15 @@ __global__ void __launch_bounds__(kGmThreads)
             commit_warp<1>(el, &empty[s]);
         }
         commit_warp<1>(el, &accb);
+    } else if (warp == 2 || warp == 3) {
+        // ---- the tokens' decode scales ----
+        for (int i = tid - 64; i < (BT < 32 ? 32 : BT); i += 64) {
+            float enc, da = 1.0f, db = 1.0f;
+            if (i < rows && a.gamax_a_mode != NVFP4_GAMAX_NONE)
+                global_scales(a.gamax_a[a.gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? row0 + i : 0], a.bound, enc, da);
+            if (i < rows && a.gamax_b) global_scales(a.gamax_b[expert], a.bound, enc, db);
+            alpha[i] = mul_rn(da, db);
+        }
     } else if (warp >= 4 && warp < 4 + G::kSfWarps) {
         // ---- the tokens' scales: rows i and, of 256-token tiles, i + 128 ----
         const int i = tid - 128;
@@ -243,35 +308,23 @@ __global__ void __launch_bounds__(kGmThreads)
             }
         }
     }
-    // ---- epilogue: warps 4-7 read their 32 accumulator lanes ----
-    if (warp >= 4) {
-        __syncwarp();
-        if (!mbar_wait(&accb, 0)) timed_out = 1;
-        __syncwarp();
-        asm volatile("tcgen05.fence::after_thread_sync;");
-        const int64_t n = n0 + 32 * (warp - 4) + lane;
-        const bool bad = timed_out != 0;
-        for (int c0 = 0; c0 < rows; c0 += 16) {
-            uint32_t v[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                : "r"(tmem + (static_cast<uint32_t>(32 * (warp - 4)) << 16) + static_cast<uint32_t>(c0)));
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // ---- epilogue: every warp a quarter of the accumulator's lanes and every other 32 columns ----
+    __syncwarp();
+    if (!mbar_wait(&accb, 0)) timed_out = 1;
+    __syncthreads();                                      // the decode scales are there, the stages free
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const bool bad = timed_out != 0;
+    const int quad = warp & 3;
+    for (int c0 = 32 * (warp >> 2); c0 < rows; c0 += 64) {
+        uint32_t v[32];
+        load_columns(tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(c0), v);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        if (nstages == 0) {                               // K == 0: the accumulator was never written
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (c0 + i >= rows || n >= a.N) break;
-                // no stage at all (K == 0): the accumulator was never written
-                const float acc = nstages ? __uint_as_float(v[i]) : 0.0f;
-                const float f = bad ? __int_as_float(0x7FC00000) : mul_rn(acc, alpha[c0 + i]);
-                const int64_t o = static_cast<int64_t>(row0 + c0 + i) * a.N + n;
-                if (ODT == NVFP4_F32) static_cast<float*>(a.out)[o] = f;
-                else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f);
-            }
+            for (int i = 0; i < 32; ++i) v[i] = 0;
         }
+        store_columns<ODT>(a, v, alpha, c0, rows, row0, n0 + 32 * quad, bad, smem + warp * kTurn, lane);
     }
-    pdl_trigger();
     asm volatile("tcgen05.fence::before_thread_sync;");
     __syncthreads();
     if (warp == 0)
@@ -304,8 +357,7 @@ constexpr int kGpStages = 6;
 constexpr int kGpSlotW = 128 * 128, kGpSlotT = kGpBT / 2 * 128;
 constexpr int kGpSlotSfw = kGmStageK * 512, kGpSlotSft = kGmStageK * 1024;
 constexpr int kGpSlot = kGpSlotW + kGpSlotT + kGpSlotSfw + kGpSlotSft;       // 34 KB
-constexpr int kGpTurn = 32 * 64;                          // bytes a store warp turns at once: 32 tokens x 32 rows of bf16
-constexpr int kGpSmem = kGpStages * kGpSlot + kGpStoreWarps * kGpTurn + 1024;
+constexpr int kGpSmem = kGpStages * kGpSlot + kGpStoreWarps * kTurn + 1024;
 constexpr int kGpGroups = 256;                            // experts whose places are kept in shared memory
 constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages of 4 steps of 4 + 8 columns
 
@@ -531,8 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
         constexpr int kCols = kGpBT / (kGpStoreWarps / 4);
         const int quad = warp & 3, part = (warp - 2) / 4;
         const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(part * kCols);
-        const bool wide = a.N % 8 == 0;
-        uint8_t* turn = smem + kGpStages * kGpSlot + (warp - 2) * kGpTurn;
+        uint8_t* turn = smem + kGpStages * kGpSlot + (warp - 2) * kTurn;
         each_tile([&](int ntile, int, int expert, int row0, int rows, int) {
             const int buf = it & 1;
             for (int i = tid - 64; i < kGpBT; i += 32 * kGpStoreWarps) {
@@ -551,17 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             uint32_t v[kCols];
 #pragma unroll
             for (int c = 0; c < kCols; c += 32)
-                if (part * kCols + c < rows)
-                    asm volatile(
-                        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                        : "=r"(v[c]), "=r"(v[c + 1]), "=r"(v[c + 2]), "=r"(v[c + 3]), "=r"(v[c + 4]), "=r"(v[c + 5]),
-                          "=r"(v[c + 6]), "=r"(v[c + 7]), "=r"(v[c + 8]), "=r"(v[c + 9]), "=r"(v[c + 10]), "=r"(v[c + 11]),
-                          "=r"(v[c + 12]), "=r"(v[c + 13]), "=r"(v[c + 14]), "=r"(v[c + 15]), "=r"(v[c + 16]),
-                          "=r"(v[c + 17]), "=r"(v[c + 18]), "=r"(v[c + 19]), "=r"(v[c + 20]), "=r"(v[c + 21]),
-                          "=r"(v[c + 22]), "=r"(v[c + 23]), "=r"(v[c + 24]), "=r"(v[c + 25]), "=r"(v[c + 26]),
-                          "=r"(v[c + 27]), "=r"(v[c + 28]), "=r"(v[c + 29]), "=r"(v[c + 30]), "=r"(v[c + 31])
-                        : "r"(from + buf * kGpBT + static_cast<uint32_t>(c)));
+                if (part * kCols + c < rows) load_columns(from + buf * kGpBT + static_cast<uint32_t>(c), v + c);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;");
             __syncwarp();
@@ -574,45 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             for (int c = 0; c < kCols; c += 32) {
                 const int col = part * kCols + c;
                 if (col >= rows) break;
-                float f[32];
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 al = *reinterpret_cast<const float4*>(&alpha[buf][col + i]);
-                    f[i] = mul_rn(__uint_as_float(v[c + i]), al.x);
-                    f[i + 1] = mul_rn(__uint_as_float(v[c + i + 1]), al.y);
-                    f[i + 2] = mul_rn(__uint_as_float(v[c + i + 2]), al.z);
-                    f[i + 3] = mul_rn(__uint_as_float(v[c + i + 3]), al.w);
-                }
-                if (bad) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __int_as_float(0x7FC00000);
-                }
-                if (ODT == NVFP4_BF16 && wide) {
-                    // a lane has one weight row of 32 tokens: turned in shared memory, four lanes store a
-                    // token's 32 rows (64 bytes) at 16 bytes each
-                    __syncwarp();                         // the last turn is read
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        *reinterpret_cast<__nv_bfloat16*>(turn + i * 64 + lane * 2) = __float2bfloat16_rn(f[i]);
-                    __syncwarp();
-                    const int64_t n = nw + (lane & 3) * 8;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        const int token = col + i + lane / 4;
-                        const uint4 o = *reinterpret_cast<const uint4*>(turn + (i + lane / 4) * 64 + (lane & 3) * 16);
-                        if (token < rows && n < a.N)
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                      static_cast<int64_t>(row0 + token) * a.N + n) = o;
-                    }
-                } else if (nw + lane < a.N) {
-                    int64_t o = static_cast<int64_t>(row0 + col) * a.N + nw + lane;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i, o += a.N) {
-                        if (col + i >= rows) break;
-                        if (ODT == NVFP4_F32) static_cast<float*>(a.out)[o] = f[i];
-                        else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(f[i]);
-                    }
-                }
+                store_columns<ODT>(a, v + c, alpha[buf], col, rows, row0, nw, bad, turn, lane);
             }
             return true;
         });
