@@ -25,6 +25,8 @@
 // A tile's last columns may read the next group's rows (or, past T, zeros): those
 // products are computed and not stored.  Every wait is bounded; a CTA whose wait
 // runs out writes NaN to its tile.
+#include <cmath>
+
 #include "nvfp4_device.cuh"
 #include "nvfp4_tensor.cuh"
 
@@ -693,18 +695,23 @@ cudaError_t launch_grouped_o(const GroupedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Whether the call takes pairs of SMs (and a workspace): where their waves are fewer than
-// 3/2 of the single SMs' ones, on the tiles to be expected (a half-filled one a group).  A
-// wave of pairs takes about 2/3 of the time of a wave of 128 x 128 tiles, two CTAs an SM
-// (measured over 13 shapes; e.g. K 4096, us pairs / single: 8 experts 1024 x 4096 27 / 30, 1
-// expert 1024 x 14336 39 / 49, 32 experts 4096 x 4096 69 / 81, but 8 experts 512 x 4096 25 / 21).
+// Whether the call takes pairs of SMs (and a workspace): by a model of both, in us, on the
+// tiles to be expected (a half-filled one a group).  A wave of pairs takes about 3.5 + K / 1024
+// us and the call 4 more (the scales' layout), a wave of 128 x 128 tiles, two CTAs an SM, 4.2 +
+// 2 K / 1024 and 2 more (fitted over 17 shapes; e.g. us pairs / single: K 4096, 4 experts
+// 1024 x 14336 44 / 49, 2 experts 4096 x 4096 39 / 49, 32 experts 2048 x 4096 64 / 59; K 1024, 8
+// experts 8192 x 1024 20 / 13).  The last wave counts half its share and half a whole one.
 static bool takes_pairs(const GroupedArgs& a) {
-    constexpr int64_t kSms = 152;
-    if (a.K <= 0 || a.E <= 0 || a.T < 33 * a.E || a.K / 64 > 8 * 65535) return false;
-    const int64_t pair_tiles = ((2 * a.T + kGpBT - 1) / kGpBT + a.E) / 2 * ((a.N + 255) / 256);
-    const int64_t tiles = ((2 * a.T + 127) / 128 + a.E) / 2 * ((a.N + 127) / 128);
-    const int64_t pair_waves = (pair_tiles + kSms / 2 - 1) / (kSms / 2), waves = (tiles + 2 * kSms - 1) / (2 * kSms);
-    return a.N > 128 && 2 * pair_waves <= 3 * waves;
+    constexpr double kSms = 152;
+    if (a.K <= 0 || a.E <= 0 || a.N <= 128 || a.T < 33 * a.E || a.K / 64 > 8 * 65535) return false;
+    const double T = static_cast<double>(a.T), half = 0.5 * static_cast<double>(a.E), k = static_cast<double>(a.K) / 1024;
+    auto waves = [](double tiles, double at_once) {
+        const double w = tiles / at_once;
+        return w <= 1 ? 1.0 : 0.5 * (w + ceil(w));
+    };
+    const double pairs = waves((T / kGpBT + half) * static_cast<double>((a.N + 255) / 256), kSms / 2);
+    const double single = waves((T / 128 + half) * static_cast<double>((a.N + 127) / 128), 2 * kSms);
+    return 4 + pairs * (3.5 + k) < 0.97 * (2 + single * (4.2 + 2 * k));
 }
 
 int64_t grouped_workspace(const GroupedArgs& a) {

@@ -355,14 +355,32 @@ def test_grouped_exact(name, N, K):
     assert np.array_equal(to_np(y).astype(np.float64), ref)
 
 
+def values_on_device(codes, scales):
+    """float64 values of codes [..., K/2] and scale bytes [..., K/16] on the device (large cases)."""
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    c = torch.stack([codes & 15, codes >> 4], dim=-1).flatten(-2).int()
+    q = grid[c & 7] * (1 - 2 * (c >> 3)).double()
+    return q * scales.view(torch.float8_e4m3fn).double().repeat_interleave(16, dim=-1)
+
+
+def grouped_reference_on_device(ca, sa, cb, sb, offsets):
+    A = values_on_device(to_dev(ca), to_dev(sa))
+    y, mag = [], []
+    for e in range(cb.shape[0]):
+        a, B = A[offsets[e]:offsets[e + 1]], values_on_device(to_dev(cb[e]), to_dev(sb[e]))
+        y.append(a @ B.t())
+        mag.append(a.abs() @ B.abs().t())
+    return torch.cat(y), torch.cat(mag)
+
+
 PAIRS = {                                                 # many tokens an expert: pairs of SMs
-    "ragged": (4, [0, 1000, 1000, 1033, 2500], 4096, 320),
-    "rows off the tiles": (3, [0, 191, 900, 1733], 6008, 192),
-    "N not of 8": (2, [0, 769, 1600], 6001, 64),
-    "one expert": (1, [0, 1536], 6144, 448),
-    "second half past N": (2, [0, 1000, 2000], 4224, 128),
+    "ragged": (4, [0, 1000, 1000, 1033, 2500], 4096, 4160),
+    "rows off the tiles": (3, [0, 191, 900, 1733], 6008, 4160),
+    "N not of 8": (2, [0, 769, 1600], 6001, 4160),
+    "one expert": (1, [0, 1536], 6144, 4224),
+    "second half past N": (2, [0, 1000, 2000], 6272, 4160),
     "many stages": (1, [0, 200], 20000, 2112),
-    "over 256 experts": (300, list(range(0, 300 * 40, 40)) + [12000], 256, 64),
+    "over 256 experts": (260, list(range(0, 260 * 100 + 1, 100)), 256, 4160),
 }
 
 
@@ -374,28 +392,29 @@ def test_grouped_pairs_exact(name, out_dtype):
     assert nv.load_library().nvfp4_grouped_mm_workspace(E, T, N, K) > 0
     rng = np.random.default_rng(E + N + K)
     ca, sa, cb, sb = grouped_inputs(rng, E, T, N, K)
-    sa = (0x38 + 8 * rng.integers(-1, 2, sa.shape)).astype(np.uint8)
-    sb = (0x38 + 8 * rng.integers(-1, 2, sb.shape)).astype(np.uint8)
-    y = to_np(grouped_gpu(ca, sa, offsets, cb, sb, out_dtype=out_dtype).float())
-    ref, mag = grouped_reference(ca, sa, cb, sb, offsets, K)
-    assert mag.max() < 2 ** 20
-    want = ref.astype(np.float32)
-    assert np.array_equal(y, want if out_dtype == "f32" else bf16_round(want))
+    sa = (0x38 + 8 * rng.integers(-1, 2, sa.shape, dtype=np.int8)).astype(np.uint8)
+    sb = (0x38 + 8 * rng.integers(-1, 2, sb.shape, dtype=np.int8)).astype(np.uint8)
+    y = grouped_gpu(ca, sa, offsets, cb, sb, out_dtype=out_dtype)
+    ref, mag = grouped_reference_on_device(ca, sa, cb, sb, offsets)
+    assert float(mag.max()) < 2 ** 20                     # multiples of 1/16: exact in fp32
+    assert torch.equal(y, ref.float() if out_dtype == "f32" else ref.float().to(torch.bfloat16))
 
 
 def test_grouped_pairs_scales_and_rows_in_no_group():
     rng = np.random.default_rng(15)
-    E, offsets, N, K, T = 3, [5, 905, 905, 2105], 4104, 320, 2200
+    E, offsets, N, K, T = 3, [5, 905, 905, 2105], 4104, 4224, 2200
     assert nv.load_library().nvfp4_grouped_mm_workspace(E, T, N, K) > 0
     ca, sa, cb, sb = grouped_inputs(rng, E, T, N, K)
     sa[:5] = sa[2105:] = 0x7F
     ga, gb = rng.uniform(0.1, 9.0, T).astype(np.float32), rng.uniform(0.1, 9.0, E).astype(np.float32)
     buf = torch.full((T, N), 5.0, device="cuda")
-    y = to_np(grouped_gpu(ca, sa, offsets, cb, sb, out_dtype="f32", out=buf, gamax_a=to_dev(ga), gamax_b=to_dev(gb)))
-    sa[:5] = sa[2105:] = 0x38
-    ref, mag = grouped_reference(ca[5:2105], sa[5:2105], cb, sb, [0, 900, 900, 2100], K, ga[5:2105], gb)
-    assert (y[:5] == 5).all() and (y[2105:] == 5).all()
-    assert (np.abs(y[5:2105] - ref) <= mag * (K / 64 + 4) * 2.0 ** -22).all()
+    y = grouped_gpu(ca, sa, offsets, cb, sb, out_dtype="f32", out=buf, gamax_a=to_dev(ga), gamax_b=to_dev(gb))
+    assert bool((y[:5] == 5).all()) and bool((y[2105:] == 5).all())
+    ref, mag = grouped_reference_on_device(ca[5:2105], sa[5:2105], cb, sb, [0, 900, 900, 2100])
+    d = torch.from_numpy(decode_scale(ga[5:2105])).cuda()[:, None]
+    g = torch.from_numpy(decode_scale(gb)).cuda()
+    d = d * torch.cat([g[0].repeat(900), g[2].repeat(1200)])[:, None]
+    assert bool(((y[5:2105].double() - ref * d).abs() <= mag * d * (K / 64 + 4) * 2.0 ** -22).all())
 
 
 @pytest.mark.parametrize("a_mode", ["none", "tensor", "row"])
