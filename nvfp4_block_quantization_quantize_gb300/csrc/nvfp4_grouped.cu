@@ -20,8 +20,8 @@
 //     stage (some stages ahead, in registers) and writes them where the tile
 //     wants them;
 //   - warps 2 and 3: the tokens' decode scales.  All warps then store the accumulator.
-// Measured: 64 tokens on 64 experts of [2048, 4096] 28.4 us (5.7 TB/s), 2 of 8 experts of
-// [1024, 1024] 3.5 us, 1999 tokens on 13 experts of [1430, 2112] 15 us.
+// Measured: 64 tokens on 64 experts of [2048, 4096] 28.1 us (5.7 TB/s), 2 of 8 experts of
+// [1024, 1024] 3.4 us, 1999 tokens on 13 experts of [1430, 2112] 12.6 us.
 // A tile's last columns may read the next group's rows (or, past T, zeros): those
 // products are computed and not stored.  Every wait is bounded; a CTA whose wait
 // runs out writes NaN to its tile.
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kGmThreads)
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
-// Measured: 8192 tokens on 8 experts of [14336, 4096] 205 us (4.7 PFLOP/s, tensor pipe 52 %
+// Measured: 8192 tokens on 8 experts of [14336, 4096] 206 us (4.7 PFLOP/s, tensor pipe 52 %
 // active); the copies alone take 184 us, 52 bytes a clock per SM from L2.
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
@@ -409,6 +409,24 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
             : "r"(smem_addr(bar)), "r"(parity)
             : "memory");
         if (ok) return true;
+    }
+    return false;
+}
+
+// both of two barriers' phases (of the second unless skip), with the two polls under way together
+__device__ __forceinline__ bool mbar_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, bool skip) {
+    for (long it = 0; it < kWaitLimit; ++it) {
+        uint32_t x, y;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%2], %3;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%4], %5;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "selp.u32 %1, 1, 0, q;\n\t}"
+            : "=r"(x), "=r"(y)
+            : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb)
+            : "memory");
+        if (x && (y || skip)) return true;
     }
     return false;
 }
@@ -553,8 +571,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             asm volatile("tcgen05.fence::after_thread_sync;");
             const uint32_t d = tmem + buf * kGpBT;
             for (int t = 0; t < nstages; ++t, ++st) {
-                const int s = st % kGpStages;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&full[s], static_cast<uint32_t>((st / kGpStages) & 1)))) {
+                // The stage is there, and the products of the stage before the last are done (their slot is free
+                // again): the scales' columns of two stages are used in turn, and a copy is not ordered behind
+                // earlier products that read what it overwrites.  The last stage's products keep the pipe busy.
+                const int s = st % kGpStages, e = max(st - 2, 0) % kGpStages;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_both(&full[s], static_cast<uint32_t>((st / kGpStages) & 1), &empty[e],
+                                                            static_cast<uint32_t>((max(st - 2, 0) / kGpStages) & 1), st < 2))) {
                     timed_out = 1;
                     return false;
                 }
@@ -562,8 +584,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
                 const uint32_t slot = smem_addr(smem) + s * kGpSlot, sf = slot + kGpSlotW + kGpSlotT;
                 const uint64_t dw = smem_desc(slot, 16, 1024, 2), dt = smem_desc(slot + kGpSlotW, 16, 1024, 2);
                 const uint64_t dsw = smem_desc(sf, 0, 128), dst = smem_desc(sf + kGpSlotSfw, 0, 128);
-                // Two stages' columns in turn: the copies of a stage follow the products of the stage
-                // before the last in the tensor pipe, which takes copies and products in issue order.
                 const uint32_t c0 = tmem + kGpColSf + static_cast<uint32_t>(st & 1) * 48;
                 const int nk = min(ksteps - t * kGmStageK, kGmStageK);
 #pragma unroll

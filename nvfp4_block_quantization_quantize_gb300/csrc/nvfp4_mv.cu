@@ -24,7 +24,7 @@
 // their sums meet through distributed shared memory at the end: no workspace, no
 // atomics, every sum in a fixed order.
 //
-// Measured: 4 tokens x [65536, 8192] 53 us (5.7 TB/s, 0.84 of the copy rate; without its
+// Measured: 4 tokens x [65536, 8192] 54 us (5.6 TB/s, 0.83 of the copy rate; without its
 // products the structure takes 51.5 us, without the scale bytes too 45.5), 1 token x
 // [14336, 4096] 9.0 us (3.7 TB/s), [1024, 1024] 2.2 us.
 //
