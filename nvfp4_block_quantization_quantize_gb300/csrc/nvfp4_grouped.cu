@@ -11,7 +11,7 @@
 // are known on the device only: the grid has the largest number of token tiles T
 // rows in E groups can need (token tiles fastest, so that the CTAs of one weight
 // tile run together), and each CTA finds its expert by a warp-wide scan of the
-// offsets (CTAs past the last tile leave at once).
+// offsets (CTAs past the last tile only take part in its barriers).
 //   - warp 0: TMA of the code tiles (256 columns of K: 128 bytes a row, 128-byte
 //     swizzle) and bulk copies of the weight's scale tiles, kStages slots deep;
 //   - warp 1: per 64 columns, scale tiles to tensor memory and one tcgen05.mma;

@@ -241,16 +241,20 @@ __device__ __forceinline__ void convert_x(const MvArgs& a, uint8_t* xs, float* u
         const uint8_t* raw = cells + raw_offset<XT, VB>(n);
         uint32_t top = 0;
         if (XT == NVFP4_X_MXFP8) {
+            // the largest scale of a group that holds anything but zeros (whose scale may be any)
             for (int i = lane; i * 4 < pieces; i += 32) {
                 const uint32_t b = sb[m * sb_stride + i];
-                top = max(top, b == 255 ? 0u : b);
+                const uint4* q = reinterpret_cast<const uint4*>(raw + 32 * i);
+                uint32_t any = q[0].x | q[0].y | q[0].z | q[0].w;
+                if (i * 4 + 2 < pieces) any |= q[1].x | q[1].y | q[1].z | q[1].w;
+                top = max(top, b == 255 || !(any & 0x7F7F7F7Fu) ? 0u : b);
             }
         } else {
             for (int i = lane; i < pieces; i += 32) top = max(top, top8<XT>(raw + kPiece * i));
         }
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         // scaled to at most 2^15: x by 2^(14 - e), e its exponent (at least -112, so that this is a
-        // float); an E4M3 element by 2^(b - top + 6)
+        // float); an E4M3 element by 2^(b - top + 6) (b above top: of zeros)
         const int e = XT == NVFP4_X_MXFP8 ? static_cast<int>(top) - 127 - 6
                                           : max(static_cast<int>(top >> 23) - 127, -112) - 14;
         if (lane == 0) up[m] = power_of_two(e);
@@ -262,7 +266,7 @@ __device__ __forceinline__ void convert_x(const MvArgs& a, uint8_t* xs, float* u
             if (XT == NVFP4_X_MXFP8) {
                 const int b = i < pieces ? sb[m * sb_stride + i / 4] : 0;
                 const __half2 f2 = __float2half2_rn(b == 255 ? __int_as_float(0x7FC00000)
-                                                             : power_of_two(max(b - static_cast<int>(top) + 6, -149)));
+                                                             : power_of_two(min(max(b - static_cast<int>(top), -155), 0) + 6));
                 f = *reinterpret_cast<const uint32_t*>(&f2);
             }
             uint32_t h[P][4];

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(MAXT, DT == NVFP4_BF16 && MAXT == 512 ? 2 : 1)
     int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     // threads of a pair stay together: every thread makes the same number of steps
     const int64_t steps = C ? 1 : (bpr + T - 1) / T;
-        constexpr bool kAhead = C == 1 && (DT == NVFP4_BF16 || MAXT == 512);     // fp32 of 1024 threads would spill
+    constexpr bool kAhead = C == 1 && (DT == NVFP4_BF16 || MAXT == 512);     // fp32 of 1024 threads would spill
     Raw<DT> raw;
     auto load = [&](int64_t r, int64_t c) {
         const int64_t blk = threadIdx.x + c * T;

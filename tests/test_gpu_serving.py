@@ -134,6 +134,31 @@ def test_mv_range(scale, x_type):
     assert (np.abs(y - xv @ wv.T) <= bound).all()
 
 
+@pytest.mark.parametrize("zero_scale", [0, 127, 254, 255])
+@pytest.mark.parametrize("M,K", [(1, 512), (5, 2064)])
+def test_mv_mxfp8_zero_groups(zero_scale, M, K):
+    """A group of zeros may have any scale: it takes no range from the small ones (NaN: the row is NaN)."""
+    rng = np.random.default_rng(K + zero_scale)
+    N, groups = 50, -(-K // 32)
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    scales = (0x38 + 8 * rng.integers(-1, 2, (N, K // 16))).astype(np.uint8)
+    x = rng.integers(-7, 8, (M, K)).astype(np.float32)
+    b = np.full((M, groups), 127 - 60, np.uint8)
+    zero = rng.random((M, groups)) < 0.4
+    zero[0] = True                                        # a token of zeros alone
+    zero[:, -1] = True
+    b[zero] = zero_scale
+    x[np.repeat(zero, 32, axis=1)[:, :K]] = 0.0
+    xd = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8)
+    xd[torch.from_numpy(x == 0)] = torch.from_numpy((rng.integers(0, 2, int((x == 0).sum())) * 128).astype(np.uint8))      # either zero
+    y = to_np(nv.nvfp4_mv(xd.cuda(), to_dev(codes), to_dev(scales), x_scales=to_dev(b), out_dtype="f32"))
+    if zero_scale == 255:
+        assert np.isnan(y).all()
+        return
+    ref = (x.astype(np.float64) * 2.0 ** -60) @ values(codes, scales, N, K).T
+    assert np.array_equal(y.astype(np.float64), ref) and (M == 1 or np.abs(ref[1:]).max() > 0)
+
+
 def test_mv_special_values():
     """NaN and infinities of x reach every product they take part in and no other token."""
     rng = np.random.default_rng(11)
