@@ -26,6 +26,7 @@
 // products are computed and not stored.  Every wait is bounded; a CTA whose wait
 // runs out writes NaN to its tile.
 #include <cmath>
+#include <type_traits>
 
 #include "nvfp4_device.cuh"
 #include "nvfp4_tensor.cuh"
@@ -355,10 +356,11 @@ __global__ void __launch_bounds__(kGmThreads)
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;
-constexpr int kGpStages = 6;
-constexpr int kGpSlotW = 128 * 128, kGpSlotT = kGpBT / 2 * 128;
-constexpr int kGpSlotSfw = kGmStageK * 512, kGpSlotSft = kGmStageK * 1024;
-constexpr int kGpSlot = kGpSlotW + kGpSlotT + kGpSlotSfw + kGpSlotSft;       // 34 KB
+constexpr int kGpStages = 3;
+constexpr int kGpStageK = 2 * kGmStageK;                  // 64-column steps of a stage, in two halves
+constexpr int kGpHalfW = 128 * 128, kGpHalfT = kGpBT / 2 * 128;              // codes of a half
+constexpr int kGpSlotSfw = kGpStageK * 512, kGpSlotSft = kGpStageK * 1024;
+constexpr int kGpSlot = 2 * (kGpHalfW + kGpHalfT) + kGpSlotSfw + kGpSlotSft;  // 68 KB
 constexpr int kGpSmem = kGpStages * kGpSlot + kGpStoreWarps * kTurn + 1024;
 constexpr int kGpGroups = 256;                            // experts whose places are kept in shared memory
 constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages of 4 steps of 4 + 8 columns
@@ -413,7 +415,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     return false;
 }
 
-// both of two barriers' phases (of the second unless skip), with the two polls under way together
+// both of two barriers' phases (of the second unless skip), with the two polls under way together; a whole warp
+// calls it and all its lanes get the same answer
 __device__ __forceinline__ bool mbar_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, bool skip) {
     for (long it = 0; it < kWaitLimit; ++it) {
         uint32_t x, y;
@@ -426,7 +429,7 @@ __device__ __forceinline__ bool mbar_wait_both(uint64_t* a, uint32_t pa, uint64_
             : "=r"(x), "=r"(y)
             : "r"(smem_addr(a)), "r"(pa), "r"(smem_addr(b)), "r"(pb)
             : "memory");
-        if (x && (y || skip)) return true;
+        if (__all_sync(0xFFFFFFFFu, x && (y || skip))) return true;
     }
     return false;
 }
@@ -440,14 +443,97 @@ __device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ---- a pair's bf16 output by TMA
+// The accumulator is read in the layout of a product's fragments: word 16 hh + 4 j + 2 m + e of
+// lane l is column 8 j + 2 (l % 4) + e of row 16 hh + 8 m + l / 4 (32 columns, the warp's 32 rows),
+// so that a pair of words is a token pair of one weight row and a transposing stmatrix turns 8
+// tokens x 32 rows at once: against two-byte stores of the 32x32b layout's rows a quarter of the
+// shared memory's time, which the copies and the products need (8192 tokens on 8 experts of
+// [14336, 4096]: without stores 158 us, with those 202, by these 193).
+__device__ __forceinline__ void load_fragments(uint32_t from, uint32_t* v) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh, v += 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+            "[%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(from + (static_cast<uint32_t>(16 * hh) << 16)));
+}
+
+// the stores of this thread's groups are out of shared memory (ALL: are done)
+template <bool ALL>
+__device__ __forceinline__ void bulk_stores_wait() {
+    if (ALL) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// store_columns for fragments: 32 tokens whole go out of shared memory (2 KB at turn, 64 bytes a token,
+// 64-byte swizzle) by TMA, the last of a tile by lanes.
+__device__ __forceinline__ void store_fragments(const GroupedArgs& a, const CUtensorMap* out, const uint32_t* v,
+                                                const float* alpha, int col, int rows, int row0, int64_t nw, bool bad,
+                                                uint8_t* turn, int lane) {
+    if (nw >= a.N) return;
+    if (lane == 0) bulk_stores_wait<false>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 al = *reinterpret_cast<const float2*>(alpha + col + 8 * j + 2 * (lane & 3));
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t* u = v + 16 * (q >> 1) + 4 * j + 2 * (q & 1);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(mul_rn(__uint_as_float(u[0]), al.x), mul_rn(__uint_as_float(u[1]), al.y));
+            w[q] = bad ? 0x7FC07FC0u : *reinterpret_cast<const uint32_t*>(&b);
+        }
+        // lane l gives the place of token 8 j + l % 8's rows 8 (l / 8) to 8 (l / 8) + 7
+        const int i = 8 * j + (lane & 7);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         smem_addr(turn + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4))),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+    if (col + 32 <= rows) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(out)),
+                         "r"(static_cast<int>(nw)), "r"(row0 + col), "r"(smem_addr(turn))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
+    }
+    __syncwarp();
+    const int64_t n = nw + (lane & 3) * 8;
+#pragma unroll
+    for (int i = lane / 4; i < 32; i += 8) {
+        const uint4 o = *reinterpret_cast<const uint4*>(turn + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
+        if (col + i < rows && n < a.N)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(row0 + col + i) * a.N + n) = o;
+    }
+    __syncwarp();
+}
+
 template <int ODT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
     k_grouped_pair(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapT,
+                   const __grid_constant__ CUtensorMap mapW2, const __grid_constant__ CUtensorMap mapT2,
                    const __grid_constant__ CUtensorMap mapSW, const __grid_constant__ CUtensorMap mapST,
+                   const __grid_constant__ CUtensorMap mapOut,
                    const GroupedArgs a, unsigned slots, unsigned all_tiles) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kGpStages], empty[kGpStages], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t full[kGpStages], done[2 * kGpStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int timed_out;
     __shared__ __align__(16) float alpha[2][kGpBT];
@@ -458,17 +544,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
     const int rank = static_cast<int>(blockIdx.x & 1);
     const unsigned pairs = gridDim.x / 2;
     const int ksteps = static_cast<int>(a.K / 64);
-    const int nstages = (ksteps + kGmStageK - 1) / kGmStageK;
+    const int nstages = (ksteps + kGpStageK - 1) / kGpStageK;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     if (tid == 32) {
-        for (int i = 0; i < kGpStages; ++i) {
-            mbar_init(&full[i]);                          // used in the first CTA: both CTAs' transactions
-            mbar_init(&empty[i]);
-        }
+        for (int i = 0; i < kGpStages; ++i) mbar_init(&full[i]);             // used in the first CTA: both CTAs' transactions
+        for (int i = 0; i < 2 * kGpStages; ++i) mbar_init(&done[i]);         // the products of a stage's half
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i]);
             mbar_init(&acc_empty[i], 2 * kGpStoreWarps);  // of both CTAs
@@ -480,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;");
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, tmem_base);      // in a uniform register, as tcgen05 operands are
     pdl_trigger();                                        // the next kernel waits for this one's end itself
     pdl_wait();
 
@@ -541,26 +625,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             const int sfw = (expert * sf_tiles + min(n0 / 128, sf_tiles - 1)) * ksteps, sft = slot * ksteps * 2;
             for (int t = 0; t < nstages; ++t, ++st) {
                 const int s = st % kGpStages;
-                if (st >= kGpStages && !mbar_wait_cluster(&empty[s], static_cast<uint32_t>((st / kGpStages - 1) & 1))) {
+                if (st >= kGpStages && !mbar_wait_cluster(&done[2 * s + 1], static_cast<uint32_t>((st / kGpStages - 1) & 1))) {
                     timed_out = 1;
                     return false;
                 }
                 if (lane == 0) {
-                    const int k0 = t * kGmStageK;
-                    uint8_t* dst = smem + s * kGpSlot;
+                    const int k0 = t * kGpStageK;
+                    uint8_t *dst = smem + s * kGpSlot, *dstT = dst + 2 * kGpHalfW, *sf = dstT + 2 * kGpHalfT;
                     const uint32_t bar = cluster_addr(&full[s], 0);
-                    if (rank == 0) mbar_expect_tx(&full[s], 2 * kGpSlot);
-                    tma_2d_pair(dst, &mapW, k0 * 32, wrow, bar);
-                    tma_2d_pair(dst + kGpSlotW, &mapT, k0 * 32, trow, bar);
-                    tma_2d_pair(dst + kGpSlotW + kGpSlotT, &mapSW, 0, sfw + k0, bar);
-                    tma_2d_pair(dst + kGpSlotW + kGpSlotT + kGpSlotSfw, &mapST, 0, sft + 2 * k0, bar);
+                    // both halves in one copy, but for a row's last, ragged piece
+                    const bool ragged = ksteps % kGmStageK && k0 + kGpStageK > ksteps;
+                    const int one = ragged && k0 + kGmStageK >= ksteps;      // that piece alone is there
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * (kGpSlot - one * (kGpHalfW + kGpHalfT)));
+                    if (!ragged) {
+                        tma_3d_pair(dst, &mapW2, 0, wrow, k0 / kGmStageK, bar);
+                        tma_3d_pair(dstT, &mapT2, 0, trow, k0 / kGmStageK, bar);
+                    } else {
+                        for (int h = 0; h < 2 - one; ++h) {
+                            tma_2d_pair(dst + h * kGpHalfW, &mapW, (k0 + h * kGmStageK) * 32, wrow, bar);
+                            tma_2d_pair(dstT + h * kGpHalfT, &mapT, (k0 + h * kGmStageK) * 32, trow, bar);
+                        }
+                    }
+                    tma_2d_pair(sf, &mapSW, 0, sfw + k0, bar);
+                    tma_2d_pair(sf + kGpSlotSfw, &mapST, 0, sft + 2 * k0, bar);
                 }
                 __syncwarp();
             }
             return true;
         });
     } else if (warp == 1 && rank == 0) {
+        // Slots and phases are counted up, and every operand is the base plus a counter's multiple: what
+        // the compiler can keep in uniform registers (division by the ring's length cannot) and issue fast.
         const uint32_t el = elect_one();
+        const uint32_t sf0 = 2 * (kGpHalfW + kGpHalfT);
+        const uint64_t dw0 = smem_desc(smem_addr(smem), 16, 1024, 2);
+        const uint64_t dt0 = smem_desc(smem_addr(smem) + 2 * kGpHalfW, 16, 1024, 2);
+        const uint64_t dsw0 = smem_desc(smem_addr(smem) + sf0, 0, 128);
+        const uint64_t dst0 = smem_desc(smem_addr(smem) + sf0 + kGpSlotSfw, 0, 128);
+        uint32_t s = 0, phase = 0;                        // of the stages
+        bool first = true;
         each_tile([&](int, int, int, int, int, int N) {
             const uint32_t idesc = instr_desc(256, N);
             const int buf = it & 1;
@@ -570,32 +673,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             }
             asm volatile("tcgen05.fence::after_thread_sync;");
             const uint32_t d = tmem + buf * kGpBT;
-            for (int t = 0; t < nstages; ++t, ++st) {
-                // The stage is there, and the products of the stage before the last are done (their slot is free
-                // again): the scales' columns of two stages are used in turn, and a copy is not ordered behind
-                // earlier products that read what it overwrites.  The last stage's products keep the pipe busy.
-                const int s = st % kGpStages, e = max(st - 2, 0) % kGpStages;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_both(&full[s], static_cast<uint32_t>((st / kGpStages) & 1), &empty[e],
-                                                            static_cast<uint32_t>((max(st - 2, 0) / kGpStages) & 1), st < 2))) {
-                    timed_out = 1;
-                    return false;
-                }
-                asm volatile("tcgen05.fence::after_thread_sync;");
-                const uint32_t slot = smem_addr(smem) + s * kGpSlot, sf = slot + kGpSlotW + kGpSlotT;
-                const uint64_t dw = smem_desc(slot, 16, 1024, 2), dt = smem_desc(slot + kGpSlotW, 16, 1024, 2);
-                const uint64_t dsw = smem_desc(sf, 0, 128), dst = smem_desc(sf + kGpSlotSfw, 0, 128);
-                const uint32_t c0 = tmem + kGpColSf + static_cast<uint32_t>(st & 1) * 48;
-                const int nk = min(ksteps - t * kGmStageK, kGmStageK);
+            // the steps of a half from the stage's offset `at` on (a branch between two issues costs about as much
+            // as an issue, so whole halves and both kinds of tiles have code of their own)
+            auto steps = [&](auto two, auto whole, uint64_t at, int half, uint32_t acc, int nk) {
+                const uint64_t dw = dw0 + at + half * (kGpHalfW / 16), dt = dt0 + at + half * (kGpHalfT / 16);
+                const uint64_t dsw = dsw0 + at + half * (kGpSlotSfw / 32), dst = dst0 + at + half * (kGpSlotSft / 32);
+                const uint32_t c0 = tmem + kGpColSf + half * 48;
 #pragma unroll
                 for (int kk = 0; kk < kGmStageK; ++kk) {
-                    if (kk >= nk) break;
+                    if (!decltype(whole)::value && kk >= nk) break;
                     const uint32_t c = c0 + kk * 12;
                     copy_scales_warp<2>(el, c, dsw + kk * 32);
                     copy_scales_warp<2>(el, c + 4, dst + kk * 64);
-                    if (N > 128) copy_scales_warp<2>(el, c + 8, dst + kk * 64 + 32);
-                    mma_f4_warp<2>(el, d, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, t + kk > 0 ? 1u : 0u);
+                    if (decltype(two)::value) copy_scales_warp<2>(el, c + 8, dst + kk * 64 + 32);
+                    mma_f4_warp<2>(el, d, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, kk > 0 ? 1u : acc);
                 }
-                commit_warp<2>(el, &empty[s]);
+            };
+            auto k_loop = [&](auto two) {
+                for (int k0 = 0; k0 < ksteps; k0 += kGpStageK) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        // The stage is there, and the products of the same half of the stage before are done: the
+                        // scales' columns of two halves are used in turn, and a copy is not ordered behind earlier
+                        // products that read what it overwrites.  The other half's products keep the pipe busy.
+                        const uint32_t before = s ? s - 1 : kGpStages - 1;
+                        if (!mbar_wait_both(&full[s], phase, &done[2 * before + half], s ? phase : phase ^ 1, first))
+                            return false;
+                        asm volatile("tcgen05.fence::after_thread_sync;");
+                        const uint64_t at = s * (kGpSlot / 16);
+                        const int nk = ksteps - k0 - half * kGmStageK;       // of a ragged stage's second half <= 0
+                        const uint32_t acc = k0 + half > 0 ? 1u : 0u;
+                        if (nk >= kGmStageK) steps(two, std::true_type{}, at, half, acc, nk);
+                        else steps(two, std::false_type{}, at, half, acc, nk);
+                        commit_warp<2>(el, &done[2 * s + half]);
+                    }
+                    first = false;
+                    if (++s == kGpStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                return true;
+            };
+            if (!__all_sync(0xFFFFFFFFu, N > 128 ? k_loop(std::true_type{}) : k_loop(std::false_type{}))) {
+                timed_out = 1;
+                return false;
             }
             commit_warp<2>(el, &acc_full[buf]);
             return true;
@@ -606,6 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
         const int quad = warp & 3, part = (warp - 2) / 4;
         const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(part * kCols);
         uint8_t* turn = smem + kGpStages * kGpSlot + (warp - 2) * kTurn;
+        const bool whole = ODT == NVFP4_BF16 && a.N % 8 == 0;                // rows of out start on 16 bytes
         each_tile([&](int ntile, int, int expert, int row0, int rows, int) {
             const int buf = it & 1;
             for (int i = tid - 64; i < kGpBT; i += 32 * kGpStoreWarps) {
@@ -624,7 +747,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             uint32_t v[kCols];
 #pragma unroll
             for (int c = 0; c < kCols; c += 32)
-                if (part * kCols + c < rows) load_columns(from + buf * kGpBT + static_cast<uint32_t>(c), v + c);
+                if (part * kCols + c < rows) {
+                    if (whole) load_fragments(from + buf * kGpBT + static_cast<uint32_t>(c), v + c);
+                    else load_columns(from + buf * kGpBT + static_cast<uint32_t>(c), v + c);
+                }
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;");
             __syncwarp();
@@ -637,10 +763,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
             for (int c = 0; c < kCols; c += 32) {
                 const int col = part * kCols + c;
                 if (col >= rows) break;
-                store_columns<ODT>(a, v + c, alpha[buf], col, rows, row0, nw, bad, turn, lane);
+                if (whole) store_fragments(a, &mapOut, v + c, alpha[buf], col, rows, row0, nw, bad, turn, lane);
+                else store_columns<ODT>(a, v + c, alpha[buf], col, rows, row0, nw, bad, turn, lane);
             }
             return true;
         });
+        if (lane == 0) bulk_stores_wait<true>();
     }
     // neither CTA leaves while the other may still read its shared memory or arrive at its barriers
     __syncwarp();
@@ -655,11 +783,14 @@ cudaError_t launch_pair(const GroupedArgs& a, cudaStream_t s) {
     const int64_t slots = pair_slots(a), ksteps = a.K / 64;
     const int64_t tiles = slots * ((a.N + 255) / 256);
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    CUtensorMap mapW = {}, mapT = {}, mapSW = {}, mapST = {};
+    CUtensorMap mapW = {}, mapT = {}, mapW2 = {}, mapT2 = {}, mapSW = {}, mapST = {}, mapOut = {};
     if (!encode_codes_map(&mapW, a.codes_b, a.E * a.N, a.K, 128) ||
         !encode_codes_map(&mapT, a.codes_a, a.T, a.K, kGpBT / 2) ||
-        !encode_scales_map(&mapSW, a.scales_b, a.E * ((a.N + 127) / 128) * ksteps, kGmStageK) ||
-        !encode_scales_map(&mapST, a.workspace, slots * ksteps * 2, 2 * kGmStageK))
+        !encode_codes_map2(&mapW2, a.codes_b, a.E * a.N, a.K, 128) ||
+        !encode_codes_map2(&mapT2, a.codes_a, a.T, a.K, kGpBT / 2) ||
+        !encode_scales_map(&mapSW, a.scales_b, a.E * ((a.N + 127) / 128) * ksteps, kGpStageK) ||
+        !encode_scales_map(&mapST, a.workspace, slots * ksteps * 2, 2 * kGpStageK) ||
+        (ODT == NVFP4_BF16 && a.N % 8 == 0 && !encode_out_map(&mapOut, a.out, a.T, a.N)))
         return cudaErrorInvalidValue;
     static thread_local int configured_dev = -1;         // the attribute and the pairs are per device
     static thread_local int pairs_at_once = 0;            // an odd SM of a GPC has no partner
@@ -681,7 +812,7 @@ cudaError_t launch_pair(const GroupedArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t pairs = tiles < pairs_at_once ? tiles : pairs_at_once;
     return launch_pdl(k_grouped_pair<ODT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGpThreads), kGpSmem, s, mapW,
-                      mapT, mapSW, mapST, a, static_cast<unsigned>(slots), static_cast<unsigned>(tiles));
+                      mapT, mapW2, mapT2, mapSW, mapST, mapOut, a, static_cast<unsigned>(slots), static_cast<unsigned>(tiles));
 }
 
 template <int BT, int ODT>

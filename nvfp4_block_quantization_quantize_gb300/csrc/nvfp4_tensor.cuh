@@ -190,6 +190,34 @@ inline bool encode_codes_map(CUtensorMap* map, const uint8_t* codes, int64_t row
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the same with two neighbouring pieces of 128 bytes of each row a box ([2][box_rows][128], each
+// piece swizzled as above); the columns past the last whole piece are left out
+inline bool encode_codes_map2(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t pieces = K < 256 ? 1 : static_cast<cuuint64_t>(K / 256);
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), pieces};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K / 2), 128};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2D map of a bf16 output [rows, N], N % 8 == 0: boxes of 32 rows x 32 columns, 64-byte swizzle
+inline bool encode_out_map(CUtensorMap* map, void* out, int64_t rows, int64_t N) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 // 2D map of `tiles` 512-byte scale tiles, boxes of box_tiles of them
 inline bool encode_scales_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles, int box_tiles) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();

@@ -405,6 +405,9 @@ PAIRS = {                                                 # many tokens an exper
     "one expert": (1, [0, 1536], 6144, 4224),
     "second half past N": (2, [0, 1000, 2000], 6272, 4160),
     "many stages": (1, [0, 200], 20000, 2112),
+    "whole stages": (1, [0, 1536], 6144, 4096),
+    "half a stage at the end": (3, [0, 700, 900, 2000], 4096, 4352),
+    "a ragged second half": (3, [0, 700, 900, 2000], 4096, 4416),
     "over 256 experts": (260, list(range(0, 260 * 100 + 1, 100)), 256, 4160),
 }
 
