@@ -404,11 +404,11 @@ PAIRS = {                                                 # many tokens an exper
     "N not of 8": (2, [0, 769, 1600], 6001, 4160),
     "one expert": (1, [0, 1536], 6144, 4224),
     "second half past N": (2, [0, 1000, 2000], 6272, 4160),
-    "many stages": (1, [0, 200], 20000, 2112),
+    "many tiles": (1, [0, 960], 20000, 2112),
     "whole stages": (1, [0, 1536], 6144, 4096),
     "half a stage at the end": (3, [0, 700, 900, 2000], 4096, 4352),
     "a ragged second half": (3, [0, 700, 900, 2000], 4096, 4416),
-    "over 256 experts": (260, list(range(0, 260 * 100 + 1, 100)), 256, 4160),
+    "over 256 experts": (257, list(range(0, 257 * 250 + 1, 250)), 512, 1088),
 }
 
 
