@@ -342,17 +342,21 @@ __global__ void __launch_bounds__(kGmThreads)
 // from L2 at the FP4 rate, more than it gives.  Two accumulators (2 x 192 of 512
 // tensor-memory columns) let the stores of one tile overlap the products of the next;
 // one persistent CTA per SM walks the tiles, token tiles fastest.
-//   warp 0       TMA of the CTA's own half of a stage, all of it signalling the first
-//                CTA's barrier (a thread's own release to the other CTA would cost
-//                about 0.9 us a stage, measured, against 0.2 us of products)
+//   warp 0       TMA of the CTA's own half of a stage of 512 columns (one copy brings both its
+//                256-column pieces of 128 bytes a row: a copy has a fixed cost), all of it
+//                signalling the first CTA's barrier (a thread's own release to the other CTA
+//                would cost about 0.9 us a stage, measured, against 0.4 us of products)
 //   warp 1       in the first CTA: scale copies and MMAs for both
 //   warps 2-9    accumulator to global memory
 // The tokens' scales are laid out for the tiles by a kernel before (k_token_scales, into
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
-// Measured: 8192 tokens on 8 experts of [14336, 4096] 206 us (4.7 PFLOP/s, tensor pipe 52 %
-// active); the copies alone take 184 us, 52 bytes a clock per SM from L2.
+// Measured: 8192 tokens on 8 experts of [14336, 4096] 189 us (5.1 PFLOP/s).  With parts left out:
+// the copies alone 140 us (about the 86 bytes a clock an SM's TMA takes in at most), products with
+// their scale copies alone 144, both without the stores 160: what is left is what they take from
+// each other in shared memory (copies write 34 KB, products and scale copies read 34 KB, stores pass
+// 6 KB a 256 columns).
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;
@@ -457,7 +461,8 @@ __device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* map, i
 // so that a pair of words is a token pair of one weight row and a transposing stmatrix turns 8
 // tokens x 32 rows at once: against two-byte stores of the 32x32b layout's rows a quarter of the
 // shared memory's time, which the copies and the products need (8192 tokens on 8 experts of
-// [14336, 4096]: without stores 158 us, with those 202, by these 193).
+// [14336, 4096]: without stores 160 us, with those 202, by these 193; two warps' rows together,
+// 128 bytes a token, gain nothing, stores by lanes from the same layout take 200).
 __device__ __forceinline__ void load_fragments(uint32_t from, uint32_t* v) {
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh, v += 16)
