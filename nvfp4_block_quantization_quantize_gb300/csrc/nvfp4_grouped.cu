@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kGmThreads)
 // instead of 32 KB for 128 x 128: a 128 x 128 tile wants about 140 bytes a clock per SM
 // from L2 at the FP4 rate, more than it gives.  Two accumulators (2 x 192 of 512
 // tensor-memory columns) let the stores of one tile overlap the products of the next;
-// one persistent CTA per SM walks the tiles, token tiles fastest.
+// one persistent CTA per SM walks the tiles.
 //   warp 0       TMA of the CTA's own half of a stage of 512 columns (one copy brings both its
 //                256-column pieces of 128 bytes a row: a copy has a fixed cost), all of it
 //                signalling the first CTA's barrier (a thread's own release to the other CTA
@@ -352,11 +352,10 @@ __global__ void __launch_bounds__(kGmThreads)
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
-// Measured: 8192 tokens on 8 experts of [14336, 4096] 189 us (5.1 PFLOP/s).  With parts left out:
-// the copies alone 140 us (about the 86 bytes a clock an SM's TMA takes in at most), products with
-// their scale copies alone 144, both without the stores 160: what is left is what they take from
-// each other in shared memory (copies write 34 KB, products and scale copies read 34 KB, stores pass
-// 6 KB a 256 columns).
+// Measured: 8192 tokens on 8 experts of [14336, 4096] 188 us (5.1 PFLOP/s; tensor pipe 56 %, L2 61 %
+// of their peaks).  With parts left out: the copies alone 140 us (about the 86 bytes a clock an SM's
+// TMA takes in at most), products with their scale copies alone 144, both without the stores 160: no
+// unit is full, the three slow each other.
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;
@@ -368,6 +367,27 @@ constexpr int kGpSlot = 2 * (kGpHalfW + kGpHalfT) + kGpSlotSfw + kGpSlotSft;  //
 constexpr int kGpSmem = kGpStages * kGpSlot + kGpStoreWarps * kTurn + 1024;
 constexpr int kGpGroups = 256;                            // experts whose places are kept in shared memory
 constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages of 4 steps of 4 + 8 columns
+
+// Tiles are walked in blocks of token tiles whose codes are about kBlockBytes, a block's token tiles
+// fastest and then its weight tiles, so that what runs together shares tokens and weights and
+// a block's tokens stay in L2.  Without blocks the weights of all experts run together: us without /
+// with, 8192 tokens on 8 experts of [4096, 14336] 229 / 187, 16384 on 64 of [2048, 7168] 197 / 141, 8192 on 8
+// of [14336, 4096] 193 / 190 (blocks of 1 MB to 4 MB 193 to 195, of 30 MB at K = 14336 197).  (Single-SM
+// tiles, one wave or few, gain nothing: 64 experts 8192 x 2048 of K 7168 129 / 119, 32 experts 4096 x 2048 of
+// K 4096 40 / 42.)
+constexpr int64_t kBlockBytes = 10 << 20;
+
+unsigned block_tiles(const GroupedArgs& a, int64_t slots) {
+    const int64_t n = kBlockBytes / (kGpBT * a.K / 2);
+    return static_cast<unsigned>(n < 3 ? 3 : n > slots ? slots : n);
+}
+
+// token tile and weight tile of `tile`
+__device__ __forceinline__ void place(unsigned tile, unsigned slots, unsigned wide, unsigned block, int& slot, int& ntile) {
+    const unsigned b = tile / (block * wide), in = tile - b * (block * wide), n = min(block, slots - b * block);
+    slot = static_cast<int>(b * block + in % n);
+    ntile = static_cast<int>(in / n);
+}
 
 // token tiles of 192 rows, at most: all full ones, and one partial one a group
 int64_t pair_slots(const GroupedArgs& a) { return a.T / kGpBT + (a.E < a.T ? a.E : a.T); }
@@ -460,7 +480,7 @@ __device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* map, i
 // lane l is column 8 j + 2 (l % 4) + e of row 16 hh + 8 m + l / 4 (32 columns, the warp's 32 rows),
 // so that a pair of words is a token pair of one weight row and a transposing stmatrix turns 8
 // tokens x 32 rows at once: against two-byte stores of the 32x32b layout's rows a quarter of the
-// shared memory's time, which the copies and the products need (8192 tokens on 8 experts of
+// shared memory's accesses (8192 tokens on 8 experts of
 // [14336, 4096]: without stores 160 us, with those 202, by these 193; two warps' rows together,
 // 128 bytes a token, gain nothing, stores by lanes from the same layout take 200).
 __device__ __forceinline__ void load_fragments(uint32_t from, uint32_t* v) {
@@ -535,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
                    const __grid_constant__ CUtensorMap mapW2, const __grid_constant__ CUtensorMap mapT2,
                    const __grid_constant__ CUtensorMap mapSW, const __grid_constant__ CUtensorMap mapST,
                    const __grid_constant__ CUtensorMap mapOut,
-                   const GroupedArgs a, unsigned slots, unsigned all_tiles) {
+                   const GroupedArgs a, unsigned slots, unsigned all_tiles, unsigned block) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[kGpStages], done[2 * kGpStages], acc_full[2], acc_empty[2];
@@ -607,17 +627,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
         }
     };
     int st = 0, it = 0;                                   // stages and (non-empty) tiles so far
+    const unsigned wide = static_cast<unsigned>((a.N + 255) / 256);
     // one pass over the pair's tiles, the same in every role
     auto each_tile = [&](auto body) {
         for (unsigned tile = blockIdx.x / 2; tile < all_tiles; tile += pairs) {
-            const int slot = static_cast<int>(tile % slots);
-            int expert, row0, rows;
+            int slot, ntile, expert, row0, rows;
+            place(tile, slots, wide, block, slot, ntile);
             find(slot, expert, row0, rows);
             // the same in all lanes; the reduction lets the compiler know
             rows = __reduce_max_sync(0xFFFFFFFFu, rows);
             if (rows == 0) continue;
             const int N = (rows + 31) / 32 * 32;
-            if (!body(static_cast<int>(tile / slots), slot, expert, row0, rows, N)) return;
+            if (!body(ntile, slot, expert, row0, rows, N)) return;
             ++it;
         }
     };
@@ -817,7 +838,7 @@ cudaError_t launch_pair(const GroupedArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t pairs = tiles < pairs_at_once ? tiles : pairs_at_once;
     return launch_pdl(k_grouped_pair<ODT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGpThreads), kGpSmem, s, mapW,
-                      mapT, mapW2, mapT2, mapSW, mapST, mapOut, a, static_cast<unsigned>(slots), static_cast<unsigned>(tiles));
+                      mapT, mapW2, mapT2, mapSW, mapST, mapOut, a, static_cast<unsigned>(slots), static_cast<unsigned>(tiles), block_tiles(a, slots));
 }
 
 template <int BT, int ODT>
