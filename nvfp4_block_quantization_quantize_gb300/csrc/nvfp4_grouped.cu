@@ -876,22 +876,22 @@ cudaError_t launch_grouped_o(const GroupedArgs& a, cudaStream_t s) {
 // tiles to be expected (a half-filled one a group; of a single group what it has).  A wave of
 // pairs takes about 2.6 + 0.7 K / 1024 us and the call 10 more (the scales' layout, the first
 // tiles' start and the last ones' end), a wave of 128 x 128 tiles, two CTAs an SM, 3.6 + 2 K / 1024
-// and 3 more; neither is faster than its bytes at 4.75 TB/s.  The last wave counts half its share and
-// half a whole one.  Fitted over 18 shapes, of which it misses the faster path of one by 2 %; us pairs /
-// single: K 4096, 4 experts 1024 x 14336 44 / 49, 2 experts 4096 x 4096 37 / 49, 8 experts 8192 x 14336
-// 194 / 292, 16 experts 2048 x 4096 45 / 40; K 1024, 4 experts 8192 x 1024 18 / 13.
+// and 3 more; neither is faster than its bytes at 5.2 and 4.8 TB/s.  The last wave counts half its share
+// and half a whole one.  Fitted over 28 shapes, on which the choice is within 2 % of the faster path; us
+// pairs / single: K 4096, 4 experts 1024 x 14336 44 / 49, 2 experts 4096 x 4096 37 / 49, 8 experts 8192 x 14336
+// 190 / 292, 16 experts 2048 x 4096 45 / 40; K 1024, 4 experts 8192 x 1024 18 / 13.
 static bool takes_pairs(const GroupedArgs& a) {
-    constexpr double kSms = 152, kRate = 4.75e6;          // bytes a us
+    constexpr double kSms = 152;
     if (a.K <= 0 || a.E <= 0 || a.N <= 128 || a.T < 33 * a.E || a.K / 64 > 8 * 65535) return false;
     const double E = static_cast<double>(a.E), T = static_cast<double>(a.T), N = static_cast<double>(a.N);
     const double k = static_cast<double>(a.K) / 1024;
-    const double least = ((E * N + T) * static_cast<double>(a.K) * 0.5625 + T * N * 2) / kRate;
+    const double mb = ((E * N + T) * static_cast<double>(a.K) * 0.5625 + T * N * 2) / 1e6;
     auto waves = [&](int rows, int cols, double at_once) {                   // of tiles of rows tokens x cols
         const double tiles = (a.E == 1 ? ceil(T / rows) : T / rows + 0.5 * E) * ceil(N / cols), w = tiles / at_once;
         return w <= 1 ? 1.0 : 0.5 * (w + ceil(w));
     };
-    const double pairs = 10 + fmax(waves(kGpBT, 256, kSms / 2) * (2.6 + 0.7 * k), least);
-    const double single = 3 + fmax(waves(128, 128, 2 * kSms) * (3.6 + 2 * k), least);
+    const double pairs = 10 + fmax(waves(kGpBT, 256, kSms / 2) * (2.6 + 0.7 * k), mb / 5.2);
+    const double single = 3 + fmax(waves(128, 128, 2 * kSms) * (3.6 + 2 * k), mb / 4.8);
     return pairs < single;
 }
 
