@@ -371,7 +371,7 @@ constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages 
 // Tiles are walked in blocks of token tiles whose codes are about kBlockBytes, a block's token tiles
 // fastest and then its weight tiles, so that what runs together shares tokens and weights and
 // a block's tokens stay in L2.  Without blocks the weights of all experts run together: us without /
-// with, 8192 tokens on 8 experts of [4096, 14336] 229 / 187, 16384 on 64 of [2048, 7168] 197 / 141, 8192 on 8
+// with, 8192 tokens on 8 experts of [4096, 14336] 229 / 192, 16384 on 64 of [2048, 7168] 197 / 142, 8192 on 8
 // of [14336, 4096] 193 / 190 (blocks of 1 MB to 4 MB 193 to 195, of 30 MB at K = 14336 197).  (Single-SM
 // tiles, one wave or few, gain nothing: 64 experts 8192 x 2048 of K 7168 129 / 119, 32 experts 4096 x 2048 of
 // K 4096 40 / 42.)
