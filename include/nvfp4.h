@@ -259,7 +259,7 @@ enum nvfp4_format { NVFP4_FMT_NVFP4 = 0, NVFP4_FMT_MXFP8 = 1 };
  *                is wanted
  * A sum of squares past fp32's range gives y = 0 for finite elements, as the
  * fp32 formula does.  EINVAL on bad shapes (K % 16), enums, pointers or eps, an
- * output that is an input or another output (but for hidden_out and hidden),
+ * output that shares a byte with an input or another output (but for hidden_out == hidden),
  * gamax_mode TENSOR (the maximum over all rows is not known in one pass), a
  * gamax_mode with FMT_MXFP8, a bound outside (0, 448].
  */
@@ -283,7 +283,8 @@ enum nvfp4_x_type { NVFP4_X_F32 = 0, NVFP4_X_BF16 = 1, NVFP4_X_MXFP8 = 2 };
  * exactly, except that what lies 2^39 below the part's largest magnitude (MXFP8:
  * 2^31 below the largest scale of its groups that are not all zeros) is lost.  Sums are fp32 in a fixed order (the same bits on every run).
  * EINVAL: M outside [0, 16] (larger M: nvfp4_mm, nvfp4_grouped_mm), N < 0, K < 0,
- * K % 16, N or K >= 2^30, bad enums, pointers or bound.
+ * K % 16, N or K >= 2^30, bad enums, pointers or bound, an out that shares a byte with an
+ * input.
  */
 int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* codes, const uint8_t* scales,
              int64_t M, int64_t N, int64_t K, int gamax_mode, const float* gamax, float scale_bound, void* out,
@@ -307,8 +308,8 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
  *                that is 0), written and read by this call alone
  * Products are exact and accumulate in fp32.  EINVAL: a negative size, K % 64,
  * E * N, T or K >= 2^30, bad enums, pointers or bound, a workspace that is too
- * small.  A CTA that stops waiting for its tensor-core work writes NaN to its tile
- * of out.
+ * small, an out or a workspace that shares a byte with an input or with the other.
+ * A CTA that stops waiting for its tensor-core work writes NaN to its tile of out.
  */
 int64_t nvfp4_grouped_mm_workspace(int64_t E, int64_t T, int64_t N, int64_t K);
 int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int64_t* offsets,

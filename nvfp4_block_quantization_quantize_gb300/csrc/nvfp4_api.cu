@@ -45,6 +45,32 @@ int check_shape(int64_t M, int64_t K) {
     return NVFP4_OK;
 }
 
+// A buffer of a call, for check_apart.
+struct Buffer {
+    const void* p;            // null = not given
+    int64_t bytes;
+    const char* name;
+};
+
+bool overlap(const Buffer& a, const Buffer& b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+    return p <= q ? q - p < static_cast<uint64_t>(a.bytes) : p - q < static_cast<uint64_t>(b.bytes);
+}
+
+// No output shares a byte with an input or another output: CTAs read their inputs while
+// others store, and through the read-only path.
+template <int NO, int NI>
+int check_apart(const Buffer (&outs)[NO], const Buffer (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (const Buffer& in : ins)
+            if (overlap(outs[i], in)) return fail(NVFP4_EINVAL, "%s must not overlap %s", outs[i].name, in.name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return fail(NVFP4_EINVAL, "%s must not overlap %s", outs[i].name, outs[j].name);
+    }
+    return NVFP4_OK;
+}
+
 bool is_row_mode(int g) { return g == NVFP4_GAMAX_ROW || g == NVFP4_GAMAX_ROW_GIVEN; }
 
 // Largest K with a columnwise output: 65535 CTA columns of 256 (1x16 row-owner
@@ -270,8 +296,6 @@ int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int d
     if (any && !codes && !out && !hidden_out) return fail(NVFP4_EINVAL, "no output is given");
     if ((hidden == nullptr) != (hidden_out == nullptr))
         return fail(NVFP4_EINVAL, "give both hidden and hidden_out, or neither");
-    if (any && (hidden_out == x || (out && (out == x || out == hidden || out == hidden_out))))
-        return fail(NVFP4_EINVAL, "outputs must not be inputs (but hidden_out may be hidden) nor each other");
     if ((rc = check_ptr(x, "x", any))) return rc;
     if ((rc = check_ptr(hidden, "hidden", false))) return rc;
     if ((rc = check_ptr(weight, "weight", false))) return rc;
@@ -286,6 +310,20 @@ int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int d
         const int err = static_cast<int>(cudaMemsetAsync(gamax, 0, static_cast<size_t>(M) * 4, stream));
         return err ? cuda_fail(err, "norm zero fill") : NVFP4_OK;
     }
+    const int64_t full = M * K * (dtype == NVFP4_F32 ? 4 : 2);
+    const bool mx = format == NVFP4_FMT_MXFP8;
+    const int64_t amax = gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_TENSOR_GIVEN ? 4 : M * 4;
+    const bool row = gamax_mode == NVFP4_GAMAX_ROW;       // gamax is written
+    const Buffer outs[] = {{hidden_out, full, "hidden_out"},
+                           {out, full, "out"},
+                           {codes, mx ? M * K : M * (K / 2), "codes"},
+                           {scales, M * (mx ? (K + 31) / 32 : K / 16), "scales"},
+                           {gamax, row ? amax : 0, "gamax"}};
+    const Buffer ins[] = {{x, full, "x"},
+                          {hidden, hidden == hidden_out ? 0 : full, "hidden"},      // updated in place: an output alone
+                          {weight, K * (weight_dtype == NVFP4_F32 ? 4 : 2), "weight"},
+                          {gamax, row ? 0 : amax, "gamax"}};
+    if ((rc = check_apart(outs, ins))) return rc;
     const nvfp4::NormArgs a{x, hidden, M, K, dtype, weight, weight_dtype, eps, hidden_out, out, format, gamax_mode,
                             gamax, scale_bound, codes, scales};
     const int err = nvfp4::launch_rmsnorm(a, stream);
@@ -319,6 +357,13 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
     if ((rc = check_ptr(gamax, "gamax", any && gamax_mode != NVFP4_GAMAX_NONE, 4))) return rc;
     if ((rc = check_ptr(out, "out", any))) return rc;
     if (!any) return NVFP4_OK;
+    const Buffer outs[] = {{out, M * N * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}};
+    const Buffer ins[] = {{x, M * K * (x_type == NVFP4_X_F32 ? 4 : x_type == NVFP4_X_BF16 ? 2 : 1), "x"},
+                          {x_scales, x_type == NVFP4_X_MXFP8 ? M * ((K + 31) / 32) : 0, "x_scales"},
+                          {codes, N * (K / 2), "codes"},
+                          {scales, N * (K / 16), "scales"},
+                          {gamax, gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? N * 4 : 4, "gamax"}};
+    if ((rc = check_apart(outs, ins))) return rc;
     if (K == 0) {
         const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(N) * (out_dtype == NVFP4_F32 ? 4 : 2);
         const int err = static_cast<int>(cudaMemsetAsync(out, 0, bytes, stream));
@@ -372,6 +417,15 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
     if (workspace_bytes < need)
         return fail(NVFP4_EINVAL, "the workspace needs %lld bytes (got %lld)", (long long)need, (long long)workspace_bytes);
     if ((rc = check_ptr(workspace, "workspace", need > 0))) return rc;
+    const Buffer outs[] = {{out, T * N * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}, {workspace, need, "workspace"}};
+    const Buffer ins[] = {{codes_a, T * (K / 2), "codes_a"},
+                          {scales_a, T * (K / 16), "scales_a"},
+                          {offsets, (E + 1) * 8, "offsets"},
+                          {codes_b, E * N * (K / 2), "codes_b"},
+                          {scales_b, E * ((N + 127) / 128 * 128) * (K / 16), "scales_b"},
+                          {gamax_a, gamax_a_mode == NVFP4_GAMAX_NONE ? 0 : gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? T * 4 : 4, "gamax_a"},
+                          {gamax_b, E * 4, "gamax_b"}};
+    if ((rc = check_apart(outs, ins))) return rc;
     const int err = nvfp4::launch_grouped_mm(a, stream);
     if (err) return cuda_fail(err, "grouped mm launch");
     return NVFP4_OK;
