@@ -278,10 +278,10 @@ enum nvfp4_x_type { NVFP4_X_F32 = 0, NVFP4_X_BF16 = 1, NVFP4_X_MXFP8 = 2 };
  *   codes, scales   [N,K/2], [N,K/16]: a rowwise 1x16 output of nvfp4_quantize
  *   gamax    NULL with gamax_mode NONE; 1 fp32 (TENSOR_GIVEN) or N (ROW_GIVEN)
  *   out      device [M,N], F32 or BF16 (RNE)
- * q * dec(s) is exact in f16.  x enters as f16 after a power-of-two scaling per
- * token and part of K: an F32 x as the sum of two f16 (22 bits), BF16 and MXFP8 x
- * exactly, except that what lies 2^39 below the part's largest magnitude (MXFP8:
- * 2^31 below the largest scale of its groups that are not all zeros) is lost.  Sums are fp32 in a fixed order (the same bits on every run).
+ * q * dec(s) is exact in f16.  x enters as f16 after a power-of-two scaling per token and
+ * part of K, an F32 x as the sum of two f16 (22 bits): each element is off by at most 2^-39
+ * of the part's largest magnitude, BF16 and MXFP8 elements down to 2^-31 and 2^-35 of it are
+ * exact.  Sums are fp32 in a fixed order (the same bits on every run).
  * EINVAL: M outside [0, 16] (larger M: nvfp4_mm, nvfp4_grouped_mm), N < 0, K < 0,
  * K % 16, N or K >= 2^30, bad enums, pointers or bound, an out that shares a byte with an
  * input.

@@ -172,13 +172,24 @@ __device__ __forceinline__ float power_of_two(int e) {
     return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
 }
 
-// 8 columns as four f16 pairs: the raw ones at r scaled by f (MXFP8: f already an f16 pair's bits)
+// 2^e twice, as f16 pairs' bits whose product it is (e in [-38, 30]): f16 itself ends at 2^15
+// and 2^-24.  An E4M3 value times the first is exact (a multiple of 2^-23, at most 2^15 for those
+// that end within f16's range), so that the second makes the only rounding.
+__device__ __forceinline__ uint2 power_of_two_f16(int e) {
+    const int first = min(max(e, -14), 15), rest = e - first;
+    return make_uint2(static_cast<uint32_t>(first + 15) * (0x00010001u << 10),
+                      rest >= -14 ? static_cast<uint32_t>(rest + 15) * (0x00010001u << 10) : 0x00010001u << (rest + 24));
+}
+
+// 8 columns as four f16 pairs: the raw ones at r scaled by f.x, an fp32's bits, or by the f16 pairs
+// f.x and f.y (MXFP8)
 template <int XT, int P>
-__device__ __forceinline__ void convert8(const uint8_t* r, uint32_t f, uint32_t (*h)[4]) {
+__device__ __forceinline__ void convert8(const uint8_t* r, uint2 f, uint32_t (*h)[4]) {
     if (XT == NVFP4_X_MXFP8) {
         const uint2 u = *reinterpret_cast<const uint2*>(r);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[0][q] = mul_f16x2(e4m3_pair((q < 2 ? u.x : u.y) >> (16 * (q & 1))), f);
+        for (int q = 0; q < 4; ++q)
+            h[0][q] = mul_f16x2(mul_f16x2(e4m3_pair((q < 2 ? u.x : u.y) >> (16 * (q & 1))), f.x), f.y);
         return;
     }
     float v[8];
@@ -197,7 +208,7 @@ __device__ __forceinline__ void convert8(const uint8_t* r, uint32_t f, uint32_t 
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        float x0 = mul_rn(v[2 * q], __uint_as_float(f)), x1 = mul_rn(v[2 * q + 1], __uint_as_float(f));
+        float x0 = mul_rn(v[2 * q], __uint_as_float(f.x)), x1 = mul_rn(v[2 * q + 1], __uint_as_float(f.x));
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const __half2 o = __floats2half2_rn(x0, x1);
@@ -226,6 +237,19 @@ __device__ __forceinline__ uint32_t top8(const uint8_t* r) {
     return max(p << 16, p & 0xFFFF0000u);
 }
 
+// largest magnitude of 16 E4M3 codes, as its 7 bits (NaN: the largest)
+__device__ __forceinline__ uint32_t top_code(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t lo = 0, hi = 0;                              // of even and odd bytes, two each
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo = __vmaxu2(lo, w[i] & 0x007F007Fu);
+        hi = __vmaxu2(hi, (w[i] >> 8) & 0x007F007Fu);
+    }
+    const uint32_t m = __vmaxu2(lo, hi);
+    return max(m & 0xFFFFu, m >> 16);
+}
+
 // Converts the copied columns of tokens wr, wr + WR, ..; up[m]: what that token's sums are to
 // be multiplied by.  sb: the tokens' E8M0 bytes of these columns, sb_stride apart.
 template <int XT, int VB>
@@ -241,33 +265,30 @@ __device__ __forceinline__ void convert_x(const MvArgs& a, uint8_t* xs, float* u
         const uint8_t* raw = cells + raw_offset<XT, VB>(n);
         uint32_t top = 0;
         if (XT == NVFP4_X_MXFP8) {
-            // the largest scale of a group that holds anything but zeros (whose scale may be any)
-            for (int i = lane; i * 4 < pieces; i += 32) {
-                const uint32_t b = sb[m * sb_stride + i];
-                const uint4* q = reinterpret_cast<const uint4*>(raw + 32 * i);
-                uint32_t any = q[0].x | q[0].y | q[0].z | q[0].w;
-                if (i * 4 + 2 < pieces) any |= q[1].x | q[1].y | q[1].z | q[1].w;
-                top = max(top, b == 255 || !(any & 0x7F7F7F7Fu) ? 0u : b);
+            // the largest exponent of a value: scale byte + 9 + the exponent of the largest code c of its columns (c / 8 - 7,
+            // below that of its three bits), at least 1; a group of zeros, whose scale may be any, has none
+            for (int i = lane; i * 2 < pieces; i += 32) {
+                const uint32_t b = sb[m * sb_stride + i / 2], c = top_code(*reinterpret_cast<const uint4*>(raw + 16 * i));
+                if (c != 0 && b != 255) top = max(top, b + (c < 8 ? 31 - __clz(c) : 2 + (c >> 3)));
             }
         } else {
             for (int i = lane; i < pieces; i += 32) top = max(top, top8<XT>(raw + kPiece * i));
         }
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         // scaled to at most 2^15: x by 2^(14 - e), e its exponent (at least -112, so that this is a
-        // float); an E4M3 element by 2^(b - top + 6) (b above top: of zeros)
-        const int e = XT == NVFP4_X_MXFP8 ? static_cast<int>(top) - 127 - 6
+        // float); an E4M3 element of scale byte b by 2^(b + 23 - top) (above 23: of zeros)
+        const int e = XT == NVFP4_X_MXFP8 ? static_cast<int>(max(top, 1u)) - 9 - 127 - 14
                                           : max(static_cast<int>(top >> 23) - 127, -112) - 14;
         if (lane == 0) up[m] = power_of_two(e);
         const float down = XT == NVFP4_X_MXFP8 ? 0.0f : power_of_two(-e);
 #pragma unroll 2
         for (int s = 0; s < steps; ++s) {
             const int i = s * 32 + lane;                  // piece of 8 columns
-            uint32_t f = __float_as_uint(down);
+            uint2 f = make_uint2(__float_as_uint(down), 0u);
             if (XT == NVFP4_X_MXFP8) {
                 const int b = i < pieces ? sb[m * sb_stride + i / 4] : 0;
-                const __half2 f2 = __float2half2_rn(b == 255 ? __int_as_float(0x7FC00000)
-                                                             : power_of_two(min(max(b - static_cast<int>(top), -155), 0) + 6));
-                f = *reinterpret_cast<const uint32_t*>(&f2);
+                f = power_of_two_f16(min(max(b - 127 - e, -38), 23));
+                if (b == 255) f.x = 0x7FFF7FFFu;          // NaN
             }
             uint32_t h[P][4];
             convert8<XT, P>(raw + kPiece * i, f, h);
