@@ -229,7 +229,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const int dev = call_device(v[0]);
         if (dev < 0) return none();
         const at::Tensor *x = tensor(v[0], dev), *w = nullptr, *hidden = nullptr;
-        if (!x || x->dim() != 2) return none();
+        if (!x || x->dim() != 2 || (v[6] != Py_True && v[6] != Py_False)) return none();
         const int64_t M = x->size(0), K = x->size(1);
         const int dt = dtype_of(*x), fmt = choice(v[5], {"nvfp4", "mxfp8"});
         if (dt < 0 || fmt < 0 || K % 16) return none();
