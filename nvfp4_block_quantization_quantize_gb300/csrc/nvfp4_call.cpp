@@ -14,6 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -130,13 +131,19 @@ PyObject* wrap(PyObject* o, const at::Tensor& t) {        // a given output is r
     return THPVariable_Wrap(t);
 }
 
+// the Python exception torch makes of the C++ one in flight (torch.OutOfMemoryError of an allocation that failed)
+PyObject* raised() {
+    HANDLE_TH_ERRORS
+    throw;
+    END_HANDLE_TH_ERRORS
+}
+
 template <class F>
 PyObject* guarded(F f) {
     try {
         return f();
-    } catch (const std::exception& e) {                   // an allocation that failed
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    } catch (...) {
+        return raised();
     }
 }
 
