@@ -108,20 +108,24 @@ bool rows_gamax(PyObject* o, int64_t rows, int dev, int* mode, const at::Tensor*
     return (*t)->numel() == 1 || (*t)->numel() == rows;
 }
 
-// the output [rows, cols]: the given tensor, or a new one (a part of `shared` when that is defined)
-bool output(PyObject* o, int64_t rows, int64_t cols, at::ScalarType type, int dev, at::Tensor* t,
-            const at::Tensor* shared = nullptr, int64_t* at = nullptr) {
-    if (given(o)) {
-        const at::Tensor* g = tensor(o, dev, type, rows * cols);
-        if (!g) return false;
-        *t = *g;
-    } else if (shared && shared->defined()) {
-        *t = part(*shared, at, rows, cols, type);
-    } else {
-        *t = empty(rows, cols, type, dev);
-    }
-    return true;
+// *t is the given output if there is one; false if it does not fit
+bool taken(PyObject* o, int64_t numel, at::ScalarType type, int dev, at::Tensor* t) {
+    if (!given(o)) return true;
+    const at::Tensor* g = tensor(o, dev, type, numel);
+    if (g) *t = *g;
+    return g != nullptr;
 }
+
+// While one lives this thread does not hold the interpreter's lock.  Allocations and launches may block (a
+// full launch queue, freed memory that other streams still use) until something that another Python thread
+// does; the arguments are the caller's and stay.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 PyObject* wrap(PyObject* o, const at::Tensor& t) {        // a given output is returned itself
     if (given(o)) {
@@ -171,14 +175,17 @@ PyObject* mv(PyObject*, PyObject* const* v, Py_ssize_t n) {
         }
         const int odt = choice(v[6], {"f32", "bf16"});
         at::Tensor out;
-        if (type < 0 || odt < 0 || !rows_gamax(v[4], N, dev, &mode, &g) ||
-            !output(v[7], M, N, odt == NVFP4_F32 ? at::kFloat : at::kBFloat16, dev, &out))
-            return none();
-        const int rc = f_mv(x->data_ptr(), static_cast<const uint8_t*>(data(xs)), type,
-                            static_cast<const uint8_t*>(codes->data_ptr()),
-                            static_cast<const uint8_t*>(scales->data_ptr()), M, N, K, mode,
-                            static_cast<const float*>(data(g)), bound, out.data_ptr(), odt,
-                            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        const at::ScalarType ot = odt == NVFP4_F32 ? at::kFloat : at::kBFloat16;
+        if (type < 0 || odt < 0 || !rows_gamax(v[4], N, dev, &mode, &g) || !taken(v[7], M * N, ot, dev, &out)) return none();
+        int rc;
+        {
+            const Unlocked unlocked;
+            if (!out.defined()) out = empty(M, N, ot, dev);
+            rc = f_mv(x->data_ptr(), static_cast<const uint8_t*>(data(xs)), type,
+                      static_cast<const uint8_t*>(codes->data_ptr()), static_cast<const uint8_t*>(scales->data_ptr()), M, N, K,
+                      mode, static_cast<const float*>(data(g)), bound, out.data_ptr(), odt,
+                      c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        }
         return rc == NVFP4_OK ? wrap(v[7], out) : none();
     });
 }
@@ -204,19 +211,23 @@ PyObject* grouped_mm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         int mode;
         const int odt = choice(v[8], {"f32", "bf16"});
         at::Tensor out;
-        if (odt < 0 || !rows_gamax(v[5], T, dev, &mode, &ga) ||
-            !output(v[9], T, N, odt == NVFP4_F32 ? at::kFloat : at::kBFloat16, dev, &out))
-            return none();
-        const int64_t need = f_grouped_ws(E, T, N, K);
-        at::Tensor ws;                                    // free for the stream's next work once this call is enqueued
-        if (need > 0) ws = empty(1, need, at::kByte, dev);
-        const int rc = f_grouped_mm(
-            static_cast<const uint8_t*>(ca->data_ptr()), static_cast<const uint8_t*>(sa->data_ptr()),
-            static_cast<const int64_t*>(off->data_ptr()), static_cast<const uint8_t*>(cb->data_ptr()),
-            static_cast<const uint8_t*>(sb->data_ptr()), E, T, N, K, mode, static_cast<const float*>(data(ga)),
-            static_cast<const float*>(data(gb)), bound, out.data_ptr(), odt,
-            need > 0 ? static_cast<uint8_t*>(ws.data_ptr()) : nullptr, need,
-            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        const at::ScalarType ot = odt == NVFP4_F32 ? at::kFloat : at::kBFloat16;
+        if (odt < 0 || !rows_gamax(v[5], T, dev, &mode, &ga) || !taken(v[9], T * N, ot, dev, &out)) return none();
+        int rc;
+        {
+            const Unlocked unlocked;
+            if (!out.defined()) out = empty(T, N, ot, dev);
+            const int64_t need = f_grouped_ws(E, T, N, K);
+            at::Tensor ws;                                // free for the stream's next work once this call is enqueued
+            if (need > 0) ws = empty(1, need, at::kByte, dev);
+            rc = f_grouped_mm(
+                static_cast<const uint8_t*>(ca->data_ptr()), static_cast<const uint8_t*>(sa->data_ptr()),
+                static_cast<const int64_t*>(off->data_ptr()), static_cast<const uint8_t*>(cb->data_ptr()),
+                static_cast<const uint8_t*>(sb->data_ptr()), E, T, N, K, mode, static_cast<const float*>(data(ga)),
+                static_cast<const float*>(data(gb)), bound, out.data_ptr(), odt,
+                need > 0 ? static_cast<uint8_t*>(ws.data_ptr()) : nullptr, need,
+                c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        }
         return rc == NVFP4_OK ? wrap(v[9], out) : none();
     });
 }
@@ -249,20 +260,29 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (given(v[2]) ? !(hidden = tensor(v[2], dev, x->scalar_type(), M * K)) : given(v[3])) return none();
         const bool want_out = given(v[7]) || v[6] == Py_True, mx = fmt == NVFP4_FMT_MXFP8;
         const int64_t cols = mx ? K : K / 2, groups = mx ? (K + 31) / 32 : K / 16;
-        const int64_t full = M * K * static_cast<int64_t>(x->element_size());
-        const int64_t bytes = (hidden ? full : 0) + (want_out ? full : 0) + M * (cols + groups) + 4 * 256;
-        int64_t at = 0;
-        if (bytes <= kShared) shared = empty(1, bytes, at::kByte, dev);
-        if ((hidden && !output(v[3], M, K, x->scalar_type(), dev, &hidden_out, &shared, &at)) ||
-            (want_out && !output(v[7], M, K, x->scalar_type(), dev, &out, &shared, &at)) ||
-            !output(v[8], M, cols, at::kByte, dev, &codes, &shared, &at) ||
-            !output(v[9], M, groups, at::kByte, dev, &scales, &shared, &at))
+        const at::ScalarType xt = x->scalar_type();
+        if ((hidden && !taken(v[3], M * K, xt, dev, &hidden_out)) || !taken(v[7], M * K, xt, dev, &out) ||
+            !taken(v[8], M * cols, at::kByte, dev, &codes) || !taken(v[9], M * groups, at::kByte, dev, &scales))
             return none();
-        const int rc = f_rmsnorm(
-            x->data_ptr(), data(hidden), M, K, dt, data(w), wdt, eps, hidden ? hidden_out.data_ptr() : nullptr,
-            want_out ? out.data_ptr() : nullptr, fmt, NVFP4_GAMAX_NONE, nullptr, 448.0f,
-            static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
-            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        int rc;
+        {
+            const Unlocked unlocked;
+            const int64_t full = M * K * static_cast<int64_t>(x->element_size());
+            const int64_t bytes = (hidden ? full : 0) + (want_out ? full : 0) + M * (cols + groups) + 4 * 256;
+            int64_t at = 0;
+            if (bytes <= kShared) shared = empty(1, bytes, at::kByte, dev);
+            auto make = [&](at::Tensor& t, int64_t n, at::ScalarType type) {
+                if (!t.defined()) t = shared.defined() ? part(shared, &at, M, n, type) : empty(M, n, type, dev);
+            };
+            if (hidden) make(hidden_out, K, xt);
+            if (want_out) make(out, K, xt);
+            make(codes, cols, at::kByte);
+            make(scales, groups, at::kByte);
+            rc = f_rmsnorm(x->data_ptr(), data(hidden), M, K, dt, data(w), wdt, eps, hidden ? hidden_out.data_ptr() : nullptr,
+                           want_out ? out.data_ptr() : nullptr, fmt, NVFP4_GAMAX_NONE, nullptr, 448.0f,
+                           static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
+                           c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        }
         if (rc != NVFP4_OK) return none();
         PyObject* d = PyDict_New();
         if (!d) return nullptr;

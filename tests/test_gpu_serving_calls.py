@@ -1,5 +1,10 @@
 """What a call of a serving operator takes and how it fails: the binding's short
 path (csrc/nvfp4_call.cpp) against the Python one."""
+import ctypes
+import shutil
+import subprocess
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -46,3 +51,43 @@ def test_a_failed_allocation_is_an_out_of_memory_error():
         torch.cuda.set_per_process_memory_fraction(1.0)
     y = nv.nvfp4_mv(x, codes, scales, out_dtype="f32")
     assert bool((y == 0).all())
+
+
+STUB = r"""
+#include <stdint.h>
+#include <time.h>
+static volatile int flag = 0;
+void set_flag(void) { flag = 1; }
+/* stands for nvfp4_mv's launch: returns NVFP4_OK when another thread has set the flag, NVFP4_ECUDA after 5 s without */
+int slow(void) {
+    struct timespec t = {0, 1000000};
+    for (int i = 0; i < 5000; ++i) {
+        if (flag) return 0;
+        nanosleep(&t, 0);
+    }
+    return 2;
+}
+"""
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    """A launch may block (a full queue) until something that another Python thread does: the interpreter's lock is
+    not held meanwhile, as ctypes does not hold it.  (The library's function is replaced by one that waits.)"""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    src, lib = tmp_path / "stub.c", tmp_path / "stub.so"
+    src.write_text(STUB)
+    subprocess.run([cc, "-shared", "-fPIC", "-o", str(lib), str(src)], check=True)
+    stub, real = ctypes.CDLL(str(lib)), nv.load_library()
+    addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value                       # noqa: E731
+    own = [addr(f) for f in (real.nvfp4_rmsnorm, real.nvfp4_mv, real.nvfp4_grouped_mm, real.nvfp4_grouped_mm_workspace)]
+    q = nv.nvfp4_quantize(to_dev(W.matrix((32, 64), seed=1, dtype="bf16")))
+    x = to_dev(W.matrix((2, 64), seed=2, dtype="bf16"))
+    nv._call.bind(own[0], addr(stub.slow), own[2], own[3])
+    try:
+        t = threading.Timer(0.05, stub.set_flag)
+        t.start()
+        y = nv._call.mv(x, q["codes"], q["scales"], None, None, 448.0, "bf16", None)
+        t.join()
+    finally:
+        nv._call.bind(*own)
+    assert y is not None                                  # None: the flag was not set within the wait
