@@ -884,9 +884,12 @@ def _check_mm_args(codes_a, scales_a, codes_b, scales_b, M, N, K, gamax_a, gamax
 # Calls on device tensors only.  A well-formed call goes through the short path
 # (csrc/nvfp4_call.cpp); it returns None for any other, which is then checked,
 # made contiguous or refused here.  A call on a given stream runs wholly on it
-# (copies and allocations too).
+# (copies and allocations too): a stream of the tensors' device; a bare handle is
+# taken for one.
 def _given_stream(stream, dev):
     if isinstance(stream, torch.cuda.Stream):
+        if stream.device != dev:
+            raise ValueError(f"nvfp4: the stream must be of {dev} (got one of {stream.device})")
         return torch.cuda.stream(stream)
     if int(stream) == 0:
         return torch.cuda.stream(torch.cuda.default_stream(dev))
