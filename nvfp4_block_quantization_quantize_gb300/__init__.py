@@ -123,7 +123,8 @@ def load_library(path: str | None = None):
             from . import _nvfp4_call
             _nvfp4_call.bind(*[ctypes.cast(f, P).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm,
                                                                      lib.nvfp4_grouped_mm_workspace)])
-            _lib, _call = lib, _nvfp4_call
+            _call = _nvfp4_call                 # before _lib, which other threads read without the lock
+            _lib = lib
         return lib
 
 
