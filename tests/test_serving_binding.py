@@ -35,7 +35,9 @@ def test_the_library_is_published_last(monkeypatch):
     def trace(frame, event, arg):
         if frame.f_code is not nv.load_library.__code__:
             return None
-        frame.f_trace_opcodes = True
+        if not frame.f_trace_opcodes:
+            frame.f_trace_opcodes = True
+            sys.settrace(trace)                           # some interpreters look at the flag here alone
         seen.append((nv._lib is None, nv._call is None))
         return trace
 
