@@ -28,12 +28,14 @@ that write.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
+import warnings
 
 import torch
 
-from .build import LIB_PATH, build  # noqa: F401  (build is re-exported)
+from .build import LIB_PATH, build, call_abi  # noqa: F401  (build is re-exported)
 
 F32, BF16 = 0, 1
 BLOCK_1X16, BLOCK_16X16 = 0, 1
@@ -70,6 +72,32 @@ class NVFP4Error(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"nvfp4 status {status}: {message}")
         self.status = status
+
+
+class _NoShortPath:
+    """Stands for csrc/nvfp4_call.cpp's module where that is not built: every call goes through the Python checks."""
+
+    @staticmethod
+    def rmsnorm(*args):
+        return None
+
+    mv = grouped_mm = rmsnorm
+
+
+def _short_path(lib):
+    """The short path of the serving operators, bound to the library's functions.  It is compiled against one
+    torch and one interpreter, which the C library is not: one for others is not used (nothing else needs it)."""
+    try:
+        m = importlib.import_module("._nvfp4_call", __name__)
+        if m.abi != call_abi():
+            raise ImportError(f"it was built for {m.abi}, this is {call_abi()}")
+    except ImportError as e:
+        warnings.warn(f"nvfp4: serving operators go without their short call path ({e}); build() makes it again",
+                      RuntimeWarning, stacklevel=3)
+        return _NoShortPath
+    m.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm,
+                                                             lib.nvfp4_grouped_mm_workspace)])
+    return m
 
 
 def load_library(path: str | None = None):
@@ -120,10 +148,7 @@ def load_library(path: str | None = None):
         lib.nvfp4_abi_version.restype = i32
         lib.nvfp4_abi_version.argtypes = []
         if path is None:
-            from . import _nvfp4_call
-            _nvfp4_call.bind(*[ctypes.cast(f, P).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm,
-                                                                     lib.nvfp4_grouped_mm_workspace)])
-            _call = _nvfp4_call                 # before _lib, which other threads read without the lock
+            _call = _short_path(lib)            # before _lib, which other threads read without the lock
             _lib = lib
         return lib
 

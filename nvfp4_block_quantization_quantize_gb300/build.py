@@ -3,8 +3,9 @@
 Each translation unit compiles in parallel with ``-gencode
 arch=compute_103a,code=sm_103a`` (GB300 only), then one shared library is
 linked with the static CUDA runtime.  Beside them g++ compiles
-``_nvfp4_call.so``, the binding's short path for the serving operators (CPython
-and torch headers; it holds no arithmetic).  The fp32 steps the method pins must
+``_nvfp4_call``, the binding's short path for the serving operators (CPython
+and torch headers; it holds no arithmetic), which is made again for another torch
+or interpreter.  The fp32 steps the method pins must
 round exactly as written, so the build keeps IEEE division / square root,
 does not flush subnormals and does not contract multiply-adds.
 """
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libnvfp4_gb300.so")
-CALL_PATH = os.path.join(PKG, "_nvfp4_call.so")
+CALL_PATH = os.path.join(PKG, "_nvfp4_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALL_ABI_PATH = os.path.join(BUILD_DIR, "_nvfp4_call.abi")      # what CALL_PATH was built for
 SOURCES = ["nvfp4_rows.cu", "nvfp4_tiles.cu", "nvfp4_aux.cu", "nvfp4_mm.cu", "nvfp4_norm.cu", "nvfp4_mv.cu",
            "nvfp4_grouped.cu", "nvfp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,16 +40,21 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is needed to build libnvfp4_gb300.so")
 
 
+def call_abi() -> str:
+    """The torch and the interpreter that the short path is compiled against (it uses their C++ and C layouts)."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _call_command(out: str) -> list[str]:
-    import sysconfig
     import torch
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     libs = ["torch_python", "torch_cuda", "torch_cpu", "c10_cuda", "c10"]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
-            os.path.join(CSRC, "nvfp4_call.cpp"), "-o", out, "-L" + os.path.join(t, "lib"), *["-l" + n for n in libs],
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", f'-DNVFP4_CALL_ABI="{call_abi()}"',
+            *[f"-I{i}" for i in inc], os.path.join(CSRC, "nvfp4_call.cpp"), "-o", out, "-L" + os.path.join(t, "lib"), *["-l" + n for n in libs],
             "-Wl,-rpath," + os.path.join(t, "lib")]
 
 
@@ -71,6 +79,8 @@ def source_digest() -> str:
 def is_stale() -> bool:
     if not os.path.exists(LIB_PATH) or not os.path.exists(CALL_PATH):
         return True
+    if not os.path.exists(CALL_ABI_PATH) or open(CALL_ABI_PATH).read() != call_abi():
+        return True
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALL_PATH))
     return any(os.path.getmtime(f) > t for f in _deps())
 
@@ -91,7 +101,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stderr
 
     def compile_call():
-        tmp = CALL_PATH + f".tmp{os.getpid()}"
+        tmp = os.path.join(BUILD_DIR, f"_nvfp4_call.tmp{os.getpid()}")
         r = subprocess.run(_call_command(tmp), capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on nvfp4_call.cpp:\n{r.stderr}")
@@ -100,7 +110,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         call = ex.submit(compile_call)
         results = list(ex.map(compile_one, SOURCES))
-        os.replace(call.result(), CALL_PATH)
     if verbose or ptxas_info:
         for obj, log in results:
             sys.stderr.write(log)
@@ -110,6 +119,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    os.replace(call.result(), CALL_PATH)        # last: the library is there without it
+    with open(CALL_ABI_PATH, "w") as f:
+        f.write(call_abi())
     return LIB_PATH
 
 

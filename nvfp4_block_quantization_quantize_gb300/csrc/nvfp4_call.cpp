@@ -318,4 +318,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_nvfp4_call", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__nvfp4_call(void) { return PyModule_Create(&module); }
+// abi: the torch and the interpreter this file was compiled against
+PyMODINIT_FUNC PyInit__nvfp4_call(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "abi", NVFP4_CALL_ABI) < 0) Py_CLEAR(m);
+    return m;
+}
