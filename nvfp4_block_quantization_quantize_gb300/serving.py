@@ -97,5 +97,5 @@ class FP4Experts:
         # back to token order, then one sum in a fixed order
         back = torch.empty_like(order)
         back[order] = torch.arange(M * k, device=x.device)
-        out = (y[back].view(M, k, -1) * p.unsqueeze(2)).sum(dim=1)
+        out = (y[back].view(M, k, y.shape[1]) * p.unsqueeze(2)).sum(dim=1)
         return out.to(x.dtype), n["hidden"]

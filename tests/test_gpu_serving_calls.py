@@ -1,5 +1,6 @@
 """What a call of a serving operator takes and how it fails: the binding's short
-path (csrc/nvfp4_call.cpp) against the Python one."""
+path (csrc/nvfp4_call.cpp) against the Python one, and the layers on batches of
+no rows."""
 import ctypes
 import shutil
 import subprocess
@@ -91,3 +92,13 @@ def test_other_threads_run_while_a_call_waits(tmp_path):
     finally:
         nv._call.bind(*own)
     assert y is not None                                  # None: the flag was not set within the wait
+
+
+def test_experts_of_an_empty_batch():
+    from nvfp4_block_quantization_quantize_gb300.serving import FP4Experts, FP4Projection
+    r = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)             # noqa: E731
+    layer = FP4Experts(r(128), r(4, 128), r(4, 128, 128), r(4, 128, 64), top_k=2)
+    out, hidden = layer(r(0, 128), r(0, 128))
+    assert out.shape == hidden.shape == (0, 128) and out.dtype == hidden.dtype == torch.bfloat16
+    y, hidden = FP4Projection(r(96, 128), r(128))(r(0, 128), r(0, 128))
+    assert y.shape == (0, 96) and hidden.shape == (0, 128)
