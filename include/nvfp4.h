@@ -279,9 +279,9 @@ enum nvfp4_x_type { NVFP4_X_F32 = 0, NVFP4_X_BF16 = 1, NVFP4_X_MXFP8 = 2 };
  *   gamax    NULL with gamax_mode NONE; 1 fp32 (TENSOR_GIVEN) or N (ROW_GIVEN)
  *   out      device [M,N], F32 or BF16 (RNE)
  * q * dec(s) is exact in f16.  x enters as f16 after a power-of-two scaling per token and
- * part of K, an F32 x as the sum of two f16 (22 bits): each element is off by at most 2^-39
- * of the part's largest magnitude, BF16 and MXFP8 elements down to 2^-31 and 2^-35 of it are
- * exact.  Sums are fp32 in a fixed order (the same bits on every run).
+ * part of K.  A BF16 or MXFP8 element is off by at most 2^-39 of the part's largest
+ * magnitude, and exact down to 2^-31 and 2^-35 of it; an F32 element, held as two f16, by at
+ * most 2^-23 of itself or 2^-50 of that magnitude.  Sums are fp32 in a fixed order (the same bits on every run).
  * EINVAL: M outside [0, 16] (larger M: nvfp4_mm, nvfp4_grouped_mm), N < 0, K < 0,
  * K % 16, N or K >= 2^30, bad enums, pointers or bound, an out that shares a byte with an
  * input.

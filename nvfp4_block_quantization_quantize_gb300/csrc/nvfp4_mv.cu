@@ -8,8 +8,10 @@
 //   - A weight decodes exactly to f16: q * dec(s) has at most 6 significant bits
 //     and lies in [2^-10, 2688].
 //   - x is scaled per token and warp by a power of two to at most 2^15 and held
-//     in shared memory as f16 (an fp32 x as hi + lo, 22 bits), in the order the
-//     MMA's B fragments are read.
+//     in shared memory as f16, in the order the MMA's B fragments are read.  An fp32
+//     x is hi + 2^-11 lo (22 bits), and the two have sums of their own until a chain's
+//     end: with lo unscaled an element would lose bits from 2^-15 of the largest on
+//     (f16 ends at 2^-24), so it does from 2^-27 on.
 //   - m16n8k16: 16 weight rows times 8 tokens.  The order of k inside a product
 //     is free as long as A and B agree, so lane (g, t) of a warp takes whole
 //     blocks: 16 * VB consecutive weights of rows g and g + 8, one 8 * VB-byte
@@ -213,10 +215,10 @@ __device__ __forceinline__ void convert8(const uint8_t* r, uint2 f, uint32_t (*h
         for (int p = 0; p < P; ++p) {
             const __half2 o = __floats2half2_rn(x0, x1);
             h[p][q] = *reinterpret_cast<const uint32_t*>(&o);
-            // what hi leaves; an infinite hi (an infinity of x) leaves nothing
+            // what hi leaves, times 2^11 (at most hi's own size); an infinite hi (an infinity of x) leaves nothing
             const float2 b = __half22float2(o);
-            x0 = isinf(b.x) ? 0.0f : sub_rn(x0, b.x);
-            x1 = isinf(b.y) ? 0.0f : sub_rn(x1, b.y);
+            x0 = isinf(b.x) ? 0.0f : mul_rn(sub_rn(x0, b.x), 2048.0f);
+            x1 = isinf(b.y) ? 0.0f : mul_rn(sub_rn(x1, b.y), 2048.0f);
         }
     }
 }
@@ -329,7 +331,7 @@ template <int XT, int NT, int VB>
 __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, const MvPlan p) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int P = XT == NVFP4_X_F32 ? 2 : 1;
-    constexpr int kChain = VB == 1 ? 2 : 8 / P;           // words of a row whose products form a chain: at most 16
+    constexpr int kChain = VB == 1 ? 2 : 8;               // words of a row whose products form a chain: at most 16
     __shared__ float red[2][kMvWarps][kMvRow<NT>];        // [token][row] of each warp, two tiles in turn
     __shared__ float up[kMvWarps][16];                    // of each part of the columns
     const cg::cluster_group cluster = cg::this_cluster();
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
                 scale_pairs<VB>(sc[u][0], s[0]);
                 scale_pairs<VB>(sc[u][1], s[1]);
                 const int at = c * (128 * VB * P);
-                float d[NT][4];
+                float d[P][NT][4];
 #pragma unroll
                 for (int j = 0; j < 2 * VB; ++j) {        // word j of each row: two products
                     uint32_t A[2][4];
@@ -471,17 +473,18 @@ __global__ void __launch_bounds__(32 * kMvWarps, kMvCtas) k_mv(const MvArgs a, c
 #pragma unroll
                         for (int h = 0; h < P; ++h) {
                             const uint4 b = *reinterpret_cast<const uint4*>(frag[q] + at + (j * P + h) * 64);
-                            if (j % kChain == 0 && h == 0)
-                                mma_f16_first(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
+                            if (j % kChain == 0)
+                                mma_f16_first(d[h][q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
                             else
-                                mma_f16(d[q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
-                            mma_f16(d[q], A[0][2], A[1][2], A[0][3], A[1][3], b.z, b.w);
+                                mma_f16(d[h][q], A[0][0], A[1][0], A[0][1], A[1][1], b.x, b.y);
+                            mma_f16(d[h][q], A[0][2], A[1][2], A[0][3], A[1][3], b.z, b.w);
                         }
-                    if (j % kChain == kChain - 1)         // the chain's end
+                    if (j % kChain == kChain - 1)         // the chains' end
 #pragma unroll
                         for (int q = 0; q < NT; ++q)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[q][i] = add_rn(acc[q][i], d[q][i]);
+                            for (int i = 0; i < 4; ++i)
+                                acc[q][i] = add_rn(acc[q][i], P == 2 ? __fmaf_rn(d[P - 1][q][i], 0x1p-11f, d[0][q][i]) : d[0][q][i]);
                 }
                 load(u);
                 if (++c == n) end_tile();

@@ -1,9 +1,10 @@
 """What nvfp4_mv keeps of activations that lie far below others of their token.
 
 x enters the product in f16 after a power-of-two scaling to the largest magnitude
-of a part of its columns: whatever the type, an element is off by at most 2^-39 of
-that magnitude (half an f16 step of 2^-24 on values scaled to [2^14, 2^15)), besides
-the rounding of fp32 to 22 bits.  Weights that are zero where x is large let the
+of a part of its columns: a bf16 or MXFP8 element is off by at most 2^-39 of that
+magnitude (half an f16 step of 2^-24 on values scaled to [2^14, 2^15)), an fp32 one,
+held as two f16, by 2^-23 of itself or 2^-50 of that magnitude (half a step of the
+second, which stands for 2^-11 of the first's).  Weights that are zero where x is large let the
 small elements alone reach the output, so nothing hides what was lost.
 """
 import numpy as np
@@ -80,3 +81,22 @@ def test_mv_mxfp8_far_ends_of_the_scales():
     y = to_np(nv.nvfp4_mv(to_dev(e4m3(x)), to_dev(codes), to_dev(scales), x_scales=to_dev(b), out_dtype="f32"))
     want = (xv @ w.T).astype(np.float32)                  # one or two products: exact in fp32
     assert np.array_equal(y, want)
+
+
+@pytest.mark.parametrize("gap", [0, 12, 15, 18, 20, 25, 27, 30, 35, 40, 60])
+@pytest.mark.parametrize("M,K", [(1, 512), (9, 2064)])
+@pytest.mark.parametrize("x_type", ["f32", "bf16"])
+def test_mv_keeps_what_is_near_the_largest_value(gap, M, K, x_type):
+    """One value 2^gap times the others' size, where the weights are zero."""
+    rng = np.random.default_rng(gap + K)
+    N = 40
+    codes, scales, w = weight(rng, N, K, np.array([0]))
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    x[:, 0] = 1.25 * 2.0 ** gap
+    xd = torch.from_numpy(x).cuda().to(torch.float32 if x_type == "f32" else torch.bfloat16)
+    xv = xd.double().cpu().numpy()
+    y = nv.nvfp4_mv(xd, to_dev(codes), to_dev(scales), out_dtype="f32")
+    top = np.abs(xv).max(axis=1, keepdims=True)
+    off = np.maximum(np.abs(xv) * 2.0 ** -23, top * 2.0 ** -50) if x_type == "f32" else np.full_like(xv, 2.0 ** -39) * top
+    bound = off @ np.abs(w).T + (np.abs(xv[:, 1:]) @ np.abs(w[:, 1:]).T) * (17 * 2.0 ** -22)
+    assert (np.abs(to_np(y).astype(np.float64) - xv @ w.T) <= bound).all()
