@@ -25,24 +25,33 @@ def _quantize_experts(w: torch.Tensor) -> dict:
 
 
 class FP4Projection:
-    """norm(x + hidden) W^T for a weight [N, K], K a multiple of 64: up to 16 rows
-    through MXFP8 activations and nvfp4_mv, more through NVFP4 activations and the FP4
-    tensor cores (nvfp4_grouped_mm with one group)."""
+    """norm(x + hidden) W^T for a weight [N, K], K a multiple of 64.
 
-    def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, eps: float = 1e-6):
+    activations: "mxfp8" (8 bits; nvfp4_mv, 16 rows at a time), "nvfp4" (4 bits; the FP4
+    tensor cores through nvfp4_grouped_mm with one group), or "auto", whichever is faster:
+    "mxfp8" up to 16 rows, "nvfp4" above.  With "auto" the precision of a token's result
+    goes by the number of rows it comes with; the other two give it the same at any."""
+
+    def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, eps: float = 1e-6, activations: str = "auto"):
+        if activations not in ("auto", "mxfp8", "nvfp4"):
+            raise ValueError(f"FP4Projection: activations {activations!r}; expected auto, mxfp8 or nvfp4")
         q = _quantize_experts(weight.unsqueeze(0))
-        self.norm_weight, self.eps = norm_weight, eps
+        self.norm_weight, self.eps, self.activations = norm_weight, eps, activations
         self.codes, self.scales, self.gamax = q["codes"], q["scales"], q["gamax"]
         self.scales_mma = nvfp4_grouped_scales_to_mma(self.scales)
+
+    def _mv(self, codes, x_scales, out_dtype):
+        return nvfp4_mv(codes, self.codes[0], self.scales[0], x_scales=x_scales, gamax=self.gamax, out_dtype=out_dtype)
 
     def __call__(self, x: torch.Tensor, hidden: torch.Tensor, out_dtype="bf16"):
         """(product [M, N], new hidden [M, K])."""
         M = x.shape[0]
-        if M <= MV_ROWS:
+        if self.activations == "mxfp8" or (self.activations == "auto" and M <= MV_ROWS):
             n = nvfp4_rmsnorm(x, self.norm_weight, hidden=hidden, eps=self.eps)
-            y = nvfp4_mv(n["codes"], self.codes[0], self.scales[0], x_scales=n["scales"], gamax=self.gamax,
-                         out_dtype=out_dtype)
-            return y, n["hidden"]
+            if M <= MV_ROWS:
+                return self._mv(n["codes"], n["scales"], out_dtype), n["hidden"]
+            parts = zip(n["codes"].split(MV_ROWS), n["scales"].split(MV_ROWS))
+            return torch.cat([self._mv(c, s, out_dtype) for c, s in parts]), n["hidden"]
         n = nvfp4_rmsnorm(x, self.norm_weight, hidden=hidden, eps=self.eps, format="nvfp4", gamax_mode="row")
         offsets = torch.zeros(2, dtype=torch.int64, device=x.device)
         offsets[1:].fill_(M)

@@ -102,3 +102,33 @@ def test_experts_of_an_empty_batch():
     assert out.shape == hidden.shape == (0, 128) and out.dtype == hidden.dtype == torch.bfloat16
     y, hidden = FP4Projection(r(96, 128), r(128))(r(0, 128), r(0, 128))
     assert y.shape == (0, 96) and hidden.shape == (0, 128)
+
+
+@pytest.mark.parametrize("activations", ["mxfp8", "nvfp4"])
+def test_projection_precision_does_not_go_by_the_batch(activations):
+    """A token's product is of the same quantized activations whatever it comes with: alone and in batches it is the
+    same sum of exact products, in orders that may differ by an fp32 step each (2^-17 of the magnitudes on both
+    sides, as test_gpu_serving_layers.py has it)."""
+    from nvfp4_block_quantization_quantize_gb300.serving import FP4Projection
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=gen).to(torch.bfloat16)      # noqa: E731
+    N, K, M = 200, 512, 70
+    w, nw, x, h = r(N, K), r(K), r(M, K), r(M, K)
+    layer = FP4Projection(w, nw, activations=activations)
+    if activations == "mxfp8":
+        n = nv.nvfp4_rmsnorm(x, nw, hidden=h)
+        mag = n["codes"].view(torch.float8_e4m3fn).double().abs() * torch.pow(2.0, n["scales"].double() - 127).repeat_interleave(32, 1)
+    else:
+        n = nv.nvfp4_rmsnorm(x, nw, hidden=h, format="nvfp4", gamax_mode="row")
+        mag = nv.nvfp4_dequantize(n["codes"], n["scales"], M, K, gamax=n["gamax"], gamax_mode="row_given",
+                                  out_dtype="f32").double().abs()
+    q = nv.nvfp4_quantize(w, gamax_mode="tensor")
+    wv = nv.nvfp4_dequantize(q["codes"], q["scales"], N, K, gamax=q["gamax"], gamax_mode="tensor_given", out_dtype="f32")
+    bound = 2 * (mag @ wv.double().abs().t()) * 2.0 ** -17
+    whole, hidden = layer(x, h, out_dtype="f32")
+    assert whole.shape == (M, N) and torch.equal(hidden, (x.float() + h.float()).to(x.dtype))
+    for a, b in ((0, 1), (3, 19), (16, 33), (69, 70)):
+        part, _ = layer(x[a:b], h[a:b], out_dtype="f32")
+        assert bool(((part.double() - whole[a:b].double()).abs() <= bound[a:b]).all())
+    with pytest.raises(ValueError, match="activations"):
+        FP4Projection(w, nw, activations="fp8")
