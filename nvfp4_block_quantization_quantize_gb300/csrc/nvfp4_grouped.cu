@@ -42,15 +42,15 @@ constexpr int kGmAhead = 4;                               // stages the token sc
 template <int BT>
 struct GmShape {
     static constexpr int kStages = BT <= 32 ? 4 : 3;
-    static constexpr int kSfbTiles = (BT + 127) / 128;    // 128-row scale tiles of the tokens
     static constexpr int kSlotW = kGmRows * 128, kSlotT = BT * 128;
-    static constexpr int kSlotSfw = kGmStageK * 512, kSlotSft = kGmStageK * 512 * kSfbTiles;
+    static constexpr int kSlotSfw = kGmStageK * 512, kSlotSft = kGmStageK * 512;
     static constexpr int kSlot = kSlotW + kSlotT + kSlotSfw + kSlotSft;
     static constexpr int kSmem = kStages * kSlot + 1024;  // + alignment slack
-    static constexpr int kSfCols = 4 + 4 * kSfbTiles;     // tensor-memory columns per step
+    static constexpr int kSfCols = 8;                     // tensor-memory columns per step: 4 of each side's scales
     static constexpr int kCols = BT + kStages * kGmStageK * kSfCols;
     static constexpr int kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static constexpr int kSfWarps = BT >= 128 ? 4 : (BT + 31) / 32;   // warps that hold tokens' scales
+    static constexpr int kSfWarps = (BT + 31) / 32;       // warps that hold tokens' scales
+    static_assert(BT <= 128, "one 128-row scale tile holds the tokens");
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -255,9 +255,7 @@ __global__ void __launch_bounds__(kGmThreads)
                 if (kk >= nk) break;
                 const uint32_t c = c0 + kk * G::kSfCols;
                 copy_scales_warp<1>(el, c, dsw + kk * 32);
-#pragma unroll
-                for (int j = 0; j < G::kSfbTiles; ++j)
-                    copy_scales_warp<1>(el, c + 4 + 4 * j, dst + (kk * G::kSfbTiles + j) * 32);
+                copy_scales_warp<1>(el, c + 4, dst + kk * 32);
                 mma_f4_warp<1>(el, tmem, dw + kk * 2, dt + kk * 2, idesc, c, c + 4, t + kk > 0 ? 1u : 0u);
             }
             commit_warp<1>(el, &empty[s]);
@@ -273,17 +271,14 @@ __global__ void __launch_bounds__(kGmThreads)
             alpha[i] = mul_rn(da, db);
         }
     } else if (warp >= 4 && warp < 4 + G::kSfWarps) {
-        // ---- the tokens' scales: rows i and, of 256-token tiles, i + 128 ----
+        // ---- the tokens' scales: row i ----
         const int i = tid - 128;
-        uint4 v[kGmAhead][G::kSfbTiles];
-        auto load = [&](int t, uint4* d) {
-#pragma unroll
-            for (int j = 0; j < G::kSfbTiles; ++j)
-                d[j] = i + 128 * j < rows ? token_scales(a, row0 + i + 128 * j, t * kGmStageK, ksteps)
-                                          : make_uint4(0, 0, 0, 0);
+        uint4 v[kGmAhead];
+        auto load = [&](int t) {
+            return i < rows ? token_scales(a, row0 + i, t * kGmStageK, ksteps) : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll
-        for (int u = 0; u < kGmAhead; ++u) load(u, v[u]);
+        for (int u = 0; u < kGmAhead; ++u) v[u] = load(u);
         bool ok = true;
         for (int t0 = 0; t0 < nstages && ok; t0 += kGmAhead) {
 #pragma unroll
@@ -297,17 +292,13 @@ __global__ void __launch_bounds__(kGmThreads)
                     break;
                 }
                 uint8_t* sf = smem + s * G::kSlot + G::kSlotW + G::kSlotT + G::kSlotSfw + (i % 32) * 16 + (i / 32) * 4;
+                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-                for (int j = 0; j < G::kSfbTiles; ++j) {
-                    const uint32_t w[4] = {v[u][j].x, v[u][j].y, v[u][j].z, v[u][j].w};
-#pragma unroll
-                    for (int kk = 0; kk < kGmStageK; ++kk)
-                        *reinterpret_cast<uint32_t*>(sf + (kk * G::kSfbTiles + j) * 512) = w[kk];
-                }
+                for (int kk = 0; kk < kGmStageK; ++kk) *reinterpret_cast<uint32_t*>(sf + kk * 512) = w[kk];
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
-                load(t + kGmAhead, v[u]);
+                v[u] = load(t + kGmAhead);
             }
         }
     }
