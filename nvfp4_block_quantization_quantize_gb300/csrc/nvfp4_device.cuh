@@ -406,8 +406,10 @@ __device__ __forceinline__ void cp_async_wait() {
 // that need no input, barrier initialisation) overlap that kernel's last
 // CTAs.  pdl_wait() blocks until the previous kernel has completed and its
 // memory is visible; a kernel calls it before its first global-memory access.
-// pdl_trigger() lets the next kernel launch; a kernel calls it once its CTA
-// has no work left.  Launched without the attribute, both are no-ops.
+// pdl_trigger() lets the next kernel launch; a quantizer kernel calls it once
+// its CTA has no work left, the serving operators' as they start (their next
+// kernel's set-up then runs beside them; it waits for their end itself).
+// Launched without the attribute, both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

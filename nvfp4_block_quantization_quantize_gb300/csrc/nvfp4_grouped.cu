@@ -145,7 +145,7 @@ __device__ __forceinline__ void store_columns(const GroupedArgs& a, const uint32
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = __int_as_float(0x7FC00000);
     }
-    if (ODT == NVFP4_BF16 && a.N % 8 == 0) {
+    if (ODT == NVFP4_BF16 && a.N % 8 == 0 && !bad) {      // (bad: copies may still come into the stages)
         __syncwarp();                                     // the last turn is read
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -321,8 +321,10 @@ __global__ void __launch_bounds__(kGmThreads)
     }
     asm volatile("tcgen05.fence::before_thread_sync;");
     __syncthreads();
-    if (warp == 0)
+    if (warp == 0) {
+        if (bad) settle();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmem));
+    }
 }
 
 // ---- many tokens an expert: pairs of SMs -------------------------------------------------------
@@ -789,6 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
     }
     // neither CTA leaves while the other may still read its shared memory or arrive at its barriers
     __syncwarp();
+    if (timed_out) settle();
     asm volatile("tcgen05.fence::before_thread_sync;");
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

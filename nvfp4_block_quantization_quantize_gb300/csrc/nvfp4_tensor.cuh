@@ -63,6 +63,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
+// A CTA one of whose waits ran out calls this before it ends: the copies it has issued take microseconds, and are
+// in after the millisecond this sleeps.
+__device__ __forceinline__ void settle() {
+    for (int i = 0; i < 1024; ++i) __nanosleep(1000);
+}
+
 // decode scale S_dec = 1 / min(6 * bound / A, FLT_MAX) of a per-tensor amax
 // (1 without one, and when A is not a positive finite number)
 __device__ __forceinline__ float decode_scale(const float* gamax, float bound) {
