@@ -48,14 +48,14 @@ int check_shape(int64_t M, int64_t K) {
 // A buffer of a call, for check_apart.
 struct Buffer {
     const void* p;            // null = not given
-    int64_t bytes;
+    uint64_t bytes;
     const char* name;
 };
 
 bool overlap(const Buffer& a, const Buffer& b) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    return p <= q ? q - p < static_cast<uint64_t>(a.bytes) : p - q < static_cast<uint64_t>(b.bytes);
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+    return p <= q ? q - p < a.bytes : p - q < b.bytes;
 }
 
 // No output shares a byte with an input or another output: CTAs read their inputs while
@@ -310,18 +310,18 @@ int nvfp4_rmsnorm(const void* x, const void* hidden, int64_t M, int64_t K, int d
         const int err = static_cast<int>(cudaMemsetAsync(gamax, 0, static_cast<size_t>(M) * 4, stream));
         return err ? cuda_fail(err, "norm zero fill") : NVFP4_OK;
     }
-    const int64_t full = M * K * (dtype == NVFP4_F32 ? 4 : 2);
+    const uint64_t m = M, k = K, full = m * k * (dtype == NVFP4_F32 ? 4 : 2);
     const bool mx = format == NVFP4_FMT_MXFP8;
-    const int64_t amax = gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_TENSOR_GIVEN ? 4 : M * 4;
+    const uint64_t amax = gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_TENSOR_GIVEN ? 4 : m * 4;
     const bool row = gamax_mode == NVFP4_GAMAX_ROW;       // gamax is written
     const Buffer outs[] = {{hidden_out, full, "hidden_out"},
                            {out, full, "out"},
-                           {codes, mx ? M * K : M * (K / 2), "codes"},
-                           {scales, M * (mx ? (K + 31) / 32 : K / 16), "scales"},
+                           {codes, mx ? m * k : m * (k / 2), "codes"},
+                           {scales, m * (mx ? (k + 31) / 32 : k / 16), "scales"},
                            {gamax, row ? amax : 0, "gamax"}};
     const Buffer ins[] = {{x, full, "x"},
                           {hidden, hidden == hidden_out ? 0 : full, "hidden"},      // updated in place: an output alone
-                          {weight, K * (weight_dtype == NVFP4_F32 ? 4 : 2), "weight"},
+                          {weight, k * (weight_dtype == NVFP4_F32 ? 4 : 2), "weight"},
                           {gamax, row ? 0 : amax, "gamax"}};
     if ((rc = check_apart(outs, ins))) return rc;
     const nvfp4::NormArgs a{x, hidden, M, K, dtype, weight, weight_dtype, eps, hidden_out, out, format, gamax_mode,
@@ -357,12 +357,13 @@ int nvfp4_mv(const void* x, const uint8_t* x_scales, int x_type, const uint8_t* 
     if ((rc = check_ptr(gamax, "gamax", any && gamax_mode != NVFP4_GAMAX_NONE, 4))) return rc;
     if ((rc = check_ptr(out, "out", any))) return rc;
     if (!any) return NVFP4_OK;
-    const Buffer outs[] = {{out, M * N * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}};
-    const Buffer ins[] = {{x, M * K * (x_type == NVFP4_X_F32 ? 4 : x_type == NVFP4_X_BF16 ? 2 : 1), "x"},
-                          {x_scales, x_type == NVFP4_X_MXFP8 ? M * ((K + 31) / 32) : 0, "x_scales"},
-                          {codes, N * (K / 2), "codes"},
-                          {scales, N * (K / 16), "scales"},
-                          {gamax, gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? N * 4 : 4, "gamax"}};
+    const uint64_t m = M, n = N, k = K;
+    const Buffer outs[] = {{out, m * n * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}};
+    const Buffer ins[] = {{x, m * k * (x_type == NVFP4_X_F32 ? 4 : x_type == NVFP4_X_BF16 ? 2 : 1), "x"},
+                          {x_scales, x_type == NVFP4_X_MXFP8 ? m * ((k + 31) / 32) : 0, "x_scales"},
+                          {codes, n * (k / 2), "codes"},
+                          {scales, n * (k / 16), "scales"},
+                          {gamax, gamax_mode == NVFP4_GAMAX_NONE ? 0 : gamax_mode == NVFP4_GAMAX_ROW_GIVEN ? n * 4 : 4, "gamax"}};
     if ((rc = check_apart(outs, ins))) return rc;
     if (K == 0) {
         const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(N) * (out_dtype == NVFP4_F32 ? 4 : 2);
@@ -417,14 +418,15 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
     if (workspace_bytes < need)
         return fail(NVFP4_EINVAL, "the workspace needs %lld bytes (got %lld)", (long long)need, (long long)workspace_bytes);
     if ((rc = check_ptr(workspace, "workspace", need > 0))) return rc;
-    const Buffer outs[] = {{out, T * N * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}, {workspace, need, "workspace"}};
-    const Buffer ins[] = {{codes_a, T * (K / 2), "codes_a"},
-                          {scales_a, T * (K / 16), "scales_a"},
-                          {offsets, (E + 1) * 8, "offsets"},
-                          {codes_b, E * N * (K / 2), "codes_b"},
-                          {scales_b, E * ((N + 127) / 128 * 128) * (K / 16), "scales_b"},
-                          {gamax_a, gamax_a_mode == NVFP4_GAMAX_NONE ? 0 : gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? T * 4 : 4, "gamax_a"},
-                          {gamax_b, E * 4, "gamax_b"}};
+    const uint64_t e = E, t = T, n = N, k = K;
+    const Buffer outs[] = {{out, t * n * (out_dtype == NVFP4_F32 ? 4 : 2), "out"}, {workspace, static_cast<uint64_t>(need), "workspace"}};
+    const Buffer ins[] = {{codes_a, t * (k / 2), "codes_a"},
+                          {scales_a, t * (k / 16), "scales_a"},
+                          {offsets, (e + 1) * 8, "offsets"},
+                          {codes_b, e * n * (k / 2), "codes_b"},
+                          {scales_b, e * ((n + 127) / 128 * 128) * (k / 16), "scales_b"},      // at most 2^63
+                          {gamax_a, gamax_a_mode == NVFP4_GAMAX_NONE ? 0 : gamax_a_mode == NVFP4_GAMAX_ROW_GIVEN ? t * 4 : 4, "gamax_a"},
+                          {gamax_b, e * 4, "gamax_b"}};
     if ((rc = check_apart(outs, ins))) return rc;
     const int err = nvfp4::launch_grouped_mm(a, stream);
     if (err) return cuda_fail(err, "grouped mm launch");
