@@ -911,7 +911,8 @@ def _check_mm_args(codes_a, scales_a, codes_b, scales_b, M, N, K, gamax_a, gamax
 # (csrc/nvfp4_call.cpp); it returns None for any other, which is then checked,
 # made contiguous or refused here.  A call on a given stream runs wholly on it
 # (copies and allocations too): a stream of the tensors' device; a bare handle is
-# taken for one.
+# taken for one.  The weights are frozen: results do not require a gradient, whatever
+# the inputs do.
 def _given_stream(stream, dev):
     if isinstance(stream, torch.cuda.Stream):
         if stream.device != dev:
@@ -969,7 +970,8 @@ def nvfp4_rmsnorm(x: torch.Tensor, weight=None, *, hidden=None, hidden_out=None,
     nvfp4_quantize gives (gamax_mode "none", "tensor_given", "row",
     "row_given"), all uint8.  "hidden" is h rounded to x's dtype: a new tensor,
     or hidden_out (which may be hidden: in place).  "out" (want_out, or a given
-    out) is the norm itself in x's dtype; want_codes=False leaves the codes out."""
+    out) is the norm itself in x's dtype; want_codes=False leaves the codes out.
+    No gradient is taken (nor by the two products below)."""
     lib = _lib or load_library()
     if stream is None and gamax_mode == "none" and want_codes and scale_bound == 448.0:
         res = _call.rmsnorm(x, weight, hidden, hidden_out, eps, format, want_out, out, codes, scales)

@@ -20,8 +20,10 @@
 //     stage (some stages ahead, in registers) and writes them where the tile
 //     wants them;
 //   - warps 2 and 3: the tokens' decode scales.  All warps then store the accumulator.
-// Measured: 64 tokens on 64 experts of [2048, 4096] 28.1 us (5.7 TB/s), 2 of 8 experts of
-// [1024, 1024] 3.4 us, 1999 tokens on 13 experts of [1430, 2112] 12.6 us.
+// Measured, in a graph of calls: 64 tokens on 64 experts of [2048, 4096] 27.9 us (5.8 TB/s), 2 of 8
+// experts of [1024, 1024] 3.6 us, 1999 tokens on 13 experts of [1430, 2112] 12.0 us; one group
+// of 64 tokens x [14336, 4096] 11.3 us, x [4096, 14336] 20.8 us (32 weight tiles for 152 SMs:
+// K is not split).
 // A tile's last columns may read the next group's rows (or, past T, zeros): those
 // products are computed and not stored.  Every wait is bounded; a CTA whose wait
 // runs out writes NaN to its tile.
@@ -345,10 +347,10 @@ __global__ void __launch_bounds__(kGmThreads)
 // the caller's workspace).  The MMA's N is the tile's token count rounded up to 32, so a
 // group's last tile costs what it needs.  A wait that runs out stops the CTA's roles; its
 // unfinished tiles become NaN.
-// Measured: 8192 tokens on 8 experts of [14336, 4096] 188 us (5.1 PFLOP/s; tensor pipe 56 %, L2 61 %
-// of their peaks).  With parts left out: the copies alone 140 us (about the 86 bytes a clock an SM's
-// TMA takes in at most), products with their scale copies alone 144, both without the stores 160: no
-// unit is full, the three slow each other.
+// Measured: 8192 tokens on 8 experts of [14336, 4096] 188 to 205 us, as calls and in a graph alike, by
+// the card and its power (4.7 to 5.1 PFLOP/s; at 189 us tensor pipe 56 %, L2 61 % of their peaks).  With
+// parts left out, on a card where the whole took 188: the copies alone 140 us (about the 86 bytes a clock
+// an SM's TMA takes in at most), products with their scale copies alone 144, both without the stores 160.
 constexpr int kGpStoreWarps = 8;                          // two for each quarter of the accumulator's lanes
 constexpr int kGpThreads = 64 + 32 * kGpStoreWarps;
 constexpr int kGpBT = 192;
@@ -366,8 +368,8 @@ constexpr uint32_t kGpColSf = 2 * kGpBT;                  // scales: two stages 
 // a block's tokens stay in L2.  Without blocks the weights of all experts run together: us without /
 // with, 8192 tokens on 8 experts of [4096, 14336] 229 / 192, 16384 on 64 of [2048, 7168] 197 / 142, 8192 on 8
 // of [14336, 4096] 193 / 190 (blocks of 1 MB to 4 MB 193 to 195, of 30 MB at K = 14336 197).  (Single-SM
-// tiles, one wave or few, gain nothing: 64 experts 8192 x 2048 of K 7168 129 / 119, 32 experts 4096 x 2048 of
-// K 4096 40 / 42.)
+// tiles go either way, so they are not cut: 64 experts 8192 x 2048 of K 7168 129 / 119, 32 experts 4096 x 2048 of
+// K 4096 40 / 42; pairs take the first.)
 constexpr int64_t kBlockBytes = 10 << 20;
 
 unsigned block_tiles(const GroupedArgs& a, int64_t slots) {
@@ -871,9 +873,11 @@ cudaError_t launch_grouped_o(const GroupedArgs& a, cudaStream_t s) {
 // pairs takes about 2.6 + 0.7 K / 1024 us and the call 10 more (the scales' layout, the first
 // tiles' start and the last ones' end), a wave of 128 x 128 tiles, two CTAs an SM, 3.6 + 2 K / 1024
 // and 3 more; neither is faster than its bytes at 5.2 and 4.8 TB/s.  The last wave counts half its share
-// and half a whole one.  Fitted over 28 shapes, on which the choice is within 2 % of the faster path; us
-// pairs / single: K 4096, 4 experts 1024 x 14336 44 / 49, 2 experts 4096 x 4096 37 / 49, 8 experts 8192 x 14336
-// 190 / 292, 16 experts 2048 x 4096 45 / 40; K 1024, 4 experts 8192 x 1024 18 / 13.
+// and half a whole one.  (Outputs are counted at two bytes, fp32 ones
+// too: a path needs or needs no workspace by the sizes alone.)  On 28 shapes the choice costs at most 1.3 % of
+// the faster path's time, but for one of 256 tokens x [4096, 4096] (11.1 / 12.0); us pairs / single: K 4096, 4
+// experts 1024 x 14336 46 / 50, 2 experts 4096 x 4096 38 / 49, 8 experts 8192 x 14336 193 / 296, 16 experts
+// 2048 x 4096 44 / 39; K 1024, 4 experts 8192 x 1024 19 / 13.
 static bool takes_pairs(const GroupedArgs& a) {
     constexpr double kSms = 152;
     if (a.K <= 0 || a.E <= 0 || a.N <= 128 || a.T < 33 * a.E || a.K / 64 > 8 * 65535) return false;

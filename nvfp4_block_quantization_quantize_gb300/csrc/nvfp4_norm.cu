@@ -8,8 +8,9 @@
 // rows).  A row belongs to one CTA: a thread holds a block of 16 elements in
 // registers from the load to the stores, so nothing is read twice; rows of over
 // 1024 blocks are read a second time instead.
-// Measured: 16384 x 4096 bf16 with the residual, MXFP8 out, 73 us (6.45 TB/s, 0.95 of the
-// copy rate); 1 x 4096 2.1 us; 2048 x 20480 79 us (read twice).
+// Measured, in a graph of calls: 16384 x 4096 bf16 with the residual, MXFP8 out, 73 us (6.45 TB/s,
+// 0.95 of the copy rate), NVFP4 out 79 us, with row amaxes 108 us (y is made twice, and the row
+// reduced twice); 1 x 4096 2.2 us; 2048 x 20480 79 us (read twice), with the residual 87.
 #include "nvfp4_block.cuh"
 
 namespace nvfp4 {

@@ -4,7 +4,8 @@ a few tokens, the products grouped by expert.
 
 The weights are quantized once with the library (1x16 blocks, one global amax a
 weight or expert).  Nothing here reads a device value on the host, so a step
-of fixed shapes can be captured in a CUDA graph.  No gradient is taken.
+of fixed shapes can be captured in a CUDA graph.  No gradient is taken: the results
+do not require one, whatever the inputs do.
 """
 from __future__ import annotations
 
@@ -28,9 +29,10 @@ class FP4Projection:
     """norm(x + hidden) W^T for a weight [N, K], K a multiple of 64.
 
     activations: "mxfp8" (8 bits; nvfp4_mv, 16 rows at a time), "nvfp4" (4 bits; the FP4
-    tensor cores through nvfp4_grouped_mm with one group), or "auto", whichever is faster:
-    "mxfp8" up to 16 rows, "nvfp4" above.  With "auto" the precision of a token's result
-    goes by the number of rows it comes with; the other two give it the same at any."""
+    tensor cores through nvfp4_grouped_mm with one group), or "auto": "mxfp8" for the 16
+    rows nvfp4_mv takes at once, "nvfp4" above.  With "auto" the precision of a token's
+    result goes by the number of rows it comes with; the other two give it the same at
+    any.  [14336, 4096] in a graph: 1 row 10 us, 16 rows 31 us in 8 bits, 64 rows 14 us in 4."""
 
     def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, eps: float = 1e-6, activations: str = "auto"):
         if activations not in ("auto", "mxfp8", "nvfp4"):
