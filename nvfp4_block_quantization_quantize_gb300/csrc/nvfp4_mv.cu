@@ -92,7 +92,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// a word's eight weights, scaled, as four f16 pairs (s holds the block's scale twice)
+// a word's eight weights, scaled, as four f16 pairs (s holds the block's scale twice).  The four-byte
+// unpack, which e2m1_decode_byte avoids, reads right here: tests compare the products of every variant of
+// the kernel bit for bit.
 __device__ __forceinline__ void weights8(uint32_t w, uint32_t s, uint32_t* h) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
