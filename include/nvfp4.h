@@ -318,6 +318,111 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
                      int out_dtype, uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * A paged cache of keys and values in NVFP4, and what a model runs around it.
+ *
+ * cache: device bytes [pages, Hkv, page_size / 16, 18 * D], 16-byte aligned, zero or
+ *   whatever (only slots that were written are read).  page_size is a multiple of
+ *   16, D the head dimension (64, 128 or 256).  A tile holds 16 tokens of a KV head:
+ *     keys' codes [16, D/2], keys' scales [16, D/16], values' codes, values' scales,
+ *   codes and scales as nvfp4_quantize lays them out.  Slot s is token s % page_size of
+ *   page s / page_size.
+ * k_mode, v_mode with k_gamax, v_gamax: the global scale of keys and of values, NONE
+ *   (NULL), TENSOR_GIVEN (1 fp32) or ROW_GIVEN (one fp32 per KV head), the same in
+ *   every call on a cache; scale_bound as in nvfp4_quantize.
+ * pages * Hkv * page_size * D is below 2^62, Hkv and D below 2^15, pages and T below 2^30.
+ */
+
+/* which elements of a head's first rotary_dim = R turn together: i and i + R/2, or 2i and 2i + 1 */
+enum nvfp4_rope_layout { NVFP4_ROPE_HALF = 0, NVFP4_ROPE_INTERLEAVED = 1 };
+
+/*
+ * nvfp4_qk_norm_rope -- norms of queries and keys for each head and their rotation by
+ * position, and optionally keys and values quantized into a cache, in one pass.
+ * Per head of D elements, in fp32:
+ *   y = x * (1 / sqrt(sum(x^2) / D + eps)) * weight     (with a weight)
+ *   the pairs (a, b) of its first R = rotary_dim elements become
+ *   magnitude * (a cos t - b sin t, b cos t + a sin t),  t = 2 pi * positions[token] * phases[pair] / 2^64
+ *   q_out = y rounded to dtype; k the same, or with a cache y quantized into it
+ *   as nvfp4_quantize quantizes an F32 tensor (1x16, RTN, the amax given), v as it comes.
+ *   q, k, v     device, dtype F32 or BF16; a token's heads are contiguous [H, D], tokens
+ *               q_stride, k_stride, v_stride elements apart (>= 0, whole 16 bytes).  v
+ *               comes with a cache and not without
+ *   q_weight, k_weight   NULL or device [D] of weight_dtype, both or neither
+ *   positions   device int64 [T];  phases  device uint64 [R/2]: turns a position, in 2^-64
+ *   rotary_dim  0 (no rotation; positions and phases NULL) .. D, a multiple of 16, of 32 with
+ *               a cache and the half layout; layout: nvfp4_rope_layout
+ *   q_out [T,Hq,D], k_out [T,Hkv,D] (NULL with a cache), of dtype
+ *   slots       device int64 [T], with a cache: where each token goes; a slot outside
+ *               [0, pages * page_size) is not written.  Slots are distinct: one that is given
+ *               twice holds bytes of both tokens (the others are right)
+ * D: a multiple of 16 up to 512; with a cache 64, 128 or 256.  EINVAL on bad sizes, enums,
+ * pointers, strides, eps or magnitude (not finite), an output that shares a byte with an input
+ * or another output.
+ */
+int nvfp4_qk_norm_rope(const void* q, const void* k, const void* v, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int dtype, const void* q_weight,
+                       const void* k_weight, int weight_dtype, float eps, const int64_t* positions,
+                       const uint64_t* phases, int64_t rotary_dim, int layout, float magnitude, void* q_out, void* k_out,
+                       uint8_t* cache, int64_t pages, int64_t page_size, const int64_t* slots, int k_mode,
+                       const float* k_gamax, int v_mode, const float* v_gamax, float scale_bound, cudaStream_t stream);
+
+/*
+ * nvfp4_cache_write -- keys and values of T tokens quantized into their slots of a cache,
+ * as nvfp4_quantize quantizes them (1x16 blocks, RTN, the amax given).
+ *   k, v    device, dtype F32 or BF16: contiguous heads [Hkv, D], tokens k_stride and
+ *           v_stride elements apart;  slots as above
+ */
+int nvfp4_cache_write(const void* k, const void* v, int64_t T, int64_t Hkv, int64_t D, int64_t k_stride,
+                      int64_t v_stride, int dtype, uint8_t* cache, int64_t pages, int64_t page_size,
+                      const int64_t* slots, int k_mode, const float* k_gamax, int v_mode, const float* v_gamax,
+                      float scale_bound, cudaStream_t stream);
+
+/*
+ * nvfp4_cache_read -- the keys and values that T slots hold, as nvfp4_dequantize gives them.
+ *   k, v    [T,Hkv,D], F32 or BF16; either may be NULL.  A slot outside [0, pages * page_size)
+ *           gives zeros
+ */
+int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t Hkv, int64_t D,
+                     const int64_t* slots, int64_t T, int k_mode, const float* k_gamax, int v_mode,
+                     const float* v_gamax, float scale_bound, void* k, void* v, int out_dtype, cudaStream_t stream);
+
+/*
+ * nvfp4_cache_attention -- attention of queries over the sequences a cache holds.
+ * Sequence b has lengths[b] keys, key j in token j % page_size of page
+ * page_table[b, j / page_size], and the queries offsets[b] .. offsets[b+1], the last of
+ * which stands at key lengths[b] - 1 and the others at the keys before it.  A query at
+ * p sees the keys j < lengths[b] with (causal) j <= p and (window > 0) j > p - window.
+ * Head h uses KV head h / (Hq / Hkv):
+ *   out = sum_j w_j v_j, w = softmax(scale * q . k_j), with a sink (fp32 [Hq], one logit a
+ *   head) among the logits but without a value; 0 for a query that sees nothing
+ *   lse (NULL or fp32 [T,Hq]) = log of the softmax's denominator, the sink's included
+ *   q          device [T,Hq,D], dtype F32 or BF16, tokens q_stride elements apart
+ *   page_table device int32 [B,width]; keys of a page outside [0, pages) are not seen
+ *   lengths    device int64 [B] (values outside [0, width * page_size] are clamped to it)
+ *   offsets    NULL (one query a sequence: T == B) or device int64 [B+1], non-decreasing in
+ *              [0, T] (values outside are clamped to it; a sequence that ends before it starts has none)
+ *   out        [T,Hq,D], F32 or BF16; rows of no sequence are not written, nor their lse
+ *   workspace  nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, page_size, dtype) bytes,
+ *              written and read by this call alone
+ * Keys and values are exact in f16.  Queries enter as f16 after a power-of-two scaling per head, off
+ * by at most 2^-39 of the head's largest magnitude (BF16), or as two f16, off by 2^-23 of themselves or
+ * 2^-39 of that magnitude (F32); weights enter the second product as f16, or as two for F32
+ * queries.  Sums, maxima and denominators are fp32, in an order that the lengths and sizes fix: the same
+ * bits on every run.  EINVAL: Hq not a multiple of Hkv, bad sizes, enums, pointers, strides, bound or
+ * scale (not finite), window < 0, a negative or too small workspace, T != B without offsets, an
+ * output that shares a byte with an input or another output.  A CTA that stops waiting for its copies
+ * writes NaN.
+ */
+int64_t nvfp4_cache_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width,
+                                        int64_t page_size, int dtype);
+int nvfp4_cache_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride, int dtype, const uint8_t* cache,
+                          int64_t pages, int64_t page_size, int64_t Hkv, int64_t D, const int32_t* page_table,
+                          int64_t B, int64_t width, const int64_t* lengths, const int64_t* offsets, int k_mode,
+                          const float* k_gamax, int v_mode, const float* v_gamax, float scale_bound, float scale,
+                          int causal, int64_t window, const float* sinks, void* out, int out_dtype, float* lse,
+                          uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
  * nvfp4_probe_divide -- diagnostic.  out[i] = a[i] / b[i] computed by the
  * device routine the plain quantizer uses for "every element is divided by the
  * decoded scale" [fp4-train, Method] (its stochastic-rounding form, which must

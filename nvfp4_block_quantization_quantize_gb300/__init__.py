@@ -13,6 +13,9 @@ Functions (same names as the C ABI):
   nvfp4_amax(x, ...)       -> tensor
   nvfp4_mm, nvfp4_mv, nvfp4_grouped_mm: products with NVFP4 weights
   nvfp4_rmsnorm(x, ...)    -> dict(codes, scales[, hidden][, out][, gamax])
+  nvfp4_rope_phases, nvfp4_qk_norm_rope, nvfp4_cache_empty, nvfp4_cache_write,
+  nvfp4_cache_read, nvfp4_cache_attention: positions, a paged cache of keys and
+  values in NVFP4, and the attention that reads it
 Calls on CUDA tensors stay on their device.  Calls on CPU tensors (the
 host-buffer path) stage their inputs on the current CUDA device and copy the
 results back (into the caller's host tensors when given, else into new pinned
@@ -29,6 +32,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib
+import math
 import os
 import threading
 import warnings
@@ -44,6 +48,7 @@ GAMAX_NONE, GAMAX_TENSOR, GAMAX_ROW, GAMAX_TENSOR_GIVEN, GAMAX_ROW_GIVEN = 0, 1,
 ERR_NONE, ERR_MAE, ERR_MSE = 0, 1, 2
 FMT_NVFP4, FMT_MXFP8 = 0, 1
 X_F32, X_BF16, X_MXFP8 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 OK, EINVAL, ECUDA = 0, 1, 2
 
 _NAMES = {
@@ -54,12 +59,14 @@ _NAMES = {
     "err_mode": {"none": ERR_NONE, "mae": ERR_MAE, "mse": ERR_MSE},
     "dtype": {"f32": F32, "bf16": BF16},
     "format": {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8},
+    "layout": {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED},
 }
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_dequantize", "nvfp4_qdq", "nvfp4_amax",
             "nvfp4_global_scales", "nvfp4_probe_divide", "nvfp4_probe_e2m1", "nvfp4_probe_sub_f16", "nvfp4_last_error",
             "nvfp4_abi_version", "nvfp4_scales_to_mma", "nvfp4_mm", "nvfp4_rmsnorm", "nvfp4_mv", "nvfp4_grouped_mm",
-            "nvfp4_grouped_mm_workspace")
+            "nvfp4_grouped_mm_workspace", "nvfp4_qk_norm_rope", "nvfp4_cache_write", "nvfp4_cache_read",
+            "nvfp4_cache_attention", "nvfp4_cache_attention_workspace")
 
 _lock = threading.Lock()
 _lib = None
@@ -143,6 +150,18 @@ def load_library(path: str | None = None):
         lib.nvfp4_grouped_mm.argtypes = [P, P, P, P, P, i64, i64, i64, i64, i32, P, P, f32, P, i32, P, i64, P]
         lib.nvfp4_grouped_mm_workspace.restype = i64
         lib.nvfp4_grouped_mm_workspace.argtypes = [i64, i64, i64, i64]
+        lib.nvfp4_qk_norm_rope.restype = i32
+        lib.nvfp4_qk_norm_rope.argtypes = [P, P, P, i64, i64, i64, i64, i64, i64, i64, i32, P, P, i32, f32, P, P, i64, i32,
+                                           f32, P, P, P, i64, i64, P, i32, P, i32, P, f32, P]
+        lib.nvfp4_cache_write.restype = i32
+        lib.nvfp4_cache_write.argtypes = [P, P, i64, i64, i64, i64, i64, i32, P, i64, i64, P, i32, P, i32, P, f32, P]
+        lib.nvfp4_cache_read.restype = i32
+        lib.nvfp4_cache_read.argtypes = [P, i64, i64, i64, i64, P, i64, i32, P, i32, P, f32, P, P, i32, P]
+        lib.nvfp4_cache_attention.restype = i32
+        lib.nvfp4_cache_attention.argtypes = [P, i64, i64, i64, i32, P, i64, i64, i64, i64, P, i64, i64, P, P, i32, P, i32,
+                                              P, f32, f32, i32, i64, P, P, i32, P, P, i64, P]
+        lib.nvfp4_cache_attention_workspace.restype = i64
+        lib.nvfp4_cache_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64, i64, i32]
         lib.nvfp4_last_error.restype = ctypes.c_char_p
         lib.nvfp4_last_error.argtypes = []
         lib.nvfp4_abi_version.restype = i32
@@ -1114,6 +1133,261 @@ def nvfp4_grouped_mm(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: tor
             scales_b.data_ptr(), E, T, N, K, gm, _addr(ga), _addr(gamax_b), scale_bound, o.data_ptr(), odt, _addr(ws),
             need)
     return o
+
+
+# ---- a cache of keys and values ---------------------------------------------------------------
+# Serving operators as well: device tensors, a given stream, no gradient.
+def nvfp4_rope_phases(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0, method: str = "linear",
+                      original: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None,
+                      device=None) -> torch.Tensor:
+    """The turns a position of each pair of a rotation, in 2^-64 (int64 [rotary_dim / 2]), for nvfp4_qk_norm_rope:
+    base^(-2 i / rotary_dim) / (2 pi), or inv_freq / (2 pi) where angles a position are given.
+
+    A context `factor` times as long: "linear" divides every frequency by it; "ntk" raises the base so
+    that the slowest pair is divided by it and the fastest stays; "yarn" divides the pairs that turn fewer than
+    beta_slow times in `original` positions, leaves those that turn more than beta_fast times, and goes from one to the
+    other along the pairs in between (its magnitude, 0.1 ln(factor) + 1, is the caller's to pass).  Made once for a
+    model, in 64 bits."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("nvfp4_rope_phases: rotary_dim must be even and positive")
+    if not factor >= 1.0 or not math.isfinite(factor):
+        raise ValueError("nvfp4_rope_phases: factor must be at least 1")
+    half = rotary_dim // 2
+    if inv_freq is not None:
+        freq = [float(f) for f in inv_freq]
+        if len(freq) != half:
+            raise ValueError(f"nvfp4_rope_phases: inv_freq must hold {half} values")
+    elif not base > 0.0:
+        raise ValueError("nvfp4_rope_phases: base must be positive")
+    else:
+        if method == "ntk" and half > 1:
+            base = base * factor ** (half / (half - 1))
+        freq = [base ** (-2 * i / rotary_dim) for i in range(half)]
+    if method == "linear":
+        freq = [f / factor for f in freq]
+    elif method == "yarn":
+        if not original or original <= 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("nvfp4_rope_phases: yarn needs original > 0 and beta_fast > beta_slow > 0")
+
+        def pair(turns):                        # the pair that makes so many turns in `original` positions
+            return half * math.log(original / (turns * 2 * math.pi)) / math.log(base)
+
+        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rotary_dim - 1)
+        keep = [1.0 - min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(half)]
+        freq = [f * k + f / factor * (1.0 - k) for f, k in zip(freq, keep)]
+    elif method != "ntk":
+        raise ValueError(f"nvfp4_rope_phases: method {method!r}; expected linear, ntk or yarn")
+    if not all(math.isfinite(f) for f in freq):
+        raise ValueError("nvfp4_rope_phases: frequencies must be finite")
+    turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) % (1 << 64) for f in freq]
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def nvfp4_cache_empty(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A cache of `pages` pages of page_size tokens: zeros, uint8 [pages, kv_heads, page_size / 16, 18 * head_dim]
+    (see nvfp4.h).  page_size a multiple of 16, head_dim 64, 128 or 256."""
+    if min(pages, page_size - 1, kv_heads) < 0 or page_size % 16 or head_dim not in (64, 128, 256):
+        raise ValueError("nvfp4_cache_empty: page_size must be a multiple of 16, head_dim 64, 128 or 256")
+    return torch.zeros((pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8,
+                       device=torch.device("cuda") if device is None else device)
+
+
+def _cache_sizes(cache, call):
+    """(device, pages, page_size, kv_heads, head_dim) of a cache tensor."""
+    if not torch.is_tensor(cache) or not cache.is_cuda or cache.dim() != 4 or cache.dtype != torch.uint8:
+        raise ValueError(f"{call}: cache must be a CUDA uint8 [pages, Hkv, page_size / 16, 18 * D] tensor")
+    if not cache.is_contiguous() or cache.shape[3] % 18:
+        raise ValueError(f"{call}: cache must be contiguous, of 18 * D bytes a tile")
+    return cache.device, cache.shape[0], cache.shape[2] * 16, cache.shape[1], cache.shape[3] // 18
+
+
+def _heads(t, name, call, dev=None, shape=None, dtype=None):
+    """(tensor, token stride) of [T, H, D] heads: contiguous within a token, tokens apart by whole 16 bytes, as
+    slices of one [T, H', D] product are; a copy of anything else."""
+    if not torch.is_tensor(t) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{call}: {name} must be a CUDA [T, heads, D] tensor")
+    _x_dtype(t)
+    if (dev is not None and t.device != dev) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{call}: {name} must be {dtype} on {dev} (got {t.dtype} on {t.device})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{call}: {name} must be {list(shape)} (got {list(t.shape)})")
+    T, H, D = t.shape
+    size = t.element_size()
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D) or (T > 1 and s[0] * size % 16) or t.data_ptr() % 16:
+        t = t.contiguous()
+        if t.data_ptr() % 16:
+            t = t.clone()
+    return t, t.stride(0) if T > 1 else H * D
+
+
+def _int_vector(t, name, n, dev, call):
+    if not torch.is_tensor(t):
+        raise ValueError(f"{call}: {name} must be an int64 CUDA tensor")
+    return _check_dev(t.contiguous(), name, torch.int64, n, dev)
+
+
+def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, phases, *, q_weight=None, k_weight=None,
+                       eps: float = 1e-6, layout="half", magnitude: float = 1.0, q_out=None, k_out=None, cache=None,
+                       v=None, slots=None, k_gamax=None, v_gamax=None, scale_bound: float = 448.0, stream=None) -> dict:
+    """Norms of queries and keys for each head (with weights [D]) and their rotation by position, in one pass
+    (see nvfp4.h): dict(q, k).
+
+    q [T, Hq, D], k [T, Hkv, D]: float32 or bfloat16 alike, slices of one product as they are.  positions:
+    int64 [T]; phases: nvfp4_rope_phases' [rotary_dim / 2] (both None: no rotation); layout "half" or
+    "interleaved".  With a cache, k and v [T, Hkv, D] are quantized into its slots [T] instead, and the
+    dict has q alone."""
+    lib = _lib or load_library()
+    call = "nvfp4_qk_norm_rope"
+    if not torch.is_tensor(q) or not q.is_cuda:
+        raise ValueError(f"{call}: q must be a CUDA [T, heads, D] tensor")
+    dev = q.device
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_qk_norm_rope(q, k, positions, phases, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                      layout=layout, magnitude=magnitude, q_out=q_out, k_out=k_out, cache=cache, v=v,
+                                      slots=slots, k_gamax=k_gamax, v_gamax=v_gamax, scale_bound=scale_bound)
+    q, qs = _heads(q, "q", call)
+    T, Hq, D = q.shape
+    k, ks = _heads(k, "k", call, dev, dtype=q.dtype)
+    Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"{call}: k must be [{T}, Hkv, {D}] (got {list(k.shape)})")
+    wdt = _x_dtype(q)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError(f"{call}: give both q_weight and k_weight, or neither")
+    if q_weight is not None:
+        wdt = _x_dtype(q_weight)
+        q_weight = _check_dev(q_weight.contiguous(), "q_weight", q_weight.dtype, D, dev)
+        k_weight = _check_dev(k_weight.contiguous(), "k_weight", q_weight.dtype, D, dev)
+    rot = 0
+    if (positions is None) != (phases is None):
+        raise ValueError(f"{call}: positions and phases go together")
+    if positions is not None:
+        positions = _int_vector(positions, "positions", T, dev, call)
+        rot = 2 * phases.numel()
+        phases = _int_vector(phases, "phases", rot // 2, dev, call)
+    if (cache is None) != (v is None) or (cache is None) != (slots is None):
+        raise ValueError(f"{call}: cache, v and slots go together")
+    pages, P, vs, km, vm, kg, vg = 0, 16, 0, GAMAX_NONE, GAMAX_NONE, None, None
+    res = {"q": torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else
+           _check_dev(q_out, "q_out", q.dtype, T * Hq * D, dev)}
+    if cache is None:
+        if k_gamax is not None or v_gamax is not None:
+            raise ValueError(f"{call}: k_gamax and v_gamax go with a cache")
+        res["k"] = torch.empty((T, Hkv, D), dtype=q.dtype, device=dev) if k_out is None else \
+            _check_dev(k_out, "k_out", q.dtype, T * Hkv * D, dev)
+    else:
+        if k_out is not None:
+            raise ValueError(f"{call}: k_out goes without a cache")
+        cdev, pages, P, H, cD = _cache_sizes(cache, call)
+        if cdev != dev or H != Hkv or cD != D:
+            raise ValueError(f"{call}: the cache must be on {dev} with {Hkv} heads of {D}")
+        v, vs = _heads(v, "v", call, dev, k.shape, q.dtype)
+        slots = _int_vector(slots, "slots", T, dev, call)
+        km, kg = _rows_gamax(k_gamax, Hkv, dev, "k_gamax")
+        vm, vg = _rows_gamax(v_gamax, Hkv, dev, "v_gamax")
+    _launch(lib, lib.nvfp4_qk_norm_rope, dev, q.data_ptr(), k.data_ptr(), _addr(v), T, Hq, Hkv, D, qs, ks, vs,
+            _x_dtype(q), _addr(q_weight), _addr(k_weight), wdt, eps, _addr(positions), _addr(phases), rot,
+            _enum("layout", layout), magnitude, res["q"].data_ptr(), _addr(res.get("k")), _addr(cache), pages, P,
+            _addr(slots), km, _addr(kg), vm, _addr(vg), scale_bound)
+    return res
+
+
+def nvfp4_cache_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *, k_gamax=None,
+                      v_gamax=None, scale_bound: float = 448.0, stream=None) -> None:
+    """Keys and values [T, Hkv, D] (float32 or bfloat16) quantized into slots [T] of a cache, in place, as
+    nvfp4_quantize does (see nvfp4.h).  slots: int64, page * page_size + token of the page, distinct; one
+    outside the cache (-1) is not written.  k_gamax, v_gamax: None, one amax or one a KV head, the same
+    for every call on a cache."""
+    lib = _lib or load_library()
+    call = "nvfp4_cache_write"
+    dev, pages, P, Hkv, D = _cache_sizes(cache, call)
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_cache_write(cache, k, v, slots, k_gamax=k_gamax, v_gamax=v_gamax, scale_bound=scale_bound)
+    k, ks = _heads(k, "k", call, dev)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, Hkv, D):
+        raise ValueError(f"{call}: k must be [T, {Hkv}, {D}] (got {list(k.shape)})")
+    v, vs = _heads(v, "v", call, dev, k.shape, k.dtype)
+    slots = _int_vector(slots, "slots", T, dev, call)
+    km, kg = _rows_gamax(k_gamax, Hkv, dev, "k_gamax")
+    vm, vg = _rows_gamax(v_gamax, Hkv, dev, "v_gamax")
+    _launch(lib, lib.nvfp4_cache_write, dev, k.data_ptr(), v.data_ptr(), T, Hkv, D, ks, vs, _x_dtype(k), cache.data_ptr(),
+            pages, P, slots.data_ptr(), km, _addr(kg), vm, _addr(vg), scale_bound)
+
+
+def nvfp4_cache_read(cache: torch.Tensor, slots: torch.Tensor, *, k_gamax=None, v_gamax=None,
+                     scale_bound: float = 448.0, out_dtype="bf16", stream=None) -> tuple:
+    """(keys, values) [T, Hkv, D] that slots [T] of a cache hold; zeros for a slot outside it."""
+    lib = _lib or load_library()
+    call = "nvfp4_cache_read"
+    dev, pages, P, Hkv, D = _cache_sizes(cache, call)
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_cache_read(cache, slots, k_gamax=k_gamax, v_gamax=v_gamax, scale_bound=scale_bound,
+                                    out_dtype=out_dtype)
+    if not torch.is_tensor(slots):
+        raise ValueError(f"{call}: slots must be an int64 CUDA tensor")
+    T = slots.numel()
+    slots = _int_vector(slots, "slots", T, dev, call)
+    km, kg = _rows_gamax(k_gamax, Hkv, dev, "k_gamax")
+    vm, vg = _rows_gamax(v_gamax, Hkv, dev, "v_gamax")
+    odt = _enum("dtype", out_dtype)
+    tdt = torch.float32 if odt == F32 else torch.bfloat16
+    k, v = (torch.empty((T, Hkv, D), dtype=tdt, device=dev) for _ in range(2))
+    _launch(lib, lib.nvfp4_cache_read, dev, cache.data_ptr(), pages, P, Hkv, D, slots.data_ptr(), T, km, _addr(kg), vm,
+            _addr(vg), scale_bound, k.data_ptr(), v.data_ptr(), odt)
+    return k, v
+
+
+def nvfp4_cache_attention(q: torch.Tensor, cache: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor, *,
+                          offsets=None, k_gamax=None, v_gamax=None, scale_bound: float = 448.0, scale=None,
+                          causal: bool = True, window: int = 0, sinks=None, out_dtype="bf16", out=None,
+                          want_lse: bool = False, stream=None):
+    """Attention of queries over the sequences a cache holds (see nvfp4.h).
+
+    q [T, Hq, D] float32 or bfloat16; pages int32 [B, width]: the pages of each sequence; lengths int64 [B]: its
+    keys, its queries' own among them; offsets int64 [B+1]: queries offsets[b] .. offsets[b+1] are
+    sequence b's, the last at its last key (None: one query a sequence).  causal: a query sees no key
+    after its own; window > 0: none but the last `window` up to its own; sinks fp32 [Hq]: a logit a head that
+    takes weight and gives none; scale: 1 / sqrt(D) unless given.  Nothing is read on the host.  Returns out
+    [T, Hq, D], with want_lse (out, lse fp32 [T, Hq]); a query that sees nothing gives 0, rows of no
+    sequence are not written."""
+    lib = _lib or load_library()
+    call = "nvfp4_cache_attention"
+    dev, n_pages, P, Hkv, D = _cache_sizes(cache, call)
+    if stream is not None:
+        with _given_stream(stream, dev):
+            return nvfp4_cache_attention(q, cache, pages, lengths, offsets=offsets, k_gamax=k_gamax, v_gamax=v_gamax,
+                                         scale_bound=scale_bound, scale=scale, causal=causal, window=window, sinks=sinks,
+                                         out_dtype=out_dtype, out=out, want_lse=want_lse)
+    q, qs = _heads(q, "q", call, dev)
+    T, Hq = q.shape[0], q.shape[1]
+    if q.shape[2] != D:
+        raise ValueError(f"{call}: q must be [T, Hq, {D}] (got {list(q.shape)})")
+    if not torch.is_tensor(pages) or pages.dim() != 2:
+        raise ValueError(f"{call}: pages must be an int32 CUDA [B, width] tensor")
+    B, width = pages.shape
+    pages = _check_dev(pages.contiguous(), "pages", torch.int32, B * width, dev)
+    lengths = _int_vector(lengths, "lengths", B, dev, call)
+    if offsets is not None:
+        offsets = _int_vector(offsets, "offsets", B + 1, dev, call)
+    if sinks is not None:
+        sinks = _check_dev(sinks.contiguous(), "sinks", torch.float32, Hq, dev)
+    km, kg = _rows_gamax(k_gamax, Hkv, dev, "k_gamax")
+    vm, vg = _rows_gamax(v_gamax, Hkv, dev, "v_gamax")
+    dt, odt = _x_dtype(q), _enum("dtype", out_dtype)
+    tdt = torch.float32 if odt == F32 else torch.bfloat16
+    o = torch.empty((T, Hq, D), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, T * Hq * D, dev)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    need = lib.nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, P, dt)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _launch(lib, lib.nvfp4_cache_attention, dev, q.data_ptr(), T, Hq, qs, dt, cache.data_ptr(), n_pages, P, Hkv, D,
+            pages.data_ptr(), B, width, lengths.data_ptr(), _addr(offsets), km, _addr(kg), vm, _addr(vg), scale_bound,
+            D ** -0.5 if scale is None else scale, int(causal), window, _addr(sinks), o.data_ptr(), odt, _addr(lse), _addr(ws), need)
+    return (o, lse) if want_lse else o
 
 
 def nvfp4_global_scales(gamax: torch.Tensor, scale_bound: float = 448.0, stream=None):

@@ -433,6 +433,260 @@ int nvfp4_grouped_mm(const uint8_t* codes_a, const uint8_t* scales_a, const int6
     return NVFP4_OK;
 }
 
+// the sizes and scales of a cache (its pointer is checked by the call); *n: its bytes
+static int check_cache(int64_t pages, int64_t page_size, int64_t Hkv, int64_t D, int64_t T, int k_mode,
+                       const float* k_gamax, int v_mode, const float* v_gamax, float scale_bound, uint64_t* n) {
+    constexpr int64_t kMax = int64_t{1} << 30, kHeads = 1 << 15;
+    if (pages < 0 || T < 0 || Hkv < 0) return fail(NVFP4_EINVAL, "pages, T and Hkv must be >= 0");
+    if (pages >= kMax || T >= kMax || Hkv >= kHeads) return fail(NVFP4_EINVAL, "pages and T must be below 2^30, Hkv below 2^15");
+    if (D != 64 && D != 128 && D != 256) return fail(NVFP4_EINVAL, "a cache's D must be 64, 128 or 256 (got %lld)", (long long)D);
+    if (page_size <= 0 || page_size % 16 || page_size >= kMax)
+        return fail(NVFP4_EINVAL, "page_size must be a multiple of 16 (got %lld)", (long long)page_size);
+    // pages * Hkv * page_size * D below 2^62
+    if (pages > 0 && Hkv > 0 && page_size > (int64_t{1} << 62) / pages / Hkv / D) return fail(NVFP4_EINVAL, "the cache is too large");
+    for (const int m : {k_mode, v_mode})
+        if (m != NVFP4_GAMAX_NONE && m != NVFP4_GAMAX_TENSOR_GIVEN && m != NVFP4_GAMAX_ROW_GIVEN)
+            return fail(NVFP4_EINVAL, "k_mode and v_mode must be NONE, TENSOR_GIVEN or ROW_GIVEN (got %d)", m);
+    if (!(scale_bound > 0.0f && scale_bound <= 448.0f)) return fail(NVFP4_EINVAL, "scale_bound must be in (0, 448]");
+    int rc;
+    if ((rc = check_ptr(k_gamax, "k_gamax", k_mode != NVFP4_GAMAX_NONE, 4))) return rc;
+    if ((rc = check_ptr(v_gamax, "v_gamax", v_mode != NVFP4_GAMAX_NONE, 4))) return rc;
+    *n = static_cast<uint64_t>(pages) * static_cast<uint64_t>(Hkv) * static_cast<uint64_t>(page_size / 16) * static_cast<uint64_t>(18 * D);
+    return NVFP4_OK;
+}
+
+static uint64_t gamax_bytes(int mode, int64_t Hkv) {
+    return mode == NVFP4_GAMAX_NONE ? 0 : mode == NVFP4_GAMAX_TENSOR_GIVEN ? 4 : static_cast<uint64_t>(Hkv) * 4;
+}
+
+// a token's heads are contiguous, tokens `stride` elements apart: whole 16 bytes
+static int check_stride(int64_t stride, int size, const char* name) {
+    if (stride < 0 || stride >= int64_t{1} << 32 || stride * size % 16)
+        return fail(NVFP4_EINVAL, "%s must be >= 0, below 2^32 and of whole 16 bytes (got %lld elements)", name, (long long)stride);
+    return NVFP4_OK;
+}
+
+static uint64_t strided_bytes(int64_t T, int64_t stride, int64_t H, int64_t D, int size) {
+    return T == 0 || H == 0 ? 0 : (static_cast<uint64_t>(T - 1) * static_cast<uint64_t>(stride) + static_cast<uint64_t>(H) * static_cast<uint64_t>(D)) * size;
+}
+
+static int run_heads(const nvfp4::HeadsArgs& a, uint64_t cache_bytes, cudaStream_t stream) {
+    const int size = a.dtype == NVFP4_F32 ? 4 : 2;
+    int rc;
+    const uint64_t t = a.T, row = static_cast<uint64_t>(a.D) * size;
+    const Buffer outs[] = {{a.q_out, t * a.Hq * row, "q_out"}, {a.k_out, t * a.Hkv * row, "k_out"}, {a.cache.data, cache_bytes, "cache"}};
+    const uint64_t w = static_cast<uint64_t>(a.D) * (a.weight_dtype == NVFP4_F32 ? 4 : 2);
+    const Buffer ins[] = {{a.q, strided_bytes(a.T, a.q_stride, a.Hq, a.D, size), "q"},
+                          {a.k, strided_bytes(a.T, a.k_stride, a.Hkv, a.D, size), "k"},
+                          {a.v, strided_bytes(a.T, a.v_stride, a.Hkv, a.D, size), "v"},
+                          {a.q_weight, w, "q_weight"},
+                          {a.k_weight, w, "k_weight"},
+                          {a.positions, t * 8, "positions"},
+                          {a.phases, static_cast<uint64_t>(a.rotary_dim) * 4, "phases"},
+                          {a.slots, t * 8, "slots"},
+                          {a.cache.k_gamax, gamax_bytes(a.cache.k_mode, a.Hkv), "k_gamax"},
+                          {a.cache.v_gamax, gamax_bytes(a.cache.v_mode, a.Hkv), "v_gamax"}};
+    if ((rc = check_apart(outs, ins))) return rc;
+    const int err = nvfp4::launch_heads(a, stream);
+    return err ? cuda_fail(err, "heads launch") : NVFP4_OK;
+}
+
+int nvfp4_qk_norm_rope(const void* q, const void* k, const void* v, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int dtype, const void* q_weight,
+                       const void* k_weight, int weight_dtype, float eps, const int64_t* positions,
+                       const uint64_t* phases, int64_t rotary_dim, int layout, float magnitude, void* q_out, void* k_out,
+                       uint8_t* cache, int64_t pages, int64_t page_size, const int64_t* slots, int k_mode,
+                       const float* k_gamax, int v_mode, const float* v_gamax, float scale_bound, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    constexpr int64_t kMax = int64_t{1} << 30, kHeads = 1 << 15;
+    const bool cached = slots != nullptr;
+    int rc;
+    uint64_t bytes = 0;
+    if (T < 0 || Hq < 0 || Hkv < 0 || T >= kMax || Hq >= kHeads || Hkv >= kHeads)
+        return fail(NVFP4_EINVAL, "T must be in [0, 2^30), Hq and Hkv in [0, 2^15)");
+    if (D <= 0 || D % 16 || D > 512) return fail(NVFP4_EINVAL, "D must be a multiple of 16 up to 512 (got %lld)", (long long)D);
+    if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad dtype %d", dtype);
+    if (weight_dtype != NVFP4_F32 && weight_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad weight_dtype %d", weight_dtype);
+    if (!(eps >= 0.0f && eps <= 3.4028234663852886e+38f)) return fail(NVFP4_EINVAL, "eps must be >= 0 and finite");
+    if (!(magnitude >= -3.4028234663852886e+38f && magnitude <= 3.4028234663852886e+38f))
+        return fail(NVFP4_EINVAL, "magnitude must be finite");
+    if (layout != NVFP4_ROPE_HALF && layout != NVFP4_ROPE_INTERLEAVED) return fail(NVFP4_EINVAL, "bad layout %d", layout);
+    if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16)
+        return fail(NVFP4_EINVAL, "rotary_dim must be a multiple of 16 up to D (got %lld)", (long long)rotary_dim);
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return fail(NVFP4_EINVAL, "give both q_weight and k_weight, or neither");
+    if (cached != (cache != nullptr) || cached != (v != nullptr) || cached == (k_out != nullptr)) {
+        if (T > 0 && Hkv > 0) return fail(NVFP4_EINVAL, "give v, cache and slots and no k_out, or k_out and none of them");
+    }
+    if (cached) {
+        if (layout == NVFP4_ROPE_HALF && rotary_dim % 32)
+            return fail(NVFP4_EINVAL, "with a cache and halves apart rotary_dim must be a multiple of 32 (got %lld)", (long long)rotary_dim);
+        if ((rc = check_cache(pages, page_size, Hkv, D, T, k_mode, k_gamax, v_mode, v_gamax, scale_bound, &bytes))) return rc;
+    }
+    const int size = dtype == NVFP4_F32 ? 4 : 2;
+    if ((rc = check_stride(q_stride, size, "q_stride"))) return rc;
+    if ((rc = check_stride(k_stride, size, "k_stride"))) return rc;
+    if ((rc = check_stride(v_stride, size, "v_stride"))) return rc;
+    const bool turned = rotary_dim > 0 && T > 0;
+    if ((rc = check_ptr(q, "q", T > 0 && Hq > 0))) return rc;
+    if ((rc = check_ptr(k, "k", T > 0 && Hkv > 0))) return rc;
+    if ((rc = check_ptr(v, "v", false))) return rc;
+    if ((rc = check_ptr(q_weight, "q_weight", false))) return rc;
+    if ((rc = check_ptr(k_weight, "k_weight", false))) return rc;
+    if ((rc = check_ptr(positions, "positions", turned, 8))) return rc;
+    if ((rc = check_ptr(phases, "phases", turned, 8))) return rc;
+    if ((rc = check_ptr(q_out, "q_out", T > 0 && Hq > 0))) return rc;
+    if ((rc = check_ptr(k_out, "k_out", false))) return rc;
+    if ((rc = check_ptr(cache, "cache", false))) return rc;
+    if ((rc = check_ptr(slots, "slots", false, 8))) return rc;
+    if (T == 0 || Hq + Hkv == 0) return NVFP4_OK;
+    nvfp4::HeadsArgs a = {};
+    a.q = Hq > 0 ? q : nullptr, a.k = Hkv > 0 ? k : nullptr, a.v = Hkv > 0 && cached ? v : nullptr;
+    a.T = T, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv), a.D = static_cast<int>(D), a.dtype = dtype;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.weight_dtype = weight_dtype, a.eps = eps;
+    a.rotary_dim = static_cast<int>(rotary_dim), a.layout = layout, a.magnitude = magnitude;
+    if (turned) a.positions = positions, a.phases = phases;
+    a.q_out = q_out, a.k_out = cached ? nullptr : k_out, a.slots = slots;
+    if (cached)
+        a.cache = {cache, pages, static_cast<int>(page_size), a.Hkv, a.D, k_mode, v_mode, k_gamax, v_gamax, scale_bound};
+    return run_heads(a, bytes, stream);
+}
+
+int nvfp4_cache_write(const void* k, const void* v, int64_t T, int64_t Hkv, int64_t D, int64_t k_stride,
+                      int64_t v_stride, int dtype, uint8_t* cache, int64_t pages, int64_t page_size,
+                      const int64_t* slots, int k_mode, const float* k_gamax, int v_mode, const float* v_gamax,
+                      float scale_bound, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    uint64_t bytes = 0;
+    int rc = check_cache(pages, page_size, Hkv, D, T, k_mode, k_gamax, v_mode, v_gamax, scale_bound, &bytes);
+    if (rc) return rc;
+    if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad dtype %d", dtype);
+    const int size = dtype == NVFP4_F32 ? 4 : 2;
+    if ((rc = check_stride(k_stride, size, "k_stride"))) return rc;
+    if ((rc = check_stride(v_stride, size, "v_stride"))) return rc;
+    const bool any = T > 0 && Hkv > 0;
+    if ((rc = check_ptr(k, "k", any))) return rc;
+    if ((rc = check_ptr(v, "v", any))) return rc;
+    if ((rc = check_ptr(slots, "slots", any, 8))) return rc;
+    if ((rc = check_ptr(cache, "cache", any && pages > 0))) return rc;
+    if (!any || pages == 0) return NVFP4_OK;
+    nvfp4::HeadsArgs a = {};
+    a.k = k, a.v = v, a.T = T, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.Hkv = static_cast<int>(Hkv), a.D = static_cast<int>(D), a.dtype = dtype, a.weight_dtype = dtype;
+    a.slots = slots;
+    a.cache = {cache, pages, static_cast<int>(page_size), a.Hkv, a.D, k_mode, v_mode, k_gamax, v_gamax, scale_bound};
+    return run_heads(a, bytes, stream);
+}
+
+int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t Hkv, int64_t D,
+                     const int64_t* slots, int64_t T, int k_mode, const float* k_gamax, int v_mode,
+                     const float* v_gamax, float scale_bound, void* k, void* v, int out_dtype, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    uint64_t bytes = 0;
+    int rc = check_cache(pages, page_size, Hkv, D, T, k_mode, k_gamax, v_mode, v_gamax, scale_bound, &bytes);
+    if (rc) return rc;
+    if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
+    const bool any = T > 0 && Hkv > 0;
+    if ((rc = check_ptr(cache, "cache", any && pages > 0))) return rc;
+    if ((rc = check_ptr(slots, "slots", any, 8))) return rc;
+    if ((rc = check_ptr(k, "k", any && !v))) return rc;
+    if ((rc = check_ptr(v, "v", false))) return rc;
+    if (!any) return NVFP4_OK;
+    const uint64_t out = static_cast<uint64_t>(T) * Hkv * D * (out_dtype == NVFP4_F32 ? 4 : 2);
+    const Buffer outs[] = {{k, out, "k"}, {v, out, "v"}};
+    const Buffer ins[] = {{cache, bytes, "cache"},
+                          {slots, static_cast<uint64_t>(T) * 8, "slots"},
+                          {k_gamax, gamax_bytes(k_mode, Hkv), "k_gamax"},
+                          {v_gamax, gamax_bytes(v_mode, Hkv), "v_gamax"}};
+    if ((rc = check_apart(outs, ins))) return rc;
+    nvfp4::CacheReadArgs a = {};
+    a.cache = {const_cast<uint8_t*>(cache), pages, static_cast<int>(page_size), static_cast<int>(Hkv), static_cast<int>(D),
+               k_mode, v_mode, k_gamax, v_gamax, scale_bound};
+    a.slots = slots, a.T = T, a.k = k, a.v = v, a.out_dtype = out_dtype;
+    const int err = nvfp4::launch_cache_read(a, stream);
+    return err ? cuda_fail(err, "cache read launch") : NVFP4_OK;
+}
+
+// the sizes that fix an attention's kernels and workspace; false where there is nothing to do or they are out of range
+static bool attend_sizes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width, int64_t page_size,
+                         int dtype, nvfp4::AttendArgs* a) {
+    constexpr int64_t kMax = int64_t{1} << 30, kHeads = 1 << 15;
+    if (T <= 0 || Hq <= 0 || Hkv <= 0 || B <= 0 || T >= kMax || Hq >= kHeads || Hkv >= kHeads || B >= kMax || Hq % Hkv ||
+        (D != 64 && D != 128 && D != 256) || width < 0 || page_size <= 0 || page_size % 16 || page_size >= kMax ||
+        width >= kMax / page_size)
+        return false;
+    a->T = T, a->Hq = static_cast<int>(Hq), a->B = B, a->width = width, a->dtype = dtype;
+    a->cache.Hkv = static_cast<int>(Hkv), a->cache.D = static_cast<int>(D), a->cache.page_size = static_cast<int>(page_size);
+    return true;
+}
+
+int64_t nvfp4_cache_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width,
+                                        int64_t page_size, int dtype) {
+    nvfp4::AttendArgs a = {};
+    return attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, &a) ? nvfp4::attend_workspace(a) : 0;
+}
+
+int nvfp4_cache_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride, int dtype, const uint8_t* cache,
+                          int64_t pages, int64_t page_size, int64_t Hkv, int64_t D, const int32_t* page_table,
+                          int64_t B, int64_t width, const int64_t* lengths, const int64_t* offsets, int k_mode,
+                          const float* k_gamax, int v_mode, const float* v_gamax, float scale_bound, float scale,
+                          int causal, int64_t window, const float* sinks, void* out, int out_dtype, float* lse,
+                          uint8_t* workspace, int64_t workspace_bytes, cudaStream_t stream) {
+    g_msg[0] = '\0';
+    constexpr int64_t kMax = int64_t{1} << 30, kHeads = 1 << 15;
+    uint64_t bytes = 0;
+    int rc = check_cache(pages, page_size, Hkv, D, T, k_mode, k_gamax, v_mode, v_gamax, scale_bound, &bytes);
+    if (rc) return rc;
+    if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad dtype %d", dtype);
+    if (out_dtype != NVFP4_F32 && out_dtype != NVFP4_BF16) return fail(NVFP4_EINVAL, "bad out_dtype %d", out_dtype);
+    if (Hq < 0 || Hq >= kHeads) return fail(NVFP4_EINVAL, "Hq must be in [0, 2^15)");
+    if (Hkv == 0 ? Hq != 0 : Hq % Hkv) return fail(NVFP4_EINVAL, "Hq must be a multiple of Hkv");
+    if (B < 0 || B >= kMax) return fail(NVFP4_EINVAL, "B must be in [0, 2^30)");
+    if (width < 0 || width >= kMax / page_size) return fail(NVFP4_EINVAL, "width * page_size must be in [0, 2^30)");
+    if (T * (Hkv > 0 ? Hq / Hkv : 0) >= kMax) return fail(NVFP4_EINVAL, "T * Hq / Hkv must be below 2^30");
+    if (!offsets && T != B) return fail(NVFP4_EINVAL, "without offsets a sequence has one query: T must be B");
+    if (causal != 0 && causal != 1) return fail(NVFP4_EINVAL, "causal must be 0 or 1 (got %d)", causal);
+    if (window < 0) return fail(NVFP4_EINVAL, "window must be >= 0");
+    if (!(scale >= -3.4028234663852886e+38f && scale <= 3.4028234663852886e+38f)) return fail(NVFP4_EINVAL, "scale must be finite");
+    if ((rc = check_stride(q_stride, dtype == NVFP4_F32 ? 4 : 2, "q_stride"))) return rc;
+    const bool any = T > 0 && Hq > 0 && B > 0;
+    const bool keys = any && width > 0 && pages > 0;
+    if ((rc = check_ptr(q, "q", any))) return rc;
+    if ((rc = check_ptr(cache, "cache", keys))) return rc;
+    if ((rc = check_ptr(page_table, "page_table", any && width > 0, 4))) return rc;
+    if ((rc = check_ptr(lengths, "lengths", any, 8))) return rc;
+    if ((rc = check_ptr(offsets, "offsets", false, 8))) return rc;
+    if ((rc = check_ptr(sinks, "sinks", false, 4))) return rc;
+    if ((rc = check_ptr(out, "out", any))) return rc;
+    if ((rc = check_ptr(lse, "lse", false, 4))) return rc;
+    nvfp4::AttendArgs a = {};
+    if (!any || !attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, &a)) return NVFP4_OK;
+    const int64_t need = nvfp4::attend_workspace(a);
+    if (workspace_bytes < need)
+        return fail(NVFP4_EINVAL, "the workspace needs %lld bytes (got %lld)", (long long)need, (long long)workspace_bytes);
+    if ((rc = check_ptr(workspace, "workspace", need > 0))) return rc;
+    const uint64_t heads = static_cast<uint64_t>(T) * static_cast<uint64_t>(Hq);
+    const Buffer outs[] = {{out, heads * D * (out_dtype == NVFP4_F32 ? 4 : 2), "out"},
+                           {lse, heads * 4, "lse"},
+                           {workspace, static_cast<uint64_t>(need), "workspace"}};
+    const Buffer ins[] = {{q, strided_bytes(T, q_stride, Hq, D, dtype == NVFP4_F32 ? 4 : 2), "q"},
+                          {cache, bytes, "cache"},
+                          {page_table, static_cast<uint64_t>(B) * static_cast<uint64_t>(width) * 4, "page_table"},
+                          {lengths, static_cast<uint64_t>(B) * 8, "lengths"},
+                          {offsets, static_cast<uint64_t>(B + 1) * 8, "offsets"},
+                          {k_gamax, gamax_bytes(k_mode, Hkv), "k_gamax"},
+                          {v_gamax, gamax_bytes(v_mode, Hkv), "v_gamax"},
+                          {sinks, static_cast<uint64_t>(Hq) * 4, "sinks"}};
+    if ((rc = check_apart(outs, ins))) return rc;
+    a.q = q, a.q_stride = q_stride;
+    a.cache = {const_cast<uint8_t*>(cache), cache ? pages : 0, a.cache.page_size, a.cache.Hkv, a.cache.D, k_mode, v_mode, k_gamax, v_gamax, scale_bound};
+    a.pages = page_table, a.lengths = lengths, a.offsets = offsets, a.scale = scale, a.causal = causal;
+    a.window = static_cast<int>(window < kMax ? window : kMax), a.sinks = sinks;
+    a.out = out, a.out_dtype = out_dtype, a.lse = lse, a.workspace = workspace;
+    const int err = nvfp4::launch_attend(a, stream);
+    return err ? cuda_fail(err, "attention launch") : NVFP4_OK;
+}
+
 int nvfp4_probe_divide(const float* a, const float* b, float* out, int64_t n, cudaStream_t stream) {
     g_msg[0] = '\0';
     if (n < 0) return fail(NVFP4_EINVAL, "n must be >= 0");

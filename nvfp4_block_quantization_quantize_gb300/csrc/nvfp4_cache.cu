@@ -1,0 +1,299 @@
+// nvfp4_cache.cu -- the heads of new tokens on their way to attention: norms of
+// queries and keys, their rotation, and keys and values quantized into a paged NVFP4
+// cache (nvfp4_qk_norm_rope, nvfp4_cache_write), and the cache read back
+// (nvfp4_cache_read).
+//
+// Per head of D elements, fp32: y = x * rsqrt(mean(x^2) + eps) * w, then pairs (a, b) of
+// its first rotary_dim elements turn to m (a cos t - b sin t, b cos t + a sin t), t = 2 pi *
+// position * phase / 2^64.  The phase is a whole number of 2^-64 turns, so position * phase wraps
+// exactly where whole turns drop out: a far position loses nothing (the angle's error is the
+// phase's rounding times the position, 2^-64 turns each).  The turn left is rounded to 2^-32.
+// Each element is read once and written once, ten to twenty operations each:
+// bound by memory, by latency for a few tokens.
+//   - A thread holds 16 elements of a head: 8 pairs.  With the pairs' halves apart (half layout) they
+//     are 8 elements of each half, else 16 in a row, so that no pair crosses threads.
+//   - A group of 4 to 32 threads holds a head; a warp takes heads of one token, so that the 8
+//     angles of a thread serve all of them, and loads the next while it works on one.
+//   - A block of 16 to quantize is a thread's own, or (half layout) made by exchanging 8 elements with the
+//     neighbouring thread: the even one quantizes the first half's block, the odd one the second's.
+#include "nvfp4_block.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kHeadsThreads = 256;
+
+// 8 elements from element e, as they are
+template <int DT>
+constexpr int kRaw8 = DT == NVFP4_BF16 ? 4 : 8;
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, int64_t e, uint32_t* w) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + e * (DT == NVFP4_BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < kRaw8<DT> / 4; ++i) {
+        const uint4 u = __ldg(p + i);
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void widen8(const uint32_t* w, float* y) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (DT == NVFP4_BF16) y[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        else y[i] = __uint_as_float(w[i % kRaw8<DT>]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* base, int64_t e, const float* y) {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + e * (DT == NVFP4_BF16 ? 2 : 4));
+    uint32_t w[kRaw8<DT>];
+#pragma unroll
+    for (int i = 0; i < kRaw8<DT>; ++i) {
+        if (DT == NVFP4_BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i % 8], y[(2 * i + 1) % 8]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            w[i] = __float_as_uint(y[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRaw8<DT> / 4; ++i) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+__device__ __forceinline__ void load_weight8(const void* base, int dtype, int e, float* y) {
+    uint32_t w[8];
+    if (dtype == NVFP4_BF16) {
+        load8<NVFP4_BF16>(base, e, w);
+        widen8<NVFP4_BF16>(w, y);
+    } else {
+        load8<NVFP4_F32>(base, e, w);
+        widen8<NVFP4_F32>(w, y);
+    }
+}
+
+// amax of KV head h (1 without a global scale, whose encode and decode scales are 1)
+__device__ __forceinline__ GScale head_scale(int mode, const float* gamax, int h, float bound) {
+    GScale g{0.0f, 1.0f, 1.0f};
+    if (mode != NVFP4_GAMAX_NONE) {
+        g.A = __ldg(gamax + (mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0));
+        global_scales(g.A, bound, g.Senc, g.Sdec);
+    }
+    return g;
+}
+
+// first byte of the tile that slot s of KV head h lies in, or null when there is no such slot
+__device__ __forceinline__ uint8_t* tile_of(const CacheArgs& c, int64_t s, int h) {
+    if (s < 0 || s >= c.pages * c.page_size) return nullptr;
+    const int64_t page = s / c.page_size;
+    const int row = static_cast<int>(s - page * c.page_size);
+    return c.data + ((page * c.Hkv + h) * (c.page_size / 16) + row / 16) * (18 * c.D);
+}
+
+// 16 elements from element e of the row that slot s is, as nvfp4_quantize quantizes them
+__device__ __forceinline__ void quantize_into(uint8_t* part, int row, int D, int e, const GScale& g, const float* y) {
+    const float own = absmax16(y);
+    const uint32_t sf = e4m3_encode(min_nd(block_s6f<true>(own, g.Senc), 448.0f));
+    const float d = mul_rn(e4m3_decode(sf), g.Sdec);
+    uint32_t w0, w1;
+    float none[1];
+    PhiloxKeys keys;                                        // nearest rounding draws nothing
+    encode_plain16<NVFP4_RTN>(y, d, own, 0, keys, w0, w1, nullptr, sf, none, false);
+    *reinterpret_cast<uint2*>(part + row * (D / 2) + e / 2) = make_uint2(w0, w1);
+    part[8 * D + row * (D / 16) + e / 16] = static_cast<uint8_t>(sf);
+}
+
+// L threads a head.  A token's heads (q, k, then v when they go to the cache) are cut into
+// `chunks` of `per` heads, one a warp.
+template <int DT, int L>
+__global__ void __launch_bounds__(kHeadsThreads) k_heads(const HeadsArgs a, int chunks, int per) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, t = lane % L, sub = lane / L;
+    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kHeadsThreads / 32) + (threadIdx.x >> 5);
+    const int64_t token = warp / chunks;
+    if (token >= a.T) return;                               // whole warps
+    const int first = static_cast<int>(warp - token * chunks) * per;
+    const int nq = a.q ? a.Hq : 0, total = nq + (a.k ? a.Hkv : 0) + (a.v ? a.Hkv : 0);
+    const int end = min(first + per, total);
+    const bool live = t < a.D / 16;
+    const bool turned = a.positions && t < a.rotary_dim / 16;
+    const bool apart = turned && a.layout == NVFP4_ROPE_HALF;
+    const int half = a.rotary_dim / 2;
+
+    float cs[8], sn[8];
+    if (turned && first < nq + a.Hkv) {
+        const uint64_t pos = static_cast<uint64_t>(__ldg(a.positions + token));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t turn = pos * __ldg(reinterpret_cast<const unsigned long long*>(a.phases) + 8 * t + i);
+            // the nearest of 2^32 parts of a turn, in [-1/2, 1/2), as half turns
+            const int32_t part = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
+            sincospif(mul_rn(static_cast<float>(part), 4.656612873077393e-10f), &sn[i], &cs[i]);     // 2^-31
+            cs[i] = mul_rn(cs[i], a.magnitude);
+            sn[i] = mul_rn(sn[i], a.magnitude);
+        }
+    }
+    const int64_t slot = a.slots ? __ldg(a.slots + token) : -1;
+    const int row = static_cast<int>((slot < 0 ? 0 : slot) % 16);
+
+    // which head j is, where its elements lie: a thread's are e0 .. e0 + 7 and e1 .. e1 + 7 (v has no pairs)
+    auto offsets = [&](bool pairs, int& e0, int& e1) {
+        e0 = pairs ? 8 * t : 16 * t;
+        e1 = pairs ? half + 8 * t : 16 * t + 8;
+    };
+    uint32_t raw[2 * kRaw8<DT>];
+    auto load = [&](int j) {
+        if (j >= end || !live) return;
+        const bool is_q = j < nq, is_v = !is_q && (!a.k || j >= nq + a.Hkv);
+        const void* base = is_q ? a.q : is_v ? a.v : a.k;
+        const int h = is_q ? j : is_v ? j - (total - a.Hkv) : j - nq;
+        const int64_t at = token * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + static_cast<int64_t>(h) * a.D;
+        int e0, e1;
+        offsets(apart && !is_v, e0, e1);
+        load8<DT>(base, at + e0, raw);
+        load8<DT>(base, at + e1, raw + kRaw8<DT>);
+    };
+    load(first + sub);
+    for (int j0 = first; j0 < end; j0 += 32 / L) {
+        const int j = j0 + sub;
+        const bool in = j < end && live;
+        const bool is_q = j < nq, is_v = !is_q && (!a.k || j >= nq + a.Hkv);
+        const int h = is_q ? j : is_v ? j - (total - a.Hkv) : j - nq;
+        int e0, e1;
+        offsets(apart && !is_v, e0, e1);
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0.0f;
+        if (in) {
+            widen8<DT>(raw, y);
+            widen8<DT>(raw + kRaw8<DT>, y + 8);
+        }
+        load(j + 32 / L);
+        const void* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+        if (a.q_weight || a.k_weight) {                     // the sums of all of the warp's heads
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s = __fmaf_rn(y[i], y[i], s);
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) s = add_rn(s, __shfl_xor_sync(kFullMask, s, o));
+            if (weight && in) {
+                const float rstd = div_rn(1.0f, __fsqrt_rn(add_rn(div_rn(s, static_cast<float>(a.D)), a.eps)));
+                float w[16];
+                load_weight8(weight, a.weight_dtype, e0, w);
+                load_weight8(weight, a.weight_dtype, e1, w + 8);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = mul_rn(mul_rn(y[i], rstd), w[i]);
+            }
+        }
+        if (turned && !is_v) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int p = apart ? i : 2 * i, q = apart ? i + 8 : 2 * i + 1;
+                const float u = y[p], v = y[q];
+                y[p] = __fmaf_rn(u, cs[i], -mul_rn(v, sn[i]));
+                y[q] = __fmaf_rn(v, cs[i], mul_rn(u, sn[i]));
+            }
+        }
+        void* out = is_q ? a.q_out : is_v ? nullptr : a.k_out;
+        if (out && in) {
+            const int64_t at = (token * (is_q ? a.Hq : a.Hkv) + h) * a.D;
+            store8<DT>(out, at + e0, y);
+            store8<DT>(out, at + e1, y + 8);
+        }
+        if (a.slots) {
+            int e = e0;
+            if (a.layout == NVFP4_ROPE_HALF && a.positions) {       // blocks of 16 from two neighbours' halves
+                const bool odd = t & 1;
+                float got[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) got[i] = __shfl_xor_sync(kFullMask, odd ? y[i] : y[i + 8], 1);
+                if (apart && !is_v) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] = odd ? got[i] : y[i];
+                        y[i + 8] = odd ? y[i + 8] : got[i];
+                    }
+                    e = odd ? half + 8 * (t - 1) : 8 * t;
+                }
+            }
+            uint8_t* tile = in && !is_q ? tile_of(a.cache, slot, h) : nullptr;
+            if (tile) {
+                const GScale g = is_v ? head_scale(a.cache.v_mode, a.cache.v_gamax, h, a.cache.bound)
+                                      : head_scale(a.cache.k_mode, a.cache.k_gamax, h, a.cache.bound);
+                quantize_into(tile + (is_v ? 9 * a.D : 0), row, a.D, e, g, y);
+            }
+        }
+    }
+}
+
+// One thread per 16 elements of a slot: 8 bytes of codes and a scale to 16 values (zeros where there is no
+// such slot).
+template <int ODT>
+__global__ void __launch_bounds__(256) k_cache_read(const CacheReadArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const CacheArgs& c = a.cache;
+    const int groups = c.D / 16;
+    const int64_t n = a.T * c.Hkv * groups * 2;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t per = a.T * c.Hkv * groups;           // keys first, then values
+        const bool is_v = i >= per;
+        const int64_t x = is_v ? i - per : i, head = x / groups, token = head / c.Hkv;
+        const int grp = static_cast<int>(x - head * groups), h = static_cast<int>(head - token * c.Hkv);
+        void* out = is_v ? a.v : a.k;
+        if (!out) continue;
+        const int64_t slot = __ldg(a.slots + token);
+        const uint8_t* tile = tile_of(c, slot, h);
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = 0.0f;
+        if (tile) {
+            const uint8_t* part = tile + (is_v ? 9 * c.D : 0);
+            const int row = static_cast<int>(slot % 16);
+            const uint2 w = *reinterpret_cast<const uint2*>(part + row * (c.D / 2) + grp * 8);
+            const float d = e4m3_decode(part[8 * c.D + row * groups + grp]);
+            const GScale g = is_v ? head_scale(c.v_mode, c.v_gamax, h, c.bound) : head_scale(c.k_mode, c.k_gamax, h, c.bound);
+            dequant16<true>(w.x, w.y, d, g.Sdec, y);
+        }
+        store8<ODT>(out, x * 16, y);
+        store8<ODT>(out, x * 16 + 8, y + 8);
+    }
+}
+
+template <int DT>
+cudaError_t launch_heads_t(const HeadsArgs& a, cudaStream_t s) {
+    const int groups = a.D / 16, L = groups <= 4 ? 4 : groups <= 8 ? 8 : groups <= 16 ? 16 : 32;
+    const int total = (a.q ? a.Hq : 0) + (a.k ? a.Hkv : 0) + (a.v ? a.Hkv : 0), step = 32 / L;
+    // few tokens: a warp takes one round of heads, so that all run at once
+    const int rounds = (total + step - 1) / step;
+    const int64_t warps = static_cast<int64_t>(sm_count()) * 16;
+    int64_t chunks = a.T >= warps ? 1 : (warps + a.T - 1) / a.T;
+    if (chunks > rounds) chunks = rounds;
+    const int per = (rounds + static_cast<int>(chunks) - 1) / static_cast<int>(chunks) * step;
+    chunks = (total + per - 1) / per;
+    const int64_t blocks = (a.T * chunks + kHeadsThreads / 32 - 1) / (kHeadsThreads / 32);
+    auto* kernel = L == 4 ? k_heads<DT, 4> : L == 8 ? k_heads<DT, 8> : L == 16 ? k_heads<DT, 16> : k_heads<DT, 32>;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kHeadsThreads), 0, s, a, static_cast<int>(chunks), per);
+}
+
+}  // namespace
+
+int launch_heads(const HeadsArgs& a, void* stream) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return static_cast<int>(a.dtype == NVFP4_BF16 ? launch_heads_t<NVFP4_BF16>(a, s) : launch_heads_t<NVFP4_F32>(a, s));
+}
+
+int launch_cache_read(const CacheReadArgs& a, void* stream) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t n = a.T * a.cache.Hkv * (a.cache.D / 16) * 2;
+    const int64_t want = (n + 255) / 256, cap = static_cast<int64_t>(sm_count()) * 32;
+    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
+    return static_cast<int>(a.out_dtype == NVFP4_BF16 ? launch_pdl(k_cache_read<NVFP4_BF16>, grid, dim3(256), 0, s, a)
+                                                      : launch_pdl(k_cache_read<NVFP4_F32>, grid, dim3(256), 0, s, a));
+}
+
+}  // namespace nvfp4

@@ -115,6 +115,61 @@ struct GroupedArgs {
     uint8_t* workspace;       // grouped_workspace() bytes
 };
 
+// a paged cache of keys and values (see nvfp4.h)
+struct CacheArgs {
+    uint8_t* data;
+    int64_t pages;
+    int page_size, Hkv, D;
+    int k_mode, v_mode;       // NONE, TENSOR_GIVEN or ROW_GIVEN (one amax per KV head)
+    const float* k_gamax;
+    const float* v_gamax;
+    float bound;
+};
+
+// norms, rotation and cache writes of T tokens' heads: q rotated to q_out (null = no q),
+// k rotated to k_out or into the cache, v into the cache
+struct HeadsArgs {
+    const void *q, *k, *v;
+    int64_t T, q_stride, k_stride, v_stride;                // strides of a token, in elements
+    int Hq, Hkv, D, dtype;
+    const void *q_weight, *k_weight;                        // null = no norm
+    int weight_dtype;
+    float eps;
+    const int64_t* positions;                               // null = no rotation
+    const uint64_t* phases;
+    int rotary_dim, layout;
+    float magnitude;
+    void *q_out, *k_out;
+    const int64_t* slots;                                   // null = no cache
+    CacheArgs cache;
+};
+
+struct CacheReadArgs {
+    CacheArgs cache;
+    const int64_t* slots;
+    int64_t T;
+    void *k, *v;
+    int out_dtype;
+};
+
+struct AttendArgs {
+    const void* q;
+    int64_t T, q_stride;
+    int Hq, dtype;
+    CacheArgs cache;
+    const int32_t* pages;                                   // [B, width]
+    int64_t B, width;
+    const int64_t* lengths;
+    const int64_t* offsets;                                 // null = one query a sequence
+    float scale;
+    int causal, window;
+    const float* sinks;
+    void* out;
+    int out_dtype;
+    float* lse;
+    uint8_t* workspace;
+};
+
 // launchers (each returns cudaGetLastError() after its launches)
 int launch_quantize_rows(const QuantArgs& a, void* stream);    // rowwise output only
 int launch_quantize_tiles(const QuantArgs& a, void* stream);   // rowwise + columnwise
@@ -127,6 +182,10 @@ int launch_rmsnorm(const NormArgs& a, void* stream);
 int launch_mv(const MvArgs& a, void* stream);
 int64_t grouped_workspace(const GroupedArgs& a);   // of E, T, N, K alone
 int launch_grouped_mm(const GroupedArgs& a, void* stream);
+int launch_heads(const HeadsArgs& a, void* stream);
+int launch_cache_read(const CacheReadArgs& a, void* stream);
+int64_t attend_workspace(const AttendArgs& a);      // of sizes and types alone
+int launch_attend(const AttendArgs& a, void* stream);
 int launch_amax(const void* x, int64_t M, int64_t K, int dtype, const float* residual, int mode,
                 float* out, void* stream);
 int launch_probe_divide(const float* a, const float* b, float* out, int64_t n, void* stream);
