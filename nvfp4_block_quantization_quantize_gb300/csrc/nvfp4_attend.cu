@@ -17,8 +17,8 @@
 // Work is counted in tiles of 16 tokens of a group, over all groups of all sequences, and
 // each CTA takes an equal run of them, whatever the lengths: a group that runs across CTAs
 // leaves its partial sums in the workspace, and k_join adds them in order.  A warp takes
-// every kWarps-th tile of its CTA's run; its own ring of shared memory is filled by bulk
-// copies, one a tile, that run ahead across groups.
+// every kWarps-th pair of tiles of its CTA's run; its own ring of shared memory is filled by bulk
+// copies, one or two a pair, that run ahead across groups.
 #include "nvfp4_block.cuh"
 #include "nvfp4_tensor.cuh"
 
@@ -26,15 +26,16 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMinTiles = kWarps;                         // tiles below which a CTA's run is not cut further
+constexpr int kMinTiles = 2 * kWarps;                     // tiles below which a CTA's run is not cut further
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNone = -__builtin_huge_valf();          // a masked logit
 constexpr float kSlack = 8.0f;                            // a weight may reach 2^8 before the maximum is raised
 
 template <int D>
 constexpr int kRecord = 18 * D;                           // bytes of a tile
 template <int D, int NT>
-constexpr int kStages = D == 64 ? 8 : D == 128 && NT == 1 ? 4 : D == 128 ? 8 : 4;
+constexpr int kStages = D == 64 ? 4 : D == 128 && NT == 1 ? 2 : D == 128 ? 4 : 2;      // pairs of tiles a warp's ring holds
 
 // ---- who does what ------------------------------------------------------------------------------
 // A sequence's share of the work.
@@ -124,6 +125,7 @@ struct Place {
     Seq s;
     int group, ta, tb;        // of the current part: tiles ta .. tb of the group's s.tiles
     bool known;               // s belongs to b
+    bool more;                // there was a part
 
     __device__ __forceinline__ void start(int64_t u0, int64_t u1, int64_t b0, int64_t before) {
         u = u0, end = u1, b = b0, base = before, known = false;
@@ -150,11 +152,6 @@ struct Place {
         return true;
     }
 };
-
-__device__ __forceinline__ const uint8_t* tile_bytes(const AttendArgs& a, int32_t page, int tile_in_page, int h) {
-    return a.cache.data + ((static_cast<int64_t>(page) * a.cache.Hkv + h) * (a.cache.page_size / 16) + tile_in_page) *
-                              (18 * a.cache.D);
-}
 
 // ---- arithmetic ---------------------------------------------------------------------------------
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
@@ -246,15 +243,15 @@ __device__ __forceinline__ void finish_row(const AttendArgs& a, int64_t token, i
         a.lse[token * a.Hq + head] = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
 }
 
-// Shared memory: rings [kWarps][kStages][record], sums [kWarps][8 NT][D + 4], (max, sum)
-// [kWarps][8 NT][2], barriers [kWarps][kStages].
+// Shared memory: rings [kWarps][kStages][2 records], sums [kWarps][8 NT][D + 4], (max, sum)
+// [kWarps][8 NT][2], barriers [kWarps][kStages], the run found, each warp's two places.
 template <int D, int NT>
 struct Shape {
     static constexpr int R = 8 * NT;                      // rows of a group tile
-    static constexpr int ring = kWarps * kStages<D, NT> * kRecord<D>;
+    static constexpr int ring = kWarps * kStages<D, NT> * 2 * kRecord<D>;
     static constexpr int sums = kWarps * R * (D + 4) * 4;
     static constexpr int stats = kWarps * R * 2 * 4;
-    static constexpr int bytes = ring + sums + stats + kWarps * kStages<D, NT> * 8 + 32;
+    static constexpr int bytes = ring + sums + stats + kWarps * kStages<D, NT> * 8 + 32 + kWarps * 2 * sizeof(Place);
 };
 
 // a partial result of a CTA: R rows of D sums, then R pairs (maximum, denominator)
@@ -298,63 +295,91 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     if (u0 >= u1) return;
 
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
-    uint8_t* const my_ring = ring + warp * kStage * kRecord<D>;
+    uint8_t* const my_ring = ring + warp * kStage * 2 * kRecord<D>;
     uint64_t* const my_bars = bars + warp * kStage;
+    Place* const places = reinterpret_cast<Place*>(found + 4) + 2 * warp;
 
-    // ---- copies, kStage tiles ahead: the place of the next tile of this warp, and its page
-    Place ahead;
-    ahead.start(u0, u1, found[2], found[3]);
-    int ahead_t = 0;
-    bool more;
-    int32_t ahead_page = -1;
-    uint32_t there = 0;                                   // stages whose tile has a page
-    auto seek = [&]() {                                   // to the first tile of this warp in the next part that has one
-        while ((more = ahead.next<R>(a))) {
-            ahead_t = ahead.ta + warp;
-            if (ahead_t < ahead.tb && ahead.s.tiles > 0) break;
-        }
+    // ---- copies, kStage pairs of tiles ahead: the place of this warp's next pair and its pages.  Pages and tiles of a page
+    // are counted along (a division a tile costs as much as decoding it)
+    const int skip_pages = 2 * kWarps / per_page, skip_tiles = 2 * kWarps % per_page;
+    const int64_t page_bytes = static_cast<int64_t>(a.cache.Hkv) * per_page * kRecord<D>;
+    if (lane < 2) places[lane].start(u0, u1, found[2], found[3]);
+    auto advance = [&](Place& p) {                        // one lane walks, all read
+        __syncwarp();
+        if (lane == 0) p.more = p.next<R>(a);
+        __syncwarp();
+        return p.more;
     };
-    auto fetch_page = [&]() {
-        if (more) ahead_page = __ldg(a.pages + ahead.b * a.width + (ahead.s.t0 + ahead_t) / per_page);
+    Place& ahead = places[0];
+    int ahead_left = 0, ahead_tile = 0;                   // tiles to the end of the part, tile of the page
+    const int32_t* ahead_table = nullptr;                 // the page's place in the table
+    const uint8_t* ahead_head = nullptr;                  // the head's first byte in page 0
+    int32_t page_a = -1, page_b = -1;                     // pages of the two tiles
+    uint32_t there = 0;                                   // tiles of stages that have a page, two bits a stage
+    auto pages = [&]() {
+        page_a = __ldg(ahead_table);
+        page_b = ahead_tile + 1 < per_page || ahead_left < 2 ? page_a : __ldg(ahead_table + 1);
+    };
+    auto seek = [&]() {                                   // to the first pair of this warp in the next part that has one
+        ahead_left = 0;
+        while (advance(ahead)) {
+            ahead_left = ahead.s.tiles > 0 ? ahead.tb - ahead.ta - 2 * warp : 0;
+            if (ahead_left > 0) break;
+        }
+        if (ahead_left <= 0) return;
+        const int tile = ahead.s.t0 + ahead.ta + 2 * warp, page = tile / per_page;
+        ahead_tile = tile - page * per_page;
+        ahead_table = a.pages + ahead.b * a.width + page;
+        ahead_head = a.cache.data + static_cast<int64_t>(ahead.group % a.cache.Hkv) * per_page * kRecord<D>;
+        pages();
     };
     auto issue = [&](int stage) {
-        if (!more) return;
-        const bool is = ahead_page >= 0 && ahead_page < a.cache.pages;
-        there = is ? there | 1u << stage : there & ~(1u << stage);
+        if (ahead_left <= 0) return;
+        const bool is_a = page_a >= 0 && page_a < a.cache.pages;
+        const bool is_b = ahead_left > 1 && page_b >= 0 && page_b < a.cache.pages;
+        there = (there & ~(3u << 2 * stage)) | (is_a ? 1u : 0u) << 2 * stage | (is_b ? 2u : 0u) << 2 * stage;
         if (lane == 0) {
-            if (is) {
-                const int t = ahead.s.t0 + ahead_t;
-                mbar_expect_tx(my_bars + stage, kRecord<D>);
-                bulk_copy(my_ring + stage * kRecord<D>,
-                          tile_bytes(a, ahead_page, t % per_page, ahead.group % a.cache.Hkv), kRecord<D>, my_bars + stage);
+            uint8_t* const dst = my_ring + stage * 2 * kRecord<D>;
+            uint64_t* const bar = my_bars + stage;
+            const uint8_t* const src = ahead_head + page_a * page_bytes + ahead_tile * kRecord<D>;
+            if (is_a && is_b && ahead_tile + 1 < per_page) {      // one piece of memory
+                mbar_expect_tx(bar, 2 * kRecord<D>);
+                bulk_copy(dst, src, 2 * kRecord<D>, bar);
+            } else if (is_a || is_b) {
+                mbar_expect_tx(bar, (is_a && is_b ? 2 : 1) * kRecord<D>);
+                if (is_a) bulk_copy(dst, src, kRecord<D>, bar);
+                if (is_b) bulk_copy(dst + kRecord<D>, ahead_head + page_b * page_bytes, kRecord<D>, bar);
             } else {                                      // no such page: nothing comes
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(my_bars + stage)) : "memory");
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
             }
         }
-        ahead_t += kWarps;
-        if (ahead_t >= ahead.tb) seek();
-        fetch_page();
+        ahead_left -= 2 * kWarps;
+        if (ahead_left <= 0) {
+            seek();
+            return;
+        }
+        ahead_table += skip_pages;
+        ahead_tile += skip_tiles;
+        if (ahead_tile >= per_page) ahead_tile -= per_page, ++ahead_table;
+        pages();
     };
     seek();
-    fetch_page();
     for (int i = 0; i < kStage; ++i) issue(i);
 
     int stage = 0;
     uint32_t phase = 0;
     bool lost = false;                                    // a wait ran out
-    Place at;
-    at.start(u0, u1, found[2], found[3]);
-    while (at.next<R>(a)) {
-        const Seq& s = at.s;
+    Place& at = places[1];
+    while (advance(at)) {
         const int h = at.group % a.cache.Hkv, rt = at.group / a.cache.Hkv;
-        const int rows = min(R, s.n * G - rt * R);
-        const int pos0 = s.len - s.n;
+        const int nrows = at.s.n * G, len = at.s.len, pos0 = len - at.s.n;
+        const int64_t row0 = at.s.row0;
 
         // ---- queries: fragments, the factor of a row's logits, and the keys a row sees
         uint32_t qf[kParts][NT][kSteps][2];
         float factor[NT][2];
         int lo[NT][2], hi[NT][2];
-        int all_lo = 0, all_hi = s.len;                   // keys that every row sees
+        int all_lo = 0, all_hi = len;                   // keys that every row sees
         const GScale gk = [&] {
             GScale g{0.0f, 1.0f, 1.0f};
             if (a.cache.k_mode != NVFP4_GAMAX_NONE) {
@@ -365,8 +390,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         }();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = min(rt * R + nt * 8 + r, s.n * G - 1);
-            const int64_t e = (s.row0 + row / G) * a.q_stride + (static_cast<int64_t>(h) * G + row % G) * D + c * (D / 4);
+            const int row = min(rt * R + nt * 8 + r, nrows - 1);
+            const int64_t e = (row0 + row / G) * a.q_stride + (static_cast<int64_t>(h) * G + row % G) * D + c * (D / 4);
             float x[D / 4];
             if (a.dtype == NVFP4_BF16) {
 #pragma unroll
@@ -407,14 +432,14 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 factor[nt][k] = mul_rn(__shfl_sync(kFullMask, mine, (2 * c + k) * 4), dec);
-                const int qrow = min(rt * R + nt * 8 + 2 * c + k, s.n * G - 1), p = pos0 + qrow / G;
-                hi[nt][k] = a.causal ? min(s.len, max(p + 1, 0)) : s.len;
+                const int qrow = min(rt * R + nt * 8 + 2 * c + k, nrows - 1), p = pos0 + qrow / G;
+                hi[nt][k] = a.causal ? min(len, max(p + 1, 0)) : len;
                 lo[nt][k] = a.window > 0 ? max(0, p - a.window + 1) : 0;
             }
         }
         {
-            const int first = rt * R / G, last = min(rt * R + R, s.n * G) - 1;
-            if (a.causal) all_hi = min(s.len, max(pos0 + first + 1, 0));
+            const int first = rt * R / G, last = min(rt * R + R, nrows) - 1;
+            if (a.causal) all_hi = min(len, max(pos0 + first + 1, 0));
             if (a.window > 0) all_lo = max(0, pos0 + last / G - a.window + 1);
         }
         const int seen_lo = a.window > 0 ? max(0, pos0 + rt * R / G - a.window + 1) : 0;
@@ -428,39 +453,46 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             den[nt][0] = den[nt][1] = 0.0f;
         }
 
-        if (s.tiles > 0) {
-            for (int t = at.ta + warp; t < at.tb; t += kWarps) {
-                const int tile = s.t0 + t, j0 = tile * 16;
-                if (!lost) lost = !__all_sync(kFullMask, mbar_wait(my_bars + stage, phase));
-                const uint8_t* rec = my_ring + stage * kRecord<D>;
-                if (there >> stage & 1 && !lost) {
-                    // S^T: MMA rows r and r + 8 are tokens (r >> 1) + 4 (r & 1) and 8 more, so that rows 2c and 2c + 1
-                    // (the pairs of the second product) are tokens c and c + 4
-                    const int tok = (r >> 1) + 4 * (r & 1);
-                    float sc[NT][4];
+        int left = at.s.tiles > 0 ? at.tb - at.ta - 2 * warp : 0, j0 = (at.s.t0 + at.ta + 2 * warp) * 16;
+        for (; left > 0; left -= 2 * kWarps, j0 += 2 * kWarps * 16) {
+            if (!lost) lost = !__all_sync(kFullMask, mbar_wait(my_bars + stage, phase));
+            const uint32_t have = there >> 2 * stage & 3u;
+            if (have && !lost) {
+                const uint8_t* rec = my_ring + stage * 2 * kRecord<D>;
+                // S^T: MMA rows r and r + 8 are tokens (r >> 1) + 4 (r & 1) and 8 more, so that rows 2c and 2c + 1
+                // (the pairs of the second product) are tokens c and c + 4
+                const int tok = (r >> 1) + 4 * (r & 1);
+                float sc[2][NT][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) sc[e][nt][0] = sc[e][nt][1] = sc[e][nt][2] = sc[e][nt][3] = 0.0f;
                     uint32_t kw[2][D / 32], ks[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint8_t* p = rec + (tok + 8 * k) * (D / 2) + c * (D / 8);
+                        const uint8_t* p = rec + e * kRecord<D> + (tok + 8 * k) * (D / 2) + c * (D / 8);
+                        if constexpr (D == 64) {
+                            const uint2 u = *reinterpret_cast<const uint2*>(p);
+                            kw[k][0] = u.x, kw[k][1] = u.y;
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < D / 64; ++i) {
-                            const uint2 u = reinterpret_cast<const uint2*>(p)[i];
-                            kw[k][2 * i] = u.x, kw[k][2 * i + 1] = u.y;
+                            for (int i = 0; i < D / 128; ++i) {
+                                const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+                                kw[k][4 * i] = u.x, kw[k][4 * i + 1] = u.y, kw[k][4 * i + 2] = u.z, kw[k][4 * i + 3] = u.w;
+                            }
                         }
-                        const uint8_t* q = rec + 8 * D + (tok + 8 * k) * (D / 16) + c * (D / 64);
+                        const uint8_t* q = rec + e * kRecord<D> + 8 * D + (tok + 8 * k) * (D / 16) + c * (D / 64);
                         ks[k] = D == 64 ? *q : D == 128 ? *reinterpret_cast<const uint16_t*>(q) : *reinterpret_cast<const uint32_t*>(q);
                     }
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i) {            // blocks of 16 of this lane
-                        uint32_t sp[2], x[2][8];
+                        uint32_t x[2][8];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t u = e4m3_pair(ks[k] >> (8 * i));
-                            sp[k] = __byte_perm(u, u, 0x1010);
-                            decode4(kw[k][2 * i], sp[k], x[k]);
-                            decode4(kw[k][2 * i + 1], sp[k], x[k] + 4);
+                            const uint32_t u = e4m3_pair(i < 2 ? ks[k] : ks[k] >> 16);
+                            const uint32_t sp = __byte_perm(u, u, i & 1 ? 0x3232 : 0x1010);
+                            decode4(kw[k][2 * i], sp, x[k]);
+                            decode4(kw[k][2 * i + 1], sp, x[k] + 4);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {             // steps of 4 elements a lane
@@ -469,82 +501,110 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int p = 0; p < kParts; ++p)
-                                    mma_f16(sc[nt], f, qf[p][nt][4 * i + j][0], qf[p][nt][4 * i + j][1]);
+                                    mma_f16(sc[e][nt], f, qf[p][nt][4 * i + j][0], qf[p][nt][4 * i + j][1]);
                         }
                     }
-                    const bool whole = j0 >= all_lo && j0 + 16 <= all_hi;
-                    if (!whole) {
+                }
+                const bool whole = have == 3u && j0 >= all_lo && j0 + 32 <= all_hi;
+                // logits less the maximum; that is raised where a weight would pass 2^kSlack
+                float w[2][NT][4];
+                bool high = false;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int j = j0 + tok + 8 * (k >> 1);
-                                if (j < lo[nt][k & 1] || j >= hi[nt][k & 1]) sc[nt][k] = __int_as_float(0xFF800000);
-                            }
-                    }
-                    // the maximum is raised where a weight would pass 2^kSlack
-                    bool high = false;
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            sc[nt][k] = mul_rn(sc[nt][k], factor[nt][k & 1]);
-                            high |= sc[nt][k] > add_rn(top[nt][k & 1], kSlack);
-                        }
-                    if (__any_sync(kFullMask, high)) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float m = max_nd(top[nt][k], max_nd(sc[nt][k], sc[nt][k + 2]));
-                                m = max_nd(m, __shfl_xor_sync(kFullMask, m, 4));
-                                m = max_nd(m, __shfl_xor_sync(kFullMask, m, 8));
-                                m = max_nd(m, __shfl_xor_sync(kFullMask, m, 16));
-                                const float less = exp2_approx(sub_rn(top[nt][k], m));
-                                top[nt][k] = m;
-                                den[nt][k] = mul_rn(den[nt][k], less);
-#pragma unroll
-                                for (int i = 0; i < kSteps; ++i) {
-                                    o[nt][i][k] = mul_rn(o[nt][i][k], less);
-                                    o[nt][i][k + 2] = mul_rn(o[nt][i][k + 2], less);
-                                }
+                            w[e][nt][k] = __fmaf_rn(sc[e][nt][k], factor[nt][k & 1], -top[nt][k & 1]);
+                            if (!whole) {
+                                const int j = j0 + 16 * e + tok + 8 * (k >> 1);
+                                if (!(have >> e & 1) || j < lo[nt][k & 1] || j >= hi[nt][k & 1]) w[e][nt][k] = kNone;
                             }
-                    }
-                    uint32_t pf[kParts][NT][2];
+                            high |= w[e][nt][k] > kSlack;
+                        }
+                if (__any_sync(kFullMask, high)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float m = top[nt][k];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int i = k; i < 4; i += 2)
+                                    if (w[e][nt][i] > kNone) m = max_nd(m, mul_rn(sc[e][nt][i], factor[nt][k]));
+                            m = max_nd(m, __shfl_xor_sync(kFullMask, m, 4));
+                            m = max_nd(m, __shfl_xor_sync(kFullMask, m, 8));
+                            m = max_nd(m, __shfl_xor_sync(kFullMask, m, 16));
+                            const float less = exp2_approx(sub_rn(top[nt][k], m));
+                            top[nt][k] = m;
+                            den[nt][k] = mul_rn(den[nt][k], less);
+#pragma unroll
+                            for (int i = 0; i < kSteps; ++i) {
+                                o[nt][i][k] = mul_rn(o[nt][i][k], less);
+                                o[nt][i][k + 2] = mul_rn(o[nt][i][k + 2], less);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int i = k; i < 4; i += 2)
+                                    if (!(w[e][nt][i] <= kNone)) w[e][nt][i] = __fmaf_rn(sc[e][nt][i], factor[nt][k], -m);
+                        }
+                }
+                uint32_t pf[2][kParts][NT][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            w[k] = exp2_approx(sub_rn(sc[nt][k], top[nt][k & 1]));
-                            den[nt][k & 1] = add_rn(den[nt][k & 1], w[k]);
+                            w[e][nt][k] = exp2_approx(w[e][nt][k]);
+                            den[nt][k & 1] = add_rn(den[nt][k & 1], w[e][nt][k]);
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t u = pack_f16(w[2 * k], w[2 * k + 1]);
-                            pf[0][nt][k] = turn8x8(u);
-                            if (F32) pf[kParts - 1][nt][k] = turn8x8(rest_f16(u, w[2 * k], w[2 * k + 1]));
+                            const uint32_t u = pack_f16(w[e][nt][2 * k], w[e][nt][2 * k + 1]);
+                            pf[e][0][nt][k] = turn8x8(u);
+                            if (F32) pf[e][kParts - 1][nt][k] = turn8x8(rest_f16(u, w[e][nt][2 * k], w[e][nt][2 * k + 1]));
                         }
                     }
-                    // O^T: this lane's tokens are c, c + 4, c + 8 and c + 12, its words of 8 elements r * kUnits ..
-                    const uint8_t* vrec = rec + 9 * D;
+                // O^T: this lane's tokens are c, c + 4, c + 8 and c + 12, its words of 8 elements r * kUnits ..
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint8_t* vrec = rec + e * kRecord<D> + 9 * D;
+                    uint32_t vw[4][kUnits], vs[4][(kUnits + 1) / 2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tk = c + 4 * k;
+                        const uint8_t* p = vrec + tk * (D / 2) + r * kUnits * 4;
+                        if constexpr (kUnits == 1) {
+                            vw[k][0] = *reinterpret_cast<const uint32_t*>(p);
+                        } else if constexpr (kUnits == 2) {
+                            const uint2 u = *reinterpret_cast<const uint2*>(p);
+                            vw[k][0] = u.x, vw[k][1] = u.y;
+                        } else {
+                            const uint4 u = *reinterpret_cast<const uint4*>(p);
+                            vw[k][0] = u.x, vw[k][1] = u.y, vw[k][2] = u.z, vw[k][3] = u.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < (kUnits + 1) / 2; ++i) {
+                            vs[k][i] = vrec[8 * D + tk * (D / 16) + r * kUnits / 2 + i];
+                            // what no row sees was perhaps never written
+                            const int j = j0 + 16 * e + tk;
+                            if (!whole && (!(have >> e & 1) || j < seen_lo || j >= len)) vs[k][i] = 0;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
-                        uint32_t w[4], sv[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int tk = c + 4 * k;
-                            w[k] = *reinterpret_cast<const uint32_t*>(vrec + tk * (D / 2) + (r * kUnits + i) * 4);
-                            sv[k] = vrec[8 * D + tk * (D / 16) + (r * kUnits + i) / 2];
-                            // what no row sees was perhaps never written
-                            if (!whole && (j0 + tk < seen_lo || j0 + tk >= s.len)) sv[k] = 0;
-                        }
-                        const uint32_t s01 = e4m3_pair(sv[0] | sv[1] << 8), s23 = e4m3_pair(sv[2] | sv[3] << 8);
+                        // two tokens' codes of one element to a byte (multiplied, not shifted: the ALU has enough to do)
+                        const uint32_t s01 = e4m3_pair(vs[1][i / 2] * 256u + vs[0][i / 2]);
+                        const uint32_t s23 = e4m3_pair(vs[3][i / 2] * 256u + vs[2][i / 2]);
+                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
                         uint32_t even01[4], odd01[4], even23[4], odd23[4];
-                        decode4((w[0] & 0x0F0F0F0Fu) | ((w[1] << 4) & 0xF0F0F0F0u), s01, even01);
-                        decode4(((w[0] >> 4) & 0x0F0F0F0Fu) | (w[1] & 0xF0F0F0F0u), s01, odd01);
-                        decode4((w[2] & 0x0F0F0F0Fu) | ((w[3] << 4) & 0xF0F0F0F0u), s23, even23);
-                        decode4(((w[2] >> 4) & 0x0F0F0F0Fu) | (w[3] & 0xF0F0F0F0u), s23, odd23);
+                        decode4((vw[0][i] & kLow) | ((vw[1][i] * 16u) & ~kLow), s01, even01);
+                        decode4(((vw[0][i] >> 4) & kLow) | (vw[1][i] & ~kLow), s01, odd01);
+                        decode4((vw[2][i] & kLow) | ((vw[3][i] * 16u) & ~kLow), s23, even23);
+                        decode4(((vw[2][i] >> 4) & kLow) | (vw[3][i] & ~kLow), s23, odd23);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t f[4] = {even01[j], odd01[j], even23[j], odd23[j]};
@@ -553,20 +613,20 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                                 if (F32) {
                                     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                                    for (int p = kParts - 1; p >= 0; --p) mma_f16(part, f, pf[p][nt][0], pf[p][nt][1]);
+                                    for (int p = kParts - 1; p >= 0; --p) mma_f16(part, f, pf[e][p][nt][0], pf[e][p][nt][1]);
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) o[nt][4 * i + j][k] = add_rn(o[nt][4 * i + j][k], part[k]);
                                 } else {
-                                    mma_f16(o[nt][4 * i + j], f, pf[0][nt][0], pf[0][nt][1]);
+                                    mma_f16(o[nt][4 * i + j], f, pf[e][0][nt][0], pf[e][0][nt][1]);
                                 }
                             }
                         }
                     }
                 }
-                __syncwarp();                             // the tile is read
-                if (!lost) issue(stage);
-                if (++stage == kStage) stage = 0, phase ^= 1;
             }
+            __syncwarp();                                 // the pair is read
+            if (!lost) issue(stage);
+            if (++stage == kStage) stage = 0, phase ^= 1;
         }
 
         // ---- the warps' sums of this part, joined in the order of the warps
@@ -591,8 +651,9 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                     dst[i] = make_float4(o[nt][2 * i][k], o[nt][2 * i][k + 2], o[nt][2 * i + 1][k], o[nt][2 * i + 1][k + 2]);
             }
         __syncthreads();
-        const int used = s.tiles > 0 ? min(kWarps, at.tb - at.ta) : 0;
-        const bool complete = at.ta == 0 && at.tb == max(s.tiles, 1);
+        const int used = at.s.tiles > 0 ? min(kWarps, (at.tb - at.ta + 1) / 2) : 0;
+        const bool complete = at.ta == 0 && at.tb == max(at.s.tiles, 1);
+        const int rows = min(R, nrows - rt * R);
         float* const part = reinterpret_cast<float*>(a.workspace) +
                             (static_cast<int64_t>(blockIdx.x) * 2 + (at.ta > 0 ? 0 : 1)) * kPart<D, NT>;
         for (int x = threadIdx.x; x < R * (D / 4); x += kWarps * 32) {
@@ -610,7 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             }
             if (complete) {
                 const int row = rt * R + q;
-                finish_row(a, s.row0 + row / G, h * G + row % G, h, d, m, l, v);
+                finish_row(a, row0 + row / G, h * G + row % G, h, d, m, l, v);
             } else {
                 *reinterpret_cast<float4*>(part + q * D + d) = make_float4(v[0], v[1], v[2], v[3]);
                 if (d == 0) part[R * D + 2 * q] = m, part[R * D + 2 * q + 1] = l;
@@ -648,19 +709,22 @@ __global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas_max) 
     const int64_t last = (g1 * ctas - 1) / units;         // the run that holds unit g1 - 1
     const int G = a.Hq / a.cache.Hkv, h = group % a.cache.Hkv, rt = group / a.cache.Hkv;
     const int rows = min(R, s.n * G - rt * R);
+    // run i - 1 has the group's first tiles as its last part, the others as their first
     const float* ws = reinterpret_cast<const float*>(a.workspace);
-    auto part = [&](int64_t run) { return ws + (run * 2 + (units * run / ctas > g0 ? 0 : 1)) * kPart<D, NT>; };
+    auto part = [&](int64_t run) { return ws + (run * 2 + (run == i - 1 ? 1 : 0)) * kPart<D, NT>; };
     for (int y = threadIdx.x; y < R * (D / 4); y += 256) {
         const int q = y / (D / 4), d = y % (D / 4) * 4;
         if (q >= rows) continue;
         float m = kLowest, l = 0.0f;
+#pragma unroll 16
         for (int64_t run = i - 1; run <= last; ++run) m = max_nd(m, part(run)[R * D + 2 * q]);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t run = i - 1; run <= last; ++run) {
             const float* p = part(run);
-            const float f = exp2_approx(sub_rn(p[R * D + 2 * q], m));
-            l = __fmaf_rn(p[R * D + 2 * q + 1], f, l);
+            const float2 st = *reinterpret_cast<const float2*>(p + R * D + 2 * q);
+            const float f = exp2_approx(sub_rn(st.x, m));
+            l = __fmaf_rn(st.y, f, l);
             const float4 u = *reinterpret_cast<const float4*>(p + q * D + d);
             v[0] = __fmaf_rn(u.x, f, v[0]), v[1] = __fmaf_rn(u.y, f, v[1]);
             v[2] = __fmaf_rn(u.z, f, v[2]), v[3] = __fmaf_rn(u.w, f, v[3]);
