@@ -15,10 +15,11 @@
 //   - Online softmax: a row's maximum is raised only when a weight would pass 2^8 (f16 holds
 //     2^15), which a vote finds without exchanging maxima.
 // Work is counted in tiles of 16 tokens of a group, over all groups of all sequences, and
-// each CTA takes an equal run of them, whatever the lengths: a group that runs across CTAs
-// leaves its partial sums in the workspace, and k_join adds them in order.  A warp takes
-// every kWarps-th pair of tiles of its CTA's run; its own ring of shared memory is filled by bulk
-// copies, one or two a pair, that run ahead across groups.
+// each warp takes an equal run of them, whatever the lengths: a warp finishes the groups that
+// lie in its run by itself, those that are cut between the warps of a CTA are joined in shared memory at its
+// end, and those cut between CTAs leave partial sums in the workspace, which k_join adds in
+// order.  A warp works on pairs of tiles; its own ring of shared memory is filled by bulk copies,
+// one or two a pair, that run ahead across groups.
 #include "nvfp4_block.cuh"
 #include "nvfp4_tensor.cuh"
 
@@ -26,7 +27,14 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMinTiles = 2 * kWarps;                     // tiles below which a CTA's run is not cut further
+// What a group costs besides its tiles (its queries, its end), in tiles: the first units of every group.  A run is not
+// cut inside them.
+#ifndef NVFP4_GC
+#define NVFP4_GC 8
+#endif
+constexpr int kGroupCost = NVFP4_GC;
+constexpr int kMinTiles = 4;                              // a warp's run is not made shorter
+static_assert(kGroupCost < kWarps * kMinTiles, "a CTA's run holds some of a group that is cut at its end");
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -__builtin_huge_valf();          // a masked logit
@@ -44,7 +52,7 @@ struct Seq {
     int n, len;               // queries, keys
     int t0, tiles;            // tiles of 16 keys that some query sees
     int runs;                 // row tiles times KV heads: groups
-    int64_t units;            // runs * max(tiles, 1): a group that sees nothing is a unit too
+    int64_t units;            // runs * (kGroupCost + tiles)
 };
 
 template <int R>
@@ -67,63 +75,90 @@ __device__ __forceinline__ Seq sequence(const AttendArgs& a, int64_t b) {
     const int G = a.Hq / a.cache.Hkv;
     const int64_t rows = static_cast<int64_t>(s.n) * G;
     s.runs = static_cast<int>((rows + R - 1) / R) * a.cache.Hkv;
-    s.units = static_cast<int64_t>(s.runs) * max(s.tiles, 1);
+    s.units = static_cast<int64_t>(s.runs) * (kGroupCost + s.tiles);
     return s;
 }
 
-// Sum of all sequences' units, and the sequence that unit x lies in with the units before it; GROUPS: with a group
-// for a unit.  Every lane of a warp calls them.
-template <int R>
-__device__ __forceinline__ int64_t total_units(const AttendArgs& a) {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int64_t b = lane; b < a.B; b += 32) sum += sequence<R>(a, b).units;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
-    return sum;
+// x / y of values that mostly fit in 32 bits (the 64-bit division costs a third of a microsecond)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if ((x | y) >> 32 == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
 }
 
-template <int R, bool GROUPS>
-__device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t x, int64_t* seq, int64_t* before) {
-    const int lane = threadIdx.x & 31;
-    int64_t base = 0;
-    for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
-        const int64_t b = b0 + lane;
-        int64_t u = 0;
-        if (b < a.B) {
-            const Seq q = sequence<R>(a, b);
-            u = GROUPS ? q.runs : q.units;
-        }
-        int64_t s = u;
+__device__ __forceinline__ int64_t scan_add(int64_t v) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(kFullMask, s, o);
-            if (lane >= o) s += v;
-        }
-        const unsigned has = __ballot_sync(kFullMask, base + s > x);
-        if (has) {
-            const int l = __ffs(has) - 1;
-            *seq = b0 + l;
-            *before = base + __shfl_sync(kFullMask, s - u, l);
-            return true;
-        }
-        base += __shfl_sync(kFullMask, s, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kFullMask, v, o);
+        if ((threadIdx.x & 31) >= o) v += u;
     }
-    return false;
+    return v;
 }
 
-// CTAs that take part, and the first unit of CTA i
-__device__ __forceinline__ int64_t parts_of(int64_t units, int64_t ctas) {
+// The sequences' shares of the work, in units or (GROUPS) in groups, added up.  A warp holds it: each lane the sequences
+// lane, lane + 32, ..; the first 32 stay in registers.
+template <int R, bool GROUPS>
+struct Shares {
+    int64_t first, upto;      // this lane's first sequence's share; that of the first sequences up to it
+    int64_t total;
+
+    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) {
+        if (b >= a.B) return 0;
+        const Seq q = sequence<R>(a, b);
+        return GROUPS ? q.runs : q.units;
+    }
+
+    __device__ __forceinline__ explicit Shares(const AttendArgs& a) {
+        const int lane = threadIdx.x & 31;
+        first = share(a, lane);
+        upto = scan_add(first);
+        total = __shfl_sync(kFullMask, upto, 31);
+        if (a.B > 32) {
+            int64_t sum = 0;
+            for (int64_t b = lane + 32; b < a.B; b += 32) sum += share(a, b);
+            total += __shfl_sync(kFullMask, scan_add(sum), 31);
+        }
+    }
+
+    // the sequence that unit x < total lies in, and the units before it
+    __device__ __forceinline__ void find(const AttendArgs& a, int64_t x, int64_t* seq, int64_t* before) const {
+        int64_t base = 0, own = first, s = upto;
+        for (int64_t b0 = 0;; b0 += 32) {
+            const unsigned has = __ballot_sync(kFullMask, base + s > x);
+            if (has || b0 + 32 >= a.B) {
+                const int l = has ? __ffs(has) - 1 : 0;
+                *seq = b0 + l;
+                *before = base + __shfl_sync(kFullMask, s - own, l);
+                return;
+            }
+            base += __shfl_sync(kFullMask, s, 31);
+            own = share(a, b0 + 32 + (threadIdx.x & 31));
+            s = scan_add(own);
+        }
+    }
+};
+
+// warps that take part
+__device__ __forceinline__ int64_t parts_of(int64_t units, int64_t warps) {
     const int64_t most = (units + kMinTiles - 1) / kMinTiles;
-    return most < ctas ? most : ctas;
+    return most < warps ? most : warps;
 }
 
-// A place in a CTA's run: a part [ta, tb) of a group's tiles.
+// where the run that would start at unit x does: at the start of x's group where x is not past the group's own cost.
+// Every lane of a warp calls it.
+template <int R>
+__device__ __forceinline__ int64_t run_start(const AttendArgs& a, const Shares<R, false>& shares, int64_t x, int64_t* seq,
+                                             int64_t* before) {
+    shares.find(a, x, seq, before);
+    const int64_t per = kGroupCost + sequence<R>(a, *seq).tiles, from = x - *before, in = from - quotient(from, per) * per;
+    return in <= kGroupCost ? x - in : x;
+}
+
+// A place in a warp's run: a part of a group, tiles ta .. tb of the group's s.tiles.
 struct Place {
     int64_t u, end;           // next unit, end of the run
     int64_t b, base;          // sequence of the unit before, units before it
     Seq s;
-    int group, ta, tb;        // of the current part: tiles ta .. tb of the group's s.tiles
+    int h, rt, ta, tb;        // the group's KV head and row tile
     bool known;               // s belongs to b
     bool more;                // there was a part
 
@@ -135,23 +170,38 @@ struct Place {
     template <int R>
     __device__ __forceinline__ bool next(const AttendArgs& a) {
         if (u >= end) return false;
-        while (true) {
-            if (!known) s = sequence<R>(a, b);
-            known = true;
-            if (u < base + s.units) break;
-            base += s.units;
-            ++b;
-            known = false;
+        if (known && u < base + s.units) {                // the sequence's next group
+            if (++h == a.cache.Hkv) h = 0, ++rt;
+        } else {
+            while (true) {
+                if (known) base += s.units, ++b;
+                s = sequence<R>(a, b);
+                known = true;
+                if (u < base + s.units) break;
+            }
+            h = rt = 0;
         }
-        const int per = max(s.tiles, 1);
-        const int64_t x = u - base;
-        group = static_cast<int>(x / per);
-        ta = static_cast<int>(x - static_cast<int64_t>(group) * per);
-        tb = static_cast<int>(min(static_cast<int64_t>(per), ta + (end - u)));
-        u += tb - ta;
+        const int per = kGroupCost + s.tiles;
+        int64_t in = u - base - (static_cast<int64_t>(rt) * a.cache.Hkv + h) * per;
+        if (in >= per) {                                  // a run that starts amid a sequence
+            const int64_t group = quotient(in, per);
+            in -= group * per;
+            rt = static_cast<int>(group / a.cache.Hkv);
+            h = static_cast<int>(group - static_cast<int64_t>(rt) * a.cache.Hkv);
+        }
+        const int from = static_cast<int>(in);
+        const int to = static_cast<int>(min(static_cast<int64_t>(per), from + (end - u)));
+        u += to - from;
+        ta = max(from - kGroupCost, 0), tb = to - kGroupCost;
         return true;
     }
 };
+
+// the query and the head of a row of a sequence's KV head
+__device__ __forceinline__ void split_row(int n, int G, int row, int* query, int* head) {
+    *query = n == 1 ? 0 : row / G;
+    *head = row - *query * G;
+}
 
 // ---- arithmetic ---------------------------------------------------------------------------------
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
@@ -215,43 +265,62 @@ __device__ __forceinline__ float power_of_two(int e) {    // e in [-126, 127]
     return __int_as_float((e + 127) << 23);
 }
 
-// 4 elements of a row from its sums v, its maximum m (of logits times log2 e) and denominator l
-__device__ __forceinline__ void finish_row(const AttendArgs& a, int64_t token, int head, int h, int d, float m, float l,
-                                           float* v) {
-    if (a.sinks) {
-        const float sink = mul_rn(__ldg(a.sinks + head), kLog2e), top = max_nd(m, sink), f = exp2_approx(sub_rn(m, top));
-        l = __fmaf_rn(l, f, exp2_approx(sub_rn(sink, top)));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = mul_rn(v[k], f);
-        m = top;
+// A row's end: its sums times `by` are its output; m its maximum (of logits times log2 e), l its denominator.
+struct Finish {
+    float by, lse;
+
+    __device__ __forceinline__ Finish(const AttendArgs& a, int head, int h, float m, float l) {
+        float enc, dec = 1.0f, f = 1.0f;
+        if (a.sinks) {
+            const float sink = mul_rn(__ldg(a.sinks + head), kLog2e), top = max_nd(m, sink);
+            f = exp2_approx(sub_rn(m, top));
+            l = __fmaf_rn(l, f, exp2_approx(sub_rn(sink, top)));
+            m = top;
+        }
+        if (a.cache.v_mode != NVFP4_GAMAX_NONE)
+            global_scales(__ldg(a.cache.v_gamax + (a.cache.v_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
+        by = l == 0.0f ? 0.0f : mul_rn(f, div_rn(dec, l));
+        lse = 0.0f;
+        if (a.lse) lse = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
     }
-    float enc, dec = 1.0f;
-    if (a.cache.v_mode != NVFP4_GAMAX_NONE)
-        global_scales(__ldg(a.cache.v_gamax + (a.cache.v_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
-    const float by = l == 0.0f ? 0.0f : div_rn(dec, l);
+
+    // 4 elements from element d
+    __device__ __forceinline__ void store(const AttendArgs& a, int64_t token, int head, int d, float* v) const {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = mul_rn(v[k], by);
-    const int64_t at = (token * a.Hq + head) * a.cache.D + d;
-    if (a.out_dtype == NVFP4_F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        for (int k = 0; k < 4; ++k) v[k] = mul_rn(v[k], by);
+        const int64_t at = (token * a.Hq + head) * a.cache.D + d;
+        if (a.out_dtype == NVFP4_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        }
+        if (a.lse && d == 0) a.lse[token * a.Hq + head] = lse;
     }
-    if (a.lse && d == 0)
-        a.lse[token * a.Hq + head] = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
-}
+};
+
+// A part of a cut group, as a warp leaves it: the first part of its run lies in `sums`, the last in its ring.
+struct Left {
+    int64_t b, first;         // its sequence; the group's first unit (-1: none)
+    int h, rt, ta, tb;
+};
 
 // Shared memory: rings [kWarps][kStages][2 records], sums [kWarps][8 NT][D + 4], (max, sum)
-// [kWarps][8 NT][2], barriers [kWarps][kStages], the run found, each warp's two places.
+// [kWarps][2][8 NT][2], barriers [kWarps][kStages], run starts [kWarps + 1] with their sequences and units before
+// [kWarps], each warp's two places and two parts left.
 template <int D, int NT>
 struct Shape {
     static constexpr int R = 8 * NT;                      // rows of a group tile
-    static constexpr int ring = kWarps * kStages<D, NT> * 2 * kRecord<D>;
-    static constexpr int sums = kWarps * R * (D + 4) * 4;
-    static constexpr int stats = kWarps * R * 2 * 4;
-    static constexpr int bytes = ring + sums + stats + kWarps * kStages<D, NT> * 8 + 32 + kWarps * 2 * sizeof(Place);
+    static constexpr int sum = R * (D + 4) * 4;           // a part's sums
+    static constexpr int one = kStages<D, NT> * 2 * kRecord<D>;       // a warp's ring, which holds a part's sums at the end
+    static_assert(one >= sum && sum % 128 == 0, "the last part's sums lie in the ring");
+    static constexpr int ring = kWarps * one;
+    static constexpr int sums = kWarps * sum;
+    static constexpr int stats = kWarps * 2 * R * 2 * 4;
+    static constexpr int bars = kWarps * kStages<D, NT> * 8;
+    static constexpr int found = (3 * kWarps + 1) * 8;
+    static constexpr int bytes = ring + sums + stats + bars + found + kWarps * 2 * (sizeof(Place) + sizeof(Left));
 };
 
 // a partial result of a CTA: R rows of D sums, then R pairs (maximum, denominator)
@@ -270,47 +339,63 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     float* const stats = reinterpret_cast<float*>(smem + S::ring + S::sums);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + S::ring + S::sums + S::stats);
     int64_t* const found = reinterpret_cast<int64_t*>(bars + kWarps * kStage);
+    Place* const all_places = reinterpret_cast<Place*>(found + 3 * kWarps + 1);
+    Left* const lefts = reinterpret_cast<Left*>(all_places + 2 * kWarps);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     if (threadIdx.x < kWarps * kStage) mbar_init(bars + threadIdx.x);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
     pdl_wait();
-    if (warp == 0) {                                      // this CTA's run of units: [u0, u1), `before` ahead of sequence b
-        int64_t u0 = 0, u1 = 0, b = 0, before = 0;
+    {                                                     // this warp's run of units, its sequence and the units before
+        int64_t u = 0, end = 0, b = 0, before = 0;
         if (split) {
-            const int64_t units = total_units<R>(a), ctas = parts_of(units, gridDim.x), i = blockIdx.x;
-            if (i < ctas) {
-                u0 = units * i / ctas, u1 = units * (i + 1) / ctas;
-                find_unit<R, false>(a, u0, &b, &before);
+            const Shares<R, false> shares(a);
+            const int64_t units = shares.total, warps = parts_of(units, gridDim.x * kWarps);
+            const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+            u = i < warps ? run_start<R>(a, shares, quotient(units * i, warps), &b, &before) : units;
+            if (warp == kWarps - 1) {
+                int64_t x, y;
+                end = i + 1 < warps ? run_start<R>(a, shares, quotient(units * (i + 1), warps), &x, &y) : units;
             }
-        } else if (find_unit<R, true>(a, blockIdx.x, &b, &before)) {      // one group
-            const int per = max(sequence<R>(a, b).tiles, 1);
-            u0 = (blockIdx.x - before) * per, u1 = u0 + per, before = 0;
+        } else {                                          // one group a CTA
+            const Shares<R, true> shares(a);
+            if (blockIdx.x < shares.total) {
+                shares.find(a, blockIdx.x, &b, &before);
+                const int tiles = sequence<R>(a, b).tiles;
+                u = (blockIdx.x - before) * (kGroupCost + tiles), before = 0;
+                end = u + kGroupCost + tiles;
+                const int t = tiles * warp / kWarps;
+                if (t > 0) u += kGroupCost + t;           // without a tile the run is empty or the group's first
+            }
         }
-        if (lane == 0) found[0] = u0, found[1] = u1, found[2] = b, found[3] = before;
+        if (lane == 0) {
+            found[warp] = u, found[kWarps + 1 + warp] = b, found[2 * kWarps + 1 + warp] = before;
+            if (warp == kWarps - 1) found[kWarps] = end;
+            lefts[2 * warp].first = lefts[2 * warp + 1].first = -1;
+        }
     }
     __syncthreads();
-    const int64_t u0 = found[0], u1 = found[1];
-    if (u0 >= u1) return;
+    const int64_t u0 = found[warp], u1 = found[warp + 1];
+    if (found[0] >= found[kWarps]) return;
 
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
-    uint8_t* const my_ring = ring + warp * kStage * 2 * kRecord<D>;
+    uint8_t* const my_ring = ring + warp * S::one;
     uint64_t* const my_bars = bars + warp * kStage;
-    Place* const places = reinterpret_cast<Place*>(found + 4) + 2 * warp;
+    Place* const places = all_places + 2 * warp;
 
     // ---- copies, kStage pairs of tiles ahead: the place of this warp's next pair and its pages.  Pages and tiles of a page
     // are counted along (a division a tile costs as much as decoding it)
-    const int skip_pages = 2 * kWarps / per_page, skip_tiles = 2 * kWarps % per_page;
+    const int skip_pages = 2 / per_page, skip_tiles = 2 % per_page;
     const int64_t page_bytes = static_cast<int64_t>(a.cache.Hkv) * per_page * kRecord<D>;
-    if (lane < 2) places[lane].start(u0, u1, found[2], found[3]);
+    if (lane == 0) places[0].start(u0, u1, found[kWarps + 1 + warp], found[2 * kWarps + 1 + warp]);
     auto advance = [&](Place& p) {                        // one lane walks, all read
         __syncwarp();
         if (lane == 0) p.more = p.next<R>(a);
         __syncwarp();
         return p.more;
     };
-    Place& ahead = places[0];
+    Place &ahead = places[0], &at = places[1];
     int ahead_left = 0, ahead_tile = 0;                   // tiles to the end of the part, tile of the page
     const int32_t* ahead_table = nullptr;                 // the page's place in the table
     const uint8_t* ahead_head = nullptr;                  // the head's first byte in page 0
@@ -320,18 +405,20 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         page_a = __ldg(ahead_table);
         page_b = ahead_tile + 1 < per_page || ahead_left < 2 ? page_a : __ldg(ahead_table + 1);
     };
-    auto seek = [&]() {                                   // to the first pair of this warp in the next part that has one
-        ahead_left = 0;
-        while (advance(ahead)) {
-            ahead_left = ahead.s.tiles > 0 ? ahead.tb - ahead.ta - 2 * warp : 0;
-            if (ahead_left > 0) break;
-        }
-        if (ahead_left <= 0) return;
-        const int tile = ahead.s.t0 + ahead.ta + 2 * warp, page = tile / per_page;
+    auto begin = [&]() {                                  // at the first pair of a part
+        const int tile = ahead.s.t0 + ahead.ta, page = tile / per_page;
         ahead_tile = tile - page * per_page;
         ahead_table = a.pages + ahead.b * a.width + page;
-        ahead_head = a.cache.data + static_cast<int64_t>(ahead.group % a.cache.Hkv) * per_page * kRecord<D>;
+        ahead_head = a.cache.data + static_cast<int64_t>(ahead.h) * per_page * kRecord<D>;
         pages();
+    };
+    auto seek = [&]() {                                   // to the next part that has a pair
+        ahead_left = 0;
+        while (advance(ahead)) {
+            ahead_left = ahead.tb - ahead.ta;
+            if (ahead_left > 0) break;
+        }
+        if (ahead_left > 0) begin();
     };
     auto issue = [&](int stage) {
         if (ahead_left <= 0) return;
@@ -353,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
             }
         }
-        ahead_left -= 2 * kWarps;
+        ahead_left -= 2;
         if (ahead_left <= 0) {
             seek();
             return;
@@ -363,15 +450,19 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         if (ahead_tile >= per_page) ahead_tile -= per_page, ++ahead_table;
         pages();
     };
-    seek();
+    bool some = advance(ahead);                           // the first part, for both places
+    if (lane == 0) at = ahead;
+    __syncwarp();
+    ahead_left = some ? ahead.tb - ahead.ta : 0;
+    if (ahead_left > 0) begin();
+    else if (some) seek();
     for (int i = 0; i < kStage; ++i) issue(i);
 
     int stage = 0;
     uint32_t phase = 0;
     bool lost = false;                                    // a wait ran out
-    Place& at = places[1];
-    while (advance(at)) {
-        const int h = at.group % a.cache.Hkv, rt = at.group / a.cache.Hkv;
+    for (; some; some = advance(at)) {
+        const int h = at.h, rt = at.rt, n = at.s.n;
         const int nrows = at.s.n * G, len = at.s.len, pos0 = len - at.s.n;
         const int64_t row0 = at.s.row0;
 
@@ -391,7 +482,9 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = min(rt * R + nt * 8 + r, nrows - 1);
-            const int64_t e = (row0 + row / G) * a.q_stride + (static_cast<int64_t>(h) * G + row % G) * D + c * (D / 4);
+            int query, head;
+            split_row(n, G, row, &query, &head);
+            const int64_t e = (row0 + query) * a.q_stride + (static_cast<int64_t>(h) * G + head) * D + c * (D / 4);
             float x[D / 4];
             if (a.dtype == NVFP4_BF16) {
 #pragma unroll
@@ -432,17 +525,18 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 factor[nt][k] = mul_rn(__shfl_sync(kFullMask, mine, (2 * c + k) * 4), dec);
-                const int qrow = min(rt * R + nt * 8 + 2 * c + k, nrows - 1), p = pos0 + qrow / G;
+                split_row(n, G, min(rt * R + nt * 8 + 2 * c + k, nrows - 1), &query, &head);
+                const int p = pos0 + query;
                 hi[nt][k] = a.causal ? min(len, max(p + 1, 0)) : len;
                 lo[nt][k] = a.window > 0 ? max(0, p - a.window + 1) : 0;
             }
         }
-        {
-            const int first = rt * R / G, last = min(rt * R + R, nrows) - 1;
-            if (a.causal) all_hi = min(len, max(pos0 + first + 1, 0));
-            if (a.window > 0) all_lo = max(0, pos0 + last / G - a.window + 1);
-        }
-        const int seen_lo = a.window > 0 ? max(0, pos0 + rt * R / G - a.window + 1) : 0;
+        int first, last, head;                            // queries of the first and the last row
+        split_row(n, G, rt * R, &first, &head);
+        split_row(n, G, min(rt * R + R, nrows) - 1, &last, &head);
+        if (a.causal) all_hi = min(len, max(pos0 + first + 1, 0));
+        if (a.window > 0) all_lo = max(0, pos0 + last - a.window + 1);
+        const int seen_lo = a.window > 0 ? max(0, pos0 + first - a.window + 1) : 0;
 
         float o[NT][kSteps][4], top[NT][2], den[NT][2];
 #pragma unroll
@@ -453,8 +547,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             den[nt][0] = den[nt][1] = 0.0f;
         }
 
-        int left = at.s.tiles > 0 ? at.tb - at.ta - 2 * warp : 0, j0 = (at.s.t0 + at.ta + 2 * warp) * 16;
-        for (; left > 0; left -= 2 * kWarps, j0 += 2 * kWarps * 16) {
+        int left = at.tb - at.ta, j0 = (at.s.t0 + at.ta) * 16;
+        for (; left > 0; left -= 2, j0 += 32) {
             if (!lost) lost = !__all_sync(kFullMask, mbar_wait(my_bars + stage, phase));
             const uint32_t have = there >> 2 * stage & 3u;
             if (have && !lost) {
@@ -508,20 +602,30 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 const bool whole = have == 3u && j0 >= all_lo && j0 + 32 <= all_hi;
                 // logits less the maximum; that is raised where a weight would pass 2^kSlack
                 float w[2][NT][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[e][nt][k] = __fmaf_rn(sc[e][nt][k], factor[nt][k & 1], -top[nt][k & 1]);
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int j = j0 + 16 * e + tok + 8 * (k >> 1);
+                                if (!(have >> e & 1) || j < lo[nt][k & 1] || j >= hi[nt][k & 1]) w[e][nt][k] = kNone;
+                            }
+                }
                 bool high = false;
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            w[e][nt][k] = __fmaf_rn(sc[e][nt][k], factor[nt][k & 1], -top[nt][k & 1]);
-                            if (!whole) {
-                                const int j = j0 + 16 * e + tok + 8 * (k >> 1);
-                                if (!(have >> e & 1) || j < lo[nt][k & 1] || j >= hi[nt][k & 1]) w[e][nt][k] = kNone;
-                            }
-                            high |= w[e][nt][k] > kSlack;
-                        }
+                        for (int k = 0; k < 4; ++k) high |= w[e][nt][k] > kSlack;
                 if (__any_sync(kFullMask, high)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -587,12 +691,16 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                             vw[k][0] = u.x, vw[k][1] = u.y, vw[k][2] = u.z, vw[k][3] = u.w;
                         }
 #pragma unroll
-                        for (int i = 0; i < (kUnits + 1) / 2; ++i) {
-                            vs[k][i] = vrec[8 * D + tk * (D / 16) + r * kUnits / 2 + i];
-                            // what no row sees was perhaps never written
-                            const int j = j0 + 16 * e + tk;
-                            if (!whole && (!(have >> e & 1) || j < seen_lo || j >= len)) vs[k][i] = 0;
-                        }
+                        for (int i = 0; i < (kUnits + 1) / 2; ++i) vs[k][i] = vrec[8 * D + tk * (D / 16) + r * kUnits / 2 + i];
+                    }
+                    if (!whole) {                         // what no row sees was perhaps never written
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < (kUnits + 1) / 2; ++i) {
+                                const int j = j0 + 16 * e + c + 4 * k;
+                                if (!(have >> e & 1) || j < seen_lo || j >= len) vs[k][i] = 0;
+                            }
                     }
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
@@ -629,7 +737,10 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             if (++stage == kStage) stage = 0, phase ^= 1;
         }
 
-        // ---- the warps' sums of this part, joined in the order of the warps
+        // ---- the end of the part: a whole group is written, what is cut is left for the CTA's end
+        const bool complete = at.ta == 0 && at.tb == at.s.tiles;
+        const int place = at.u >= u1 && at.ta == 0 ? 1 : 0;       // the run's last part, which it did not start amid
+        __syncwarp();                                     // the last part's sums go into the ring: its copies are in and read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -640,73 +751,112 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 l = add_rn(l, __shfl_xor_sync(kFullMask, l, 8));
                 l = add_rn(l, __shfl_xor_sync(kFullMask, l, 16));
                 if (lost) l = __int_as_float(0x7FC00000);
-                if (r == 0) {
-                    stats[(warp * R + q) * 2] = top[nt][k];
-                    stats[(warp * R + q) * 2 + 1] = l;
-                }
                 // elements (r kUnits + i) * 8 + 2 j (and + 1) of row q
-                float4* dst = reinterpret_cast<float4*>(sums + (warp * R + q) * (D + 4) + r * kUnits * 8);
+                if (complete) {
+                    const int row = rt * R + q;
+                    if (row < nrows) {
+                        int query, hd;
+                        split_row(n, G, row, &query, &hd);
+                        const Finish f(a, h * G + hd, h, top[nt][k], l);
+                        const int64_t token = row0 + query;
 #pragma unroll
-                for (int i = 0; i < kSteps / 2; ++i)
-                    dst[i] = make_float4(o[nt][2 * i][k], o[nt][2 * i][k + 2], o[nt][2 * i + 1][k], o[nt][2 * i + 1][k + 2]);
+                        for (int i = 0; i < kSteps / 2; ++i) {
+                            float v[4] = {o[nt][2 * i][k], o[nt][2 * i][k + 2], o[nt][2 * i + 1][k], o[nt][2 * i + 1][k + 2]};
+                            f.store(a, token, h * G + hd, r * kUnits * 8 + 4 * i, v);
+                        }
+                    }
+                } else {
+                    float* const st = stats + (2 * warp + place) * R * 2;
+                    if (r == 0) st[2 * q] = top[nt][k], st[2 * q + 1] = l;
+                    float* const to = place ? reinterpret_cast<float*>(my_ring) : sums + warp * (S::sum / 4);
+                    float4* dst = reinterpret_cast<float4*>(to + q * (D + 4) + r * kUnits * 8);
+#pragma unroll
+                    for (int i = 0; i < kSteps / 2; ++i)
+                        dst[i] = make_float4(o[nt][2 * i][k], o[nt][2 * i][k + 2], o[nt][2 * i + 1][k], o[nt][2 * i + 1][k + 2]);
+                }
             }
-        __syncthreads();
-        const int used = at.s.tiles > 0 ? min(kWarps, (at.tb - at.ta + 1) / 2) : 0;
-        const bool complete = at.ta == 0 && at.tb == max(at.s.tiles, 1);
-        const int rows = min(R, nrows - rt * R);
+        if (!complete && lane == 0) {
+            Left& x = lefts[2 * warp + place];
+            x.b = at.b, x.h = h, x.rt = rt, x.ta = at.ta, x.tb = at.tb;
+            x.first = at.base + (static_cast<int64_t>(rt) * a.cache.Hkv + h) * (kGroupCost + at.s.tiles);
+        }
+    }
+    if (lost) settle();
+
+    // ---- the parts that this CTA's warps left, joined in their order
+    __syncthreads();
+    static_assert(2 * kWarps <= 32, "a lane for each part");
+    const int64_t mine = lane < 2 * kWarps ? lefts[lane].first : -1;
+    const unsigned parts = __ballot_sync(kFullMask, mine >= 0);
+    const unsigned below = parts & ((1u << lane) - 1u);
+    const int64_t previous = __shfl_sync(kFullMask, mine, below ? 31 - __clz(below) : 0);
+    unsigned firsts = __ballot_sync(kFullMask, mine >= 0 && (!below || previous != mine));
+    while (firsts) {
+        const int i = __ffs(firsts) - 1;
+        firsts &= firsts - 1;
+        const unsigned group = parts & ~((1u << i) - 1u) & (firsts ? (1u << (__ffs(firsts) - 1)) - 1u : ~0u);      // its parts
+        const Left x = lefts[i];
+        const int tb = lefts[31 - __clz(group)].tb;
+        const Seq s = sequence<R>(a, x.b);
+        const bool complete = x.ta == 0 && tb == s.tiles;
+        const int rows = min(R, s.n * G - x.rt * R);
         float* const part = reinterpret_cast<float*>(a.workspace) +
-                            (static_cast<int64_t>(blockIdx.x) * 2 + (at.ta > 0 ? 0 : 1)) * kPart<D, NT>;
-        for (int x = threadIdx.x; x < R * (D / 4); x += kWarps * 32) {
-            const int q = x / (D / 4), d = x % (D / 4) * 4;
+                            (static_cast<int64_t>(blockIdx.x) * 2 + (x.ta > 0 ? 0 : 1)) * kPart<D, NT>;
+        for (int y = threadIdx.x; y < R * (D / 4); y += kWarps * 32) {
+            const int q = y / (D / 4), d = y % (D / 4) * 4;
             if (q >= rows) continue;
-            float m = kLowest, l = 0.0f;
-            for (int w = 0; w < used; ++w) m = max_nd(m, stats[(w * R + q) * 2]);
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int w = 0; w < used; ++w) {
-                const float f = exp2_approx(sub_rn(stats[(w * R + q) * 2], m));
-                l = __fmaf_rn(stats[(w * R + q) * 2 + 1], f, l);
-                const float4 u = *reinterpret_cast<const float4*>(sums + (w * R + q) * (D + 4) + d);
+            float m = kLowest, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (unsigned left = group; left; left &= left - 1) m = max_nd(m, stats[((__ffs(left) - 1) * R + q) * 2]);
+            for (unsigned left = group; left; left &= left - 1) {
+                const int k = __ffs(left) - 1;
+                const float f = exp2_approx(sub_rn(stats[(k * R + q) * 2], m));
+                l = __fmaf_rn(stats[(k * R + q) * 2 + 1], f, l);
+                const float* from = k & 1 ? reinterpret_cast<const float*>(ring + (k >> 1) * S::one) : sums + (k >> 1) * (S::sum / 4);
+                const float4 u = *reinterpret_cast<const float4*>(from + q * (D + 4) + d);
                 v[0] = __fmaf_rn(u.x, f, v[0]), v[1] = __fmaf_rn(u.y, f, v[1]);
                 v[2] = __fmaf_rn(u.z, f, v[2]), v[3] = __fmaf_rn(u.w, f, v[3]);
             }
             if (complete) {
-                const int row = rt * R + q;
-                finish_row(a, row0 + row / G, h * G + row % G, h, d, m, l, v);
+                int query, head;
+                split_row(s.n, G, x.rt * R + q, &query, &head);
+                Finish(a, x.h * G + head, x.h, m, l).store(a, s.row0 + query, x.h * G + head, d, v);
             } else {
                 *reinterpret_cast<float4*>(part + q * D + d) = make_float4(v[0], v[1], v[2], v[3]);
                 if (d == 0) part[R * D + 2 * q] = m, part[R * D + 2 * q + 1] = l;
             }
         }
-        __syncthreads();
     }
-    if (lost) settle();
 }
 
-// A group that several CTAs took parts of, joined in their order: CTA i joins it if the i-th run is the second
+// A group that several CTAs took parts of, joined in their order: by CTA i of here if CTA i + 1 of k_attend is the second
 // that holds some of it.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas_max) {
+__global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas) {
     constexpr int R = 8 * NT;
     __shared__ int64_t found[3];
     pdl_trigger();
     pdl_wait();
+    const int64_t i = blockIdx.x + 1;
     if (threadIdx.x < 32) {
-        const int64_t units = total_units<R>(a), ctas = parts_of(units, ctas_max), i = blockIdx.x + 1;
+        const Shares<R, false> shares(a);
+        const int64_t warps = parts_of(shares.total, static_cast<int64_t>(ctas) * kWarps);
         int64_t b = 0, before = 0;
-        if (i < ctas) find_unit<R, false>(a, units * i / ctas, &b, &before);
-        if (threadIdx.x == 0) found[0] = i < ctas ? units : 0, found[1] = b, found[2] = before;
+        const bool in = i * kWarps < warps;
+        if (in) shares.find(a, quotient(shares.total * i * kWarps, warps), &b, &before);
+        if (threadIdx.x == 0) found[0] = in ? shares.total : 0, found[1] = b, found[2] = before;
     }
     __syncthreads();
     const int64_t units = found[0];
     if (units == 0) return;
-    const int64_t ctas = parts_of(units, ctas_max), i = blockIdx.x + 1;
-    const int64_t x = units * i / ctas;                   // where run i starts
+    const int64_t warps = parts_of(units, static_cast<int64_t>(ctas) * kWarps);
+    const int64_t x = quotient(units * i * kWarps, warps);            // where CTA i's run starts
     const Seq s = sequence<R>(a, found[1]);
-    const int per = max(s.tiles, 1);
-    const int group = static_cast<int>((x - found[2]) / per);
+    const int per = kGroupCost + s.tiles;
+    const int group = static_cast<int>(quotient(x - found[2], per));
     const int64_t g0 = found[2] + static_cast<int64_t>(group) * per, g1 = g0 + per;
-    if (x == g0 || units * (i - 1) / ctas > g0) return;   // not cut here, or joined by an earlier CTA
-    const int64_t last = (g1 * ctas - 1) / units;         // the run that holds unit g1 - 1
+    // not cut here, or joined by an earlier CTA
+    if (x - g0 <= kGroupCost || quotient(units * (i - 1) * kWarps, warps) > g0 + kGroupCost) return;
+    const int64_t last = quotient(g1 * warps - 1, units) / kWarps;           // the CTA that holds unit g1 - 1
     const int G = a.Hq / a.cache.Hkv, h = group % a.cache.Hkv, rt = group / a.cache.Hkv;
     const int rows = min(R, s.n * G - rt * R);
     // run i - 1 has the group's first tiles as its last part, the others as their first
@@ -729,8 +879,9 @@ __global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas_max) 
             v[0] = __fmaf_rn(u.x, f, v[0]), v[1] = __fmaf_rn(u.y, f, v[1]);
             v[2] = __fmaf_rn(u.z, f, v[2]), v[3] = __fmaf_rn(u.w, f, v[3]);
         }
-        const int row = rt * R + q;
-        finish_row(a, s.row0 + row / G, h * G + row % G, h, d, m, l, v);
+        int query, head;
+        split_row(s.n, G, rt * R + q, &query, &head);
+        Finish(a, h * G + head, h, m, l).store(a, s.row0 + query, h * G + head, d, v);
     }
 }
 
