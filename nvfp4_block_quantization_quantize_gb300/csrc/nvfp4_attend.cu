@@ -308,7 +308,7 @@ struct Left {
 
 // Shared memory: rings [kWarps][kStages][2 records], sums [kWarps][8 NT][D + 4], (max, sum)
 // [kWarps][2][8 NT][2], barriers [kWarps][kStages], run starts [kWarps + 1] with their sequences and units before
-// [kWarps], each warp's two places and two parts left.
+// [kWarps] each and all units, each warp's two places and two parts left.
 template <int D, int NT>
 struct Shape {
     static constexpr int R = 8 * NT;                      // rows of a group tile
@@ -319,13 +319,26 @@ struct Shape {
     static constexpr int sums = kWarps * sum;
     static constexpr int stats = kWarps * 2 * R * 2 * 4;
     static constexpr int bars = kWarps * kStages<D, NT> * 8;
-    static constexpr int found = (3 * kWarps + 1) * 8;
+    static constexpr int found = (3 * kWarps + 2) * 8;
     static constexpr int bytes = ring + sums + stats + bars + found + kWarps * 2 * (sizeof(Place) + sizeof(Left));
+};
+
+// What k_join is to do for a CTA of k_attend: the group that its run starts amid, if the CTA before has its first
+// tiles, which the CTAs up to `last` took parts of.
+struct Cut {
+    int64_t row0;             // the sequence's first query
+    int n, h, rt, last;       // its queries (0: nothing to do); the group's KV head and row tile
 };
 
 // a partial result of a CTA: R rows of D sums, then R pairs (maximum, denominator)
 template <int D, int NT>
 constexpr int64_t kPart = 8 * NT * (D + 2);
+
+// the workspace: two partial results a CTA, then a Cut each
+template <int D, int NT>
+__device__ __forceinline__ Cut* cuts(const AttendArgs& a, int64_t ctas) {
+    return reinterpret_cast<Cut*>(reinterpret_cast<float*>(a.workspace) + ctas * 2 * kPart<D, NT>);
+}
 
 // F32: queries and weights enter the products as two f16, and a tile's sums are added in fp32
 template <int D, int NT, bool F32>
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     float* const stats = reinterpret_cast<float*>(smem + S::ring + S::sums);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + S::ring + S::sums + S::stats);
     int64_t* const found = reinterpret_cast<int64_t*>(bars + kWarps * kStage);
-    Place* const all_places = reinterpret_cast<Place*>(found + 3 * kWarps + 1);
+    Place* const all_places = reinterpret_cast<Place*>(found + 3 * kWarps + 2);
     Left* const lefts = reinterpret_cast<Left*>(all_places + 2 * kWarps);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -348,10 +361,11 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     pdl_trigger();
     pdl_wait();
     {                                                     // this warp's run of units, its sequence and the units before
-        int64_t u = 0, end = 0, b = 0, before = 0;
+        int64_t u = 0, end = 0, b = 0, before = 0, units = 0;
         if (split) {
             const Shares<R, false> shares(a);
-            const int64_t units = shares.total, warps = parts_of(units, gridDim.x * kWarps);
+            units = shares.total;
+            const int64_t warps = parts_of(units, gridDim.x * kWarps);
             const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
             u = i < warps ? run_start<R>(a, shares, quotient(units * i, warps), &b, &before) : units;
             if (warp == kWarps - 1) {
@@ -371,12 +385,14 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         }
         if (lane == 0) {
             found[warp] = u, found[kWarps + 1 + warp] = b, found[2 * kWarps + 1 + warp] = before;
-            if (warp == kWarps - 1) found[kWarps] = end;
+            if (warp == kWarps - 1) found[kWarps] = end, found[3 * kWarps + 1] = units;
             lefts[2 * warp].first = lefts[2 * warp + 1].first = -1;
         }
     }
     __syncthreads();
     const int64_t u0 = found[warp], u1 = found[warp + 1];
+    Cut* const cut = split ? cuts<D, NT>(a, gridDim.x) + blockIdx.x : nullptr;
+    if (split && threadIdx.x == 0) cut->n = 0;
     if (found[0] >= found[kWarps]) return;
 
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
@@ -800,6 +816,12 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         const Seq s = sequence<R>(a, x.b);
         const bool complete = x.ta == 0 && tb == s.tiles;
         const int rows = min(R, s.n * G - x.rt * R);
+        if (threadIdx.x == 0 && x.ta > 0 && !complete) {  // cut at this CTA's start; the first such cut of the group?
+            const int64_t units = found[3 * kWarps + 1], warps = parts_of(units, static_cast<int64_t>(gridDim.x) * kWarps);
+            const int64_t g1 = x.first + kGroupCost + s.tiles;
+            if (quotient(units * (static_cast<int64_t>(blockIdx.x) - 1) * kWarps, warps) <= x.first + kGroupCost)
+                *cut = Cut{s.row0, s.n, x.h, x.rt, static_cast<int>(quotient(g1 * warps - 1, units) / kWarps)};
+        }
         float* const part = reinterpret_cast<float*>(a.workspace) +
                             (static_cast<int64_t>(blockIdx.x) * 2 + (x.ta > 0 ? 0 : 1)) * kPart<D, NT>;
         for (int y = threadIdx.x; y < R * (D / 4); y += kWarps * 32) {
@@ -828,60 +850,54 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     }
 }
 
-// A group that several CTAs took parts of, joined in their order: by CTA i of here if CTA i + 1 of k_attend is the second
-// that holds some of it.
+// A group that several CTAs took parts of, joined in their order; a row a warp.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas) {
-    constexpr int R = 8 * NT;
-    __shared__ int64_t found[3];
+    constexpr int R = 8 * NT, kCols = (D + 127) / 128;    // float4 columns a lane
     pdl_trigger();
     pdl_wait();
-    const int64_t i = blockIdx.x + 1;
-    if (threadIdx.x < 32) {
-        const Shares<R, false> shares(a);
-        const int64_t warps = parts_of(shares.total, static_cast<int64_t>(ctas) * kWarps);
-        int64_t b = 0, before = 0;
-        const bool in = i * kWarps < warps;
-        if (in) shares.find(a, quotient(shares.total * i * kWarps, warps), &b, &before);
-        if (threadIdx.x == 0) found[0] = in ? shares.total : 0, found[1] = b, found[2] = before;
-    }
-    __syncthreads();
-    const int64_t units = found[0];
-    if (units == 0) return;
-    const int64_t warps = parts_of(units, static_cast<int64_t>(ctas) * kWarps);
-    const int64_t x = quotient(units * i * kWarps, warps);            // where CTA i's run starts
-    const Seq s = sequence<R>(a, found[1]);
-    const int per = kGroupCost + s.tiles;
-    const int group = static_cast<int>(quotient(x - found[2], per));
-    const int64_t g0 = found[2] + static_cast<int64_t>(group) * per, g1 = g0 + per;
-    // not cut here, or joined by an earlier CTA
-    if (x - g0 <= kGroupCost || quotient(units * (i - 1) * kWarps, warps) > g0 + kGroupCost) return;
-    const int64_t last = quotient(g1 * warps - 1, units) / kWarps;           // the CTA that holds unit g1 - 1
-    const int G = a.Hq / a.cache.Hkv, h = group % a.cache.Hkv, rt = group / a.cache.Hkv;
-    const int rows = min(R, s.n * G - rt * R);
-    // run i - 1 has the group's first tiles as its last part, the others as their first
-    const float* ws = reinterpret_cast<const float*>(a.workspace);
-    auto part = [&](int64_t run) { return ws + (run * 2 + (run == i - 1 ? 1 : 0)) * kPart<D, NT>; };
-    for (int y = threadIdx.x; y < R * (D / 4); y += 256) {
-        const int q = y / (D / 4), d = y % (D / 4) * 4;
-        if (q >= rows) continue;
+    const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const Cut cut = cuts<D, NT>(a, ctas)[i];
+    if (cut.n == 0) return;
+    const int G = a.Hq / a.cache.Hkv, rows = min(R, cut.n * G - cut.rt * R), runs = cut.last - i + 2;
+    // CTA i - 1 has the group's first tiles as its last part, the others as their first
+    const float* const ws = reinterpret_cast<const float*>(a.workspace);
+    auto part = [&](int run) { return ws + (static_cast<int64_t>(i - 1 + run) * 2 + (run == 0 ? 1 : 0)) * kPart<D, NT>; };
+    for (int q = threadIdx.x >> 5; q < rows; q += 8) {
         float m = kLowest, l = 0.0f;
-#pragma unroll 16
-        for (int64_t run = i - 1; run <= last; ++run) m = max_nd(m, part(run)[R * D + 2 * q]);
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int run = lane; run < runs; run += 32) m = max_nd(m, part(run)[R * D + 2 * q]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max_nd(m, __shfl_xor_sync(kFullMask, m, o));
+        float v[kCols][4] = {};
+        for (int first = 0; first < runs; first += 32) {
+            float f = 0.0f;
+            if (first + lane < runs) {
+                const float2 st = *reinterpret_cast<const float2*>(part(first + lane) + R * D + 2 * q);
+                f = exp2_approx(sub_rn(st.x, m));
+                l = __fmaf_rn(st.y, f, l);
+            }
+            const int here = min(32, runs - first);
 #pragma unroll 8
-        for (int64_t run = i - 1; run <= last; ++run) {
-            const float* p = part(run);
-            const float2 st = *reinterpret_cast<const float2*>(p + R * D + 2 * q);
-            const float f = exp2_approx(sub_rn(st.x, m));
-            l = __fmaf_rn(st.y, f, l);
-            const float4 u = *reinterpret_cast<const float4*>(p + q * D + d);
-            v[0] = __fmaf_rn(u.x, f, v[0]), v[1] = __fmaf_rn(u.y, f, v[1]);
-            v[2] = __fmaf_rn(u.z, f, v[2]), v[3] = __fmaf_rn(u.w, f, v[3]);
+            for (int k = 0; k < here; ++k) {
+                const float g = __shfl_sync(kFullMask, f, k);
+                const float* p = part(first + k) + q * D;
+#pragma unroll
+                for (int x = 0; x < kCols; ++x)
+                    if (D >= 128 || lane < D / 4) {
+                        const float4 u = reinterpret_cast<const float4*>(p)[x * 32 + lane];
+                        v[x][0] = __fmaf_rn(u.x, g, v[x][0]), v[x][1] = __fmaf_rn(u.y, g, v[x][1]);
+                        v[x][2] = __fmaf_rn(u.z, g, v[x][2]), v[x][3] = __fmaf_rn(u.w, g, v[x][3]);
+                    }
+            }
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l = add_rn(l, __shfl_xor_sync(kFullMask, l, o));
         int query, head;
-        split_row(s.n, G, rt * R + q, &query, &head);
-        Finish(a, h * G + head, h, m, l).store(a, s.row0 + query, h * G + head, d, v);
+        split_row(cut.n, G, cut.rt * R + q, &query, &head);
+        const Finish end(a, cut.h * G + head, cut.h, m, l);
+#pragma unroll
+        for (int x = 0; x < kCols; ++x)
+            if (D >= 128 || lane < D / 4) end.store(a, cut.row0 + query, cut.h * G + head, (x * 32 + lane) * 4, v[x]);
     }
 }
 
@@ -943,7 +959,7 @@ int64_t attend_workspace(const AttendArgs& a) {
     const int R = two_tiles(a) ? 16 : 8;
     int split;
     const int64_t grid = grid_of(a, R, &split);
-    return split ? grid * 2 * R * (a.cache.D + 2) * 4 : 0;
+    return split ? grid * (2 * R * (a.cache.D + 2) * 4 + static_cast<int64_t>(sizeof(Cut))) : 0;
 }
 
 int launch_attend(const AttendArgs& a, void* stream) {
