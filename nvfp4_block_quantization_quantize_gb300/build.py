@@ -27,7 +27,8 @@ LIB_PATH = os.path.join(PKG, "libnvfp4_gb300.so")
 CALL_PATH = os.path.join(PKG, "_nvfp4_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALL_ABI_PATH = os.path.join(BUILD_DIR, "_nvfp4_call.abi")      # what CALL_PATH was built for
 SOURCES = ["nvfp4_rows.cu", "nvfp4_tiles.cu", "nvfp4_aux.cu", "nvfp4_mm.cu", "nvfp4_norm.cu", "nvfp4_mv.cu",
-           "nvfp4_grouped.cu", "nvfp4_cache.cu", "nvfp4_attend.cu", "nvfp4_api.cu"]
+           "nvfp4_grouped.cu", "nvfp4_cache.cu", "nvfp4_attend.cu",
+           "nvfp4_attend_many.cu", "nvfp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-ftz=false",
          "-prec-div=true", "-prec-sqrt=true", "-fmad=false", "-I", INCLUDE]

@@ -20,123 +20,19 @@
 // end, and those cut between CTAs leave partial sums in the workspace, which k_join adds in
 // order.  A warp works on pairs of tiles; its own ring of shared memory is filled by bulk copies,
 // one or two a pair, that run ahead across groups.
-#include "nvfp4_block.cuh"
-#include "nvfp4_tensor.cuh"
+#include "nvfp4_attend.cuh"
 
 namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 8;
-// What a group costs besides its tiles (its queries, its end), in tiles: the first units of every group.  A run is not
-// cut inside them.
-#ifndef NVFP4_GC
-#define NVFP4_GC 8
-#endif
-constexpr int kGroupCost = NVFP4_GC;
 constexpr int kMinTiles = 4;                              // a warp's run is not made shorter
 static_assert(kGroupCost < kWarps * kMinTiles, "a CTA's run holds some of a group that is cut at its end");
-constexpr float kLowest = -3.4028234663852886e38f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNone = -__builtin_huge_valf();          // a masked logit
-constexpr float kSlack = 8.0f;                            // a weight may reach 2^8 before the maximum is raised
 
-template <int D>
-constexpr int kRecord = 18 * D;                           // bytes of a tile
 template <int D, int NT>
 constexpr int kStages = D == 64 ? 4 : D == 128 && NT == 1 ? 2 : D == 128 ? 4 : 2;      // pairs of tiles a warp's ring holds
 
 // ---- who does what ------------------------------------------------------------------------------
-// A sequence's share of the work.
-struct Seq {
-    int64_t row0;             // its first query
-    int n, len;               // queries, keys
-    int t0, tiles;            // tiles of 16 keys that some query sees
-    int runs;                 // row tiles times KV heads: groups
-    int64_t units;            // runs * (kGroupCost + tiles)
-};
-
-template <int R>
-__device__ __forceinline__ Seq sequence(const AttendArgs& a, int64_t b) {
-    Seq s;
-    int64_t end;
-    if (a.offsets) {
-        s.row0 = min(max(__ldg(a.offsets + b), int64_t{0}), a.T);
-        end = min(max(__ldg(a.offsets + b + 1), int64_t{0}), a.T);
-    } else {
-        s.row0 = b;
-        end = b + 1;
-    }
-    s.n = end > s.row0 ? static_cast<int>(end - s.row0) : 0;
-    const int64_t cap = a.width * a.cache.page_size;
-    s.len = static_cast<int>(min(max(__ldg(a.lengths + b), int64_t{0}), cap));
-    const int first = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
-    s.t0 = first / 16;
-    s.tiles = max(0, (s.len + 15) / 16 - s.t0);
-    const int G = a.Hq / a.cache.Hkv;
-    const int64_t rows = static_cast<int64_t>(s.n) * G;
-    s.runs = static_cast<int>((rows + R - 1) / R) * a.cache.Hkv;
-    s.units = static_cast<int64_t>(s.runs) * (kGroupCost + s.tiles);
-    return s;
-}
-
-// x / y of values that mostly fit in 32 bits (the 64-bit division costs a third of a microsecond)
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    if ((x | y) >> 32 == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
-}
-
-__device__ __forceinline__ int64_t scan_add(int64_t v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(kFullMask, v, o);
-        if ((threadIdx.x & 31) >= o) v += u;
-    }
-    return v;
-}
-
-// The sequences' shares of the work, in units or (GROUPS) in groups, added up.  A warp holds it: each lane the sequences
-// lane, lane + 32, ..; the first 32 stay in registers.
-template <int R, bool GROUPS>
-struct Shares {
-    int64_t first, upto;      // this lane's first sequence's share; that of the first sequences up to it
-    int64_t total;
-
-    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) {
-        if (b >= a.B) return 0;
-        const Seq q = sequence<R>(a, b);
-        return GROUPS ? q.runs : q.units;
-    }
-
-    __device__ __forceinline__ explicit Shares(const AttendArgs& a) {
-        const int lane = threadIdx.x & 31;
-        first = share(a, lane);
-        upto = scan_add(first);
-        total = __shfl_sync(kFullMask, upto, 31);
-        if (a.B > 32) {
-            int64_t sum = 0;
-            for (int64_t b = lane + 32; b < a.B; b += 32) sum += share(a, b);
-            total += __shfl_sync(kFullMask, scan_add(sum), 31);
-        }
-    }
-
-    // the sequence that unit x < total lies in, and the units before it
-    __device__ __forceinline__ void find(const AttendArgs& a, int64_t x, int64_t* seq, int64_t* before) const {
-        int64_t base = 0, own = first, s = upto;
-        for (int64_t b0 = 0;; b0 += 32) {
-            const unsigned has = __ballot_sync(kFullMask, base + s > x);
-            if (has || b0 + 32 >= a.B) {
-                const int l = has ? __ffs(has) - 1 : 0;
-                *seq = b0 + l;
-                *before = base + __shfl_sync(kFullMask, s - own, l);
-                return;
-            }
-            base += __shfl_sync(kFullMask, s, 31);
-            own = share(a, b0 + 32 + (threadIdx.x & 31));
-            s = scan_add(own);
-        }
-    }
-};
-
 // warps that take part
 __device__ __forceinline__ int64_t parts_of(int64_t units, int64_t warps) {
     const int64_t most = (units + kMinTiles - 1) / kMinTiles;
@@ -197,44 +93,12 @@ struct Place {
     }
 };
 
-// the query and the head of a row of a sequence's KV head
-__device__ __forceinline__ void split_row(int n, int G, int row, int* query, int* head) {
-    *query = n == 1 ? 0 : row / G;
-    *head = row - *query * G;
-}
-
 // ---- arithmetic ---------------------------------------------------------------------------------
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t bytes) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bytes)));
-    return h;
-}
-
-// a word's four code bytes as f16 pairs times the pair s
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t s, uint32_t* h) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = mul_f16x2(h[i], s);
 }
 
 // an 8 x 8 matrix of 16-bit values, a row's pair a lane, turned
@@ -244,61 +108,11 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {   // 2 ulp
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // what f16 pair h leaves of lo and hi
 __device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return pack_f16(sub_rn(lo, v.x), sub_rn(hi, v.y));
 }
-
-__device__ __forceinline__ float power_of_two(int e) {    // e in [-126, 127]
-    return __int_as_float((e + 127) << 23);
-}
-
-// A row's end: its sums times `by` are its output; m its maximum (of logits times log2 e), l its denominator.
-struct Finish {
-    float by, lse;
-
-    __device__ __forceinline__ Finish(const AttendArgs& a, int head, int h, float m, float l) {
-        float enc, dec = 1.0f, f = 1.0f;
-        if (a.sinks) {
-            const float sink = mul_rn(__ldg(a.sinks + head), kLog2e), top = max_nd(m, sink);
-            f = exp2_approx(sub_rn(m, top));
-            l = __fmaf_rn(l, f, exp2_approx(sub_rn(sink, top)));
-            m = top;
-        }
-        if (a.cache.v_mode != NVFP4_GAMAX_NONE)
-            global_scales(__ldg(a.cache.v_gamax + (a.cache.v_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
-        by = l == 0.0f ? 0.0f : mul_rn(f, div_rn(dec, l));
-        lse = 0.0f;
-        if (a.lse) lse = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
-    }
-
-    // 4 elements from element d
-    __device__ __forceinline__ void store(const AttendArgs& a, int64_t token, int head, int d, float* v) const {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = mul_rn(v[k], by);
-        const int64_t at = (token * a.Hq + head) * a.cache.D + d;
-        if (a.out_dtype == NVFP4_F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-        }
-        if (a.lse && d == 0) a.lse[token * a.Hq + head] = lse;
-    }
-};
 
 // A part of a cut group, as a warp leaves it: the first part of its run lies in `sums`, the last in its ring.
 struct Left {
@@ -953,6 +767,14 @@ cudaError_t launch_d(const AttendArgs& a, cudaStream_t s) {
     return launch_t<D, 1, false>(a, s);
 }
 
+// Sequences of more rows than this go to the tensor-memory kernel.
+constexpr int kManyRows = 64;
+
+// whether a sequence may have that many
+bool may_have_many(const AttendArgs& a) {
+    return a.offsets && a.dtype == NVFP4_BF16 && a.cache.D <= 128 && a.T * (a.Hq / a.cache.Hkv) > kManyRows;
+}
+
 }  // namespace
 
 int64_t attend_workspace(const AttendArgs& a) {
@@ -962,9 +784,17 @@ int64_t attend_workspace(const AttendArgs& a) {
     return split ? grid * (2 * R * (a.cache.D + 2) * 4 + static_cast<int64_t>(sizeof(Cut))) : 0;
 }
 
-int launch_attend(const AttendArgs& a, void* stream) {
+int launch_attend(const AttendArgs& given, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return static_cast<int>(a.cache.D == 64 ? launch_d<64>(a, s) : a.cache.D == 128 ? launch_d<128>(a, s) : launch_d<256>(a, s));
+    AttendArgs a = given;
+    const bool many = may_have_many(a);
+    a.rows_above = 0, a.rows_upto = many ? kManyRows : 1 << 30;
+    cudaError_t e = a.cache.D == 64 ? launch_d<64>(a, s) : a.cache.D == 128 ? launch_d<128>(a, s) : launch_d<256>(a, s);
+    if (e == cudaSuccess && many) {
+        a.rows_above = kManyRows, a.rows_upto = 1 << 30;
+        e = launch_attend_many(a, s);
+    }
+    return static_cast<int>(e);
 }
 
 }  // namespace nvfp4

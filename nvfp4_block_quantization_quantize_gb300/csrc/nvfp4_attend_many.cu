@@ -1,0 +1,549 @@
+// nvfp4_attend_many.cu -- attention of many queries a sequence over a paged NVFP4 cache: the
+// sequences of nvfp4_cache_attention with more rows than the warp-level kernel is for.
+//
+// The rows are a sequence's queries times the heads that share a KV head; two tiles of
+// 128 rows share each block of 128 keys.  4 D operations a row and key: bound by the tensor
+// cores (tcgen05, f16, fp32 sums in tensor memory), with 256 rows' softmax and the decoding of a block beside them.
+//   - Producers (a warpgroup) load the next block's codes into registers while they decode the present one
+//     to f16 in shared memory, exactly (q * dec(s)); keys and values lie alike, 64 elements of a token to 128
+//     swizzled bytes: K-major for S = Q K^T, MN-major for O += P V.
+//   - One warp issues the products: S of tile A, S of B, then for each block O of a tile and its next S.
+//     While one tile's softmax runs the other's products do.
+//   - A softmax warpgroup a tile, a thread a row: S out of tensor memory, weights back as f16 over S,
+//     which P V reads from there.  The maximum is raised only when a weight would pass 2^8; O, in tensor
+//     memory too, is then rescaled.
+// Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
+#include "nvfp4_attend.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kRows = 256;                                // of a group: two tiles of 128
+constexpr int kKeys = 128;                                // of a block
+constexpr int kThreadsMany = 512;                         // softmax A, softmax B, producers, products
+
+template <int D>
+struct Many {
+    static constexpr int half = kKeys * 128;              // 64 elements of 128 tokens
+    static constexpr int tile = D / 64 * half;            // Q of a tile, K or V of a block
+    static constexpr int stages = 2;                      // blocks of K, and of V
+    static constexpr int q = 0, k = 2 * tile, v = k + stages * tile;
+    static constexpr int factor = v + stages * tile;      // [256] fp32
+    static constexpr int bars = factor + kRows * 4;
+    static constexpr int bytes = bars + 256 + 1024;       // and up to 1023 to align
+    // tensor memory: S (and P over it) of A and B, O of A and B
+    static constexpr int s_col = 0, o_col = 2 * kKeys;
+    static constexpr int cols = 2 * kKeys + 2 * D <= 256 ? 256 : 512;
+    static_assert(2 * kKeys + 2 * D <= 512, "O of two tiles fits");
+};
+
+enum Bar { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
+           kPFull = kSFull + 2, kOFull = kPFull + 2, kBars = kOFull + 2 };
+
+// ---- tcgen05 --------------------------------------------------------------------------------------
+// .kind::f16: f16 operands, fp32 sums; B K-major or MN-major
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn) {
+    return 1u << 4 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(N >> 3) << 17 | static_cast<uint32_t>(M >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(ta), "l"(db), "r"(idesc), "r"(acc), "r"(el)
+        : "memory");
+}
+
+// 32 columns of this thread's row
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A warp's wait; it ends too when another one has run out.  False then, for all lanes.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
+    uint32_t ok = 0;
+    for (long it = 0; it < kWaitLimit && !ok; ++it) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (!ok && (it & 15) == 15 && *lost) break;
+    }
+    if (!ok) *lost = 1;
+    return __all_sync(kFullMask, ok);
+}
+
+// A group: 256 rows of a sequence's KV head, and its blocks of keys.
+struct Item {
+    Seq s;
+    int64_t b;
+    int h, rt, rows, blocks, j0;      // rows of it; the first key of its first block
+    int first, last;                  // queries of its first and last row
+};
+
+template <class S>
+__device__ __forceinline__ Item item_of(const AttendArgs& a, const S& shares, int64_t x) {
+    Item t;
+    int64_t before;
+    shares.find(a, x, &t.b, &before);
+    t.s = sequence<kRows>(a, t.b);
+    const int run = static_cast<int>(x - before), G = a.Hq / a.cache.Hkv;
+    // the last rows first: with a causal mask they have the most keys
+    t.h = run % a.cache.Hkv, t.rt = t.s.runs / a.cache.Hkv - 1 - run / a.cache.Hkv;
+    t.rows = min(kRows, t.s.n * G - t.rt * kRows);
+    int head;
+    split_row(t.s.n, G, t.rt * kRows, &t.first, &head);
+    split_row(t.s.n, G, t.rt * kRows + t.rows - 1, &t.last, &head);
+    const int pos0 = t.s.len - t.s.n;
+    const int lo = a.window > 0 ? max(0, pos0 + t.first - a.window + 1) : 0;
+    const int hi = a.causal ? min(t.s.len, max(pos0 + t.last + 1, 0)) : t.s.len;
+    t.j0 = lo / 16 * 16;
+    t.blocks = hi > t.j0 ? (hi - t.j0 + kKeys - 1) / kKeys : 0;
+    return t;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArgs a) {
+    using M = Many<D>;
+    constexpr int kGroups = D / 16;                       // blocks of 16 elements of a token
+    extern __shared__ uint8_t dynamic[];
+    uint8_t* const smem = dynamic + (1024 - smem_addr(dynamic) % 1024) % 1024;
+    float* const factors = reinterpret_cast<float*>(smem + M::factor);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + M::bars);
+    uint32_t* const tmem_base = reinterpret_cast<uint32_t*>(bars + kBars);
+    volatile int* const lost = reinterpret_cast<volatile int*>(tmem_base + 1);
+    uint32_t* const there = tmem_base + 2;                // [4]: the tiles of a block that have a page
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, t = threadIdx.x & 127;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_base)),
+                     "r"(M::cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < kBars; ++i) {
+            const bool threads = i == kQFull || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull);
+            mbar_init(bars + i, threads ? 128 : 1);
+        }
+        *lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t tmem = *tmem_base;
+    const Shares<kRows, true> shares(a);
+    const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
+    uint32_t n = 0, items = 0;                            // blocks and items so far
+    bool ok = true;
+
+    if (wg == 2) {
+        // ---- producers
+        uint2 w[kGroups];                                 // the next half block's codes: 128 tokens' D / 16 groups over 128 threads
+        uint8_t sc[kGroups];
+        constexpr int kAtOnce = 128 / (16 * kGroups) > 0 ? 128 / (16 * kGroups) : 1;      // tiles the threads cover at once
+        constexpr int kTurns = 8 / kAtOnce;
+        static_assert(16 * kGroups * kAtOnce == 128 && kTurns == kGroups, "a thread takes D / 16 groups");
+        const int in_tile = t % (16 * kGroups), mine = t / (16 * kGroups);      // group of a tile; which of the tiles at once
+        const int token = in_tile / kGroups, grp = in_tile % kGroups;
+        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x, ++items) {
+            const Item it = item_of(a, shares, x);
+            if (it.blocks == 0) {
+                --items;
+                continue;
+            }
+            const int pos0 = it.s.len - it.s.n;
+            const int seen_lo = a.window > 0 ? max(0, pos0 + it.first - a.window + 1) : 0;
+            const int32_t* const table = a.pages + it.b * a.width;
+            const int tiles_end = (it.s.len + 15) / 16;
+            // a lane below 8 holds the page of a tile of the block whose loads come next (-1: none), and its first byte
+            int32_t page = -1;
+            int tip = 0;
+            auto find_pages = [&](int block) {
+                page = -1;
+                const int tl = it.j0 / 16 + block * 8 + (lane & 7);
+                if (block < it.blocks && tl < tiles_end) {
+                    const int p = tl / per_page;
+                    tip = tl - p * per_page;
+                    page = __ldg(table + p);
+                    if (page < 0 || page >= a.cache.pages) page = -1;
+                }
+            };
+            auto load = [&](bool is_v) {
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int from = i * kAtOnce + mine;
+                    const int32_t p = __shfl_sync(kFullMask, page, from);
+                    const int tp = __shfl_sync(kFullMask, tip, from);
+                    w[i] = make_uint2(0u, 0u);
+                    sc[i] = 0;
+                    if (p >= 0) {
+                        const uint8_t* rec = a.cache.data +
+                            ((static_cast<int64_t>(p) * a.cache.Hkv + it.h) * per_page + tp) * kRecord<D> + (is_v ? 9 * D : 0);
+                        w[i] = __ldg(reinterpret_cast<const uint2*>(rec) + in_tile);
+                        sc[i] = __ldg(rec + 8 * D + in_tile);
+                    }
+                }
+            };
+            // 16 elements a turn to two 16-byte pieces; the upper half's threads store the second piece first, so that
+            // 8 threads' pieces lie in 8 bank groups
+            auto store = [&](uint8_t* base, bool is_v, int j0) {
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int row = (i * kAtOnce + mine) * 16 + token;
+                    uint32_t s = sc[i], h[8];
+                    if (is_v && (j0 + row < seen_lo || j0 + row >= it.s.len)) s = 0;      // perhaps never written
+                    const uint32_t u = e4m3_pair(s | s << 8);
+                    decode4(w[i].x, u, h);
+                    decode4(w[i].y, u, h + 4);
+                    uint8_t* const p = base + grp / 4 * M::half + row * 128;
+                    const int c0 = 2 * (grp % 4), swap = grp / 4 & 1;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    *reinterpret_cast<uint4*>(p + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(p + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+                }
+            };
+            find_pages(0);
+            load(false);
+            // ---- this item's queries, two rows a thread
+            if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
+            for (int tile = 0; ok && tile < 2; ++tile) {
+                const int r = tile * 128 + t;
+                if (tile == 1 && it.rows <= 128) break;
+                const bool in = r < it.rows;
+                int query, head;
+                split_row(it.s.n, G, it.rt * kRows + min(r, it.rows - 1), &query, &head);
+                const uint16_t* src = static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
+                                      (static_cast<int64_t>(it.h) * G + head) * D;
+                uint32_t top = 0;
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(top, u.x), u.y), u.z), u.w);
+                }
+                top = max(top << 16, top & 0xFFFF0000u);
+                const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
+                const float down = copysignf(power_of_two(-ex), a.scale);
+                float dec = 1.0f, enc;
+                if (a.cache.k_mode != NVFP4_GAMAX_NONE)
+                    global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? it.h : 0)), a.cache.bound, enc, dec);
+                factors[r] = mul_rn(power_of_two(ex), mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec));
+                uint8_t* const dst = smem + M::q + tile * M::tile + t * 128;
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = in ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                    *reinterpret_cast<uint4*>(dst + i / 8 * M::half + (((i & 7) ^ (t & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+            if (!ok) break;
+            fence_async();
+            arrive(bars + kQFull);
+            // ---- its blocks
+            for (int blk = 0; blk < it.blocks; ++blk, ++n) {
+                const int st = n & 1;
+                const uint32_t ph = n >> 1 & 1;
+                const int j0 = it.j0 + blk * kKeys;
+                if (n >= 2 && !(ok = wait(bars + kKEmpty + st, ph ^ 1, lost))) break;
+                store(smem + M::k + st * M::tile, false, j0);
+                const unsigned have = __ballot_sync(kFullMask, lane < 8 && page >= 0);
+                if (t == 0) there[n & 3] = have;
+                fence_async();
+                arrive(bars + kKFull + st);
+                load(true);
+                if (n >= 2 && !(ok = wait(bars + kVEmpty + st, ph ^ 1, lost))) break;
+                store(smem + M::v + st * M::tile, true, j0);
+                fence_async();
+                arrive(bars + kVFull + st);
+                find_pages(blk + 1);
+                load(false);
+            }
+        }
+    } else if (warp == 12) {
+        // ---- products
+        const uint32_t el = elect_one();
+        const uint32_t id_s = idesc_f16(128, kKeys, false), id_o = idesc_f16(128, D, true);
+        auto qk = [&](int tile, int st) {
+            const uint64_t q = smem_desc(smem_addr(smem) + M::q + tile * M::tile, 16, 1024, 2);
+            const uint64_t k = smem_desc(smem_addr(smem) + M::k + st * M::tile, 16, 1024, 2);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint64_t step = (i / 4 * M::half + i % 4 * 32) >> 4;
+                mma_ss(el, tmem + M::s_col + tile * kKeys, q + step, k + step, id_s, i > 0);
+            }
+            commit_warp<1>(el, bars + kSFull + tile);
+        };
+        auto pv = [&](int tile, int st, bool first) {
+            const uint64_t v = smem_desc(smem_addr(smem) + M::v + st * M::tile, M::half, 1024, 2);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+                mma_ts(el, tmem + M::o_col + tile * D, tmem + M::s_col + tile * kKeys + i * 8, v + (i * 2048 >> 4), id_o, !first || i > 0);
+        };
+        uint32_t turn_b = 0;                              // blocks that tile B took part in
+        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x) {
+            const Item it = item_of(a, shares, x);
+            if (it.blocks == 0) continue;
+            const bool two = it.rows > 128;
+            if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
+            if (!(ok = wait(bars + kKFull + (n & 1), n >> 1 & 1, lost))) break;
+            fence_after();
+            qk(0, n & 1);
+            if (two) qk(1, n & 1);
+            commit_warp<1>(el, bars + kKEmpty + (n & 1));
+            for (int blk = 0; blk < it.blocks; ++blk, ++n) {
+                const bool more = blk + 1 < it.blocks;
+                const int st = n & 1, st1 = (n + 1) & 1;
+                if (!(ok = wait(bars + kVFull + st, n >> 1 & 1, lost))) break;
+                if (!(ok = wait(bars + kPFull, n & 1, lost))) break;
+                fence_after();
+                pv(0, st, blk == 0);
+                if (!more) commit_warp<1>(el, bars + kOFull);
+                if (more) {
+                    if (!(ok = wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost))) break;
+                    fence_after();
+                    qk(0, st1);
+                }
+                if (two) {
+                    if (!(ok = wait(bars + kPFull + 1, turn_b++ & 1, lost))) break;
+                    fence_after();
+                    pv(1, st, blk == 0);
+                    if (!more) commit_warp<1>(el, bars + kOFull + 1);
+                }
+                commit_warp<1>(el, bars + kVEmpty + st);
+                if (more) {
+                    if (two) qk(1, st1);
+                    commit_warp<1>(el, bars + kKEmpty + st1);
+                }
+            }
+            if (!ok) break;
+            commit_warp<1>(el, bars + kQEmpty);
+            ++items;
+        }
+    } else if (wg < 2) {
+        // ---- softmax of tile wg: this thread's row
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;           // 32 lanes of tensor memory a warp
+        const uint32_t s_at = tmem + lanes + M::s_col + wg * kKeys, o_at = tmem + lanes + M::o_col + wg * D;
+        uint32_t turn = 0, mine = 0;                      // blocks and items that this tile took part in
+        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x) {
+            const Item it = item_of(a, shares, x);
+            const int r = wg * 128 + t, row = it.rt * kRows + r;
+            int query, head;
+            split_row(it.s.n, G, min(row, it.s.n * G - 1), &query, &head);
+            float m = kLowest, l = 0.0f;
+            if (it.blocks > 0 && wg * 128 < it.rows) {
+                const int p = it.s.len - it.s.n + query;
+                const int hi = a.causal ? min(it.s.len, max(p + 1, 0)) : it.s.len, lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+                if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
+                const float c = factors[r];
+                for (int blk = 0; blk < it.blocks; ++blk, ++turn) {
+                    const uint32_t block = n + blk;
+                    const int j0 = it.j0 + blk * kKeys;
+                    // (a tile that sat out an item keeps its own count of S and P)
+                    if (!(ok = wait(bars + kSFull + wg, turn & 1, lost))) break;
+                    fence_after();
+                    const uint32_t have = there[block & 3];
+                    const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
+                    uint32_t v[32];
+                    float top = kNone;
+#pragma unroll
+                    for (int q = 0; q < kKeys / 32; ++q) {
+                        __syncwarp();
+                        tmem_load32(s_at + 32 * q, v);
+                        tmem_wait_load();
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = 32 * q + i;
+                                if ((have >> (j / 16) & 1) && j0 + j >= lo && j0 + j < hi) top = max_nd(top, __uint_as_float(v[i]));
+                            }
+                        }
+                    }
+                    // raised where a weight would pass 2^kSlack
+                    const bool raise = __fmaf_rn(top, c, -m) > kSlack && top > kNone;
+                    if (__any_sync(kFullMask, raise)) {       // for the warp's 32 rows
+                        const float to = raise ? mul_rn(top, c) : m, less = exp2_approx(sub_rn(m, to));
+                        m = to;
+                        l = mul_rn(l, less);
+                        if (blk > 0) {
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                tmem_load32(o_at + 32 * q, v);
+                                tmem_wait_load();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
+                                tmem_store32(o_at + 32 * q, v);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < kKeys / 32; ++q) {
+                        tmem_load32(s_at + 32 * q, v);
+                        tmem_wait_load();
+                        uint32_t h[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float y[2];
+                            unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(c, c), pack2(-m, -m)), y[0], y[1]);
+                            if (!whole) {
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int j = 32 * q + i + k;
+                                    if (!((have >> (j / 16) & 1) && j0 + j >= lo && j0 + j < hi)) y[k] = kNone;
+                                }
+                            }
+                            y[0] = exp2_approx(y[0]);
+                            y[1] = exp2_approx(y[1]);
+                            l = add_rn(l, add_rn(y[0], y[1]));
+                            h[i / 2] = pack_f16(y[0], y[1]);
+                        }
+                        tmem_store16(s_at + 16 * q, h);
+                    }
+                    tmem_wait_store();
+                    fence_before();
+                    arrive(bars + kPFull + wg);
+                }
+                if (!ok) break;
+                if (!(ok = wait(bars + kOFull + wg, mine & 1, lost))) break;
+                fence_after();
+                ++mine;
+            }
+            if (it.blocks > 0) {
+                n += it.blocks;
+                ++items;
+            }
+            // ---- the row's output (a group without keys gives zeros)
+            if (wg * 128 < it.rows) {
+                const Finish f(a, it.h * G + head, it.h, m, l);
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    if (it.blocks > 0) {
+                        __syncwarp();
+                        tmem_load32(o_at + 32 * q, v);
+                        tmem_wait_load();
+                    }
+                    if (r < it.rows)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float y[4] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])};
+                            f.store(a, it.s.row0 + query, it.h * G + head, 32 * q + i, y);
+                        }
+                }
+                fence_before();
+            }
+        }
+        if (!ok) {                                        // NaN to every row that this thread may have left
+            for (int64_t x = blockIdx.x; x < shares.total; x += gridDim.x) {
+                const Item it = item_of(a, shares, x);
+                const int r = wg * 128 + t;
+                if (r >= it.rows) continue;
+                int query, head;
+                split_row(it.s.n, G, it.rt * kRows + r, &query, &head);
+                const Finish f(a, it.h * G + head, it.h, 0.0f, __int_as_float(0x7FC00000));
+                for (int d = 0; d < D; d += 4) {
+                    float y[4] = {f.by, f.by, f.by, f.by};
+                    f.store(a, it.s.row0 + query, it.h * G + head, d, y);
+                }
+            }
+        }
+    }
+    if (!ok) settle();
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(M::cols));
+    }
+}
+
+template <int D>
+cudaError_t launch_many(const AttendArgs& a, cudaStream_t s) {
+    static thread_local int dev_of = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev_of != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(k_attend_many<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D>::bytes);
+        if (e != cudaSuccess) return e;
+        dev_of = dev;
+    }
+    const int64_t rows = a.T * (a.Hq / a.cache.Hkv);
+    const int64_t items = (rows / kRows + (a.B < rows ? a.B : rows)) * a.cache.Hkv;      // at most
+    const int64_t grid = items < sm_count() ? items : sm_count();
+    return launch_pdl(k_attend_many<D>, dim3(static_cast<unsigned>(grid)), dim3(kThreadsMany), Many<D>::bytes, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s) {
+    return a.cache.D == 64 ? launch_many<64>(a, s) : launch_many<128>(a, s);
+}
+
+}  // namespace nvfp4

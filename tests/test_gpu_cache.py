@@ -229,6 +229,17 @@ CASES = [
     ([0, 0], None, 4, 2, 128, 16, "f32", "none", {"sinks": True}),
     ([700 + 13 * i for i in range(70)], None, 16, 2, 128, 16, "bf16", "head", {}),
     ([1 + i % 40 for i in range(100)], None, 3, 3, 64, 16, "bf16", "none", {}),
+    # many rows a sequence (the tensor-memory kernel), next to few, none, and queries before the first key
+    ([64], [64], 2, 1, 128, 16, "bf16", "none", {}),
+    ([65], [65], 1, 1, 64, 16, "bf16", "head", {}),
+    ([1000, 5, 0, 129, 3000], [300, 5, 0, 129, 1], 8, 2, 128, 32, "bf16", "head", {"sinks": True}),
+    ([1000, 5, 0, 129, 3000], [300, 5, 0, 129, 1], 8, 2, 64, 16, "bf16", "tensor", {"window": 200}),
+    ([40, 513, 0], [100, 70, 80], 5, 1, 128, 48, "bf16", "none", {}),
+    ([700, 900], [700, 900], 6, 2, 128, 64, "bf16", "none", {"causal": False, "window": 64}),
+    ([5000], [257], 4, 4, 128, 64, "bf16", "tensor", {}),
+    ([400 + 37 * i for i in range(30)], [65 + 7 * i for i in range(30)], 6, 3, 64, 16, "bf16", "none", {}),
+    ([900], [450], 12, 4, 128, 64, "bf16", "head", {"window": 1}),
+    ([900], [450], 12, 4, 128, 64, "bf16", "head", {"scale": -0.05}),
 ]
 
 
