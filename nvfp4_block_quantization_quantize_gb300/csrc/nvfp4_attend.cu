@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int i = k; i < 4; i += 2)
-                                    if (w[e][nt][i] > kNone) m = max_nd(m, mul_rn(sc[e][nt][i], factor[nt][k]));
+                                    if (w[e][nt][i] > kNone) m = max_nd(m, __fmul_ru(sc[e][nt][i], factor[nt][k]));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 4));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 8));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 16));

@@ -22,6 +22,10 @@ constexpr int kRows = 256;                                // of a group: two til
 constexpr int kKeys = 128;                                // of a block
 constexpr int kThreadsMany = 512;                         // softmax A, softmax B, producers, products
 
+// registers of a thread after the launch's 128 are shared out anew
+constexpr int kSoftmaxRegisters = 176, kProducerRegisters = 96, kProductRegisters = 64;
+static_assert(256 * kSoftmaxRegisters + 128 * kProducerRegisters + 128 * kProductRegisters <= kThreadsMany * 128, "no more than were launched");
+
 template <int D>
 struct Many {
     static constexpr int half = kKeys * 128;              // 64 elements of 128 tokens
@@ -90,15 +94,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -114,6 +109,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // A warp's wait; it ends too when another one has run out.  False then, for all lanes.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
@@ -161,6 +161,49 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, const S& shares, in
     return t;
 }
 
+// bits from .. to - 1 of 32
+__device__ __forceinline__ uint32_t columns(int from, int to) {
+    const uint32_t below = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+    return from >= 32 ? 0u : from <= 0 ? below : below & ~((1u << from) - 1u);
+}
+
+// The maximum of this thread's row raised to that of the block, l and the row of O rescaled, for the rows of a warp that
+// need it (the others keep theirs): (maximum, l).  The maximum is rounded up, so that no logit exceeds it.  Out of line: it
+// runs for the first blocks of a group.
+template <int D>
+__device__ __noinline__ float2 raised(float m, float l, bool need, float c, int lo, int hi, uint32_t have, uint32_t s_at,
+                                     uint32_t o_at, bool sums) {
+    float top = kNone;
+#pragma unroll 1
+    for (int q = 0; q < kKeys / 32; ++q) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_load32(s_at + 32 * q, v);
+        tmem_wait_load();
+        const uint32_t see = columns(lo - 32 * q, hi - 32 * q) &
+                             ((have >> 2 * q & 1 ? 0xFFFFu : 0u) | (have >> 2 * q & 2 ? 0xFFFF0000u : 0u));
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (see >> i & 1) top = max_nd(top, __uint_as_float(v[i]));
+    }
+    const float to = need ? __fmul_ru(top, c) : m, less = exp2_approx(sub_rn(m, to));
+    if (sums) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_load32(o_at + 32 * q, v);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
+            tmem_store32(o_at + 32 * q, v);
+        }
+        tmem_wait_store();
+    }
+    __syncwarp();
+    return make_float2(to, mul_rn(l, less));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArgs a) {
     using M = Many<D>;
@@ -201,8 +244,9 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
 
     if (wg == 2) {
         // ---- producers
+        registers_down<kProducerRegisters>();
         uint2 w[kGroups];                                 // the next half block's codes: 128 tokens' D / 16 groups over 128 threads
-        uint8_t sc[kGroups];
+        uint32_t sc[kGroups];
         constexpr int kAtOnce = 128 / (16 * kGroups) > 0 ? 128 / (16 * kGroups) : 1;      // tiles the threads cover at once
         constexpr int kTurns = 8 / kAtOnce;
         static_assert(16 * kGroups * kAtOnce == 128 && kTurns == kGroups, "a thread takes D / 16 groups");
@@ -218,51 +262,53 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             const int seen_lo = a.window > 0 ? max(0, pos0 + it.first - a.window + 1) : 0;
             const int32_t* const table = a.pages + it.b * a.width;
             const int tiles_end = (it.s.len + 15) / 16;
-            // a lane below 8 holds the page of a tile of the block whose loads come next (-1: none), and its first byte
-            int32_t page = -1;
-            int tip = 0;
+            // a lane below 8 holds where a tile of the block whose loads come next lies in the cache (-1: nowhere)
+            int64_t at = -1;
             auto find_pages = [&](int block) {
-                page = -1;
+                at = -1;
                 const int tl = it.j0 / 16 + block * 8 + (lane & 7);
                 if (block < it.blocks && tl < tiles_end) {
                     const int p = tl / per_page;
-                    tip = tl - p * per_page;
-                    page = __ldg(table + p);
-                    if (page < 0 || page >= a.cache.pages) page = -1;
+                    const int32_t page = __ldg(table + p);
+                    if (page >= 0 && page < a.cache.pages)
+                        at = ((static_cast<int64_t>(page) * a.cache.Hkv + it.h) * per_page + (tl - p * per_page)) * kRecord<D>;
                 }
             };
             auto load = [&](bool is_v) {
+                const uint8_t* const codes = a.cache.data + (is_v ? 9 * D : 0) + in_tile * 8;
+                const uint8_t* const scales = a.cache.data + (is_v ? 17 * D : 8 * D) + in_tile;
 #pragma unroll
                 for (int i = 0; i < kTurns; ++i) {
-                    const int from = i * kAtOnce + mine;
-                    const int32_t p = __shfl_sync(kFullMask, page, from);
-                    const int tp = __shfl_sync(kFullMask, tip, from);
+                    const int64_t from = __shfl_sync(kFullMask, at, i * kAtOnce + mine);
                     w[i] = make_uint2(0u, 0u);
                     sc[i] = 0;
-                    if (p >= 0) {
-                        const uint8_t* rec = a.cache.data +
-                            ((static_cast<int64_t>(p) * a.cache.Hkv + it.h) * per_page + tp) * kRecord<D> + (is_v ? 9 * D : 0);
-                        w[i] = __ldg(reinterpret_cast<const uint2*>(rec) + in_tile);
-                        sc[i] = __ldg(rec + 8 * D + in_tile);
+                    if (from >= 0) {
+                        w[i] = __ldg(reinterpret_cast<const uint2*>(codes + from));
+                        sc[i] = __ldg(scales + from);
                     }
                 }
             };
-            // 16 elements a turn to two 16-byte pieces; the upper half's threads store the second piece first, so that
+            // 16 elements a turn to two 16-byte pieces; the upper half's threads store their second piece first, so that
             // 8 threads' pieces lie in 8 bank groups
+            const int swap = grp / 4 & 1, piece = 2 * (grp % 4) + swap;
+            const uint32_t to = grp / 4 * M::half + (mine * 16 + token) * 128;
+            const uint32_t first = to + ((piece ^ (token & 7)) << 4), second = to + (((piece ^ 1) ^ (token & 7)) << 4);
             auto store = [&](uint8_t* base, bool is_v, int j0) {
+                if (is_v && (j0 < seen_lo || j0 + kKeys > it.s.len)) {      // some were perhaps never written
+#pragma unroll
+                    for (int i = 0; i < kTurns; ++i) {
+                        const int j = j0 + (i * kAtOnce + mine) * 16 + token;
+                        if (j < seen_lo || j >= it.s.len) sc[i] = 0;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < kTurns; ++i) {
-                    const int row = (i * kAtOnce + mine) * 16 + token;
-                    uint32_t s = sc[i], h[8];
-                    if (is_v && (j0 + row < seen_lo || j0 + row >= it.s.len)) s = 0;      // perhaps never written
-                    const uint32_t u = e4m3_pair(s | s << 8);
-                    decode4(w[i].x, u, h);
-                    decode4(w[i].y, u, h + 4);
-                    uint8_t* const p = base + grp / 4 * M::half + row * 128;
-                    const int c0 = 2 * (grp % 4), swap = grp / 4 & 1;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    *reinterpret_cast<uint4*>(p + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-                    *reinterpret_cast<uint4*>(p + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+                    const uint32_t u = e4m3_pair(sc[i] * 257u);
+                    uint32_t h[4];
+                    decode4(swap ? w[i].y : w[i].x, u, h);
+                    *reinterpret_cast<uint4*>(base + first + i * kAtOnce * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+                    decode4(swap ? w[i].x : w[i].y, u, h);
+                    *reinterpret_cast<uint4*>(base + second + i * kAtOnce * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             };
             find_pages(0);
@@ -310,7 +356,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 const int j0 = it.j0 + blk * kKeys;
                 if (n >= 2 && !(ok = wait(bars + kKEmpty + st, ph ^ 1, lost))) break;
                 store(smem + M::k + st * M::tile, false, j0);
-                const unsigned have = __ballot_sync(kFullMask, lane < 8 && page >= 0);
+                const unsigned have = __ballot_sync(kFullMask, lane < 8 && at >= 0);
                 if (t == 0) there[n & 3] = have;
                 fence_async();
                 arrive(bars + kKFull + st);
@@ -323,8 +369,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 load(false);
             }
         }
-    } else if (warp == 12) {
+    } else if (wg == 3) {
         // ---- products
+        registers_down<kProductRegisters>();
+        if (warp == 12) {
         const uint32_t el = elect_one();
         const uint32_t id_s = idesc_f16(128, kKeys, false), id_o = idesc_f16(128, D, true);
         auto qk = [&](int tile, int st) {
@@ -383,8 +431,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             commit_warp<1>(el, bars + kQEmpty);
             ++items;
         }
-    } else if (wg < 2) {
+        }
+    } else {
         // ---- softmax of tile wg: this thread's row
+        registers_up<kSoftmaxRegisters>();
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;           // 32 lanes of tensor memory a warp
         const uint32_t s_at = tmem + lanes + M::s_col + wg * kKeys, o_at = tmem + lanes + M::o_col + wg * D;
         uint32_t turn = 0, mine = 0;                      // blocks and items that this tile took part in
@@ -407,64 +457,47 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     fence_after();
                     const uint32_t have = there[block & 3];
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
-                    uint32_t v[32];
-                    float top = kNone;
+                    // weights by the present maximum, which is nearly always high enough; where one would pass 2^kSlack
+                    // it is raised and they are made again
+                    uint32_t h[kKeys / 2];
+                    for (int again = 0;; ++again) {
+                        float more = 0.0f, high = kNone;
 #pragma unroll
-                    for (int q = 0; q < kKeys / 32; ++q) {
-                        __syncwarp();
-                        tmem_load32(s_at + 32 * q, v);
-                        tmem_wait_load();
-                        if (whole) {
+                        for (int q = 0; q < kKeys / 32; ++q) {
+                            uint32_t v[32];
+                            tmem_load32(s_at + 32 * q, v);
+                            tmem_wait_load();
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int j = 32 * q + i;
-                                if ((have >> (j / 16) & 1) && j0 + j >= lo && j0 + j < hi) top = max_nd(top, __uint_as_float(v[i]));
+                            for (int i = 0; i < 32; i += 2) {
+                                float y0, y1;
+                                unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(c, c), pack2(-m, -m)), y0, y1);
+                                v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
                             }
-                        }
-                    }
-                    // raised where a weight would pass 2^kSlack
-                    const bool raise = __fmaf_rn(top, c, -m) > kSlack && top > kNone;
-                    if (__any_sync(kFullMask, raise)) {       // for the warp's 32 rows
-                        const float to = raise ? mul_rn(top, c) : m, less = exp2_approx(sub_rn(m, to));
-                        m = to;
-                        l = mul_rn(l, less);
-                        if (blk > 0) {
-#pragma unroll
-                            for (int q = 0; q < D / 32; ++q) {
-                                tmem_load32(o_at + 32 * q, v);
-                                tmem_wait_load();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
-                                tmem_store32(o_at + 32 * q, v);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < kKeys / 32; ++q) {
-                        tmem_load32(s_at + 32 * q, v);
-                        tmem_wait_load();
-                        uint32_t h[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float y[2];
-                            unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(c, c), pack2(-m, -m)), y[0], y[1]);
                             if (!whole) {
+                                const uint32_t see = columns(lo - j0 - 32 * q, hi - j0 - 32 * q) &
+                                                     ((have >> 2 * q & 1 ? 0xFFFFu : 0u) | (have >> 2 * q & 2 ? 0xFFFF0000u : 0u));
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int j = 32 * q + i + k;
-                                    if (!((have >> (j / 16) & 1) && j0 + j >= lo && j0 + j < hi)) y[k] = kNone;
-                                }
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(see >> i & 1)) v[i] = 0xFF800000u;
                             }
-                            y[0] = exp2_approx(y[0]);
-                            y[1] = exp2_approx(y[1]);
-                            l = add_rn(l, add_rn(y[0], y[1]));
-                            h[i / 2] = pack_f16(y[0], y[1]);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float y0 = __uint_as_float(v[i]), y1 = __uint_as_float(v[i + 1]);
+                                high = max3(high, y0, y1);
+                                y0 = exp2_approx(y0), y1 = exp2_approx(y1);
+                                more = add_rn(more, add_rn(y0, y1));
+                                h[16 * q + i / 2] = pack_f16(y0, y1);
+                            }
                         }
-                        tmem_store16(s_at + 16 * q, h);
+                        if (again || !__any_sync(kFullMask, high > kSlack)) {
+                            l = add_rn(l, more);
+                            break;
+                        }
+                        const float2 x = raised<D>(m, l, high > kSlack, c, lo - j0, hi - j0, have, s_at, o_at, blk > 0);
+                        m = x.x, l = x.y;
                     }
+                    tmem_store32(s_at, h);
+                    tmem_store32(s_at + 32, h + 32);
                     tmem_wait_store();
                     fence_before();
                     arrive(bars + kPFull + wg);
