@@ -10,8 +10,9 @@
 //   - One warp issues the products: S of tile A, S of B, then for each block O of a tile and its next S.
 //     While one tile's softmax runs the other's products do.
 //   - A softmax warpgroup a tile, a thread a row: S out of tensor memory, weights back as f16 over S,
-//     which P V reads from there.  The maximum is raised only when a weight would pass 2^8; O, in tensor
-//     memory too, is then rescaled.
+//     which P V reads from there.  Weights are made by the maximum as it stands: while a block's sum is at most
+//     2^15 each of them fits f16, and no maximum is looked for.  Else it is raised to the block's, O, in tensor
+//     memory too, is rescaled and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
 #include "nvfp4_attend.cuh"
 
@@ -23,7 +24,7 @@ constexpr int kKeys = 128;                                // of a block
 constexpr int kThreadsMany = 512;                         // softmax A, softmax B, producers, products
 
 // registers of a thread after the launch's 128 are shared out anew
-constexpr int kSoftmaxRegisters = 176, kProducerRegisters = 96, kProductRegisters = 64;
+constexpr int kSoftmaxRegisters = 176, kProducerRegisters = 88, kProductRegisters = 72;
 static_assert(256 * kSoftmaxRegisters + 128 * kProducerRegisters + 128 * kProductRegisters <= kThreadsMany * 128, "no more than were launched");
 
 template <int D>
@@ -37,8 +38,8 @@ struct Many {
     static constexpr int bytes = bars + 256 + 1024;       // and up to 1023 to align
     // tensor memory: S (and P over it) of A and B, O of A and B
     static constexpr int s_col = 0, o_col = 2 * kKeys;
-    static constexpr int cols = 2 * kKeys + 2 * D <= 256 ? 256 : 512;
-    static_assert(2 * kKeys + 2 * D <= 512, "O of two tiles fits");
+    static constexpr int cols = 512;
+    static_assert(2 * kKeys + 2 * D <= cols, "O of two tiles fits");
 };
 
 enum Bar { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
@@ -94,7 +95,25 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// until loads are in; v: what they gave, so that nothing uses it before
+__device__ __forceinline__ void tmem_wait_load(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -118,6 +137,7 @@ __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.
 // A warp's wait; it ends too when another one has run out.  False then, for all lanes.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
     uint32_t ok = 0;
+#pragma unroll 1
     for (long it = 0; it < kWaitLimit && !ok; ++it) {
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -131,6 +151,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     if (!ok) *lost = 1;
     return __all_sync(kFullMask, ok);
 }
+
+template <int N>
+struct Constant {
+    static constexpr int value = N;
+};
 
 // A group: 256 rows of a sequence's KV head, and its blocks of keys.
 struct Item {
@@ -167,33 +192,44 @@ __device__ __forceinline__ uint32_t columns(int from, int to) {
     return from >= 32 ? 0u : from <= 0 ? below : below & ~((1u << from) - 1u);
 }
 
+constexpr float kMostSum = 32768.0f;                      // of a block's weights: each fits f16
+
+// The keys of a block that a row sees: from lo to hi, relative to the block, of tiles that have a page.
+struct Seen {
+    int lo, hi;
+    uint32_t have;
+
+    __device__ __forceinline__ uint32_t of(int q) const {  // columns 32 q ..
+        return columns(lo - 32 * q, hi - 32 * q) & ((have >> 2 * q & 1 ? 0xFFFFu : 0u) | (have >> 2 * q & 2 ? 0xFFFF0000u : 0u));
+    }
+};
+
 // The maximum of this thread's row raised to that of the block, l and the row of O rescaled, for the rows of a warp that
 // need it (the others keep theirs): (maximum, l).  The maximum is rounded up, so that no logit exceeds it.  Out of line: it
 // runs for the first blocks of a group.
 template <int D>
-__device__ __noinline__ float2 raised(float m, float l, bool need, float c, int lo, int hi, uint32_t have, uint32_t s_at,
-                                     uint32_t o_at, bool sums) {
+__device__ __noinline__ float2 raised(float m, float l, bool need, float c, Seen seen, uint32_t s_at, uint32_t o_at, bool sums) {
     float top = kNone;
 #pragma unroll 1
     for (int q = 0; q < kKeys / 32; ++q) {
         uint32_t v[32];
         __syncwarp();
         tmem_load32(s_at + 32 * q, v);
-        tmem_wait_load();
-        const uint32_t see = columns(lo - 32 * q, hi - 32 * q) &
-                             ((have >> 2 * q & 1 ? 0xFFFFu : 0u) | (have >> 2 * q & 2 ? 0xFFFF0000u : 0u));
+        tmem_wait_load(v);
+        const uint32_t see = seen.of(q);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (see >> i & 1) top = max_nd(top, __uint_as_float(v[i]));
     }
-    const float to = need ? __fmul_ru(top, c) : m, less = exp2_approx(sub_rn(m, to));
+    need = need && top > kNone;
+    const float to = need ? fmaxf(m, __fmul_ru(top, c)) : m, less = exp2_approx(sub_rn(m, to));
     if (sums) {
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
             uint32_t v[32];
             __syncwarp();
             tmem_load32(o_at + 32 * q, v);
-            tmem_wait_load();
+            tmem_wait_load(v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
             tmem_store32(o_at + 32 * q, v);
@@ -202,6 +238,30 @@ __device__ __noinline__ float2 raised(float m, float l, bool need, float c, int 
     }
     __syncwarp();
     return make_float2(to, mul_rn(l, less));
+}
+
+// The weights of a block some of whose keys a row does not see: their sum; with `store` they go over S.
+__device__ __noinline__ float masked_weights(float m, float c, Seen seen, uint32_t s_at, bool store) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < kKeys / 32; ++q) {
+        uint32_t v[32], h[16];
+        __syncwarp();
+        tmem_load32(s_at + 32 * q, v);
+        tmem_wait_load(v);
+        const uint32_t see = seen.of(q);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float y = see >> i & 1 ? exp2_approx(__fmaf_rn(__uint_as_float(v[i]), c, -m)) : 0.0f;
+            sum = add_rn(sum, y);
+            v[i] = __float_as_uint(y);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[i] = pack_f16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        __syncwarp();
+        if (store) tmem_store16(s_at + 16 * q, h);
+    }
+    return sum;
 }
 
 template <int D>
@@ -236,11 +296,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     fence_after();
     pdl_trigger();
     pdl_wait();
-    const uint32_t tmem = *tmem_base;
+    constexpr uint32_t tmem = 0;                          // all of it: the products' operands are constants
     const Shares<kRows, true> shares(a);
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
     uint32_t n = 0, items = 0;                            // blocks and items so far
-    bool ok = true;
+    bool ok = *tmem_base == 0;
 
     if (wg == 2) {
         // ---- producers
@@ -375,9 +435,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         if (warp == 12) {
         const uint32_t el = elect_one();
         const uint32_t id_s = idesc_f16(128, kKeys, false), id_o = idesc_f16(128, D, true);
+        const uint32_t base = smem_addr(smem);
+        // (tile and stage are constants where these are called)
         auto qk = [&](int tile, int st) {
-            const uint64_t q = smem_desc(smem_addr(smem) + M::q + tile * M::tile, 16, 1024, 2);
-            const uint64_t k = smem_desc(smem_addr(smem) + M::k + st * M::tile, 16, 1024, 2);
+            const uint64_t q = smem_desc(base + M::q + tile * M::tile, 16, 1024, 2);
+            const uint64_t k = smem_desc(base + M::k + st * M::tile, 16, 1024, 2);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const uint64_t step = (i / 4 * M::half + i % 4 * 32) >> 4;
@@ -386,10 +448,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             commit_warp<1>(el, bars + kSFull + tile);
         };
         auto pv = [&](int tile, int st, bool first) {
-            const uint64_t v = smem_desc(smem_addr(smem) + M::v + st * M::tile, M::half, 1024, 2);
+            const uint64_t v = smem_desc(base + M::v + st * M::tile, M::half, 1024, 2);
 #pragma unroll
             for (int i = 0; i < kKeys / 16; ++i)
-                mma_ts(el, tmem + M::o_col + tile * D, tmem + M::s_col + tile * kKeys + i * 8, v + (i * 2048 >> 4), id_o, !first || i > 0);
+                mma_ts(el, tmem + M::o_col + tile * D, tmem + M::s_col + tile * kKeys + i * 8, v + (i * 2048 >> 4), id_o,
+                       i > 0 ? 1u : !first);
         };
         uint32_t turn_b = 0;                              // blocks that tile B took part in
         for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x) {
@@ -399,24 +462,30 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
             if (!(ok = wait(bars + kKFull + (n & 1), n >> 1 & 1, lost))) break;
             fence_after();
-            qk(0, n & 1);
-            if (two) qk(1, n & 1);
-            commit_warp<1>(el, bars + kKEmpty + (n & 1));
-            for (int blk = 0; blk < it.blocks; ++blk, ++n) {
+            auto start = [&](auto stage) {
+                constexpr int st = decltype(stage)::value;
+                qk(0, st);
+                if (two) qk(1, st);
+                commit_warp<1>(el, bars + kKEmpty + st);
+            };
+            if (n & 1) start(Constant<1>());
+            else start(Constant<0>());
+            // block blk's O, the next one's S
+            auto turn = [&](auto stage, int blk) {
+                constexpr int st = decltype(stage)::value, st1 = st ^ 1;
                 const bool more = blk + 1 < it.blocks;
-                const int st = n & 1, st1 = (n + 1) & 1;
-                if (!(ok = wait(bars + kVFull + st, n >> 1 & 1, lost))) break;
-                if (!(ok = wait(bars + kPFull, n & 1, lost))) break;
+                if (!wait(bars + kVFull + st, n >> 1 & 1, lost) || !wait(bars + kPFull, n & 1, lost)) return false;
                 fence_after();
                 pv(0, st, blk == 0);
-                if (!more) commit_warp<1>(el, bars + kOFull);
                 if (more) {
-                    if (!(ok = wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost))) break;
+                    if (!wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost)) return false;
                     fence_after();
                     qk(0, st1);
+                } else {
+                    commit_warp<1>(el, bars + kOFull);
                 }
                 if (two) {
-                    if (!(ok = wait(bars + kPFull + 1, turn_b++ & 1, lost))) break;
+                    if (!wait(bars + kPFull + 1, turn_b++ & 1, lost)) return false;
                     fence_after();
                     pv(1, st, blk == 0);
                     if (!more) commit_warp<1>(el, bars + kOFull + 1);
@@ -426,7 +495,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     if (two) qk(1, st1);
                     commit_warp<1>(el, bars + kKEmpty + st1);
                 }
-            }
+                ++n;
+                return true;
+            };
+            for (int blk = 0; ok && blk < it.blocks; ++blk) ok = n & 1 ? turn(Constant<1>(), blk) : turn(Constant<0>(), blk);
             if (!ok) break;
             commit_warp<1>(el, bars + kQEmpty);
             ++items;
@@ -457,47 +529,47 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     fence_after();
                     const uint32_t have = there[block & 3];
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
-                    // weights by the present maximum, which is nearly always high enough; where one would pass 2^kSlack
-                    // it is raised and they are made again
-                    uint32_t h[kKeys / 2];
-                    for (int again = 0;; ++again) {
-                        float more = 0.0f, high = kNone;
+                    const Seen seen{lo - j0, hi - j0, have};
+                    if (whole) {
+                        uint32_t h[kKeys / 2];
+                        for (int again = 0;; ++again) {
+                            uint64_t sum = 0;                     // two fp32
+                            uint32_t v[2][32];
+                            tmem_load32(s_at, v[0]);
 #pragma unroll
-                        for (int q = 0; q < kKeys / 32; ++q) {
-                            uint32_t v[32];
-                            tmem_load32(s_at + 32 * q, v);
-                            tmem_wait_load();
+                            for (int q = 0; q < kKeys / 32; ++q) {
+                                tmem_wait_load(v[q & 1]);
+                                if (q + 1 < kKeys / 32) tmem_load32(s_at + 32 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float y0, y1;
-                                unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack2(c, c), pack2(-m, -m)), y0, y1);
-                                v[i] = __float_as_uint(y0), v[i + 1] = __float_as_uint(y1);
+                                for (int i = 0; i < 32; i += 2) {
+                                    float y0, y1;
+                                    unpack2(fma2(pack2(__uint_as_float(v[q & 1][i]), __uint_as_float(v[q & 1][i + 1])), pack2(c, c),
+                                                 pack2(-m, -m)), y0, y1);
+                                    y0 = exp2_approx(y0), y1 = exp2_approx(y1);
+                                    sum = add2(sum, pack2(y0, y1));
+                                    h[16 * q + i / 2] = pack_f16(y0, y1);
+                                }
                             }
-                            if (!whole) {
-                                const uint32_t see = columns(lo - j0 - 32 * q, hi - j0 - 32 * q) &
-                                                     ((have >> 2 * q & 1 ? 0xFFFFu : 0u) | (have >> 2 * q & 2 ? 0xFFFF0000u : 0u));
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!(see >> i & 1)) v[i] = 0xFF800000u;
+                            float a0, a1;
+                            unpack2(sum, a0, a1);
+                            const float more = add_rn(a0, a1);
+                            if (again || !__any_sync(kFullMask, more > kMostSum)) {
+                                l = add_rn(l, more);
+                                break;
                             }
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float y0 = __uint_as_float(v[i]), y1 = __uint_as_float(v[i + 1]);
-                                high = max3(high, y0, y1);
-                                y0 = exp2_approx(y0), y1 = exp2_approx(y1);
-                                more = add_rn(more, add_rn(y0, y1));
-                                h[16 * q + i / 2] = pack_f16(y0, y1);
-                            }
+                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, blk > 0);
+                            m = x.x, l = x.y;
                         }
-                        if (again || !__any_sync(kFullMask, high > kSlack)) {
-                            l = add_rn(l, more);
-                            break;
+                        tmem_store32(s_at, h);
+                        tmem_store32(s_at + 32, h + 32);
+                    } else {
+                        const bool need = masked_weights(m, c, seen, s_at, false) > kMostSum;
+                        if (__any_sync(kFullMask, need)) {
+                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, blk > 0);
+                            m = x.x, l = x.y;
                         }
-                        const float2 x = raised<D>(m, l, high > kSlack, c, lo - j0, hi - j0, have, s_at, o_at, blk > 0);
-                        m = x.x, l = x.y;
+                        l = add_rn(l, masked_weights(m, c, seen, s_at, true));
                     }
-                    tmem_store32(s_at, h);
-                    tmem_store32(s_at + 32, h + 32);
                     tmem_wait_store();
                     fence_before();
                     arrive(bars + kPFull + wg);
@@ -521,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     if (it.blocks > 0) {
                         __syncwarp();
                         tmem_load32(o_at + 32 * q, v);
-                        tmem_wait_load();
+                        tmem_wait_load(v);
                     }
                     if (r < it.rows)
 #pragma unroll
