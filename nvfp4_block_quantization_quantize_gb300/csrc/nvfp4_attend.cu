@@ -33,6 +33,16 @@ template <int D, int NT>
 constexpr int kStages = D == 64 ? 4 : D == 128 && NT == 1 ? 2 : D == 128 ? 4 : 2;      // pairs of tiles a warp's ring holds
 
 // ---- who does what ------------------------------------------------------------------------------
+template <int R>
+struct Units {
+    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) { return sequence<R>(a, b).units; }
+};
+
+template <int R>
+struct Groups {
+    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) { return sequence<R>(a, b).runs; }
+};
+
 // warps that take part
 __device__ __forceinline__ int64_t parts_of(int64_t units, int64_t warps) {
     const int64_t most = (units + kMinTiles - 1) / kMinTiles;
@@ -42,7 +52,7 @@ __device__ __forceinline__ int64_t parts_of(int64_t units, int64_t warps) {
 // where the run that would start at unit x does: at the start of x's group where x is not past the group's own cost.
 // Every lane of a warp calls it.
 template <int R>
-__device__ __forceinline__ int64_t run_start(const AttendArgs& a, const Shares<R, false>& shares, int64_t x, int64_t* seq,
+__device__ __forceinline__ int64_t run_start(const AttendArgs& a, const Shares<Units<R>>& shares, int64_t x, int64_t* seq,
                                              int64_t* before) {
     shares.find(a, x, seq, before);
     const int64_t per = kGroupCost + sequence<R>(a, *seq).tiles, from = x - *before, in = from - quotient(from, per) * per;
@@ -137,23 +147,6 @@ struct Shape {
     static constexpr int bytes = ring + sums + stats + bars + found + kWarps * 2 * (sizeof(Place) + sizeof(Left));
 };
 
-// What k_join is to do for a CTA of k_attend: the group that its run starts amid, if the CTA before has its first
-// tiles, which the CTAs up to `last` took parts of.
-struct Cut {
-    int64_t row0;             // the sequence's first query
-    int n, h, rt, last;       // its queries (0: nothing to do); the group's KV head and row tile
-};
-
-// a partial result of a CTA: R rows of D sums, then R pairs (maximum, denominator)
-template <int D, int NT>
-constexpr int64_t kPart = 8 * NT * (D + 2);
-
-// the workspace: two partial results a CTA, then a Cut each
-template <int D, int NT>
-__device__ __forceinline__ Cut* cuts(const AttendArgs& a, int64_t ctas) {
-    return reinterpret_cast<Cut*>(reinterpret_cast<float*>(a.workspace) + ctas * 2 * kPart<D, NT>);
-}
-
 // F32: queries and weights enter the products as two f16, and a tile's sums are added in fp32
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_attend(const AttendArgs a, int split) {
@@ -177,7 +170,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     {                                                     // this warp's run of units, its sequence and the units before
         int64_t u = 0, end = 0, b = 0, before = 0, units = 0;
         if (split) {
-            const Shares<R, false> shares(a);
+            const Shares<Units<R>> shares(a);
             units = shares.total;
             const int64_t warps = parts_of(units, gridDim.x * kWarps);
             const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -187,7 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 end = i + 1 < warps ? run_start<R>(a, shares, quotient(units * (i + 1), warps), &x, &y) : units;
             }
         } else {                                          // one group a CTA
-            const Shares<R, true> shares(a);
+            const Shares<Groups<R>> shares(a);
             if (blockIdx.x < shares.total) {
                 shares.find(a, blockIdx.x, &b, &before);
                 const int tiles = sequence<R>(a, b).tiles;
@@ -205,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     }
     __syncthreads();
     const int64_t u0 = found[warp], u1 = found[warp + 1];
-    Cut* const cut = split ? cuts<D, NT>(a, gridDim.x) + blockIdx.x : nullptr;
+    Cut* const cut = split ? cuts<D, R>(a, gridDim.x) + blockIdx.x : nullptr;
     if (split && threadIdx.x == 0) cut->n = 0;
     if (found[0] >= found[kWarps]) return;
 
@@ -637,7 +630,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 *cut = Cut{s.row0, s.n, x.h, x.rt, static_cast<int>(quotient(g1 * warps - 1, units) / kWarps)};
         }
         float* const part = reinterpret_cast<float*>(a.workspace) +
-                            (static_cast<int64_t>(blockIdx.x) * 2 + (x.ta > 0 ? 0 : 1)) * kPart<D, NT>;
+                            (static_cast<int64_t>(blockIdx.x) * 2 + (x.ta > 0 ? 0 : 1)) * kPart<D, R>;
         for (int y = threadIdx.x; y < R * (D / 4); y += kWarps * 32) {
             const int q = y / (D / 4), d = y % (D / 4) * 4;
             if (q >= rows) continue;
@@ -661,57 +654,6 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 if (d == 0) part[R * D + 2 * q] = m, part[R * D + 2 * q + 1] = l;
             }
         }
-    }
-}
-
-// A group that several CTAs took parts of, joined in their order; a row a warp.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas) {
-    constexpr int R = 8 * NT, kCols = (D + 127) / 128;    // float4 columns a lane
-    pdl_trigger();
-    pdl_wait();
-    const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
-    const Cut cut = cuts<D, NT>(a, ctas)[i];
-    if (cut.n == 0) return;
-    const int G = a.Hq / a.cache.Hkv, rows = min(R, cut.n * G - cut.rt * R), runs = cut.last - i + 2;
-    // CTA i - 1 has the group's first tiles as its last part, the others as their first
-    const float* const ws = reinterpret_cast<const float*>(a.workspace);
-    auto part = [&](int run) { return ws + (static_cast<int64_t>(i - 1 + run) * 2 + (run == 0 ? 1 : 0)) * kPart<D, NT>; };
-    for (int q = threadIdx.x >> 5; q < rows; q += 8) {
-        float m = kLowest, l = 0.0f;
-        for (int run = lane; run < runs; run += 32) m = max_nd(m, part(run)[R * D + 2 * q]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = max_nd(m, __shfl_xor_sync(kFullMask, m, o));
-        float v[kCols][4] = {};
-        for (int first = 0; first < runs; first += 32) {
-            float f = 0.0f;
-            if (first + lane < runs) {
-                const float2 st = *reinterpret_cast<const float2*>(part(first + lane) + R * D + 2 * q);
-                f = exp2_approx(sub_rn(st.x, m));
-                l = __fmaf_rn(st.y, f, l);
-            }
-            const int here = min(32, runs - first);
-#pragma unroll 8
-            for (int k = 0; k < here; ++k) {
-                const float g = __shfl_sync(kFullMask, f, k);
-                const float* p = part(first + k) + q * D;
-#pragma unroll
-                for (int x = 0; x < kCols; ++x)
-                    if (D >= 128 || lane < D / 4) {
-                        const float4 u = reinterpret_cast<const float4*>(p)[x * 32 + lane];
-                        v[x][0] = __fmaf_rn(u.x, g, v[x][0]), v[x][1] = __fmaf_rn(u.y, g, v[x][1]);
-                        v[x][2] = __fmaf_rn(u.z, g, v[x][2]), v[x][3] = __fmaf_rn(u.w, g, v[x][3]);
-                    }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l = add_rn(l, __shfl_xor_sync(kFullMask, l, o));
-        int query, head;
-        split_row(cut.n, G, cut.rt * R + q, &query, &head);
-        const Finish end(a, cut.h * G + head, cut.h, m, l);
-#pragma unroll
-        for (int x = 0; x < kCols; ++x)
-            if (D >= 128 || lane < D / 4) end.store(a, cut.row0 + query, cut.h * G + head, (x * 32 + lane) * 4, v[x]);
     }
 }
 
@@ -754,8 +696,7 @@ cudaError_t launch_t(const AttendArgs& a, cudaStream_t s) {
     int split;
     const int64_t grid = grid_of(a, S::R, &split);
     cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), S::bytes, s, a, split);
-    if (e == cudaSuccess && split && grid > 1)
-        e = launch_pdl(k_join<D, NT>, dim3(static_cast<unsigned>(grid - 1)), dim3(256), 0, s, a, static_cast<int>(grid));
+    if (e == cudaSuccess && split) e = launch_join<D, S::R>(a, static_cast<int>(grid), s);
     return e;
 }
 
@@ -777,11 +718,13 @@ bool may_have_many(const AttendArgs& a) {
 
 }  // namespace
 
-int64_t attend_workspace(const AttendArgs& a) {
+int64_t attend_workspace(const AttendArgs& a) {           // both kernels', one after the other
     const int R = two_tiles(a) ? 16 : 8;
     int split;
     const int64_t grid = grid_of(a, R, &split);
-    return split ? grid * (2 * R * (a.cache.D + 2) * 4 + static_cast<int64_t>(sizeof(Cut))) : 0;
+    const int64_t few = split ? grid * (2 * R * (a.cache.D + 2) * 4 + static_cast<int64_t>(sizeof(Cut))) : 0;
+    const int64_t many = may_have_many(a) ? attend_many_workspace(a) : 0;
+    return few > many ? few : many;
 }
 
 int launch_attend(const AttendArgs& given, void* stream) {

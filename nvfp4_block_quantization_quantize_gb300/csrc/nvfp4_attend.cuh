@@ -68,18 +68,14 @@ __device__ __forceinline__ int64_t scan_add(int64_t v) {
     return v;
 }
 
-// The sequences' shares of the work, in units or (GROUPS) in groups, added up.  A warp holds it: each lane the sequences
-// lane, lane + 32, ..; the first 32 stay in registers.
-template <int R, bool GROUPS>
+// The sequences' shares of the work, F::share(a, b), added up.  A warp holds it: each lane the sequences lane, lane + 32, ..;
+// the first 32 stay in registers.
+template <class F>
 struct Shares {
     int64_t first, upto;      // this lane's first sequence's share; that of the first sequences up to it
     int64_t total;
 
-    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) {
-        if (b >= a.B) return 0;
-        const Seq q = sequence<R>(a, b);
-        return GROUPS ? q.runs : q.units;
-    }
+    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) { return b < a.B ? F::share(a, b) : 0; }
 
     __device__ __forceinline__ explicit Shares(const AttendArgs& a) {
         const int lane = threadIdx.x & 31;
@@ -194,9 +190,85 @@ struct Finish {
     }
 };
 
+// What k_join is to do for a CTA: the group that its run starts amid, if the CTA before has its first
+// tiles, which the CTAs up to `last` took parts of.
+struct Cut {
+    int64_t row0;             // the sequence's first query
+    int n, h, rt, last;       // its queries (0: nothing to do); the group's KV head and row tile
+};
+
+// a partial result of a CTA: R rows of D sums, then R pairs (maximum, denominator)
+template <int D, int R>
+constexpr int64_t kPart = R * (D + 2);
+
+// the workspace: two partial results a CTA, then a Cut each
+template <int D, int R>
+__device__ __forceinline__ Cut* cuts(const AttendArgs& a, int64_t ctas) {
+    return reinterpret_cast<Cut*>(reinterpret_cast<float*>(a.workspace) + ctas * 2 * kPart<D, R>);
+}
+
+// A group that several CTAs took parts of, joined in their order; a row a warp, 8 rows a CTA.
+template <int D, int R>
+__global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas) {
+    constexpr int kCols = (D + 127) / 128;    // float4 columns a lane
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const Cut cut = cuts<D, R>(a, ctas)[i];
+    if (cut.n == 0) return;
+    const int G = a.Hq / a.cache.Hkv, rows = min(R, cut.n * G - cut.rt * R), runs = cut.last - i + 2;
+    // CTA i - 1 has the group's first tiles as its last part, the others as their first
+    const float* const ws = reinterpret_cast<const float*>(a.workspace);
+    auto part = [&](int run) { return ws + (static_cast<int64_t>(i - 1 + run) * 2 + (run == 0 ? 1 : 0)) * kPart<D, R>; };
+    const int q = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (q < rows) {
+        float m = kLowest, l = 0.0f;
+        for (int run = lane; run < runs; run += 32) m = max_nd(m, part(run)[R * D + 2 * q]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max_nd(m, __shfl_xor_sync(kFullMask, m, o));
+        float v[kCols][4] = {};
+        for (int first = 0; first < runs; first += 32) {
+            float f = 0.0f;
+            if (first + lane < runs) {
+                const float2 st = *reinterpret_cast<const float2*>(part(first + lane) + R * D + 2 * q);
+                f = exp2_approx(sub_rn(st.x, m));
+                l = __fmaf_rn(st.y, f, l);
+            }
+            const int here = min(32, runs - first);
+#pragma unroll 8
+            for (int k = 0; k < here; ++k) {
+                const float g = __shfl_sync(kFullMask, f, k);
+                const float* p = part(first + k) + q * D;
+#pragma unroll
+                for (int x = 0; x < kCols; ++x)
+                    if (D >= 128 || lane < D / 4) {
+                        const float4 u = reinterpret_cast<const float4*>(p)[x * 32 + lane];
+                        v[x][0] = __fmaf_rn(u.x, g, v[x][0]), v[x][1] = __fmaf_rn(u.y, g, v[x][1]);
+                        v[x][2] = __fmaf_rn(u.z, g, v[x][2]), v[x][3] = __fmaf_rn(u.w, g, v[x][3]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l = add_rn(l, __shfl_xor_sync(kFullMask, l, o));
+        int query, head;
+        split_row(cut.n, G, cut.rt * R + q, &query, &head);
+        const Finish end(a, cut.h * G + head, cut.h, m, l);
+#pragma unroll
+        for (int x = 0; x < kCols; ++x)
+            if (D >= 128 || lane < D / 4) end.store(a, cut.row0 + query, cut.h * G + head, (x * 32 + lane) * 4, v[x]);
+    }
+}
+
+template <int D, int R>
+cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t s) {
+    if (ctas < 2) return cudaSuccess;
+    return launch_pdl(k_join<D, R>, dim3(static_cast<unsigned>(ctas - 1), R / 8), dim3(256), 0, s, a, ctas);
+}
+
 }  // namespace
 
 // the kernel of many queries a sequence, which takes the sequences of more than a.rows_above rows
 cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s);
+int64_t attend_many_workspace(const AttendArgs& a);
 
 }  // namespace nvfp4

@@ -24,23 +24,8 @@ constexpr int kKeys = 128;                                // of a block
 constexpr int kThreadsMany = 512;                         // softmax A, softmax B, producers, products
 
 // registers of a thread after the launch's 128 are shared out anew
-constexpr int kSoftmaxRegisters = 176, kProducerRegisters = 88, kProductRegisters = 72;
+constexpr int kSoftmaxRegisters = 168, kProducerRegisters = 104, kProductRegisters = 72;
 static_assert(256 * kSoftmaxRegisters + 128 * kProducerRegisters + 128 * kProductRegisters <= kThreadsMany * 128, "no more than were launched");
-
-template <int D>
-struct Many {
-    static constexpr int half = kKeys * 128;              // 64 elements of 128 tokens
-    static constexpr int tile = D / 64 * half;            // Q of a tile, K or V of a block
-    static constexpr int stages = 2;                      // blocks of K, and of V
-    static constexpr int q = 0, k = 2 * tile, v = k + stages * tile;
-    static constexpr int factor = v + stages * tile;      // [256] fp32
-    static constexpr int bars = factor + kRows * 4;
-    static constexpr int bytes = bars + 256 + 1024;       // and up to 1023 to align
-    // tensor memory: S (and P over it) of A and B, O of A and B
-    static constexpr int s_col = 0, o_col = 2 * kKeys;
-    static constexpr int cols = 512;
-    static_assert(2 * kKeys + 2 * D <= cols, "O of two tiles fits");
-};
 
 enum Bar { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
            kPFull = kSFull + 2, kOFull = kPFull + 2, kBars = kOFull + 2 };
@@ -123,12 +108,6 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 template <int N>
 __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -157,34 +136,140 @@ struct Constant {
     static constexpr int value = N;
 };
 
-// A group: 256 rows of a sequence's KV head, and its blocks of keys.
-struct Item {
-    Seq s;
-    int64_t b;
-    int h, rt, rows, blocks, j0;      // rows of it; the first key of its first block
-    int first, last;                  // queries of its first and last row
+// The work of a sequence, in keys that its groups of 256 rows are to look at: w0 + rt * step a group of row tile rt (the
+// first kGroupKeys for what it costs besides).  With a causal mask the row tiles look at more and more; that they look at whole
+// blocks, and a window cuts off the first keys, is not counted.
+constexpr int kGroupKeys = 256;
+constexpr int kMinKeys = 512;                             // a CTA's run is not made shorter
+
+struct Load {
+    int64_t w0;
+    int rts, step;
+
+    __device__ __forceinline__ Load(const AttendArgs& a, const Seq& s) {
+        const int G = a.Hq / a.cache.Hkv, queries = (kRows + G - 1) / G;
+        rts = s.runs / a.cache.Hkv;
+        step = a.causal && !a.window ? queries : 0;
+        w0 = kGroupKeys + (step ? max(s.len - s.n, 0) + step : a.window ? min(s.len, a.window + queries) : s.len);
+    }
+    __device__ __forceinline__ int64_t before(int64_t rt) const { return rt * w0 + rt * (rt - 1) / 2 * step; }
+    __device__ __forceinline__ int64_t of(int rt) const { return w0 + static_cast<int64_t>(rt) * step; }
 };
 
-template <class S>
-__device__ __forceinline__ Item item_of(const AttendArgs& a, const S& shares, int64_t x) {
-    Item t;
+struct Keys {
+    __device__ __forceinline__ static int64_t share(const AttendArgs& a, int64_t b) {
+        const Load l(a, sequence<kRows>(a, b));
+        return l.before(l.rts) * a.cache.Hkv;
+    }
+};
+
+// A place in the work: before block blk of a group (b: a.B at the end of all), whose share of the work ends at key `until`.
+struct Spot {
+    int64_t b, until;
+    int rt, h, blk;
+
+    __device__ __forceinline__ bool group_of(const Spot& o) const { return b == o.b && rt == o.rt && h == o.h; }
+};
+
+// 256 rows of a sequence's KV head, and its blocks of keys
+struct Item {
+    Seq s;
+    int rows, blocks, j0;             // the first key of its first block
+    int first, last;                  // queries of its first and last row
+
+    __device__ __forceinline__ Item(const AttendArgs& a, const Seq& seq, int rt) : s(seq) {
+        const int G = a.Hq / a.cache.Hkv;
+        rows = min(kRows, s.n * G - rt * kRows);
+        int head;
+        split_row(s.n, G, rt * kRows, &first, &head);
+        split_row(s.n, G, rt * kRows + rows - 1, &last, &head);
+        const int pos0 = s.len - s.n;
+        const int lo = a.window > 0 ? max(0, pos0 + first - a.window + 1) : 0;
+        const int hi = a.causal ? min(s.len, max(pos0 + last + 1, 0)) : s.len;
+        j0 = lo / 16 * 16;
+        blocks = hi > j0 ? (hi - j0 + kKeys - 1) / kKeys : 0;
+    }
+};
+
+// where the run that would start at key x of all does.  Every lane of a warp calls it.
+__device__ __forceinline__ Spot spot_of(const AttendArgs& a, const Shares<Keys>& shares, int64_t x) {
+    Spot p{a.B, 0, 0, 0, 0};
+    if (x >= shares.total) return p;
     int64_t before;
-    shares.find(a, x, &t.b, &before);
-    t.s = sequence<kRows>(a, t.b);
-    const int run = static_cast<int>(x - before), G = a.Hq / a.cache.Hkv;
-    // the last rows first: with a causal mask they have the most keys
-    t.h = run % a.cache.Hkv, t.rt = t.s.runs / a.cache.Hkv - 1 - run / a.cache.Hkv;
-    t.rows = min(kRows, t.s.n * G - t.rt * kRows);
-    int head;
-    split_row(t.s.n, G, t.rt * kRows, &t.first, &head);
-    split_row(t.s.n, G, t.rt * kRows + t.rows - 1, &t.last, &head);
-    const int pos0 = t.s.len - t.s.n;
-    const int lo = a.window > 0 ? max(0, pos0 + t.first - a.window + 1) : 0;
-    const int hi = a.causal ? min(t.s.len, max(pos0 + t.last + 1, 0)) : t.s.len;
-    t.j0 = lo / 16 * 16;
-    t.blocks = hi > t.j0 ? (hi - t.j0 + kKeys - 1) / kKeys : 0;
-    return t;
+    shares.find(a, x, &p.b, &before);
+    const Seq s = sequence<kRows>(a, p.b);
+    const Load l(a, s);
+    x -= before;
+    int lo = 0, hi = l.rts - 1;                           // the last row tile that does not start after x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (l.before(mid) * a.cache.Hkv <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    x -= l.before(lo) * a.cache.Hkv;
+    const int64_t w = l.of(lo);
+    p.rt = lo;
+    p.h = static_cast<int>(quotient(x, w));
+    p.until = before + l.before(lo) * a.cache.Hkv + (p.h + 1) * w;
+    p.blk = static_cast<int>(quotient((x - p.h * w) * Item(a, s, lo).blocks, w));
+    return p;
 }
+
+// CTAs that take part
+__device__ __forceinline__ int64_t runs_of(int64_t keys, int64_t ctas) {
+    const int64_t most = (keys + kMinKeys - 1) / kMinKeys;
+    return most < ctas ? most : ctas;
+}
+
+// A CTA's run of parts of groups, as a warp walks along it (in shared memory; one lane walks).
+struct Run {
+    Spot at, end;
+    Seq s;
+    bool known, first, more;          // s is at.b's; nothing was done yet; there is a part: blocks at.blk .. to of at's group
+
+    __device__ __forceinline__ void look(const AttendArgs& a) {
+        while (true) {
+            // (a run that ends where it starts, amid a group, is an empty part of it)
+            more = at.b < a.B && (!at.group_of(end) || (first ? end.blk > 0 : at.blk < end.blk));
+            if (!more) return;
+            if (!known) s = sequence<kRows>(a, at.b);
+            known = true;
+            if (s.runs > 0) return;
+            ++at.b, at.rt = at.h = at.blk = 0, known = first = false;
+        }
+    }
+    __device__ __forceinline__ void start(const AttendArgs& a, const Spot& from, const Spot& to) {
+        at = from, end = to, known = false, first = true;
+        look(a);
+    }
+    __device__ __forceinline__ void step(const AttendArgs& a) {
+        first = false;
+        at.blk = at.group_of(end) ? end.blk : 0;
+        if (!at.group_of(end) && ++at.h == a.cache.Hkv) {
+            at.h = 0;
+            if (++at.rt == s.runs / a.cache.Hkv) at.rt = 0, ++at.b, known = false;
+        }
+        look(a);
+    }
+    __device__ __forceinline__ int to(const Item& it) const { return at.group_of(end) ? end.blk : it.blocks; }
+};
+
+template <int D>
+struct Many {
+    static constexpr int half = kKeys * 128;              // 64 elements of 128 tokens
+    static constexpr int tile = D / 64 * half;            // Q of a tile, K or V of a block
+    static constexpr int stages = 2;                      // blocks of K, and of V
+    static constexpr int q = 0, k = 2 * tile, v = k + stages * tile;
+    static constexpr int factor = v + stages * tile;      // [256] fp32
+    static constexpr int bars = factor + kRows * 4;
+    static constexpr int spots = bars + 256;              // where the runs of the CTA before, of this and the next start
+    static constexpr int runs = spots + 3 * sizeof(Spot); // of each warp
+    static constexpr int bytes = runs + 16 * sizeof(Run) + 1024;      // and up to 1023 to align
+    // tensor memory: S (and P over it) of A and B, O of A and B
+    static constexpr int s_col = 0, o_col = 2 * kKeys;
+    static constexpr int cols = 512;
+    static_assert(2 * kKeys + 2 * D <= cols, "O of two tiles fits");
+};
 
 // bits from .. to - 1 of 32
 __device__ __forceinline__ uint32_t columns(int from, int to) {
@@ -267,7 +352,6 @@ __device__ __noinline__ float masked_weights(float m, float c, Seen seen, uint32
 template <int D>
 __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArgs a) {
     using M = Many<D>;
-    constexpr int kGroups = D / 16;                       // blocks of 16 elements of a token
     extern __shared__ uint8_t dynamic[];
     uint8_t* const smem = dynamic + (1024 - smem_addr(dynamic) % 1024) % 1024;
     float* const factors = reinterpret_cast<float*>(smem + M::factor);
@@ -297,82 +381,99 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     pdl_trigger();
     pdl_wait();
     constexpr uint32_t tmem = 0;                          // all of it: the products' operands are constants
-    const Shares<kRows, true> shares(a);
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
-    uint32_t n = 0, items = 0;                            // blocks and items so far
+    Spot* const spots = reinterpret_cast<Spot*>(smem + M::spots);
+    Run& run = reinterpret_cast<Run*>(smem + M::runs)[warp];
+    Cut* const cut = cuts<D, kRows>(a, gridDim.x) + blockIdx.x;
+    if (warp < 3) {
+        const Shares<Keys> shares(a);
+        const int64_t ctas = runs_of(shares.total, gridDim.x), i = static_cast<int64_t>(blockIdx.x) - 1 + warp;
+        const Spot p = spot_of(a, shares, i < 0 ? 0 : i < ctas ? quotient(shares.total * i, ctas) : shares.total);
+        if (lane == 0) spots[warp] = p;
+        if (warp == 1 && lane == 0) cut->last = p.blk > 0 ? static_cast<int>(quotient(p.until * ctas - 1, shares.total)) : 0;
+    }
+    __syncthreads();
+    if (lane == 0) run.start(a, spots[1], spots[2]);
+    if (threadIdx.x == 0) {                               // a group is cut at this run's start, and here first?
+        const Spot& p = spots[1];
+        const bool is = p.blk > 0 && !(spots[0].group_of(p) && spots[0].blk > 0);
+        cut->n = is ? run.s.n : 0, cut->row0 = run.s.row0, cut->h = p.h, cut->rt = p.rt;
+    }
+    __syncwarp();
+    auto step = [&]() {
+        __syncwarp();
+        if (lane == 0) run.step(a);
+        __syncwarp();
+    };
+    uint32_t n = 0, items = 0;                            // blocks and parts with blocks so far
     bool ok = *tmem_base == 0;
 
     if (wg == 2) {
         // ---- producers
         registers_down<kProducerRegisters>();
-        uint2 w[kGroups];                                 // the next half block's codes: 128 tokens' D / 16 groups over 128 threads
-        uint32_t sc[kGroups];
-        constexpr int kAtOnce = 128 / (16 * kGroups) > 0 ? 128 / (16 * kGroups) : 1;      // tiles the threads cover at once
-        constexpr int kTurns = 8 / kAtOnce;
-        static_assert(16 * kGroups * kAtOnce == 128 && kTurns == kGroups, "a thread takes D / 16 groups");
-        const int in_tile = t % (16 * kGroups), mine = t / (16 * kGroups);      // group of a tile; which of the tiles at once
-        const int token = in_tile / kGroups, grp = in_tile % kGroups;
-        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x, ++items) {
-            const Item it = item_of(a, shares, x);
-            if (it.blocks == 0) {
-                --items;
-                continue;
-            }
+        // A thread takes 32 elements of a token: kPairs threads a token, kTokens tokens at once, kPairs turns a block.
+        constexpr int kPairs = D / 32, kTokens = 128 / kPairs;
+        const int token = t / kPairs, pair = t % kPairs, row = token % 16;
+        // 32 elements are four 16-byte pieces of the swizzled row; the upper half's threads begin with the third, so that 8
+        // threads' pieces lie in 8 bank groups
+        const int upper = pair >> 1;
+        uint32_t piece[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            piece[j] = upper * M::half + token * 128 + ((((pair & 1) * 4 + (j ^ 2 * upper)) ^ (token & 7)) << 4);
+        uint4 kw[kPairs], vw[kPairs];                     // the next block's codes and scales
+        uint32_t ks[kPairs], vs[kPairs];
+        for (; ok && run.more; step()) {
+            const Item it(a, run.s, run.at.rt);
+            const int h = run.at.h, from = run.at.blk, to = run.to(it);
+            if (from == to) continue;
             const int pos0 = it.s.len - it.s.n;
             const int seen_lo = a.window > 0 ? max(0, pos0 + it.first - a.window + 1) : 0;
-            const int32_t* const table = a.pages + it.b * a.width;
+            const int32_t* const table = a.pages + run.at.b * a.width;
             const int tiles_end = (it.s.len + 15) / 16;
-            // a lane below 8 holds where a tile of the block whose loads come next lies in the cache (-1: nowhere)
-            int64_t at = -1;
-            auto find_pages = [&](int block) {
-                at = -1;
-                const int tl = it.j0 / 16 + block * 8 + (lane & 7);
-                if (block < it.blocks && tl < tiles_end) {
-                    const int p = tl / per_page;
-                    const int32_t page = __ldg(table + p);
-                    if (page >= 0 && page < a.cache.pages)
-                        at = ((static_cast<int64_t>(page) * a.cache.Hkv + it.h) * per_page + (tl - p * per_page)) * kRecord<D>;
-                }
+            // a lane below 8 holds a tile of a block: its page, and where it lies in the cache (-1: nowhere)
+            auto tile_of_lane = [&](int block) { return it.j0 / 16 + block * 8 + (lane & 7); };
+            auto page_of = [&](int block) {
+                const int tl = tile_of_lane(block);
+                return block < to && tl < tiles_end ? __ldg(table + tl / per_page) : -1;
             };
-            auto load = [&](bool is_v) {
-                const uint8_t* const codes = a.cache.data + (is_v ? 9 * D : 0) + in_tile * 8;
-                const uint8_t* const scales = a.cache.data + (is_v ? 17 * D : 8 * D) + in_tile;
+            auto place_of = [&](int block, int32_t page) {
+                return page >= 0 && page < a.cache.pages
+                           ? ((static_cast<int64_t>(page) * a.cache.Hkv + h) * per_page + tile_of_lane(block) % per_page) * kRecord<D>
+                           : -1;
+            };
+            auto load = [&](int64_t at, uint4* w, uint32_t* sc, int part) {
+                const uint8_t* const codes = a.cache.data + part + row * (D / 2) + pair * 16;
+                const uint8_t* const scales = a.cache.data + part + 8 * D + row * (D / 16) + pair * 2;
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int64_t from = __shfl_sync(kFullMask, at, i * kAtOnce + mine);
-                    w[i] = make_uint2(0u, 0u);
+                for (int i = 0; i < kPairs; ++i) {
+                    const int64_t x = __shfl_sync(kFullMask, at, (i * kTokens + token) / 16);
+                    w[i] = make_uint4(0u, 0u, 0u, 0u);
                     sc[i] = 0;
-                    if (from >= 0) {
-                        w[i] = __ldg(reinterpret_cast<const uint2*>(codes + from));
-                        sc[i] = __ldg(scales + from);
+                    if (x >= 0) {
+                        w[i] = __ldg(reinterpret_cast<const uint4*>(codes + x));
+                        sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + x));
                     }
                 }
             };
-            // 16 elements a turn to two 16-byte pieces; the upper half's threads store their second piece first, so that
-            // 8 threads' pieces lie in 8 bank groups
-            const int swap = grp / 4 & 1, piece = 2 * (grp % 4) + swap;
-            const uint32_t to = grp / 4 * M::half + (mine * 16 + token) * 128;
-            const uint32_t first = to + ((piece ^ (token & 7)) << 4), second = to + (((piece ^ 1) ^ (token & 7)) << 4);
-            auto store = [&](uint8_t* base, bool is_v, int j0) {
-                if (is_v && (j0 < seen_lo || j0 + kKeys > it.s.len)) {      // some were perhaps never written
+            auto store = [&](uint8_t* base, const uint4* w, const uint32_t* sc) {
 #pragma unroll
-                    for (int i = 0; i < kTurns; ++i) {
-                        const int j = j0 + (i * kAtOnce + mine) * 16 + token;
-                        if (j < seen_lo || j >= it.s.len) sc[i] = 0;
+                for (int i = 0; i < kPairs; ++i) {
+                    const uint32_t u = e4m3_pair(sc[i]);
+                    const uint32_t s0 = __byte_perm(u, u, upper ? 0x3232 : 0x1010), s1 = __byte_perm(u, u, upper ? 0x1010 : 0x3232);
+                    const uint32_t x[4] = {upper ? w[i].z : w[i].x, upper ? w[i].w : w[i].y, upper ? w[i].x : w[i].z,
+                                           upper ? w[i].y : w[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+                        decode4(x[j], j < 2 ? s0 : s1, o);
+                        *reinterpret_cast<uint4*>(base + piece[j] + i * kTokens * 128) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const uint32_t u = e4m3_pair(sc[i] * 257u);
-                    uint32_t h[4];
-                    decode4(swap ? w[i].y : w[i].x, u, h);
-                    *reinterpret_cast<uint4*>(base + first + i * kAtOnce * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
-                    decode4(swap ? w[i].x : w[i].y, u, h);
-                    *reinterpret_cast<uint4*>(base + second + i * kAtOnce * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
             };
-            find_pages(0);
-            load(false);
+            int64_t at = place_of(from, page_of(from));
+            load(at, kw, ks, 0);
+            load(at, vw, vs, 9 * D);
             // ---- this item's queries, two rows a thread
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
             for (int tile = 0; ok && tile < 2; ++tile) {
@@ -380,9 +481,9 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 if (tile == 1 && it.rows <= 128) break;
                 const bool in = r < it.rows;
                 int query, head;
-                split_row(it.s.n, G, it.rt * kRows + min(r, it.rows - 1), &query, &head);
+                split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
                 const uint16_t* src = static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
-                                      (static_cast<int64_t>(it.h) * G + head) * D;
+                                      (static_cast<int64_t>(h) * G + head) * D;
                 uint32_t top = 0;
                 for (int i = 0; i < D / 8; ++i) {
                     const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
@@ -393,41 +494,49 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 const float down = copysignf(power_of_two(-ex), a.scale);
                 float dec = 1.0f, enc;
                 if (a.cache.k_mode != NVFP4_GAMAX_NONE)
-                    global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? it.h : 0)), a.cache.bound, enc, dec);
+                    global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
                 factors[r] = mul_rn(power_of_two(ex), mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec));
                 uint8_t* const dst = smem + M::q + tile * M::tile + t * 128;
                 for (int i = 0; i < D / 8; ++i) {
                     const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t h[4];
+                    uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = in ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
-                    *reinterpret_cast<uint4*>(dst + i / 8 * M::half + (((i & 7) ^ (t & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        o[k] = in ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                    *reinterpret_cast<uint4*>(dst + i / 8 * M::half + (((i & 7) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (!ok) break;
             fence_async();
             arrive(bars + kQFull);
             // ---- its blocks
-            for (int blk = 0; blk < it.blocks; ++blk, ++n) {
-                const int st = n & 1;
+            for (int blk = from; blk < to; ++blk, ++n) {
+                const int st = n & 1, j0 = it.j0 + blk * kKeys;
                 const uint32_t ph = n >> 1 & 1;
-                const int j0 = it.j0 + blk * kKeys;
+                const int32_t page = page_of(blk + 1);
                 if (n >= 2 && !(ok = wait(bars + kKEmpty + st, ph ^ 1, lost))) break;
-                store(smem + M::k + st * M::tile, false, j0);
+                store(smem + M::k + st * M::tile, kw, ks);
                 const unsigned have = __ballot_sync(kFullMask, lane < 8 && at >= 0);
                 if (t == 0) there[n & 3] = have;
                 fence_async();
                 arrive(bars + kKFull + st);
-                load(true);
+                at = place_of(blk + 1, page);
+                load(at, kw, ks, 0);
+                if (j0 < seen_lo || j0 + kKeys > it.s.len) {      // some values were perhaps never written
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        const int j = j0 + i * kTokens + token;
+                        if (j < seen_lo || j >= it.s.len) vs[i] = 0;
+                    }
+                }
                 if (n >= 2 && !(ok = wait(bars + kVEmpty + st, ph ^ 1, lost))) break;
-                store(smem + M::v + st * M::tile, true, j0);
+                store(smem + M::v + st * M::tile, vw, vs);
                 fence_async();
                 arrive(bars + kVFull + st);
-                find_pages(blk + 1);
-                load(false);
+                load(at, vw, vs, 9 * D);
             }
+            ++items;
         }
     } else if (wg == 3) {
         // ---- products
@@ -455,9 +564,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                        i > 0 ? 1u : !first);
         };
         uint32_t turn_b = 0;                              // blocks that tile B took part in
-        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x) {
-            const Item it = item_of(a, shares, x);
-            if (it.blocks == 0) continue;
+        for (; ok && run.more; step()) {
+            const Item it(a, run.s, run.at.rt);
+            const int from = run.at.blk, to = run.to(it);
+            if (from == to) continue;
             const bool two = it.rows > 128;
             if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
             if (!(ok = wait(bars + kKFull + (n & 1), n >> 1 & 1, lost))) break;
@@ -473,10 +583,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             // block blk's O, the next one's S
             auto turn = [&](auto stage, int blk) {
                 constexpr int st = decltype(stage)::value, st1 = st ^ 1;
-                const bool more = blk + 1 < it.blocks;
+                const bool more = blk + 1 < to;
                 if (!wait(bars + kVFull + st, n >> 1 & 1, lost) || !wait(bars + kPFull, n & 1, lost)) return false;
                 fence_after();
-                pv(0, st, blk == 0);
+                pv(0, st, blk == from);
                 if (more) {
                     if (!wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost)) return false;
                     fence_after();
@@ -487,7 +597,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 if (two) {
                     if (!wait(bars + kPFull + 1, turn_b++ & 1, lost)) return false;
                     fence_after();
-                    pv(1, st, blk == 0);
+                    pv(1, st, blk == from);
                     if (!more) commit_warp<1>(el, bars + kOFull + 1);
                 }
                 commit_warp<1>(el, bars + kVEmpty + st);
@@ -498,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 ++n;
                 return true;
             };
-            for (int blk = 0; ok && blk < it.blocks; ++blk) ok = n & 1 ? turn(Constant<1>(), blk) : turn(Constant<0>(), blk);
+            for (int blk = from; ok && blk < to; ++blk) ok = n & 1 ? turn(Constant<1>(), blk) : turn(Constant<0>(), blk);
             if (!ok) break;
             commit_warp<1>(el, bars + kQEmpty);
             ++items;
@@ -510,19 +620,20 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;           // 32 lanes of tensor memory a warp
         const uint32_t s_at = tmem + lanes + M::s_col + wg * kKeys, o_at = tmem + lanes + M::o_col + wg * D;
         uint32_t turn = 0, mine = 0;                      // blocks and items that this tile took part in
-        for (int64_t x = blockIdx.x; ok && x < shares.total; x += gridDim.x) {
-            const Item it = item_of(a, shares, x);
-            const int r = wg * 128 + t, row = it.rt * kRows + r;
+        for (; ok && run.more; step()) {
+            const Item it(a, run.s, run.at.rt);
+            const int h = run.at.h, from = run.at.blk, to = run.to(it);
+            const int r = wg * 128 + t;
             int query, head;
-            split_row(it.s.n, G, min(row, it.s.n * G - 1), &query, &head);
+            split_row(it.s.n, G, min(run.at.rt * kRows + r, it.s.n * G - 1), &query, &head);
             float m = kLowest, l = 0.0f;
-            if (it.blocks > 0 && wg * 128 < it.rows) {
+            if (from < to && wg * 128 < it.rows) {
                 const int p = it.s.len - it.s.n + query;
                 const int hi = a.causal ? min(it.s.len, max(p + 1, 0)) : it.s.len, lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
                 if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
                 const float c = factors[r];
-                for (int blk = 0; blk < it.blocks; ++blk, ++turn) {
-                    const uint32_t block = n + blk;
+                for (int blk = from; blk < to; ++blk, ++turn) {
+                    const uint32_t block = n + blk - from;
                     const int j0 = it.j0 + blk * kKeys;
                     // (a tile that sat out an item keeps its own count of S and P)
                     if (!(ok = wait(bars + kSFull + wg, turn & 1, lost))) break;
@@ -531,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
                     const Seen seen{lo - j0, hi - j0, have};
                     if (whole) {
-                        uint32_t h[kKeys / 2];
+                        uint32_t p16[kKeys / 2];
                         for (int again = 0;; ++again) {
                             uint64_t sum = 0;                     // two fp32
                             uint32_t v[2][32];
@@ -547,7 +658,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                                                  pack2(-m, -m)), y0, y1);
                                     y0 = exp2_approx(y0), y1 = exp2_approx(y1);
                                     sum = add2(sum, pack2(y0, y1));
-                                    h[16 * q + i / 2] = pack_f16(y0, y1);
+                                    p16[16 * q + i / 2] = pack_f16(y0, y1);
                                 }
                             }
                             float a0, a1;
@@ -557,15 +668,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                                 l = add_rn(l, more);
                                 break;
                             }
-                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, blk > 0);
+                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, blk > from);
                             m = x.x, l = x.y;
                         }
-                        tmem_store32(s_at, h);
-                        tmem_store32(s_at + 32, h + 32);
+                        tmem_store32(s_at, p16);
+                        tmem_store32(s_at + 32, p16 + 32);
                     } else {
                         const bool need = masked_weights(m, c, seen, s_at, false) > kMostSum;
                         if (__any_sync(kFullMask, need)) {
-                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, blk > 0);
+                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, blk > from);
                             m = x.x, l = x.y;
                         }
                         l = add_rn(l, masked_weights(m, c, seen, s_at, true));
@@ -579,18 +690,19 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 fence_after();
                 ++mine;
             }
-            if (it.blocks > 0) {
-                n += it.blocks;
-                ++items;
-            }
-            // ---- the row's output (a group without keys gives zeros)
+            if (from < to) n += to - from, ++items;
+            // ---- the row's output (a group without keys gives zeros), or its part of it
             if (wg * 128 < it.rows) {
-                const Finish f(a, it.h * G + head, it.h, m, l);
+                const bool complete = from == 0 && to == it.blocks;
+                float* const part = reinterpret_cast<float*>(a.workspace) +
+                                    (static_cast<int64_t>(blockIdx.x) * 2 + (from > 0 ? 0 : 1)) * kPart<D, kRows>;
+                const Finish f(a, h * G + head, h, m, l);
+#pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    if (it.blocks > 0) {
+                    if (from < to) {
                         __syncwarp();
                         tmem_load32(o_at + 32 * q, v);
                         tmem_wait_load(v);
@@ -599,23 +711,36 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             float y[4] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])};
-                            f.store(a, it.s.row0 + query, it.h * G + head, 32 * q + i, y);
+                            if (complete) f.store(a, it.s.row0 + query, h * G + head, 32 * q + i, y);
+                            else *reinterpret_cast<float4*>(part + r * D + 32 * q + i) = make_float4(y[0], y[1], y[2], y[3]);
                         }
                 }
+                if (!complete && r < it.rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
+                __syncwarp();
                 fence_before();
             }
         }
-        if (!ok) {                                        // NaN to every row that this thread may have left
-            for (int64_t x = blockIdx.x; x < shares.total; x += gridDim.x) {
-                const Item it = item_of(a, shares, x);
-                const int r = wg * 128 + t;
+        if (!ok) {                                        // NaN to the rows of this run, and to its parts' denominators
+            __syncwarp();
+            if (lane == 0) run.start(a, spots[1], spots[2]);
+            __syncwarp();
+            for (; run.more; step()) {
+                const Item it(a, run.s, run.at.rt);
+                const int h = run.at.h, from = run.at.blk, r = wg * 128 + t;
                 if (r >= it.rows) continue;
                 int query, head;
-                split_row(it.s.n, G, it.rt * kRows + r, &query, &head);
-                const Finish f(a, it.h * G + head, it.h, 0.0f, __int_as_float(0x7FC00000));
-                for (int d = 0; d < D; d += 4) {
-                    float y[4] = {f.by, f.by, f.by, f.by};
-                    f.store(a, it.s.row0 + query, it.h * G + head, d, y);
+                split_row(it.s.n, G, run.at.rt * kRows + r, &query, &head);
+                if (from == 0 && run.to(it) == it.blocks) {
+                    const float nan = __int_as_float(0x7FC00000);
+                    const Finish f(a, h * G + head, h, 0.0f, nan);
+                    for (int d = 0; d < D; d += 4) {
+                        float y[4] = {nan, nan, nan, nan};
+                        f.store(a, it.s.row0 + query, h * G + head, d, y);
+                    }
+                } else {
+                    float* const part = reinterpret_cast<float*>(a.workspace) +
+                                        (static_cast<int64_t>(blockIdx.x) * 2 + (from > 0 ? 0 : 1)) * kPart<D, kRows>;
+                    *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(0.0f, __int_as_float(0x7FC00000));
                 }
             }
         }
@@ -639,13 +764,17 @@ cudaError_t launch_many(const AttendArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         dev_of = dev;
     }
-    const int64_t rows = a.T * (a.Hq / a.cache.Hkv);
-    const int64_t items = (rows / kRows + (a.B < rows ? a.B : rows)) * a.cache.Hkv;      // at most
-    const int64_t grid = items < sm_count() ? items : sm_count();
-    return launch_pdl(k_attend_many<D>, dim3(static_cast<unsigned>(grid)), dim3(kThreadsMany), Many<D>::bytes, s, a);
+    const int grid = sm_count();
+    cudaError_t e = launch_pdl(k_attend_many<D>, dim3(static_cast<unsigned>(grid)), dim3(kThreadsMany), Many<D>::bytes, s, a);
+    if (e == cudaSuccess) e = launch_join<D, kRows>(a, grid, s);
+    return e;
 }
 
 }  // namespace
+
+int64_t attend_many_workspace(const AttendArgs& a) {
+    return static_cast<int64_t>(sm_count()) * (2 * kRows * (a.cache.D + 2) * 4 + static_cast<int64_t>(sizeof(Cut)));
+}
 
 cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s) {
     return a.cache.D == 64 ? launch_many<64>(a, s) : launch_many<128>(a, s);
