@@ -402,8 +402,8 @@ int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int
  *   offsets    NULL (one query a sequence: T == B) or device int64 [B+1], non-decreasing in
  *              [0, T] (values outside are clamped to it; a sequence that ends before it starts has none)
  *   out        [T,Hq,D], F32 or BF16; rows of no sequence are not written, nor their lse
- *   workspace  nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, page_size, dtype) bytes,
- *              written and read by this call alone
+ *   workspace  nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, page_size, dtype, ragged) bytes
+ *              (ragged: 1 with offsets, 0 without), written and read by this call alone
  * Keys and values are exact in f16.  Queries enter as f16 after a power-of-two scaling per head, off
  * by at most 2^-39 of the head's largest magnitude (BF16), or as two f16, off by 2^-23 of themselves or
  * 2^-39 of that magnitude (F32); weights enter the second product as f16, or as two for F32
@@ -414,7 +414,7 @@ int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int
  * writes NaN.
  */
 int64_t nvfp4_cache_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width,
-                                        int64_t page_size, int dtype);
+                                        int64_t page_size, int dtype, int ragged);
 int nvfp4_cache_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride, int dtype, const uint8_t* cache,
                           int64_t pages, int64_t page_size, int64_t Hkv, int64_t D, const int32_t* page_table,
                           int64_t B, int64_t width, const int64_t* lengths, const int64_t* offsets, int k_mode,

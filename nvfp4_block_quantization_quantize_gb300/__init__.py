@@ -161,7 +161,7 @@ def load_library(path: str | None = None):
         lib.nvfp4_cache_attention.argtypes = [P, i64, i64, i64, i32, P, i64, i64, i64, i64, P, i64, i64, P, P, i32, P, i32,
                                               P, f32, f32, i32, i64, P, P, i32, P, P, i64, P]
         lib.nvfp4_cache_attention_workspace.restype = i64
-        lib.nvfp4_cache_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64, i64, i32]
+        lib.nvfp4_cache_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64, i64, i32, i32]
         lib.nvfp4_last_error.restype = ctypes.c_char_p
         lib.nvfp4_last_error.argtypes = []
         lib.nvfp4_abi_version.restype = i32
@@ -1382,7 +1382,7 @@ def nvfp4_cache_attention(q: torch.Tensor, cache: torch.Tensor, pages: torch.Ten
     tdt = torch.float32 if odt == F32 else torch.bfloat16
     o = torch.empty((T, Hq, D), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, T * Hq * D, dev)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    need = lib.nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, P, dt)
+    need = lib.nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, P, dt, int(offsets is not None))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _launch(lib, lib.nvfp4_cache_attention, dev, q.data_ptr(), T, Hq, qs, dt, cache.data_ptr(), n_pages, P, Hkv, D,
             pages.data_ptr(), B, width, lengths.data_ptr(), _addr(offsets), km, _addr(kg), vm, _addr(vg), scale_bound,

@@ -609,21 +609,21 @@ int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int
 
 // the sizes that fix an attention's kernels and workspace; false where there is nothing to do or they are out of range
 static bool attend_sizes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width, int64_t page_size,
-                         int dtype, nvfp4::AttendArgs* a) {
+                         int dtype, int ragged, nvfp4::AttendArgs* a) {
     constexpr int64_t kMax = int64_t{1} << 30, kHeads = 1 << 15;
     if (T <= 0 || Hq <= 0 || Hkv <= 0 || B <= 0 || T >= kMax || Hq >= kHeads || Hkv >= kHeads || B >= kMax || Hq % Hkv ||
         (D != 64 && D != 128 && D != 256) || width < 0 || page_size <= 0 || page_size % 16 || page_size >= kMax ||
         width >= kMax / page_size)
         return false;
-    a->T = T, a->Hq = static_cast<int>(Hq), a->B = B, a->width = width, a->dtype = dtype;
+    a->T = T, a->Hq = static_cast<int>(Hq), a->B = B, a->width = width, a->dtype = dtype, a->ragged = ragged;
     a->cache.Hkv = static_cast<int>(Hkv), a->cache.D = static_cast<int>(D), a->cache.page_size = static_cast<int>(page_size);
     return true;
 }
 
 int64_t nvfp4_cache_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t width,
-                                        int64_t page_size, int dtype) {
+                                        int64_t page_size, int dtype, int ragged) {
     nvfp4::AttendArgs a = {};
-    return attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, &a) ? nvfp4::attend_workspace(a) : 0;
+    return attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, ragged, &a) ? nvfp4::attend_workspace(a) : 0;
 }
 
 int nvfp4_cache_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride, int dtype, const uint8_t* cache,
@@ -660,7 +660,7 @@ int nvfp4_cache_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride
     if ((rc = check_ptr(out, "out", any))) return rc;
     if ((rc = check_ptr(lse, "lse", false, 4))) return rc;
     nvfp4::AttendArgs a = {};
-    if (!any || !attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, &a)) return NVFP4_OK;
+    if (!any || !attend_sizes(T, Hq, Hkv, D, B, width, page_size, dtype, offsets != nullptr, &a)) return NVFP4_OK;
     const int64_t need = nvfp4::attend_workspace(a);
     if (workspace_bytes < need)
         return fail(NVFP4_EINVAL, "the workspace needs %lld bytes (got %lld)", (long long)need, (long long)workspace_bytes);

@@ -669,7 +669,7 @@ constexpr int kSmall = 512;                               // keys up to which a 
 
 int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
     const int64_t G = a.Hq / a.cache.Hkv;
-    const int64_t tiles = a.offsets ? a.T * G / R + a.B : a.B * ((G + R - 1) / R);
+    const int64_t tiles = a.ragged ? a.T * G / R + a.B : a.B * ((G + R - 1) / R);
     return tiles * a.cache.Hkv;
 }
 
@@ -713,7 +713,7 @@ constexpr int kManyRows = 64;
 
 // whether a sequence may have that many
 bool may_have_many(const AttendArgs& a) {
-    return a.offsets && a.dtype == NVFP4_BF16 && a.cache.D <= 128 && a.T * (a.Hq / a.cache.Hkv) > kManyRows;
+    return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && (a.ragged ? a.T : 1) * (a.Hq / a.cache.Hkv) > kManyRows;
 }
 
 }  // namespace

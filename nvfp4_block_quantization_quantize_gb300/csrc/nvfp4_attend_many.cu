@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     if (threadIdx.x == 32) {
         for (int i = 0; i < kBars; ++i) {
             const bool threads = i == kQFull || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull);
-            mbar_init(bars + i, threads ? 128 : 1);
+            mbar_init(bars + i, threads ? 128 : i == kQEmpty ? 9 : 1);       // the products' end and 8 softmax warps
         }
         *lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -627,11 +627,16 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             int query, head;
             split_row(it.s.n, G, min(run.at.rt * kRows + r, it.s.n * G - 1), &query, &head);
             float m = kLowest, l = 0.0f;
+            float c = 0.0f;
+            if (from < to) {                              // (a tile that has no rows waits too: it must not fall a part behind)
+                if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
+                c = factors[r];
+                __syncwarp();
+                if (lane == 0) arrive(bars + kQEmpty);
+            }
             if (from < to && wg * 128 < it.rows) {
                 const int p = it.s.len - it.s.n + query;
                 const int hi = a.causal ? min(it.s.len, max(p + 1, 0)) : it.s.len, lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-                if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
-                const float c = factors[r];
                 for (int blk = from; blk < to; ++blk, ++turn) {
                     const uint32_t block = n + blk - from;
                     const int j0 = it.j0 + blk * kKeys;

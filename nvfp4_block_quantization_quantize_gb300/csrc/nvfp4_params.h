@@ -161,6 +161,7 @@ struct AttendArgs {
     int64_t B, width;
     const int64_t* lengths;
     const int64_t* offsets;                                 // null = one query a sequence
+    int ragged;                                             // offsets are given (where sizes alone count)
     float scale;
     int causal, window;
     const float* sinks;
