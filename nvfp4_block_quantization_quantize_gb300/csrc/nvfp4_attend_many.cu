@@ -36,24 +36,37 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn) {
     return 1u << 4 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(N >> 3) << 17 | static_cast<uint32_t>(M >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+// A matrix descriptor's upper word is the same for all operands of a kind; the lower is an address (in 16 bytes) and the
+// step between pieces along the other way.  Steps are added where the product is issued: as values of their own they would
+// fill the registers.
+constexpr uint32_t kDescUpper = 1024 >> 4 | 1u << 14 | 2u << 29;      // 8 rows of 128 swizzled bytes apart (smem_desc)
+
+template <int STEP_A, int STEP_B>
+__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint32_t da, uint32_t db, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(el)
+        "add.u32 x, %1, %6;\n\t"
+        "add.u32 y, %2, %7;\n\t"
+        "mov.b64 da, {x, %8};\n\t"
+        "mov.b64 db, {y, %8};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(da), "r"(db), "r"(idesc), "r"(acc), "r"(el), "n"(STEP_A), "n"(STEP_B), "n"(kDescUpper)
         : "memory");
 }
 
 // A from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
+template <int STEP_B>
+__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t ta, uint32_t db, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(ta), "l"(db), "r"(idesc), "r"(acc), "r"(el)
+        "add.u32 y, %2, %6;\n\t"
+        "mov.b64 db, {y, %7};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(ta), "r"(db), "r"(idesc), "r"(acc), "r"(el), "n"(STEP_B), "n"(kDescUpper)
         : "memory");
 }
 
@@ -108,6 +121,20 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// 16 bytes of codes and 2 of scales, zeros where not wanted (without a branch)
+__device__ __forceinline__ void load_if(bool wanted, const uint8_t* codes, const uint8_t* scales, uint4& w, uint32_t& sc) {
+    uint16_t s;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b16 %4, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%5];\n\t"
+        "@p ld.global.nc.b16 %4, [%6];\n\t}"
+        : "=&r"(w.x), "=&r"(w.y), "=&r"(w.z), "=&r"(w.w), "=&h"(s)
+        : "l"(codes), "l"(scales), "r"(static_cast<int>(wanted)));
+    sc = s;
+}
+
 template <int N>
 __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -135,6 +162,14 @@ template <int N>
 struct Constant {
     static constexpr int value = N;
 };
+
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F f) {           // f(0) .. f(N - 1), each with its constant
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(Constant<N - 1>());
+    }
+}
 
 // The work of a sequence, in keys that its groups of 256 rows are to look at: w0 + rt * step a group of row tile rt (the
 // first kGroupKeys for what it costs besides).  With a causal mask the row tiles look at more and more; that they look at whole
@@ -264,7 +299,7 @@ struct Many {
     static constexpr int bars = factor + kRows * 4;
     static constexpr int spots = bars + 256;              // where the runs of the CTA before, of this and the next start
     static constexpr int runs = spots + 3 * sizeof(Spot); // of each warp
-    static constexpr int bytes = runs + 16 * sizeof(Run) + 1024;      // and up to 1023 to align
+    static constexpr int bytes = runs + 16 * sizeof(Run);
     // tensor memory: S (and P over it) of A and B, O of A and B
     static constexpr int s_col = 0, o_col = 2 * kKeys;
     static constexpr int cols = 512;
@@ -352,8 +387,7 @@ __device__ __noinline__ float masked_weights(float m, float c, Seen seen, uint32
 template <int D>
 __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArgs a) {
     using M = Many<D>;
-    extern __shared__ uint8_t dynamic[];
-    uint8_t* const smem = dynamic + (1024 - smem_addr(dynamic) % 1024) % 1024;
+    extern __shared__ __align__(1024) uint8_t smem[];     // (where it is not, the CTA gives up below)
     float* const factors = reinterpret_cast<float*>(smem + M::factor);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + M::bars);
     uint32_t* const tmem_base = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -406,7 +440,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         __syncwarp();
     };
     uint32_t n = 0, items = 0;                            // blocks and parts with blocks so far
-    bool ok = *tmem_base == 0;
+    bool ok = *tmem_base == 0 && smem_addr(smem) % 1024 == 0;
 
     if (wg == 2) {
         // ---- producers
@@ -421,6 +455,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             piece[j] = upper * M::half + token * 128 + ((((pair & 1) * 4 + (j ^ 2 * upper)) ^ (token & 7)) << 4);
+        const int skip_pages = 8 / per_page, skip_tiles = 8 % per_page;
         uint4 kw[kPairs], vw[kPairs];                     // the next block's codes and scales
         uint32_t ks[kPairs], vs[kPairs];
         for (; ok && run.more; step()) {
@@ -429,31 +464,28 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             if (from == to) continue;
             const int pos0 = it.s.len - it.s.n;
             const int seen_lo = a.window > 0 ? max(0, pos0 + it.first - a.window + 1) : 0;
-            const int32_t* const table = a.pages + run.at.b * a.width;
-            const int tiles_end = (it.s.len + 15) / 16;
-            // a lane below 8 holds a tile of a block: its page, and where it lies in the cache (-1: nowhere)
-            auto tile_of_lane = [&](int block) { return it.j0 / 16 + block * 8 + (lane & 7); };
-            auto page_of = [&](int block) {
-                const int tl = tile_of_lane(block);
-                return block < to && tl < tiles_end ? __ldg(table + tl / per_page) : -1;
+            // a lane below 8 holds a tile of the block whose loads come next: its number (tl), its page's place in the table
+            // and its place in the page, counted along
+            const int tiles_end = min((it.s.len + 15) / 16, it.j0 / 16 + to * 8);
+            int tl = it.j0 / 16 + from * 8 + (lane & 7);
+            const int32_t* table = a.pages + run.at.b * a.width + tl / per_page;
+            int tip = tl % per_page;
+            auto page_of = [&]() { return tl < tiles_end ? __ldg(table) : -1; };
+            // its number in the cache (-1: none); the next block's tile
+            auto place_of = [&](int32_t page) {
+                const int place = page >= 0 && page < a.cache.pages ? (page * a.cache.Hkv + h) * per_page + tip : -1;
+                tl += 8, tip += skip_tiles, table += skip_pages;
+                if (tip >= per_page) tip -= per_page, ++table;
+                return place;
             };
-            auto place_of = [&](int block, int32_t page) {
-                return page >= 0 && page < a.cache.pages
-                           ? ((static_cast<int64_t>(page) * a.cache.Hkv + h) * per_page + tile_of_lane(block) % per_page) * kRecord<D>
-                           : -1;
-            };
-            auto load = [&](int64_t at, uint4* w, uint32_t* sc, int part) {
+            auto load = [&](int at, uint4* w, uint32_t* sc, int part) {
                 const uint8_t* const codes = a.cache.data + part + row * (D / 2) + pair * 16;
                 const uint8_t* const scales = a.cache.data + part + 8 * D + row * (D / 16) + pair * 2;
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) {
-                    const int64_t x = __shfl_sync(kFullMask, at, (i * kTokens + token) / 16);
-                    w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    sc[i] = 0;
-                    if (x >= 0) {
-                        w[i] = __ldg(reinterpret_cast<const uint4*>(codes + x));
-                        sc[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + x));
-                    }
+                    const int x = __shfl_sync(kFullMask, at, (i * kTokens + token) / 16);
+                    const int64_t from = static_cast<int64_t>(x) * kRecord<D>;
+                    load_if(x >= 0, codes + from, scales + from, w[i], sc[i]);
                 }
             };
             auto store = [&](uint8_t* base, const uint4* w, const uint32_t* sc) {
@@ -471,7 +503,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     }
                 }
             };
-            int64_t at = place_of(from, page_of(from));
+            int at = place_of(page_of());
             load(at, kw, ks, 0);
             load(at, vw, vs, 9 * D);
             // ---- this item's queries, two rows a thread
@@ -514,14 +546,14 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             for (int blk = from; blk < to; ++blk, ++n) {
                 const int st = n & 1, j0 = it.j0 + blk * kKeys;
                 const uint32_t ph = n >> 1 & 1;
-                const int32_t page = page_of(blk + 1);
+                const int32_t page = page_of();               // of the next block's tile
                 if (n >= 2 && !(ok = wait(bars + kKEmpty + st, ph ^ 1, lost))) break;
                 store(smem + M::k + st * M::tile, kw, ks);
                 const unsigned have = __ballot_sync(kFullMask, lane < 8 && at >= 0);
                 if (t == 0) there[n & 3] = have;
                 fence_async();
                 arrive(bars + kKFull + st);
-                at = place_of(blk + 1, page);
+                at = place_of(page);
                 load(at, kw, ks, 0);
                 if (j0 < seen_lo || j0 + kKeys > it.s.len) {      // some values were perhaps never written
 #pragma unroll
@@ -544,24 +576,22 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         if (warp == 12) {
         const uint32_t el = elect_one();
         const uint32_t id_s = idesc_f16(128, kKeys, false), id_o = idesc_f16(128, D, true);
-        const uint32_t base = smem_addr(smem);
+        const uint32_t base = smem_addr(smem) >> 4;
         // (tile and stage are constants where these are called)
         auto qk = [&](int tile, int st) {
-            const uint64_t q = smem_desc(base + M::q + tile * M::tile, 16, 1024, 2);
-            const uint64_t k = smem_desc(base + M::k + st * M::tile, 16, 1024, 2);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint64_t step = (i / 4 * M::half + i % 4 * 32) >> 4;
-                mma_ss(el, tmem + M::s_col + tile * kKeys, q + step, k + step, id_s, i > 0);
-            }
+            const uint32_t q = base + ((M::q + tile * M::tile) >> 4) + (1u << 16), k = base + ((M::k + st * M::tile) >> 4) + (1u << 16);
+            unrolled<D / 16>([&](auto step) {
+                constexpr int i = decltype(step)::value, at = (i / 4 * M::half + i % 4 * 32) >> 4;
+                mma_ss<at, at>(el, tmem + M::s_col + tile * kKeys, q, k, id_s, i > 0);
+            });
             commit_warp<1>(el, bars + kSFull + tile);
         };
         auto pv = [&](int tile, int st, bool first) {
-            const uint64_t v = smem_desc(base + M::v + st * M::tile, M::half, 1024, 2);
-#pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-                mma_ts(el, tmem + M::o_col + tile * D, tmem + M::s_col + tile * kKeys + i * 8, v + (i * 2048 >> 4), id_o,
-                       i > 0 ? 1u : !first);
+            const uint32_t v = base + ((M::v + st * M::tile) >> 4) + (static_cast<uint32_t>(M::half >> 4) << 16);
+            unrolled<kKeys / 16>([&](auto step) {
+                constexpr int i = decltype(step)::value;
+                mma_ts<(i * 2048 >> 4)>(el, tmem + M::o_col + tile * D, tmem + M::s_col + tile * kKeys + i * 8, v, id_o, i > 0 ? 1u : !first);
+            });
         };
         uint32_t turn_b = 0;                              // blocks that tile B took part in
         for (; ok && run.more; step()) {
