@@ -4,9 +4,9 @@
 // The rows are a sequence's queries times the heads that share a KV head; two tiles of
 // 128 rows share each block of 128 keys.  4 D operations a row and key: bound by the tensor
 // cores (tcgen05, f16, fp32 sums in tensor memory), with 256 rows' softmax and the decoding of a block beside them.
-//   - Producers (a warpgroup) load the next block's codes into registers while they decode the present one
-//     to f16 in shared memory, exactly (q * dec(s)); keys and values lie alike, 64 elements of a token to 128
-//     swizzled bytes: K-major for S = Q K^T, MN-major for O += P V.
+//   - Producers (a warpgroup for keys, one for values) load the next block's codes into registers while they decode
+//     the present one to f16 in shared memory, exactly (q * dec(s)); keys and values lie alike, 64 elements of a
+//     token to 128 swizzled bytes: K-major for S = Q K^T, MN-major for O += P V.
 //   - One warp issues the products: S of tile A, S of B, then for each block O of a tile and its next S.
 //     While one tile's softmax runs the other's products do.
 //   - A softmax warpgroup a tile, a thread a row: S out of tensor memory, weights back as f16 over S,
@@ -21,11 +21,13 @@ namespace {
 
 constexpr int kRows = 256;                                // of a group: two tiles of 128
 constexpr int kKeys = 128;                                // of a block
-constexpr int kThreadsMany = 512;                         // softmax A, softmax B, producers, products
+constexpr int kThreadsMany = 640;                         // warpgroups: softmax A, softmax B, keys, products, values
+constexpr int kLaunchRegisters = 96;                      // of a thread
 
-// registers of a thread after the launch's 128 are shared out anew
-constexpr int kSoftmaxRegisters = 168, kProducerRegisters = 104, kProductRegisters = 72;
-static_assert(256 * kSoftmaxRegisters + 128 * kProducerRegisters + 128 * kProductRegisters <= kThreadsMany * 128, "no more than were launched");
+// registers of a thread after they are shared out anew
+constexpr int kSoftmaxRegisters = 128, kProducerRegisters = 80, kProductRegisters = 64;
+static_assert(128 * (2 * kSoftmaxRegisters + 2 * kProducerRegisters + kProductRegisters) <= kThreadsMany * kLaunchRegisters,
+              "no more than were launched");
 
 enum Bar { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
            kPFull = kSFull + 2, kOFull = kPFull + 2, kBars = kOFull + 2 };
@@ -299,7 +301,7 @@ struct Many {
     static constexpr int bars = factor + kRows * 4;
     static constexpr int spots = bars + 256;              // where the runs of the CTA before, of this and the next start
     static constexpr int runs = spots + 3 * sizeof(Spot); // of each warp
-    static constexpr int bytes = runs + 16 * sizeof(Run);
+    static constexpr int bytes = runs + kThreadsMany / 32 * sizeof(Run);
     // tensor memory: S (and P over it) of A and B, O of A and B
     static constexpr int s_col = 0, o_col = 2 * kKeys;
     static constexpr int cols = 512;
@@ -403,8 +405,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < kBars; ++i) {
-            const bool threads = i == kQFull || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull);
-            mbar_init(bars + i, threads ? 128 : i == kQEmpty ? 9 : 1);       // the products' end and 8 softmax warps
+            const bool threads = (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull);
+            mbar_init(bars + i, i == kQFull ? 256 : threads ? 128 : i == kQEmpty ? 9 : 1);       // (the products' end and 8 softmax warps)
         }
         *lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -442,8 +444,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     uint32_t n = 0, items = 0;                            // blocks and parts with blocks so far
     bool ok = *tmem_base == 0 && smem_addr(smem) % 1024 == 0;
 
-    if (wg == 2) {
-        // ---- producers
+    if (wg == 2 || wg == 4) {
+        // ---- producers: of keys and Q of tile A, of values and Q of tile B
         registers_down<kProducerRegisters>();
         // A thread takes 32 elements of a token: kPairs threads a token, kTokens tokens at once, kPairs turns a block.
         constexpr int kPairs = D / 32, kTokens = 128 / kPairs;
@@ -451,13 +453,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         // 32 elements are four 16-byte pieces of the swizzled row; the upper half's threads begin with the third, so that 8
         // threads' pieces lie in 8 bank groups
         const int upper = pair >> 1;
-        uint32_t piece[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            piece[j] = upper * M::half + token * 128 + ((((pair & 1) * 4 + (j ^ 2 * upper)) ^ (token & 7)) << 4);
+        const uint32_t piece = upper * M::half + token * 128 + (((pair & 1) * 4 ^ 2 * upper ^ token & 7) << 4);    // the j-th: ^ j << 4
         const int skip_pages = 8 / per_page, skip_tiles = 8 % per_page;
-        uint4 kw[kPairs], vw[kPairs];                     // the next block's codes and scales
-        uint32_t ks[kPairs], vs[kPairs];
+        const bool values = wg == 4;
+        uint64_t *const full = bars + (values ? kVFull : kKFull), *const empty = bars + (values ? kVEmpty : kKEmpty);
+        uint8_t* const ring = smem + (values ? M::v : M::k);
+        const int codes = (values ? 9 * D : 0) + row * (D / 2) + pair * 16;       // in a tile
+        const int scales = (values ? 17 * D : 8 * D) + row * (D / 16) + pair * 2;
+        uint4 w[kPairs];                                  // the next block's codes and scales
+        uint32_t sc[kPairs];
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
             const int h = run.at.h, from = run.at.blk, to = run.to(it);
@@ -478,39 +482,20 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 if (tip >= per_page) tip -= per_page, ++table;
                 return place;
             };
-            auto load = [&](int at, uint4* w, uint32_t* sc, int part) {
-                const uint8_t* const codes = a.cache.data + part + row * (D / 2) + pair * 16;
-                const uint8_t* const scales = a.cache.data + part + 8 * D + row * (D / 16) + pair * 2;
+            auto load = [&](int at) {
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) {
                     const int x = __shfl_sync(kFullMask, at, (i * kTokens + token) / 16);
-                    const int64_t from = static_cast<int64_t>(x) * kRecord<D>;
-                    load_if(x >= 0, codes + from, scales + from, w[i], sc[i]);
-                }
-            };
-            auto store = [&](uint8_t* base, const uint4* w, const uint32_t* sc) {
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i) {
-                    const uint32_t u = e4m3_pair(sc[i]);
-                    const uint32_t s0 = __byte_perm(u, u, upper ? 0x3232 : 0x1010), s1 = __byte_perm(u, u, upper ? 0x1010 : 0x3232);
-                    const uint32_t x[4] = {upper ? w[i].z : w[i].x, upper ? w[i].w : w[i].y, upper ? w[i].x : w[i].z,
-                                           upper ? w[i].y : w[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t o[4];
-                        decode4(x[j], j < 2 ? s0 : s1, o);
-                        *reinterpret_cast<uint4*>(base + piece[j] + i * kTokens * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    const uint8_t* const tile = a.cache.data + static_cast<int64_t>(x) * kRecord<D>;
+                    load_if(x >= 0, tile + codes, tile + scales, w[i], sc[i]);
                 }
             };
             int at = place_of(page_of());
-            load(at, kw, ks, 0);
-            load(at, vw, vs, 9 * D);
-            // ---- this item's queries, two rows a thread
+            load(at);
+            // ---- this item's queries, a row a thread
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
-            for (int tile = 0; ok && tile < 2; ++tile) {
-                const int r = tile * 128 + t;
-                if (tile == 1 && it.rows <= 128) break;
+            const int tile = values ? 1 : 0, r = tile * 128 + t;
+            if (ok && tile * 128 < it.rows) {
                 const bool in = r < it.rows;
                 int query, head;
                 split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
@@ -545,28 +530,35 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             // ---- its blocks
             for (int blk = from; blk < to; ++blk, ++n) {
                 const int st = n & 1, j0 = it.j0 + blk * kKeys;
-                const uint32_t ph = n >> 1 & 1;
                 const int32_t page = page_of();               // of the next block's tile
-                if (n >= 2 && !(ok = wait(bars + kKEmpty + st, ph ^ 1, lost))) break;
-                store(smem + M::k + st * M::tile, kw, ks);
-                const unsigned have = __ballot_sync(kFullMask, lane < 8 && at >= 0);
-                if (t == 0) there[n & 3] = have;
-                fence_async();
-                arrive(bars + kKFull + st);
-                at = place_of(page);
-                load(at, kw, ks, 0);
-                if (j0 < seen_lo || j0 + kKeys > it.s.len) {      // some values were perhaps never written
+                if (values && (j0 < seen_lo || j0 + kKeys > it.s.len)) {      // some were perhaps never written
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i) {
                         const int j = j0 + i * kTokens + token;
-                        if (j < seen_lo || j >= it.s.len) vs[i] = 0;
+                        if (j < seen_lo || j >= it.s.len) sc[i] = 0;
                     }
                 }
-                if (n >= 2 && !(ok = wait(bars + kVEmpty + st, ph ^ 1, lost))) break;
-                store(smem + M::v + st * M::tile, vw, vs);
+                if (n >= 2 && !(ok = wait(empty + st, (n >> 1 & 1) ^ 1, lost))) break;
+                uint8_t* const base = ring + st * M::tile;
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const uint32_t u = e4m3_pair(sc[i]);
+                    const uint32_t s0 = __byte_perm(u, u, upper ? 0x3232 : 0x1010), s1 = __byte_perm(u, u, upper ? 0x1010 : 0x3232);
+                    const uint32_t x[4] = {upper ? w[i].z : w[i].x, upper ? w[i].w : w[i].y, upper ? w[i].x : w[i].z,
+                                           upper ? w[i].y : w[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+                        decode4(x[j], j < 2 ? s0 : s1, o);
+                        *reinterpret_cast<uint4*>(base + (piece ^ j << 4) + i * kTokens * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                const unsigned have = __ballot_sync(kFullMask, lane < 8 && at >= 0);
+                if (t == 0 && !values) there[n & 3] = have;
                 fence_async();
-                arrive(bars + kVFull + st);
-                load(at, vw, vs, 9 * D);
+                arrive(full + st);
+                at = place_of(page);
+                load(at);
             }
             ++items;
         }
