@@ -492,36 +492,37 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             };
             int at = place_of(page_of());
             load(at);
-            // ---- this item's queries, a row a thread
+            // ---- this item's queries: D / 8 threads a row, a warp 32 rows
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
-            const int tile = values ? 1 : 0, r = tile * 128 + t;
+            const int tile = values ? 1 : 0;
             if (ok && tile * 128 < it.rows) {
-                const bool in = r < it.rows;
-                int query, head;
-                split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
-                const uint16_t* src = static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
-                                      (static_cast<int64_t>(h) * G + head) * D;
-                uint32_t top = 0;
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                    top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(top, u.x), u.y), u.z), u.w);
-                }
-                top = max(top << 16, top & 0xFFFF0000u);
-                const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
-                const float down = copysignf(power_of_two(-ex), a.scale);
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
                 float dec = 1.0f, enc;
                 if (a.cache.k_mode != NVFP4_GAMAX_NONE)
                     global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
-                factors[r] = mul_rn(power_of_two(ex), mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec));
-                uint8_t* const dst = smem + M::q + tile * M::tile + t * 128;
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                const float all = mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec);
+                const int q = lane % kLanes;
+#pragma unroll 4
+                for (int i = 0; i < 32 / kAtOnce; ++i) {
+                    const int in_tile = (warp & 3) * 32 + i * kAtOnce + lane / kLanes, r = tile * 128 + in_tile;
+                    int query, head;
+                    split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
+                                                                         (static_cast<int64_t>(h) * G + head) * D) + q);
+                    uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y), u.z), u.w);
+                    top = max(top << 16, top & 0xFFFF0000u);
+#pragma unroll
+                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+                    const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
+                    const float down = copysignf(power_of_two(-ex), a.scale);
+                    if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
                     uint32_t o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = in ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
-                    *reinterpret_cast<uint4*>(dst + i / 8 * M::half + (((i & 7) ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int k = 0; k < 4; ++k)           // rows past the group's last are zeros
+                        o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                    *reinterpret_cast<uint4*>(smem + M::q + tile * M::tile + q / 8 * M::half + in_tile * 128 + (((q & 7) ^ (in_tile & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (!ok) break;
