@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kRows = 256;                                // of a group: two tiles of 128
 constexpr int kKeys = 128;                                // of a block
-constexpr int kThreadsMany = 640;                         // warpgroups: softmax A, softmax B, keys, products, values
+constexpr int kThreadsMany = 640;                         // warpgroups: products, softmax A, softmax B, keys, values
 constexpr int kLaunchRegisters = 96;                      // of a thread
 
 // registers of a thread after they are shared out anew
@@ -142,22 +142,30 @@ __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sy
 template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+__device__ __forceinline__ bool done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
+
 // A warp's wait; it ends too when another one has run out.  False then, for all lanes.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
-    uint32_t ok = 0;
-#pragma unroll 1
-    for (long it = 0; it < kWaitLimit && !ok; ++it) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (!ok && (it & 15) == 15 && *lost) break;
+__device__ __forceinline__ bool long_wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
+    for (long it = 0; it < kWaitLimit; ++it) {
+        if (__all_sync(kFullMask, done(bar, parity))) return true;
+        if ((it & 15) == 15 && __any_sync(kFullMask, *lost)) return false;
     }
-    if (!ok) *lost = 1;
-    return __all_sync(kFullMask, ok);
+    *lost = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* lost) {
+    return __all_sync(kFullMask, done(bar, parity)) || long_wait(bar, parity, lost);
 }
 
 template <int N>
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     uint32_t n = 0, items = 0;                            // blocks and parts with blocks so far
     bool ok = *tmem_base == 0 && smem_addr(smem) % 1024 == 0;
 
-    if (wg == 2 || wg == 4) {
+    if (wg >= 3) {
         // ---- producers: of keys and Q of tile A, of values and Q of tile B
         registers_down<kProducerRegisters>();
         // A thread takes 32 elements of a token: kPairs threads a token, kTokens tokens at once, kPairs turns a block.
@@ -563,10 +571,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             }
             ++items;
         }
-    } else if (wg == 3) {
-        // ---- products
+    } else if (wg == 0) {
+        // ---- products (the oldest warp: the first to issue)
         registers_down<kProductRegisters>();
-        if (warp == 12) {
+        if (warp == 0) {
         const uint32_t el = elect_one();
         const uint32_t id_s = idesc_f16(128, kKeys, false), id_o = idesc_f16(128, D, true);
         const uint32_t base = smem_addr(smem) >> 4;
@@ -607,12 +615,12 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             auto turn = [&](auto stage, int blk) {
                 constexpr int st = decltype(stage)::value, st1 = st ^ 1;
                 const bool more = blk + 1 < to;
-                if (!wait(bars + kVFull + st, n >> 1 & 1, lost) || !wait(bars + kPFull, n & 1, lost)) return false;
+                if (!wait(bars + kVFull + st, n >> 1 & 1, lost)) return false;
+                if (more && !wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost)) return false;
+                if (!wait(bars + kPFull, n & 1, lost)) return false;
                 fence_after();
                 pv(0, st, blk == from);
                 if (more) {
-                    if (!wait(bars + kKFull + st1, (n + 1) >> 1 & 1, lost)) return false;
-                    fence_after();
                     qk(0, st1);
                 } else {
                     commit_warp<1>(el, bars + kOFull);
@@ -638,15 +646,16 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         }
         }
     } else {
-        // ---- softmax of tile wg: this thread's row
+        // ---- softmax of a tile: this thread's row
         registers_up<kSoftmaxRegisters>();
+        const int tile = wg - 1;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;           // 32 lanes of tensor memory a warp
-        const uint32_t s_at = tmem + lanes + M::s_col + wg * kKeys, o_at = tmem + lanes + M::o_col + wg * D;
+        const uint32_t s_at = tmem + lanes + M::s_col + tile * kKeys, o_at = tmem + lanes + M::o_col + tile * D;
         uint32_t turn = 0, mine = 0;                      // blocks and items that this tile took part in
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
             const int h = run.at.h, from = run.at.blk, to = run.to(it);
-            const int r = wg * 128 + t;
+            const int r = tile * 128 + t;
             int query, head;
             split_row(it.s.n, G, min(run.at.rt * kRows + r, it.s.n * G - 1), &query, &head);
             float m = kLowest, l = 0.0f;
@@ -657,14 +666,14 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 __syncwarp();
                 if (lane == 0) arrive(bars + kQEmpty);
             }
-            if (from < to && wg * 128 < it.rows) {
+            if (from < to && tile * 128 < it.rows) {
                 const int p = it.s.len - it.s.n + query;
                 const int hi = a.causal ? min(it.s.len, max(p + 1, 0)) : it.s.len, lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
                 for (int blk = from; blk < to; ++blk, ++turn) {
                     const uint32_t block = n + blk - from;
                     const int j0 = it.j0 + blk * kKeys;
                     // (a tile that sat out an item keeps its own count of S and P)
-                    if (!(ok = wait(bars + kSFull + wg, turn & 1, lost))) break;
+                    if (!(ok = wait(bars + kSFull + tile, turn & 1, lost))) break;
                     fence_after();
                     const uint32_t have = there[block & 3];
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
@@ -711,16 +720,16 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     }
                     tmem_wait_store();
                     fence_before();
-                    arrive(bars + kPFull + wg);
+                    arrive(bars + kPFull + tile);
                 }
                 if (!ok) break;
-                if (!(ok = wait(bars + kOFull + wg, mine & 1, lost))) break;
+                if (!(ok = wait(bars + kOFull + tile, mine & 1, lost))) break;
                 fence_after();
                 ++mine;
             }
             if (from < to) n += to - from, ++items;
             // ---- the row's output (a group without keys gives zeros), or its part of it
-            if (wg * 128 < it.rows) {
+            if (tile * 128 < it.rows) {
                 const bool complete = from == 0 && to == it.blocks;
                 float* const part = reinterpret_cast<float*>(a.workspace) +
                                     (static_cast<int64_t>(blockIdx.x) * 2 + (from > 0 ? 0 : 1)) * kPart<D, kRows>;
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
             __syncwarp();
             for (; run.more; step()) {
                 const Item it(a, run.s, run.at.rt);
-                const int h = run.at.h, from = run.at.blk, r = wg * 128 + t;
+                const int h = run.at.h, from = run.at.blk, r = tile * 128 + t;
                 if (r >= it.rows) continue;
                 int query, head;
                 split_row(it.s.n, G, run.at.rt * kRows + r, &query, &head);
