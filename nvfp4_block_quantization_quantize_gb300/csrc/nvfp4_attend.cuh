@@ -155,6 +155,18 @@ __device__ __forceinline__ float power_of_two(int e) {    // e in [-126, 127]
     return __int_as_float((e + 127) << 23);
 }
 
+// 32 bytes, in one piece if the address is a multiple of 32
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // A row's end: its sums times `by` are its output; m its maximum (of logits times log2 e), l its denominator.
 struct Finish {
     float by, lse;
@@ -172,6 +184,29 @@ struct Finish {
         by = l == 0.0f ? 0.0f : mul_rn(f, div_rn(dec, l));
         lse = 0.0f;
         if (a.lse) lse = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
+    }
+
+    // 16 elements from element d, as two or four 32-byte pieces where the output lies on 32 bytes
+    __device__ __forceinline__ void store16(const AttendArgs& a, int64_t token, int head, int d, const uint32_t* v) const {
+        const int64_t at = (token * a.Hq + head) * a.cache.D + d;
+        float y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = mul_rn(__uint_as_float(v[k]), by);
+        const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+        if (a.out_dtype == NVFP4_F32) {
+            float* const p = static_cast<float*>(a.out) + at;
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) store32(p + k, reinterpret_cast<const uint32_t*>(y + k), wide);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            store32(static_cast<uint16_t*>(a.out) + at, w, wide);
+        }
+        if (a.lse && d == 0) a.lse[token * a.Hq + head] = lse;
     }
 
     // 4 elements from element d

@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 }
             };
             int at = place_of(page_of());
-            load(at);
             // ---- this item's queries: D / 8 threads a row, a warp 32 rows
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
             const int tile = values ? 1 : 0;
@@ -510,32 +509,42 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
                 const float all = mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec);
                 const int q = lane % kLanes;
-#pragma unroll 4
-                for (int i = 0; i < 32 / kAtOnce; ++i) {
-                    const int in_tile = (warp & 3) * 32 + i * kAtOnce + lane / kLanes, r = tile * 128 + in_tile;
-                    int query, head;
-                    split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
-                                                                         (static_cast<int64_t>(h) * G + head) * D) + q);
-                    uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y), u.z), u.w);
-                    top = max(top << 16, top & 0xFFFF0000u);
+                constexpr int kBatch = 8;                 // loads under way together
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32 / kAtOnce; i0 += kBatch) {
+                    uint4 u[kBatch];
 #pragma unroll
-                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
-                    const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
-                    const float down = copysignf(power_of_two(-ex), a.scale);
-                    if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
-                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t o[4];
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = tile * 128 + (warp & 3) * 32 + (i0 + i) * kAtOnce + lane / kLanes;
+                        int query, head;
+                        split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
+                        u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
+                                                                    (static_cast<int64_t>(h) * G + head) * D) + q);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)           // rows past the group's last are zeros
-                        o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
-                    *reinterpret_cast<uint4*>(smem + M::q + tile * M::tile + q / 8 * M::half + in_tile * 128 + (((q & 7) ^ (in_tile & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int in_tile = (warp & 3) * 32 + (i0 + i) * kAtOnce + lane / kLanes, r = tile * 128 + in_tile;
+                        uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u[i].x), u[i].y), u[i].z), u[i].w);
+                        top = max(top << 16, top & 0xFFFF0000u);
+#pragma unroll
+                        for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+                        const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
+                        const float down = copysignf(power_of_two(-ex), a.scale);
+                        if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
+                        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)       // rows past the group's last are zeros
+                            o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                        *reinterpret_cast<uint4*>(smem + M::q + tile * M::tile + q / 8 * M::half + in_tile * 128 + (((q & 7) ^ (in_tile & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
                 }
             }
             if (!ok) break;
             fence_async();
             arrive(bars + kQFull);
+            load(at);
             // ---- its blocks
             for (int blk = from; blk < to; ++blk, ++n) {
                 const int st = n & 1, j0 = it.j0 + blk * kKeys;
@@ -744,13 +753,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                         tmem_load32(o_at + 32 * q, v);
                         tmem_wait_load(v);
                     }
-                    if (r < it.rows)
+                    if (r < it.rows) {
+                        if (complete) {
+                            f.store16(a, it.s.row0 + query, h * G + head, 32 * q, v);
+                            f.store16(a, it.s.row0 + query, h * G + head, 32 * q + 16, v + 16);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float y[4] = {__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])};
-                            if (complete) f.store(a, it.s.row0 + query, h * G + head, 32 * q + i, y);
-                            else *reinterpret_cast<float4*>(part + r * D + 32 * q + i) = make_float4(y[0], y[1], y[2], y[3]);
+                            for (int i = 0; i < 32; i += 8) store32(part + r * D + 32 * q + i, v + i, reinterpret_cast<uintptr_t>(a.workspace) % 32 == 0);
                         }
+                    }
                 }
                 if (!complete && r < it.rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
                 __syncwarp();
