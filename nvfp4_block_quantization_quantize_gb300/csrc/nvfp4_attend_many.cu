@@ -30,7 +30,7 @@ static_assert(128 * (2 * kSoftmaxRegisters + 2 * kProducerRegisters + kProductRe
               "no more than were launched");
 
 enum Bar { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2,
-           kPFull = kSFull + 2, kOFull = kPFull + 2, kBars = kOFull + 2 };
+           kPFull = kSFull + 2, kOFull = kPFull + 2, kRaw = kOFull + 2, kBars = kRaw + 2 };
 
 // ---- tcgen05 --------------------------------------------------------------------------------------
 // .kind::f16: f16 operands, fp32 sums; B K-major or MN-major
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < kBars; ++i) {
-            const bool threads = (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull);
+            const bool threads = (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull) || i >= kRaw;
             mbar_init(bars + i, i == kQFull ? 256 : threads ? 128 : i == kQEmpty ? 9 : 1);       // (the products' end and 8 softmax warps)
         }
         *lost = 0;
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         const int scales = (values ? 17 * D : 8 * D) + row * (D / 16) + pair * 2;
         uint4 w[kPairs];                                  // the next block's codes and scales
         uint32_t sc[kPairs];
+        uint32_t raws = 0;                                // copies of queries so far
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
             const int h = run.at.h, from = run.at.blk, to = run.to(it);
@@ -499,46 +500,44 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 }
             };
             int at = place_of(page_of());
-            // ---- this item's queries: D / 8 threads a row, a warp 32 rows
+            // ---- this item's queries: copied as they are, a row a thread, then made f16 where they lie (its pieces in their
+            // swizzled order), D / 8 threads a row
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
             const int tile = values ? 1 : 0;
             if (ok && tile * 128 < it.rows) {
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+                uint8_t* const dst = smem + M::q + tile * M::tile;
+                int query, head;
+                split_row(it.s.n, G, run.at.rt * kRows + min(tile * 128 + t, it.rows - 1), &query, &head);
+                const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
+                                            (static_cast<int64_t>(h) * G + head) * D;
+                mbar_expect_tx(bars + kRaw + tile, 2 * D);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) bulk_copy(dst + i * M::half + t * 128, src + 64 * i, 128, bars + kRaw + tile);
                 float dec = 1.0f, enc;
                 if (a.cache.k_mode != NVFP4_GAMAX_NONE)
                     global_scales(__ldg(a.cache.k_gamax + (a.cache.k_mode == NVFP4_GAMAX_ROW_GIVEN ? h : 0)), a.cache.bound, enc, dec);
                 const float all = mul_rn(mul_rn(fabsf(a.scale), kLog2e), dec);
+                ok = wait(bars + kRaw + tile, raws++ & 1, lost);
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
                 const int q = lane % kLanes;
-                constexpr int kBatch = 8;                 // loads under way together
 #pragma unroll 1
-                for (int i0 = 0; i0 < 32 / kAtOnce; i0 += kBatch) {
-                    uint4 u[kBatch];
+                for (int i = 0; ok && i < 32; i += kAtOnce) {
+                    const int in_tile = (warp & 3) * 32 + i + lane / kLanes, r = tile * 128 + in_tile;
+                    uint8_t* const at = dst + q / 8 * M::half + in_tile * 128;
+                    const uint4 u = *reinterpret_cast<const uint4*>(at + (q & 7) * 16);
+                    uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y), u.z), u.w);
+                    top = max(top << 16, top & 0xFFFF0000u);
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = tile * 128 + (warp & 3) * 32 + (i0 + i) * kAtOnce + lane / kLanes;
-                        int query, head;
-                        split_row(it.s.n, G, run.at.rt * kRows + min(r, it.rows - 1), &query, &head);
-                        u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (it.s.row0 + query) * a.q_stride +
-                                                                    (static_cast<int64_t>(h) * G + head) * D) + q);
-                    }
+                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));      // all have read
+                    const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
+                    const float down = copysignf(power_of_two(-ex), a.scale);
+                    if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
+                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int in_tile = (warp & 3) * 32 + (i0 + i) * kAtOnce + lane / kLanes, r = tile * 128 + in_tile;
-                        uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u[i].x), u[i].y), u[i].z), u[i].w);
-                        top = max(top << 16, top & 0xFFFF0000u);
-#pragma unroll
-                        for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
-                        const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
-                        const float down = copysignf(power_of_two(-ex), a.scale);
-                        if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
-                        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)       // rows past the group's last are zeros
-                            o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
-                        *reinterpret_cast<uint4*>(smem + M::q + tile * M::tile + q / 8 * M::half + in_tile * 128 + (((q & 7) ^ (in_tile & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)           // rows past the group's last are zeros
+                        o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                    *reinterpret_cast<uint4*>(at + (((q & 7) ^ (in_tile & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (!ok) break;
