@@ -155,18 +155,6 @@ __device__ __forceinline__ float power_of_two(int e) {    // e in [-126, 127]
     return __int_as_float((e + 127) << 23);
 }
 
-// 32 bytes, in one piece if the address is a multiple of 32
-__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-
 // A row's end: its sums times `by` are its output; m its maximum (of logits times log2 e), l its denominator.
 struct Finish {
     float by, lse;

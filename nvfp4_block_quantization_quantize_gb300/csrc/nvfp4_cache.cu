@@ -84,13 +84,23 @@ __device__ __forceinline__ GScale head_scale(int mode, const float* gamax, int h
     return g;
 }
 
-// first byte of the tile that slot s of KV head h lies in, or null when there is no such slot
-__device__ __forceinline__ uint8_t* tile_of(const CacheArgs& c, int64_t s, int h) {
-    if (s < 0 || s >= c.pages * c.page_size) return nullptr;
-    const int64_t page = s / c.page_size;
-    const int row = static_cast<int>(s - page * c.page_size);
-    return c.data + ((page * c.Hkv + h) * (c.page_size / 16) + row / 16) * (18 * c.D);
+// Where a slot lies: its page's first byte plus its tile's place there, for head 0 (null: there is no such slot), and its row
+// of the tile.
+struct Place {
+    uint8_t* tile;
+    int row;
+};
+
+__device__ __forceinline__ Place place_of(const CacheArgs& c, int64_t s) {
+    if (s < 0 || s >= c.pages * c.page_size) return {nullptr, 0};
+    int64_t page;                                         // (a 64-bit division costs more than a block's quantization)
+    if (s >> 31 == 0) page = static_cast<uint32_t>(s) / static_cast<uint32_t>(c.page_size);
+    else page = s / c.page_size;
+    const int in = static_cast<int>(s - page * c.page_size);
+    return {c.data + (page * c.Hkv * (c.page_size / 16) + in / 16) * (18 * c.D), in % 16};
 }
+
+__device__ __forceinline__ int64_t head_bytes(const CacheArgs& c) { return static_cast<int64_t>(c.page_size / 16) * (18 * c.D); }
 
 // 16 elements from element e of the row that slot s is, as nvfp4_quantize quantizes them
 __device__ __forceinline__ void quantize_into(uint8_t* part, int row, int D, int e, const GScale& g, const float* y) {
@@ -106,106 +116,113 @@ __device__ __forceinline__ void quantize_into(uint8_t* part, int row, int D, int
 }
 
 // L threads a head.  A token's heads (q, k, then v when they go to the cache) are cut into
-// `chunks` of `per` heads, one a warp.
-template <int DT, int L>
-__global__ void __launch_bounds__(kHeadsThreads) k_heads(const HeadsArgs a, int chunks, int per) {
+// `chunks` of `per` heads, one a warp.  TURN: norms and rotation, of pairs half the rotated elements apart (HALF) or of
+// neighbours; CACHE: k and v go to the cache.
+// Registers for as many warps as keep memory busy: 64 a thread without a cache (bf16), 80 with.
+enum Turn { kNoTurn, kHalf, kNeighbours };
+
+template <int DT, int L, Turn TURN, bool CACHE>
+__global__ void __launch_bounds__(kHeadsThreads, DT == NVFP4_BF16 && !(TURN != kNoTurn && CACHE) ? 4 : 3) k_heads(const HeadsArgs a, int chunks, int per) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, t = lane % L, sub = lane / L;
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kHeadsThreads / 32) + (threadIdx.x >> 5);
-    const int64_t token = warp / chunks;
+    const uint32_t warp = blockIdx.x * (kHeadsThreads / 32) + (threadIdx.x >> 5);      // (several chunks: few tokens)
+    const int64_t token = warp / static_cast<uint32_t>(chunks);
     if (token >= a.T) return;                               // whole warps
-    const int first = static_cast<int>(warp - token * chunks) * per;
+    const int first = static_cast<int>(warp % static_cast<uint32_t>(chunks)) * per;
     const int nq = a.q ? a.Hq : 0, total = nq + (a.k ? a.Hkv : 0) + (a.v ? a.Hkv : 0);
     const int end = min(first + per, total);
     const bool live = t < a.D / 16;
-    const bool turned = a.positions && t < a.rotary_dim / 16;
-    const bool apart = turned && a.layout == NVFP4_ROPE_HALF;
+    const bool turned = TURN != kNoTurn && t < a.rotary_dim / 16;
+    const bool apart = TURN == kHalf && turned;
     const int half = a.rotary_dim / 2;
 
     float cs[8], sn[8];
-    if (turned && first < nq + a.Hkv) {
+    if (TURN != kNoTurn && turned && first < nq + a.Hkv) {
         const uint64_t pos = static_cast<uint64_t>(__ldg(a.positions + token));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint64_t turn = pos * __ldg(reinterpret_cast<const unsigned long long*>(a.phases) + 8 * t + i);
             // the nearest of 2^32 parts of a turn, in [-1/2, 1/2), as half turns
             const int32_t part = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
-            sincospif(mul_rn(static_cast<float>(part), 4.656612873077393e-10f), &sn[i], &cs[i]);     // 2^-31
-            cs[i] = mul_rn(cs[i], a.magnitude);
-            sn[i] = mul_rn(sn[i], a.magnitude);
+            float sine, cosine;
+            sincospif(mul_rn(static_cast<float>(part), 4.656612873077393e-10f), &sine, &cosine);     // 2^-31
+            cs[i] = mul_rn(cosine, a.magnitude);
+            sn[i] = mul_rn(sine, a.magnitude);
         }
     }
-    const int64_t slot = a.slots ? __ldg(a.slots + token) : -1;
-    const int row = static_cast<int>((slot < 0 ? 0 : slot) % 16);
+    Place place{nullptr, 0};
+    if (CACHE) place = place_of(a.cache, __ldg(a.slots + token));
 
-    // which head j is, where its elements lie: a thread's are e0 .. e0 + 7 and e1 .. e1 + 7 (v has no pairs)
-    auto offsets = [&](bool pairs, int& e0, int& e1) {
-        e0 = pairs ? 8 * t : 16 * t;
-        e1 = pairs ? half + 8 * t : 16 * t + 8;
-    };
+    // Where a thread's elements of a head lie: e0 .. e0 + 7 and e1 .. e1 + 7 (v has no pairs).  A token's heads are one
+    // after the other.
+    const int e0_qk = apart ? 8 * t : 16 * t, e1_qk = apart ? half + 8 * t : 16 * t + 8;
+    constexpr int kSize = DT == NVFP4_BF16 ? 2 : 4;
+    const uint8_t* const q_in = static_cast<const uint8_t*>(a.q) + token * a.q_stride * kSize;
+    const uint8_t* const k_in = static_cast<const uint8_t*>(a.k) + token * a.k_stride * kSize;
+    const uint8_t* const v_in = static_cast<const uint8_t*>(a.v) + token * a.v_stride * kSize;
+    const int nk = nq + (a.k ? a.Hkv : 0);                // the first head of v
     uint32_t raw[2 * kRaw8<DT>];
     auto load = [&](int j) {
         if (j >= end || !live) return;
-        const bool is_q = j < nq, is_v = !is_q && (!a.k || j >= nq + a.Hkv);
-        const void* base = is_q ? a.q : is_v ? a.v : a.k;
-        const int h = is_q ? j : is_v ? j - (total - a.Hkv) : j - nq;
-        const int64_t at = token * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + static_cast<int64_t>(h) * a.D;
-        int e0, e1;
-        offsets(apart && !is_v, e0, e1);
-        load8<DT>(base, at + e0, raw);
-        load8<DT>(base, at + e1, raw + kRaw8<DT>);
+        const bool is_v = CACHE && j >= nk;
+        const uint8_t* const head = j < nq ? q_in + j * a.D * kSize : is_v ? v_in + (j - nk) * a.D * kSize : k_in + (j - nq) * a.D * kSize;
+        load8<DT>(head, is_v ? 16 * t : e0_qk, raw);
+        load8<DT>(head, is_v ? 16 * t + 8 : e1_qk, raw + kRaw8<DT>);
     };
     load(first + sub);
     for (int j0 = first; j0 < end; j0 += 32 / L) {
         const int j = j0 + sub;
         const bool in = j < end && live;
-        const bool is_q = j < nq, is_v = !is_q && (!a.k || j >= nq + a.Hkv);
-        const int h = is_q ? j : is_v ? j - (total - a.Hkv) : j - nq;
-        int e0, e1;
-        offsets(apart && !is_v, e0, e1);
+        const bool is_q = j < nq, is_v = CACHE && j >= nk;
+        const int e0 = is_v ? 16 * t : e0_qk, e1 = is_v ? 16 * t + 8 : e1_qk;
         float y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = 0.0f;
         if (in) {
             widen8<DT>(raw, y);
             widen8<DT>(raw + kRaw8<DT>, y + 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = 0.0f;
         }
         load(j + 32 / L);
-        const void* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
-        if (a.q_weight || a.k_weight) {                     // the sums of all of the warp's heads
+        if (TURN != kNoTurn && a.q_weight) {                // the sums of all of the warp's heads
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s = __fmaf_rn(y[i], y[i], s);
 #pragma unroll
             for (int o = L / 2; o; o >>= 1) s = add_rn(s, __shfl_xor_sync(kFullMask, s, o));
-            if (weight && in) {
-                const float rstd = div_rn(1.0f, __fsqrt_rn(add_rn(div_rn(s, static_cast<float>(a.D)), a.eps)));
-                float w[16];
+            if (!is_v && in) {
+                const void* const weight = is_q ? a.q_weight : a.k_weight;
+                const float rstd = __frsqrt_rn(add_rn(div_rn(s, static_cast<float>(a.D)), a.eps));
+                float w[8];
                 load_weight8(weight, a.weight_dtype, e0, w);
-                load_weight8(weight, a.weight_dtype, e1, w + 8);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = mul_rn(mul_rn(y[i], rstd), w[i]);
+                for (int i = 0; i < 8; ++i) y[i] = mul_rn(mul_rn(y[i], rstd), w[i]);
+                load_weight8(weight, a.weight_dtype, e1, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i + 8] = mul_rn(mul_rn(y[i + 8], rstd), w[i]);
             }
         }
-        if (turned && !is_v) {
+        if (TURN != kNoTurn && turned && !is_v) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int p = apart ? i : 2 * i, q = apart ? i + 8 : 2 * i + 1;
+                constexpr bool kApart = TURN == kHalf;
+                const int p = kApart ? i : 2 * i, q = kApart ? i + 8 : 2 * i + 1;
                 const float u = y[p], v = y[q];
                 y[p] = __fmaf_rn(u, cs[i], -mul_rn(v, sn[i]));
                 y[q] = __fmaf_rn(v, cs[i], mul_rn(u, sn[i]));
             }
         }
-        void* out = is_q ? a.q_out : is_v ? nullptr : a.k_out;
-        if (out && in) {
-            const int64_t at = (token * (is_q ? a.Hq : a.Hkv) + h) * a.D;
-            store8<DT>(out, at + e0, y);
-            store8<DT>(out, at + e1, y + 8);
+        if (in && (is_q || !CACHE)) {
+            uint8_t* const out = static_cast<uint8_t*>(is_q ? a.q_out : a.k_out) +
+                                 (token * (is_q ? a.Hq : a.Hkv) + (is_q ? j : j - nq)) * a.D * kSize;
+            store8<DT>(out, e0, y);
+            store8<DT>(out, e1, y + 8);
         }
-        if (a.slots) {
+        if (CACHE) {
             int e = e0;
-            if (a.layout == NVFP4_ROPE_HALF && a.positions) {       // blocks of 16 from two neighbours' halves
+            const int h = j - (is_v ? nk : nq);
+            if (TURN == kHalf) {       // blocks of 16 from two neighbours' halves
                 const bool odd = t & 1;
                 float got[8];
 #pragma unroll
@@ -219,48 +236,58 @@ __global__ void __launch_bounds__(kHeadsThreads) k_heads(const HeadsArgs a, int 
                     e = odd ? half + 8 * (t - 1) : 8 * t;
                 }
             }
-            uint8_t* tile = in && !is_q ? tile_of(a.cache, slot, h) : nullptr;
-            if (tile) {
+            if (in && !is_q && place.tile) {
+                uint8_t* const tile = place.tile + h * head_bytes(a.cache);
                 const GScale g = is_v ? head_scale(a.cache.v_mode, a.cache.v_gamax, h, a.cache.bound)
                                       : head_scale(a.cache.k_mode, a.cache.k_gamax, h, a.cache.bound);
-                quantize_into(tile + (is_v ? 9 * a.D : 0), row, a.D, e, g, y);
+                quantize_into(tile + (is_v ? 9 * a.D : 0), place.row, a.D, e, g, y);
             }
         }
     }
 }
 
-// One thread per 16 elements of a slot: 8 bytes of codes and a scale to 16 values (zeros where there is no
-// such slot).
-template <int ODT>
-__global__ void __launch_bounds__(256) k_cache_read(const CacheReadArgs a) {
+// A warp takes part of a slot's blocks of 16 elements, keys first, then values, a thread a block: 8 bytes of codes and a
+// scale to 16 values (zeros where there is no such slot).  LG: log2 of the blocks of a head.
+template <int ODT, int LG>
+__global__ void __launch_bounds__(256) k_cache_read(const CacheReadArgs a, int chunks) {
     pdl_trigger();
     pdl_wait();
     const CacheArgs& c = a.cache;
-    const int groups = c.D / 16;
-    const int64_t n = a.T * c.Hkv * groups * 2;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t per = a.T * c.Hkv * groups;           // keys first, then values
-        const bool is_v = i >= per;
-        const int64_t x = is_v ? i - per : i, head = x / groups, token = head / c.Hkv;
-        const int grp = static_cast<int>(x - head * groups), h = static_cast<int>(head - token * c.Hkv);
-        void* out = is_v ? a.v : a.k;
+    const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t token = warp / static_cast<uint32_t>(chunks);
+    if (token >= a.T) return;
+    const int chunk = static_cast<int>(warp % static_cast<uint32_t>(chunks)), half = c.Hkv << LG;
+    const Place place = place_of(c, __ldg(a.slots + token));
+    const bool wide = (reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) % 32 == 0;
+    for (int i = chunk * 32 + (threadIdx.x & 31); i < 2 * half; i += chunks * 32) {
+        const bool is_v = i >= half;
+        const int x = is_v ? i - half : i, h = x >> LG, grp = x & ((1 << LG) - 1);
+        void* const out = is_v ? a.v : a.k;
         if (!out) continue;
-        const int64_t slot = __ldg(a.slots + token);
-        const uint8_t* tile = tile_of(c, slot, h);
         float y[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) y[j] = 0.0f;
-        if (tile) {
-            const uint8_t* part = tile + (is_v ? 9 * c.D : 0);
-            const int row = static_cast<int>(slot % 16);
-            const uint2 w = *reinterpret_cast<const uint2*>(part + row * (c.D / 2) + grp * 8);
-            const float d = e4m3_decode(part[8 * c.D + row * groups + grp]);
+        if (place.tile) {
+            const uint8_t* part = place.tile + h * head_bytes(c) + (is_v ? 9 * c.D : 0);
+            const uint2 w = *reinterpret_cast<const uint2*>(part + place.row * (c.D / 2) + grp * 8);
+            const float d = e4m3_decode(part[8 * c.D + (place.row << LG) + grp]);
             const GScale g = is_v ? head_scale(c.v_mode, c.v_gamax, h, c.bound) : head_scale(c.k_mode, c.k_gamax, h, c.bound);
             dequant16<true>(w.x, w.y, d, g.Sdec, y);
         }
-        store8<ODT>(out, x * 16, y);
-        store8<ODT>(out, x * 16 + 8, y + 8);
+        uint8_t* const to = static_cast<uint8_t*>(out) + (token * half + x) * (ODT == NVFP4_BF16 ? 32 : 64);
+        uint32_t w[ODT == NVFP4_BF16 ? 8 : 16];
+        if (ODT == NVFP4_BF16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j % (ODT == NVFP4_BF16 ? 8 : 16)] = __float_as_uint(y[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < (ODT == NVFP4_BF16 ? 8 : 16); j += 8) store32(to + 4 * j, w + j, wide);
     }
 }
 
@@ -276,8 +303,21 @@ cudaError_t launch_heads_t(const HeadsArgs& a, cudaStream_t s) {
     const int per = (rounds + static_cast<int>(chunks) - 1) / static_cast<int>(chunks) * step;
     chunks = (total + per - 1) / per;
     const int64_t blocks = (a.T * chunks + kHeadsThreads / 32 - 1) / (kHeadsThreads / 32);
-    auto* kernel = L == 4 ? k_heads<DT, 4> : L == 8 ? k_heads<DT, 8> : L == 16 ? k_heads<DT, 16> : k_heads<DT, 32>;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kHeadsThreads), 0, s, a, static_cast<int>(chunks), per);
+    const bool cache = a.slots != nullptr;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const int n = static_cast<int>(chunks);
+    auto go = [&](auto* kernel) { return launch_pdl(kernel, grid, dim3(kHeadsThreads), 0, s, a, n, per); };
+    const bool apart = a.layout == NVFP4_ROPE_HALF;         // (norms alone: whichever)
+    if (!a.q && !a.positions && !a.k_weight && cache)       // nvfp4_cache_write
+        return L == 4 ? go(k_heads<DT, 4, kNoTurn, true>) : L == 8 ? go(k_heads<DT, 8, kNoTurn, true>) : go(k_heads<DT, 16, kNoTurn, true>);
+    if (cache && apart) return L == 4 ? go(k_heads<DT, 4, kHalf, true>) : L == 8 ? go(k_heads<DT, 8, kHalf, true>) : go(k_heads<DT, 16, kHalf, true>);
+    if (cache)
+        return L == 4 ? go(k_heads<DT, 4, kNeighbours, true>) : L == 8 ? go(k_heads<DT, 8, kNeighbours, true>) : go(k_heads<DT, 16, kNeighbours, true>);
+    if (apart)
+        return L == 4 ? go(k_heads<DT, 4, kHalf, false>) : L == 8 ? go(k_heads<DT, 8, kHalf, false>)
+               : L == 16 ? go(k_heads<DT, 16, kHalf, false>) : go(k_heads<DT, 32, kHalf, false>);
+    return L == 4 ? go(k_heads<DT, 4, kNeighbours, false>) : L == 8 ? go(k_heads<DT, 8, kNeighbours, false>)
+           : L == 16 ? go(k_heads<DT, 16, kNeighbours, false>) : go(k_heads<DT, 32, kNeighbours, false>);
 }
 
 }  // namespace
@@ -289,11 +329,16 @@ int launch_heads(const HeadsArgs& a, void* stream) {
 
 int launch_cache_read(const CacheReadArgs& a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t n = a.T * a.cache.Hkv * (a.cache.D / 16) * 2;
-    const int64_t want = (n + 255) / 256, cap = static_cast<int64_t>(sm_count()) * 32;
-    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
-    return static_cast<int>(a.out_dtype == NVFP4_BF16 ? launch_pdl(k_cache_read<NVFP4_BF16>, grid, dim3(256), 0, s, a)
-                                                      : launch_pdl(k_cache_read<NVFP4_F32>, grid, dim3(256), 0, s, a));
+    // few slots: a warp takes one round of blocks, so that all run at once
+    const int rounds = (2 * a.cache.Hkv * (a.cache.D / 16) + 31) / 32;
+    const int64_t warps = static_cast<int64_t>(sm_count()) * 32;
+    int64_t chunks = a.T >= warps ? 1 : (warps + a.T - 1) / a.T;
+    if (chunks > rounds) chunks = rounds;
+    const dim3 grid(static_cast<unsigned>((a.T * chunks + 7) / 8));
+    auto go = [&](auto* kernel) { return static_cast<int>(launch_pdl(kernel, grid, dim3(256), 0, s, a, static_cast<int>(chunks))); };
+    if (a.out_dtype == NVFP4_BF16)
+        return a.cache.D == 64 ? go(k_cache_read<NVFP4_BF16, 2>) : a.cache.D == 128 ? go(k_cache_read<NVFP4_BF16, 3>) : go(k_cache_read<NVFP4_BF16, 4>);
+    return a.cache.D == 64 ? go(k_cache_read<NVFP4_F32, 2>) : a.cache.D == 128 ? go(k_cache_read<NVFP4_F32, 3>) : go(k_cache_read<NVFP4_F32, 4>);
 }
 
 }  // namespace nvfp4

@@ -454,6 +454,18 @@ __device__ __forceinline__ void load16(const void* base, int64_t elem0, float* y
     }
 }
 
+// 32 bytes, in one piece if the address is a multiple of 32
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // A thread's slot of P 16-byte pieces (P = 2 or 4) in a per-thread copy ring,
 // with piece c stored at position c ^ swz: each 32-byte sector keeps its two
 // pieces together (so the copies fill whole sectors), while a quarter warp's
