@@ -88,7 +88,7 @@ class _NoShortPath:
     def rmsnorm(*args):
         return None
 
-    mv = grouped_mm = rmsnorm
+    mv = grouped_mm = qk_norm_rope = cache_write = cache_read = cache_attention = rmsnorm
 
 
 def _short_path(lib):
@@ -104,6 +104,9 @@ def _short_path(lib):
         return _NoShortPath
     m.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.nvfp4_rmsnorm, lib.nvfp4_mv, lib.nvfp4_grouped_mm,
                                                              lib.nvfp4_grouped_mm_workspace)])
+    m.bind_cache(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.nvfp4_qk_norm_rope, lib.nvfp4_cache_write,
+                                                                   lib.nvfp4_cache_read, lib.nvfp4_cache_attention,
+                                                                   lib.nvfp4_cache_attention_workspace)])
     return m
 
 
@@ -1238,6 +1241,11 @@ def nvfp4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions, phases, *, q
     "interleaved".  With a cache, k and v [T, Hkv, D] are quantized into its slots [T] instead, and the
     dict has q alone."""
     lib = _lib or load_library()
+    if stream is None:
+        res = _call.qk_norm_rope(q, k, positions, phases, q_weight, k_weight, eps, layout, magnitude, q_out, k_out, cache, v,
+                                 slots, k_gamax, v_gamax, scale_bound)
+        if res is not None:
+            return res
     call = "nvfp4_qk_norm_rope"
     if not torch.is_tensor(q) or not q.is_cuda:
         raise ValueError(f"{call}: q must be a CUDA [T, heads, D] tensor")
@@ -1301,6 +1309,8 @@ def nvfp4_cache_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slo
     outside the cache (-1) is not written.  k_gamax, v_gamax: None, one amax or one a KV head, the same
     for every call on a cache."""
     lib = _lib or load_library()
+    if stream is None and _call.cache_write(cache, k, v, slots, k_gamax, v_gamax, scale_bound):
+        return
     call = "nvfp4_cache_write"
     dev, pages, P, Hkv, D = _cache_sizes(cache, call)
     if stream is not None:
@@ -1322,6 +1332,10 @@ def nvfp4_cache_read(cache: torch.Tensor, slots: torch.Tensor, *, k_gamax=None, 
                      scale_bound: float = 448.0, out_dtype="bf16", stream=None) -> tuple:
     """(keys, values) [T, Hkv, D] that slots [T] of a cache hold; zeros for a slot outside it."""
     lib = _lib or load_library()
+    if stream is None:
+        res = _call.cache_read(cache, slots, k_gamax, v_gamax, scale_bound, out_dtype)
+        if res is not None:
+            return res
     call = "nvfp4_cache_read"
     dev, pages, P, Hkv, D = _cache_sizes(cache, call)
     if stream is not None:
@@ -1356,6 +1370,11 @@ def nvfp4_cache_attention(q: torch.Tensor, cache: torch.Tensor, pages: torch.Ten
     [T, Hq, D], with want_lse (out, lse fp32 [T, Hq]); a query that sees nothing gives 0, rows of no
     sequence are not written."""
     lib = _lib or load_library()
+    if stream is None:
+        res = _call.cache_attention(q, cache, pages, lengths, offsets, k_gamax, v_gamax, scale_bound, scale, causal, window,
+                                    sinks, out_dtype, out, want_lse)
+        if res is not None:
+            return res
     call = "nvfp4_cache_attention"
     dev, n_pages, P, Hkv, D = _cache_sizes(cache, call)
     if stream is not None:
@@ -1382,7 +1401,8 @@ def nvfp4_cache_attention(q: torch.Tensor, cache: torch.Tensor, pages: torch.Ten
     tdt = torch.float32 if odt == F32 else torch.bfloat16
     o = torch.empty((T, Hq, D), dtype=tdt, device=dev) if out is None else _check_dev(out, "out", tdt, T * Hq * D, dev)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    need = lib.nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, P, dt, int(offsets is not None))
+    with torch.cuda.device(dev):                # (its size goes by the device's SMs)
+        need = lib.nvfp4_cache_attention_workspace(T, Hq, Hkv, D, B, width, P, dt, int(offsets is not None))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _launch(lib, lib.nvfp4_cache_attention, dev, q.data_ptr(), T, Hq, qs, dt, cache.data_ptr(), n_pages, P, Hkv, D,
             pages.data_ptr(), B, width, lengths.data_ptr(), _addr(offsets), km, _addr(kg), vm, _addr(vg), scale_bound,

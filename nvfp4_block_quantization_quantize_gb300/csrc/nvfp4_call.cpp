@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "nvfp4.h"
@@ -27,6 +28,11 @@ decltype(&nvfp4_rmsnorm) f_rmsnorm = nullptr;
 decltype(&nvfp4_mv) f_mv = nullptr;
 decltype(&nvfp4_grouped_mm) f_grouped_mm = nullptr;
 decltype(&nvfp4_grouped_mm_workspace) f_grouped_ws = nullptr;
+decltype(&nvfp4_qk_norm_rope) f_rope = nullptr;
+decltype(&nvfp4_cache_write) f_cache_write = nullptr;
+decltype(&nvfp4_cache_read) f_cache_read = nullptr;
+decltype(&nvfp4_cache_attention) f_attention = nullptr;
+decltype(&nvfp4_cache_attention_workspace) f_attention_ws = nullptr;
 
 PyObject* none() { Py_RETURN_NONE; }
 
@@ -295,6 +301,228 @@ PyObject* rmsnorm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
+// ---- a cache of keys and values ----------------------------------------------------------------
+// [T, H, D] heads of a floating type, a token's contiguous, tokens whole 16 bytes apart
+const at::Tensor* heads(PyObject* o, int dev, int64_t* stride) {
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.get_device() != dev || t.dim() != 3 || t.numel() == 0 || dtype_of(t) < 0) return nullptr;
+    const int64_t size = static_cast<int64_t>(t.element_size());
+    if (t.stride(2) != 1 || t.stride(1) != t.size(2) || t.stride(0) < 0 || t.stride(0) * size % 16 ||
+        reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+        return nullptr;
+    *stride = t.stride(0);
+    return &t;
+}
+
+// a cache and the global scales of its keys and values
+struct Cache {
+    const at::Tensor *t = nullptr, *k_gamax, *v_gamax;
+    int k_mode, v_mode;
+    int64_t pages, page_size, Hkv, D;
+
+    bool take(PyObject* o, PyObject* kg, PyObject* vg, int dev) {
+        t = tensor(o, dev);
+        if (!t || t->scalar_type() != at::kByte || t->dim() != 4 || t->numel() == 0 || t->size(3) % 18) return false;
+        pages = t->size(0), Hkv = t->size(1), page_size = t->size(2) * 16, D = t->size(3) / 18;
+        return rows_gamax(kg, Hkv, dev, &k_mode, &k_gamax) && rows_gamax(vg, Hkv, dev, &v_mode, &v_gamax);
+    }
+    uint8_t* bytes() const { return static_cast<uint8_t*>(t->data_ptr()); }
+    const float* kg() const { return static_cast<const float*>(data(k_gamax)); }
+    const float* vg() const { return static_cast<const float*>(data(v_gamax)); }
+};
+
+at::Tensor empty3(int64_t a, int64_t b, int64_t c, at::ScalarType type, int dev) {
+    return at::detail::empty_cuda({a, b, c}, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+}
+
+cudaStream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
+
+// qk_norm_rope(q, k, positions, phases, q_weight, k_weight, eps, layout, magnitude, q_out, k_out, cache, v, slots, k_gamax,
+// v_gamax, scale_bound)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        float eps, magnitude, bound;
+        if (n != 17 || !f_rope || !number(v[6], &eps) || !number(v[8], &magnitude) || !number(v[16], &bound)) return none();
+        const int dev = call_device(v[0]);
+        if (dev < 0) return none();
+        int64_t qs, ks, vs = 0;
+        const at::Tensor *q = heads(v[0], dev, &qs), *k = heads(v[1], dev, &ks), *x = nullptr;
+        if (!q || !k) return none();
+        const int64_t T = q->size(0), Hq = q->size(1), D = q->size(2), Hkv = k->size(1);
+        const at::ScalarType type = q->scalar_type();
+        if (k->size(0) != T || k->size(2) != D || k->scalar_type() != type) return none();
+        const at::Tensor *pos = nullptr, *phases = nullptr, *qw = nullptr, *kw = nullptr, *slots = nullptr;
+        int64_t rot = 0;
+        if (given(v[2]) != given(v[3]) || given(v[4]) != given(v[5]) || given(v[11]) != given(v[12]) || given(v[11]) != given(v[13]))
+            return none();
+        if (given(v[2])) {
+            phases = tensor(v[3], dev);
+            if (!phases || phases->scalar_type() != at::kLong || !(pos = tensor(v[2], dev, at::kLong, T))) return none();
+            rot = 2 * phases->numel();
+        }
+        int wdt = dtype_of(*q);
+        if (given(v[4])) {
+            qw = tensor(v[4], dev);
+            if (!qw || qw->numel() != D || (wdt = dtype_of(*qw)) < 0 || !(kw = tensor(v[5], dev, qw->scalar_type(), D))) return none();
+        }
+        const int layout = choice(v[7], {"half", "interleaved"});
+        if (layout < 0) return none();
+        Cache c;
+        c.k_mode = c.v_mode = NVFP4_GAMAX_NONE, c.k_gamax = c.v_gamax = nullptr, c.pages = 0, c.page_size = 16;
+        if (given(v[11])) {
+            if (given(v[10]) || !c.take(v[11], v[14], v[15], dev) || c.Hkv != Hkv || c.D != D) return none();
+            x = heads(v[12], dev, &vs);
+            if (!x || x->sizes() != k->sizes() || x->scalar_type() != type || !(slots = tensor(v[13], dev, at::kLong, T))) return none();
+        } else if (given(v[14]) || given(v[15])) {
+            return none();
+        }
+        at::Tensor qo, ko;
+        if (!taken(v[9], T * Hq * D, type, dev, &qo) || !taken(v[10], T * Hkv * D, type, dev, &ko)) return none();
+        int rc;
+        {
+            const Unlocked unlocked;
+            if (!qo.defined()) qo = empty3(T, Hq, D, type, dev);
+            if (!c.t && !ko.defined()) ko = empty3(T, Hkv, D, type, dev);
+            rc = f_rope(q->data_ptr(), k->data_ptr(), data(x), T, Hq, Hkv, D, qs, ks, vs, dtype_of(*q), data(qw), data(kw), wdt,
+                        eps, static_cast<const int64_t*>(data(pos)), static_cast<const uint64_t*>(data(phases)), rot, layout,
+                        magnitude, qo.data_ptr(), c.t ? nullptr : ko.data_ptr(), c.t ? c.bytes() : nullptr, c.pages,
+                        c.page_size, static_cast<const int64_t*>(data(slots)), c.k_mode, c.kg(), c.v_mode, c.vg(), bound,
+                        stream_of(dev));
+        }
+        if (rc != NVFP4_OK) return none();
+        PyObject* d = PyDict_New();
+        if (!d) return nullptr;
+        if (!put(d, "q", wrap(v[9], qo)) || (!c.t && !put(d, "k", wrap(v[10], ko)))) {
+            Py_DECREF(d);
+            return nullptr;
+        }
+        return d;
+    });
+}
+
+// cache_write(cache, k, v, slots, k_gamax, v_gamax, scale_bound): True when it is enqueued
+PyObject* cache_write(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        float bound;
+        if (n != 7 || !f_cache_write || !number(v[6], &bound)) return none();
+        const int dev = call_device(v[0]);
+        if (dev < 0) return none();
+        Cache c;
+        int64_t ks, vs;
+        const at::Tensor *k = heads(v[1], dev, &ks), *x = heads(v[2], dev, &vs);
+        if (!k || !x || !c.take(v[0], v[4], v[5], dev)) return none();
+        const int64_t T = k->size(0);
+        if (k->size(1) != c.Hkv || k->size(2) != c.D || x->sizes() != k->sizes() || x->scalar_type() != k->scalar_type()) return none();
+        const at::Tensor* slots = tensor(v[3], dev, at::kLong, T);
+        if (!slots) return none();
+        int rc;
+        {
+            const Unlocked unlocked;
+            rc = f_cache_write(k->data_ptr(), x->data_ptr(), T, c.Hkv, c.D, ks, vs, dtype_of(*k), c.bytes(), c.pages, c.page_size,
+                               static_cast<const int64_t*>(slots->data_ptr()), c.k_mode, c.kg(), c.v_mode, c.vg(), bound,
+                               stream_of(dev));
+        }
+        if (rc != NVFP4_OK) return none();
+        Py_RETURN_TRUE;
+    });
+}
+
+PyObject* pair(PyObject* a, PyObject* b) {                // takes both references
+    PyObject* t = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    return t;
+}
+
+// cache_read(cache, slots, k_gamax, v_gamax, scale_bound, out_dtype)
+PyObject* cache_read(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        float bound;
+        if (n != 6 || !f_cache_read || !number(v[4], &bound)) return none();
+        const int dev = call_device(v[0]);
+        if (dev < 0) return none();
+        Cache c;
+        const at::Tensor* slots = tensor(v[1], dev);
+        const int odt = choice(v[5], {"f32", "bf16"});
+        if (!slots || slots->scalar_type() != at::kLong || slots->numel() == 0 || odt < 0 || !c.take(v[0], v[2], v[3], dev)) return none();
+        const int64_t T = slots->numel();
+        const at::ScalarType ot = odt == NVFP4_F32 ? at::kFloat : at::kBFloat16;
+        at::Tensor k, x;
+        int rc;
+        {
+            const Unlocked unlocked;
+            k = empty3(T, c.Hkv, c.D, ot, dev);
+            x = empty3(T, c.Hkv, c.D, ot, dev);
+            rc = f_cache_read(c.bytes(), c.pages, c.page_size, c.Hkv, c.D, static_cast<const int64_t*>(slots->data_ptr()), T,
+                              c.k_mode, c.kg(), c.v_mode, c.vg(), bound, k.data_ptr(), x.data_ptr(), odt, stream_of(dev));
+        }
+        return rc == NVFP4_OK ? pair(THPVariable_Wrap(k), THPVariable_Wrap(x)) : none();
+    });
+}
+
+// cache_attention(q, cache, pages, lengths, offsets, k_gamax, v_gamax, scale_bound, scale, causal, window, sinks, out_dtype,
+// out, want_lse)
+PyObject* cache_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        float bound, scale;
+        if (n != 15 || !f_attention || !number(v[7], &bound)) return none();
+        const int dev = call_device(v[0]);
+        if (dev < 0 || !PyBool_Check(v[9]) || !PyLong_Check(v[10]) || !PyBool_Check(v[14])) return none();
+        int64_t qs;
+        Cache c;
+        const at::Tensor *q = heads(v[0], dev, &qs), *pages = tensor(v[2], dev);
+        if (!q || !pages || pages->scalar_type() != at::kInt || pages->dim() != 2 || !c.take(v[1], v[5], v[6], dev)) return none();
+        const int64_t T = q->size(0), Hq = q->size(1), B = pages->size(0), width = pages->size(1);
+        const at::Tensor *lengths = tensor(v[3], dev, at::kLong, B), *offsets = nullptr, *sinks = nullptr;
+        if (!lengths || q->size(2) != c.D || B == 0 || width == 0) return none();
+        if (given(v[4]) && !(offsets = tensor(v[4], dev, at::kLong, B + 1))) return none();
+        if (given(v[11]) && !(sinks = tensor(v[11], dev, at::kFloat, Hq))) return none();
+        if (!given(v[8])) scale = static_cast<float>(std::pow(static_cast<double>(c.D), -0.5));
+        else if (!number(v[8], &scale)) return none();
+        const int64_t window = PyLong_AsLongLong(v[10]);
+        if (window == -1 && PyErr_Occurred()) {
+            PyErr_Clear();
+            return none();
+        }
+        const int odt = choice(v[12], {"f32", "bf16"});
+        at::Tensor out, lse, ws;
+        const at::ScalarType ot = odt == NVFP4_F32 ? at::kFloat : at::kBFloat16;
+        if (odt < 0 || !taken(v[13], T * Hq * c.D, ot, dev, &out)) return none();
+        const bool want_lse = v[14] == Py_True;
+        int rc;
+        {
+            const Unlocked unlocked;
+            const int dt = dtype_of(*q);
+            if (!out.defined()) out = empty3(T, Hq, c.D, ot, dev);
+            if (want_lse) lse = empty(T, Hq, at::kFloat, dev);
+            const int64_t need = f_attention_ws(T, Hq, c.Hkv, c.D, B, width, c.page_size, dt, offsets ? 1 : 0);
+            if (need > 0) ws = empty(1, need, at::kByte, dev);      // free for the stream's next work once this call is enqueued
+            rc = f_attention(q->data_ptr(), T, Hq, qs, dt, c.bytes(), c.pages, c.page_size, c.Hkv, c.D,
+                             static_cast<const int32_t*>(pages->data_ptr()), B, width,
+                             static_cast<const int64_t*>(lengths->data_ptr()), static_cast<const int64_t*>(data(offsets)),
+                             c.k_mode, c.kg(), c.v_mode, c.vg(), bound, scale, v[9] == Py_True, window,
+                             static_cast<const float*>(data(sinks)), out.data_ptr(), odt,
+                             want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                             need > 0 ? static_cast<uint8_t*>(ws.data_ptr()) : nullptr, need, stream_of(dev));
+        }
+        if (rc != NVFP4_OK) return none();
+        return want_lse ? pair(wrap(v[13], out), THPVariable_Wrap(lse)) : wrap(v[13], out);
+    });
+}
+
+// bind_cache(qk_norm_rope, cache_write, cache_read, cache_attention, cache_attention_workspace)
+PyObject* bind_cache(PyObject*, PyObject* args) {
+    unsigned long long a, b, c, d, e;
+    if (!PyArg_ParseTuple(args, "KKKKK", &a, &b, &c, &d, &e)) return nullptr;
+    f_rope = reinterpret_cast<decltype(f_rope)>(static_cast<uintptr_t>(a));
+    f_cache_write = reinterpret_cast<decltype(f_cache_write)>(static_cast<uintptr_t>(b));
+    f_cache_read = reinterpret_cast<decltype(f_cache_read)>(static_cast<uintptr_t>(c));
+    f_attention = reinterpret_cast<decltype(f_attention)>(static_cast<uintptr_t>(d));
+    f_attention_ws = reinterpret_cast<decltype(f_attention_ws)>(static_cast<uintptr_t>(e));
+    Py_RETURN_NONE;
+}
+
 // bind(rmsnorm, mv, grouped_mm, grouped_mm_workspace): the addresses of the C ABI's functions in the loaded library
 PyObject* bind(PyObject*, PyObject* args) {
     unsigned long long a, b, c, d;
@@ -308,6 +536,11 @@ PyObject* bind(PyObject*, PyObject* args) {
 
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
+    {"bind_cache", bind_cache, METH_VARARGS, nullptr},
+    {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(qk_norm_rope)), METH_FASTCALL, nullptr},
+    {"cache_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_write)), METH_FASTCALL, nullptr},
+    {"cache_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_read)), METH_FASTCALL, nullptr},
+    {"cache_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_attention)), METH_FASTCALL, nullptr},
     {"mv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mv)), METH_FASTCALL, nullptr},
     {"grouped_mm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grouped_mm)), METH_FASTCALL, nullptr},
     {"rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rmsnorm)), METH_FASTCALL, nullptr},
