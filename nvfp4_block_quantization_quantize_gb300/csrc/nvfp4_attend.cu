@@ -49,14 +49,26 @@ __device__ __forceinline__ int64_t parts_of(int64_t units, int64_t warps) {
     return most < warps ? most : warps;
 }
 
-// where the run that would start at unit x does: at the start of x's group where x is not past the group's own cost.
-// Every lane of a warp calls it.
+// Where a warp's run starts: unit u, `in` units into a group of sequence b, which has `before` units ahead of it.
+struct Start {
+    int64_t u, b, before, group;
+    Seq s;
+    int in;
+};
+
+// The run that would start at unit x starts at x's group where x is not past the group's own cost.  Every lane of a
+// warp calls it.
 template <int R>
-__device__ __forceinline__ int64_t run_start(const AttendArgs& a, const Shares<Units<R>>& shares, int64_t x, int64_t* seq,
-                                             int64_t* before) {
-    shares.find(a, x, seq, before);
-    const int64_t per = kGroupCost + sequence<R>(a, *seq).tiles, from = x - *before, in = from - quotient(from, per) * per;
-    return in <= kGroupCost ? x - in : x;
+__device__ __forceinline__ Start run_start(const AttendArgs& a, const Shares<Units<R>>& shares, int64_t x) {
+    Start t;
+    shares.find(a, x, &t.b, &t.before);
+    t.s = sequence<R>(a, t.b);
+    const int64_t per = kGroupCost + t.s.tiles, from = x - t.before;
+    t.group = quotient(from, per);
+    t.in = static_cast<int>(from - t.group * per);
+    if (t.in <= kGroupCost) x -= t.in, t.in = 0;
+    t.u = x;
+    return t;
 }
 
 // A place in a warp's run: a part of a group, tiles ta .. tb of the group's s.tiles.
@@ -65,40 +77,33 @@ struct Place {
     int64_t b, base;          // sequence of the unit before, units before it
     Seq s;
     int h, rt, ta, tb;        // the group's KV head and row tile
-    bool known;               // s belongs to b
     bool more;                // there was a part
 
-    __device__ __forceinline__ void start(int64_t u0, int64_t u1, int64_t b0, int64_t before) {
-        u = u0, end = u1, b = b0, base = before, known = false;
+    // at the first part of the run from t to unit u1
+    __device__ __forceinline__ void start(const AttendArgs& a, const Start& t, int64_t u1) {
+        end = u1, b = t.b, base = t.before, s = t.s, more = t.u < u1;
+        const int per = kGroupCost + s.tiles, to = static_cast<int>(min(static_cast<int64_t>(per), t.in + (u1 - t.u)));
+        rt = static_cast<int>(quotient(t.group, a.cache.Hkv));
+        h = static_cast<int>(t.group - static_cast<int64_t>(rt) * a.cache.Hkv);
+        u = t.u + (to - t.in), ta = max(t.in - kGroupCost, 0), tb = to - kGroupCost;
     }
 
     // the next part; false at the end of the run
     template <int R>
     __device__ __forceinline__ bool next(const AttendArgs& a) {
         if (u >= end) return false;
-        if (known && u < base + s.units) {                // the sequence's next group
+        if (u < base + s.units) {                         // the sequence's next group
             if (++h == a.cache.Hkv) h = 0, ++rt;
         } else {
-            while (true) {
-                if (known) base += s.units, ++b;
+            do {
+                base += s.units, ++b;
                 s = sequence<R>(a, b);
-                known = true;
-                if (u < base + s.units) break;
-            }
+            } while (u >= base + s.units);
             h = rt = 0;
         }
-        const int per = kGroupCost + s.tiles;
-        int64_t in = u - base - (static_cast<int64_t>(rt) * a.cache.Hkv + h) * per;
-        if (in >= per) {                                  // a run that starts amid a sequence
-            const int64_t group = quotient(in, per);
-            in -= group * per;
-            rt = static_cast<int>(group / a.cache.Hkv);
-            h = static_cast<int>(group - static_cast<int64_t>(rt) * a.cache.Hkv);
-        }
-        const int from = static_cast<int>(in);
-        const int to = static_cast<int>(min(static_cast<int64_t>(per), from + (end - u)));
-        u += to - from;
-        ta = max(from - kGroupCost, 0), tb = to - kGroupCost;
+        const int to = static_cast<int>(min(static_cast<int64_t>(kGroupCost + s.tiles), end - u));
+        u += to;
+        ta = 0, tb = to - kGroupCost;
         return true;
     }
 };
@@ -126,13 +131,12 @@ __device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi) {
 
 // A part of a cut group, as a warp leaves it: the first part of its run lies in `sums`, the last in its ring.
 struct Left {
-    int64_t b, first;         // its sequence; the group's first unit (-1: none)
-    int h, rt, ta, tb;
+    int64_t first, row0;      // the group's first unit (-1: none); its sequence's first query
+    int n, h, rt, ta, tb, tiles;
 };
 
 // Shared memory: rings [kWarps][kStages][2 records], sums [kWarps][8 NT][D + 4], (max, sum)
-// [kWarps][2][8 NT][2], barriers [kWarps][kStages], run starts [kWarps + 1] with their sequences and units before
-// [kWarps] each and all units, each warp's two places and two parts left.
+// [kWarps][2][8 NT][2], barriers [kWarps][kStages], each warp's two places and two parts left.
 template <int D, int NT>
 struct Shape {
     static constexpr int R = 8 * NT;                      // rows of a group tile
@@ -143,8 +147,7 @@ struct Shape {
     static constexpr int sums = kWarps * sum;
     static constexpr int stats = kWarps * 2 * R * 2 * 4;
     static constexpr int bars = kWarps * kStages<D, NT> * 8;
-    static constexpr int found = (3 * kWarps + 2) * 8;
-    static constexpr int bytes = ring + sums + stats + bars + found + kWarps * 2 * (sizeof(Place) + sizeof(Left));
+    static constexpr int bytes = ring + sums + stats + bars + kWarps * 2 * (sizeof(Place) + sizeof(Left));
 };
 
 // F32: queries and weights enter the products as two f16, and a tile's sums are added in fp32
@@ -158,60 +161,61 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
     float* const sums = reinterpret_cast<float*>(smem + S::ring);
     float* const stats = reinterpret_cast<float*>(smem + S::ring + S::sums);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + S::ring + S::sums + S::stats);
-    int64_t* const found = reinterpret_cast<int64_t*>(bars + kWarps * kStage);
-    Place* const all_places = reinterpret_cast<Place*>(found + 3 * kWarps + 2);
+    Place* const all_places = reinterpret_cast<Place*>(bars + kWarps * kStage);
     Left* const lefts = reinterpret_cast<Left*>(all_places + 2 * kWarps);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    if (threadIdx.x < kWarps * kStage) mbar_init(bars + threadIdx.x);
+    if (lane < kStage) mbar_init(bars + warp * kStage + lane);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
     pdl_wait();
-    {                                                     // this warp's run of units, its sequence and the units before
-        int64_t u = 0, end = 0, b = 0, before = 0, units = 0;
+    Place* const places = all_places + 2 * warp;
+    Cut* const cut = split ? cuts<D, R>(a, gridDim.x) + blockIdx.x : nullptr;
+    if (split && threadIdx.x == 0) cut->n = 0;
+    int64_t units = 0;
+    {                                                     // this warp's run
+        Start t = {};
+        int64_t end = 0;
         if (split) {
             const Shares<Units<R>> shares(a);
             units = shares.total;
-            const int64_t warps = parts_of(units, gridDim.x * kWarps);
+            const int64_t warps = parts_of(units, static_cast<int64_t>(gridDim.x) * kWarps);
             const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-            u = i < warps ? run_start<R>(a, shares, quotient(units * i, warps), &b, &before) : units;
-            if (warp == kWarps - 1) {
-                int64_t x, y;
-                end = i + 1 < warps ? run_start<R>(a, shares, quotient(units * (i + 1), warps), &x, &y) : units;
+            if (i < warps) {
+                t = run_start<R>(a, shares, quotient(units * i, warps));
+                end = i + 1 < warps ? run_start<R>(a, shares, quotient(units * (i + 1), warps)).u : units;
             }
         } else {                                          // one group a CTA
             const Shares<Groups<R>> shares(a);
             if (blockIdx.x < shares.total) {
-                shares.find(a, blockIdx.x, &b, &before);
-                const int tiles = sequence<R>(a, b).tiles;
-                u = (blockIdx.x - before) * (kGroupCost + tiles), before = 0;
-                end = u + kGroupCost + tiles;
-                const int t = tiles * warp / kWarps;
-                if (t > 0) u += kGroupCost + t;           // without a tile the run is empty or the group's first
+                shares.find(a, blockIdx.x, &t.b, &t.before);
+                t.s = sequence<R>(a, t.b);
+                t.group = blockIdx.x - t.before, t.before = 0;
+                const int64_t first = t.group * (kGroupCost + t.s.tiles);
+                auto at = [&](int w) {                    // the first warp of those without a tile has the group's start
+                    const int x = t.s.tiles * w / kWarps;
+                    return w == kWarps ? kGroupCost + t.s.tiles : x > 0 ? kGroupCost + x : 0;
+                };
+                t.in = at(warp), t.u = first + t.in;
+                end = first + at(warp + 1);
             }
         }
         if (lane == 0) {
-            found[warp] = u, found[kWarps + 1 + warp] = b, found[2 * kWarps + 1 + warp] = before;
-            if (warp == kWarps - 1) found[kWarps] = end, found[3 * kWarps + 1] = units;
+            places[0].start(a, t, end);
+            places[1] = places[0];
             lefts[2 * warp].first = lefts[2 * warp + 1].first = -1;
         }
     }
-    __syncthreads();
-    const int64_t u0 = found[warp], u1 = found[warp + 1];
-    Cut* const cut = split ? cuts<D, R>(a, gridDim.x) + blockIdx.x : nullptr;
-    if (split && threadIdx.x == 0) cut->n = 0;
-    if (found[0] >= found[kWarps]) return;
+    __syncwarp();
 
     const int G = a.Hq / a.cache.Hkv, per_page = a.cache.page_size / 16;
     uint8_t* const my_ring = ring + warp * S::one;
     uint64_t* const my_bars = bars + warp * kStage;
-    Place* const places = all_places + 2 * warp;
 
     // ---- copies, kStage pairs of tiles ahead: the place of this warp's next pair and its pages.  Pages and tiles of a page
     // are counted along (a division a tile costs as much as decoding it)
     const int skip_pages = 2 / per_page, skip_tiles = 2 % per_page;
     const int64_t page_bytes = static_cast<int64_t>(a.cache.Hkv) * per_page * kRecord<D>;
-    if (lane == 0) places[0].start(u0, u1, found[kWarps + 1 + warp], found[2 * kWarps + 1 + warp]);
     auto advance = [&](Place& p) {                        // one lane walks, all read
         __syncwarp();
         if (lane == 0) p.more = p.next<R>(a);
@@ -273,9 +277,16 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         if (ahead_tile >= per_page) ahead_tile -= per_page, ++ahead_table;
         pages();
     };
-    bool some = advance(ahead);                           // the first part, for both places
-    if (lane == 0) at = ahead;
-    __syncwarp();
+    bool some = ahead.more;
+    if (some) {                                           // the first queries, while the pages and tiles are fetched
+        const int row = min(ahead.rt * R + (NT == 1 ? r : lane >> 1), ahead.s.n * G - 1), size = a.dtype == NVFP4_BF16 ? 2 : 4;
+        int query, head;
+        split_row(ahead.s.n, G, row, &query, &head);
+        const uint8_t* const q = static_cast<const uint8_t*>(a.q) + ((ahead.s.row0 + query) * a.q_stride +
+                                                                     (static_cast<int64_t>(ahead.h) * G + head) * D) * size;
+        for (int i = NT == 1 ? c : lane & 1; i < D * size / 128; i += NT == 1 ? 4 : 2)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i * 128));
+    }
     ahead_left = some ? ahead.tb - ahead.ta : 0;
     if (ahead_left > 0) begin();
     else if (some) seek();
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 
         // ---- the end of the part: a whole group is written, what is cut is left for the CTA's end
         const bool complete = at.ta == 0 && at.tb == at.s.tiles;
-        const int place = at.u >= u1 && at.ta == 0 ? 1 : 0;       // the run's last part, which it did not start amid
+        const int place = at.u >= at.end && at.ta == 0 ? 1 : 0;       // the run's last part, which it did not start amid
         __syncwarp();                                     // the last part's sums go into the ring: its copies are in and read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             }
         if (!complete && lane == 0) {
             Left& x = lefts[2 * warp + place];
-            x.b = at.b, x.h = h, x.rt = rt, x.ta = at.ta, x.tb = at.tb;
+            x.row0 = row0, x.n = n, x.h = h, x.rt = rt, x.ta = at.ta, x.tb = at.tb, x.tiles = at.s.tiles;
             x.first = at.base + (static_cast<int64_t>(rt) * a.cache.Hkv + h) * (kGroupCost + at.s.tiles);
         }
     }
@@ -620,14 +631,13 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         const unsigned group = parts & ~((1u << i) - 1u) & (firsts ? (1u << (__ffs(firsts) - 1)) - 1u : ~0u);      // its parts
         const Left x = lefts[i];
         const int tb = lefts[31 - __clz(group)].tb;
-        const Seq s = sequence<R>(a, x.b);
-        const bool complete = x.ta == 0 && tb == s.tiles;
-        const int rows = min(R, s.n * G - x.rt * R);
+        const bool complete = x.ta == 0 && tb == x.tiles;
+        const int rows = min(R, x.n * G - x.rt * R);
         if (threadIdx.x == 0 && x.ta > 0 && !complete) {  // cut at this CTA's start; the first such cut of the group?
-            const int64_t units = found[3 * kWarps + 1], warps = parts_of(units, static_cast<int64_t>(gridDim.x) * kWarps);
-            const int64_t g1 = x.first + kGroupCost + s.tiles;
+            const int64_t warps = parts_of(units, static_cast<int64_t>(gridDim.x) * kWarps);
+            const int64_t g1 = x.first + kGroupCost + x.tiles;
             if (quotient(units * (static_cast<int64_t>(blockIdx.x) - 1) * kWarps, warps) <= x.first + kGroupCost)
-                *cut = Cut{s.row0, s.n, x.h, x.rt, static_cast<int>(quotient(g1 * warps - 1, units) / kWarps)};
+                *cut = Cut{x.row0, x.n, x.h, x.rt, static_cast<int>(quotient(g1 * warps - 1, units) / kWarps)};
         }
         float* const part = reinterpret_cast<float*>(a.workspace) +
                             (static_cast<int64_t>(blockIdx.x) * 2 + (x.ta > 0 ? 0 : 1)) * kPart<D, R>;
@@ -635,11 +645,15 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             const int q = y / (D / 4), d = y % (D / 4) * 4;
             if (q >= rows) continue;
             float m = kLowest, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (unsigned left = group; left; left &= left - 1) m = max_nd(m, stats[((__ffs(left) - 1) * R + q) * 2]);
-            for (unsigned left = group; left; left &= left - 1) {
-                const int k = __ffs(left) - 1;
-                const float f = exp2_approx(sub_rn(stats[(k * R + q) * 2], m));
-                l = __fmaf_rn(stats[(k * R + q) * 2 + 1], f, l);
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; ++k)
+                if (group >> k & 1) m = max_nd(m, stats[(k * R + q) * 2]);
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; ++k) {
+                if (!(group >> k & 1)) continue;
+                const float2 st = *reinterpret_cast<const float2*>(stats + (k * R + q) * 2);
+                const float f = exp2_approx(sub_rn(st.x, m));
+                l = __fmaf_rn(st.y, f, l);
                 const float* from = k & 1 ? reinterpret_cast<const float*>(ring + (k >> 1) * S::one) : sums + (k >> 1) * (S::sum / 4);
                 const float4 u = *reinterpret_cast<const float4*>(from + q * (D + 4) + d);
                 v[0] = __fmaf_rn(u.x, f, v[0]), v[1] = __fmaf_rn(u.y, f, v[1]);
@@ -647,8 +661,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
             }
             if (complete) {
                 int query, head;
-                split_row(s.n, G, x.rt * R + q, &query, &head);
-                Finish(a, x.h * G + head, x.h, m, l).store(a, s.row0 + query, x.h * G + head, d, v);
+                split_row(x.n, G, x.rt * R + q, &query, &head);
+                Finish(a, x.h * G + head, x.h, m, l).store(a, x.row0 + query, x.h * G + head, d, v);
             } else {
                 *reinterpret_cast<float4*>(part + q * D + d) = make_float4(v[0], v[1], v[2], v[3]);
                 if (d == 0) part[R * D + 2 * q] = m, part[R * D + 2 * q + 1] = l;
@@ -678,7 +692,7 @@ int64_t grid_of(const AttendArgs& a, int R, int* split) {
     const int64_t cap = a.width * a.cache.page_size;
     const int64_t runs = runs_bound(a, R);
     *split = cap > kSmall || runs > (int64_t{1} << 20);
-    return *split ? static_cast<int64_t>(sm_count()) * 2 : runs;
+    return *split ? static_cast<int64_t>(sm_count()) * (a.cache.D <= 128 && R == 8 ? 2 : 1) : runs;      // as many as run at once
 }
 
 template <int D, int NT, bool F32>
