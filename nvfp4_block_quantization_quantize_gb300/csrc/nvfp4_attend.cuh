@@ -230,62 +230,95 @@ __device__ __forceinline__ Cut* cuts(const AttendArgs& a, int64_t ctas) {
     return reinterpret_cast<Cut*>(reinterpret_cast<float*>(a.workspace) + ctas * 2 * kPart<D, R>);
 }
 
-// A group that several CTAs took parts of, joined in their order; a row a warp, 8 rows a CTA.
+// A group that several CTAs took parts of, joined: 8 rows a CTA, kSub warps a row, each of which adds every kSub-th part in
+// their order; the first then adds the warps' sums in theirs.  Bound by latency: a long sequence alone makes 38 parts a
+// group, which four warps read in three turns (one warp a row took 10 us of a 47 us call); with 256 rows a group
+// most CTAs have nothing to do, and small ones end sooner.
+template <int R>
+constexpr int kSub = R <= 16 ? 4 : 1;
+
 template <int D, int R>
-__global__ void __launch_bounds__(256) k_join(const AttendArgs a, int ctas) {
-    constexpr int kCols = (D + 127) / 128;    // float4 columns a lane
+__global__ void __launch_bounds__(256 * kSub<R>) k_join(const AttendArgs a, int ctas) {
+    constexpr int S = kSub<R>, kCols = (D + 127) / 128, kBatch = S > 1 ? 4 : 2;      // float4 columns a lane; parts loaded together
+    constexpr int kStep = D < 128 ? D / 4 : 32;           // lanes that have columns
+    __shared__ float sums[S > 1 ? 8 * S : 1][S > 1 ? D + 2 : 1];
     pdl_trigger();
     pdl_wait();
-    const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int i = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % S;
     const Cut cut = cuts<D, R>(a, ctas)[i];
     if (cut.n == 0) return;
     const int G = a.Hq / a.cache.Hkv, rows = min(R, cut.n * G - cut.rt * R), runs = cut.last - i + 2;
+    const int q = blockIdx.y * 8 + warp / S;
+    if (S == 1 && q >= rows) return;
     // CTA i - 1 has the group's first tiles as its last part, the others as their first
     const float* const ws = reinterpret_cast<const float*>(a.workspace);
     auto part = [&](int run) { return ws + (static_cast<int64_t>(i - 1 + run) * 2 + (run == 0 ? 1 : 0)) * kPart<D, R>; };
-    const int q = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (q < rows) {
-        float m = kLowest, l = 0.0f;
-        for (int run = lane; run < runs; run += 32) m = max_nd(m, part(run)[R * D + 2 * q]);
+    float m = kLowest, l = 0.0f, v[kCols][4] = {};
+    auto add = [&](float pm, float pl, const float4* u) {
+        const float top = max_nd(m, pm), f = exp2_approx(sub_rn(m, top)), g = exp2_approx(sub_rn(pm, top));
+        m = top, l = __fmaf_rn(l, f, mul_rn(pl, g));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = max_nd(m, __shfl_xor_sync(kFullMask, m, o));
-        float v[kCols][4] = {};
-        for (int first = 0; first < runs; first += 32) {
-            float f = 0.0f;
-            if (first + lane < runs) {
-                const float2 st = *reinterpret_cast<const float2*>(part(first + lane) + R * D + 2 * q);
-                f = exp2_approx(sub_rn(st.x, m));
-                l = __fmaf_rn(st.y, f, l);
-            }
-            const int here = min(32, runs - first);
-#pragma unroll 8
-            for (int k = 0; k < here; ++k) {
-                const float g = __shfl_sync(kFullMask, f, k);
-                const float* p = part(first + k) + q * D;
-#pragma unroll
-                for (int x = 0; x < kCols; ++x)
-                    if (D >= 128 || lane < D / 4) {
-                        const float4 u = reinterpret_cast<const float4*>(p)[x * 32 + lane];
-                        v[x][0] = __fmaf_rn(u.x, g, v[x][0]), v[x][1] = __fmaf_rn(u.y, g, v[x][1]);
-                        v[x][2] = __fmaf_rn(u.z, g, v[x][2]), v[x][3] = __fmaf_rn(u.w, g, v[x][3]);
-                    }
-            }
+        for (int x = 0; x < kCols; ++x) {
+            v[x][0] = __fmaf_rn(v[x][0], f, mul_rn(u[x].x, g)), v[x][1] = __fmaf_rn(v[x][1], f, mul_rn(u[x].y, g));
+            v[x][2] = __fmaf_rn(v[x][2], f, mul_rn(u[x].z, g)), v[x][3] = __fmaf_rn(v[x][3], f, mul_rn(u[x].w, g));
         }
+    };
+    if (q < rows) {
+        for (int first = sub; first < runs; first += S * kBatch) {
+            float2 st[kBatch];
+            float4 u[kBatch][kCols];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) l = add_rn(l, __shfl_xor_sync(kFullMask, l, o));
-        int query, head;
-        split_row(cut.n, G, cut.rt * R + q, &query, &head);
-        const Finish end(a, cut.h * G + head, cut.h, m, l);
+            for (int k = 0; k < kBatch; ++k) {
+                const int run = first + k * S;
+                st[k] = make_float2(kLowest, 0.0f);
+                if (run < runs) st[k] = *reinterpret_cast<const float2*>(part(run) + R * D + 2 * q);
 #pragma unroll
-        for (int x = 0; x < kCols; ++x)
-            if (D >= 128 || lane < D / 4) end.store(a, cut.row0 + query, cut.h * G + head, (x * 32 + lane) * 4, v[x]);
+                for (int x = 0; x < kCols; ++x) {
+                    u[k][x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (run < runs && lane < kStep) u[k][x] = reinterpret_cast<const float4*>(part(run) + q * D)[x * 32 + lane];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) add(st[k].x, st[k].y, u[k]);
+        }
+        if (S > 1 && sub > 0) {
+            float* const mine = sums[warp % (8 * S)];
+#pragma unroll
+            for (int x = 0; x < kCols; ++x)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (lane < kStep) mine[(x * 4 + k) * kStep + lane] = v[x][k];
+            if (lane == 0) mine[D] = m, mine[D + 1] = l;
+        }
     }
+    if (S > 1) {
+        __syncthreads();
+        if (sub > 0 || q >= rows) return;
+        for (int w = 1; w < S; ++w) {
+            const float* const other = sums[(warp + w) % (8 * S)];
+            float4 u[kCols];
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) {
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = lane < kStep ? other[(x * 4 + k) * kStep + lane] : 0.0f;
+                u[x] = make_float4(y[0], y[1], y[2], y[3]);
+            }
+            add(other[D], other[D + 1], u);
+        }
+    }
+    int query, head;
+    split_row(cut.n, G, cut.rt * R + q, &query, &head);
+    const Finish end(a, cut.h * G + head, cut.h, m, l);
+#pragma unroll
+    for (int x = 0; x < kCols; ++x)
+        if (lane < kStep) end.store(a, cut.row0 + query, cut.h * G + head, (x * 32 + lane) * 4, v[x]);
 }
 
 template <int D, int R>
 cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t s) {
     if (ctas < 2) return cudaSuccess;
-    return launch_pdl(k_join<D, R>, dim3(static_cast<unsigned>(ctas - 1), R / 8), dim3(256), 0, s, a, ctas);
+    return launch_pdl(k_join<D, R>, dim3(static_cast<unsigned>(ctas - 1), R / 8), dim3(256 * kSub<R>), 0, s, a, ctas);
 }
 
 }  // namespace
