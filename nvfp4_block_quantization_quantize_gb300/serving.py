@@ -1,6 +1,7 @@
 """Layers of a served model on frozen NVFP4 weights, made of the serving
 operators: the norm that adds the residual stream and quantizes, the product of
-a few tokens, the products grouped by expert.
+a few tokens, the products grouped by expert, and the cache of keys and values with the attention
+that reads it.
 
 The weights are quantized once with the library (1x16 blocks, one global amax a
 weight or expert).  Nothing here reads a device value on the host, so a step
@@ -11,7 +12,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (nvfp4_grouped_mm, nvfp4_grouped_scales_to_mma, nvfp4_mv, nvfp4_quantize, nvfp4_rmsnorm)
+from . import (nvfp4_cache_attention, nvfp4_grouped_mm, nvfp4_grouped_scales_to_mma, nvfp4_mv, nvfp4_qk_norm_rope,
+               nvfp4_quantize, nvfp4_rmsnorm)
 
 MV_ROWS = 16                                    # the most rows nvfp4_mv takes
 
@@ -45,6 +47,19 @@ class FP4Projection:
     def _mv(self, codes, x_scales, out_dtype):
         return nvfp4_mv(codes, self.codes[0], self.scales[0], x_scales=x_scales, gamax=self.gamax, out_dtype=out_dtype)
 
+    def product(self, x: torch.Tensor, out_dtype="bf16"):
+        """x W^T [M, N] of x [M, K] as it is: without the norm."""
+        M = x.shape[0]
+        if self.activations == "mxfp8" or (self.activations == "auto" and M <= MV_ROWS):
+            if M <= MV_ROWS:                        # x itself: the product takes 16 bits as it takes 8
+                return self._mv(x, None, out_dtype)
+            return torch.cat([self._mv(t.contiguous(), None, out_dtype) for t in x.split(MV_ROWS)])
+        q = nvfp4_quantize(x.contiguous(), gamax_mode="row")
+        offsets = torch.zeros(2, dtype=torch.int64, device=x.device)
+        offsets[1:].fill_(M)
+        return nvfp4_grouped_mm(q["codes"], q["scales"], offsets, self.codes, self.scales_mma, gamax_a=q["gamax"],
+                                gamax_b=self.gamax, out_dtype=out_dtype)
+
     def __call__(self, x: torch.Tensor, hidden: torch.Tensor, out_dtype="bf16"):
         """(product [M, N], new hidden [M, K])."""
         M = x.shape[0]
@@ -60,6 +75,45 @@ class FP4Projection:
         y = nvfp4_grouped_mm(n["codes"], n["scales"], offsets, self.codes, self.scales_mma, gamax_a=n["gamax"],
                              gamax_b=self.gamax, out_dtype=out_dtype)
         return y, n["hidden"]
+
+
+class FP4Attention:
+    """A layer's attention over a paged cache in NVFP4: queries, keys and values of norm(x + hidden) by one
+    projection, norms of their heads and rotation with the keys' and values' way into the cache, attention, and the
+    projection back.
+
+    qkv [(q_heads + 2 kv_heads) * head_dim, D] (queries, then keys, then values), out [D, q_heads * head_dim];
+    head_dim 64, 128 or 256, D a multiple of 64.  q_norm, k_norm: weights [head_dim] of the heads' norms, or None;
+    phases, layout, magnitude: the rotation (nvfp4_rope_phases).  k_gamax, v_gamax: the cache's global amaxes (None, one, or one
+    a KV head), the same for a cache's life.  activations: as FP4Projection's, for both products."""
+
+    def __init__(self, norm_weight, qkv, out, q_heads: int, kv_heads: int, *, phases, q_norm=None, k_norm=None, layout="half",
+                 magnitude: float = 1.0, eps: float = 1e-6, k_gamax=None, v_gamax=None, window: int = 0, sinks=None,
+                 activations: str = "auto"):
+        head_dim = out.shape[1] // max(q_heads, 1)
+        if kv_heads < 1 or q_heads % kv_heads or out.shape[1] != q_heads * head_dim or \
+                tuple(qkv.shape) != ((q_heads + 2 * kv_heads) * head_dim, out.shape[0]):
+            raise ValueError("FP4Attention: qkv [(q_heads + 2 kv_heads) * head_dim, D] and out [D, q_heads * head_dim]")
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.qkv = FP4Projection(qkv, norm_weight, eps, activations)
+        self.back = FP4Projection(out, None, eps, activations)
+        self.rope = dict(phases=phases, q_weight=q_norm, k_weight=k_norm, eps=eps, layout=layout, magnitude=magnitude)
+        self.gamax = dict(k_gamax=k_gamax, v_gamax=v_gamax)
+        self.window, self.sinks = window, sinks
+
+    def __call__(self, x: torch.Tensor, hidden: torch.Tensor, cache, pages, lengths, slots, positions, offsets=None):
+        """(layer output [M, D] in x's dtype, new hidden [M, D]).
+
+        slots, positions [M]: where each token goes in the cache, and where it stands; pages [B, width], lengths [B] (these
+        tokens among them) and offsets as nvfp4_cache_attention takes them."""
+        M, H, Hk = x.shape[0], self.q_heads, self.kv_heads
+        y, hidden = self.qkv(x, hidden, "bf16")
+        y = y.view(M, H + 2 * Hk, self.head_dim)
+        q = nvfp4_qk_norm_rope(y[:, :H], y[:, H:H + Hk], positions, cache=cache, v=y[:, H + Hk:], slots=slots, **self.rope,
+                               **self.gamax)["q"]
+        o = nvfp4_cache_attention(q, cache, pages, lengths, offsets=offsets, window=self.window, sinks=self.sinks, **self.gamax)
+        out = self.back.product(o.view(M, H * self.head_dim), "f32" if x.dtype == torch.float32 else "bf16")
+        return out, hidden
 
 
 class FP4Experts:
