@@ -20,6 +20,11 @@
 // end, and those cut between CTAs leave partial sums in the workspace, which k_join adds in
 // order.  A warp works on pairs of tiles; its own ring of shared memory is filled by bulk copies,
 // one or two a pair, that run ahead across groups.
+// Measured: 64 sequences of 512 to 32768 keys, 8 KV heads of 128 and 64 query heads (655 MB), 128 us, 5.1 TB/s of the 6.7 of a
+// copy; one sequence of 131072 keys (151 MB) 45 us, one of 200 6.8 us.  Bound by issue and latency: a pair of tiles takes some
+// 630 instructions of a warp (half of them the decoding: a word of eight codes is 4 conversions), and with the registers for
+// 16 warps an SM the slots are 61 % full, the ALUs 55 to 65 %.  Tiles alone instead of pairs took 228 us, divisions to
+// find a tile's place 258, masks on every tile 187, runs shared by a CTA's warps 157.
 #include "nvfp4_attend.cuh"
 
 namespace nvfp4 {
@@ -672,14 +677,17 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 }
 
 // ---- launches -----------------------------------------------------------------------------------
-// Row tiles of 16 where groups of 8 rows would be read more than once (the cache is then decoded
-// once for both), but not for the widest heads or fp32, whose fragments fill the registers.
+// Row tiles of 16 where the cache is then decoded fewer times for all rows: a tile of 16 takes about 1.6 times as long as one
+// of 8 (16 sequences of 8192 keys, 8 KV heads of 128: 16 rows 57 us and 67 in tiles of 8; 24 rows 95 and 94; 8 rows 54
+// and 42).  Not for the widest heads or fp32, whose fragments fill the registers.
 bool two_tiles(const AttendArgs& a) {
     const int64_t rows = (a.T * (a.Hq / a.cache.Hkv) + a.B - 1) / a.B;      // of a sequence, in the mean
-    return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && rows > 8;
+    return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && (rows + 15) / 16 * 8 < (rows + 7) / 8 * 5;
 }
 
-constexpr int kSmall = 512;                               // keys up to which a group is not cut
+// Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1000 keys of one sequence 10.7 us,
+// cut 11.2, of 32 sequences 14.5 and 20.5; 200 keys of one 7.0 and 11.1.
+constexpr int kSmall = 1024;
 
 int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
     const int64_t G = a.Hq / a.cache.Hkv;
@@ -722,12 +730,10 @@ cudaError_t launch_d(const AttendArgs& a, cudaStream_t s) {
     return launch_t<D, 1, false>(a, s);
 }
 
-// Sequences of more rows than this go to the tensor-memory kernel.
-constexpr int kManyRows = 64;
-
-// whether a sequence may have that many
+// whether k_attend_many may take a sequence
 bool may_have_many(const AttendArgs& a) {
-    return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && (a.ragged ? a.T : 1) * (a.Hq / a.cache.Hkv) > kManyRows;
+    return a.dtype == NVFP4_BF16 && a.cache.D <= 128 &&
+           is_many((a.ragged ? a.T : 1) * (a.Hq / a.cache.Hkv), a.width * a.cache.page_size);
 }
 
 }  // namespace
@@ -745,10 +751,10 @@ int launch_attend(const AttendArgs& given, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     AttendArgs a = given;
     const bool many = may_have_many(a);
-    a.rows_above = 0, a.rows_upto = many ? kManyRows : 1 << 30;
+    a.take = many ? kTakeFew : kTakeAll;
     cudaError_t e = a.cache.D == 64 ? launch_d<64>(a, s) : a.cache.D == 128 ? launch_d<128>(a, s) : launch_d<256>(a, s);
     if (e == cudaSuccess && many) {
-        a.rows_above = kManyRows, a.rows_upto = 1 << 30;
+        a.take = kTakeMany;
         e = launch_attend_many(a, s);
     }
     return static_cast<int>(e);

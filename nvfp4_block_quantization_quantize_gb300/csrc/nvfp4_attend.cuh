@@ -13,12 +13,24 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -__builtin_huge_valf();          // a masked logit
 constexpr float kSlack = 8.0f;                            // a weight may reach 2^8 before the maximum is raised
 // What a group costs besides its tiles (its queries, its end), in tiles: the first units of every group.  A run is not
-// cut inside them.
+// cut inside them.  64 ragged sequences took 138 us with 2, 133 with 6 and with 12, 135 with 20.
 constexpr int kGroupCost = 8;
 
 template <int D>
 constexpr int kRecord = 18 * D;                           // bytes of a tile
+
 // ---- who does what ------------------------------------------------------------------------------
+// Sequences that the tensor-memory kernel (k_attend_many) takes: of 48 rows and more (8 sequences of 8192 keys, 8 KV heads of
+// 128, the other kernel's launch with each: 48 rows 74 us there and 86 by the warp-level kernel, 32 rows 74 and 65, 96 rows 75
+// and 144), unless they are so short that its start costs more than its rate gains (600 keys, 4 KV heads, 64 rows: 38 us
+// there and 20).
+constexpr int kManyRows = 48;
+constexpr int64_t kManyWork = int64_t{1} << 18;           // rows times keys
+
+enum Take { kTakeAll, kTakeFew, kTakeMany };
+
+__host__ __device__ __forceinline__ bool is_many(int64_t rows, int64_t keys) { return rows >= kManyRows && rows * keys >= kManyWork; }
+
 // A sequence's share of the work.
 struct Seq {
     int64_t row0;             // its first query
@@ -47,7 +59,7 @@ __device__ __forceinline__ Seq sequence(const AttendArgs& a, int64_t b) {
     s.tiles = max(0, (s.len + 15) / 16 - s.t0);
     const int G = a.Hq / a.cache.Hkv;
     const int64_t rows = static_cast<int64_t>(s.n) * G;
-    if (rows <= a.rows_above || rows > a.rows_upto) s.n = 0;      // another kernel's
+    if (a.take != kTakeAll && is_many(rows, s.len) != (a.take == kTakeMany)) s.n = 0;      // the other kernel's
     s.runs = s.n ? static_cast<int>((rows + R - 1) / R) * a.cache.Hkv : 0;
     s.units = static_cast<int64_t>(s.runs) * (kGroupCost + s.tiles);
     return s;
@@ -233,7 +245,7 @@ __device__ __forceinline__ Cut* cuts(const AttendArgs& a, int64_t ctas) {
 // A group that several CTAs took parts of, joined: 8 rows a CTA, kSub warps a row, each of which adds every kSub-th part in
 // their order; the first then adds the warps' sums in theirs.  Bound by latency: a long sequence alone makes 38 parts a
 // group, which four warps read in three turns (one warp a row took 10 us of a 47 us call); with 256 rows a group
-// most CTAs have nothing to do, and small ones end sooner.
+// most CTAs have nothing to do, and small ones end sooner.  Of 131072 keys' 45 us it takes 9, elsewhere 3 to 4.
 template <int R>
 constexpr int kSub = R <= 16 ? 4 : 1;
 
@@ -323,7 +335,7 @@ cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-// the kernel of many queries a sequence, which takes the sequences of more than a.rows_above rows
+// the kernel of many queries a sequence
 cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s);
 int64_t attend_many_workspace(const AttendArgs& a);
 

@@ -1,5 +1,5 @@
 // nvfp4_attend_many.cu -- attention of many queries a sequence over a paged NVFP4 cache: the
-// sequences of nvfp4_cache_attention with more rows than the warp-level kernel is for.
+// sequences of nvfp4_cache_attention with more rows than the warp-level kernel is for (is_many).
 //
 // The rows are a sequence's queries times the heads that share a KV head; two tiles of
 // 128 rows share each block of 128 keys.  4 D operations a row and key: bound by the tensor
@@ -14,6 +14,11 @@
 //     2^15 each of them fits f16, and no maximum is looked for.  Else it is raised to the block's, O, in tensor
 //     memory too, is rescaled and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
+// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 712 us, 1.45 PFLOP/s (of 1.92 of a large
+// product; the warp-level kernel's way took 4.9 ms).  A maximum looked for in each block took 1.78 ms, one warpgroup
+// decoding keys and values 0.81 ms.  What is left is shared: without the softmax's arithmetic 713 of then 771 us, without the
+// decoding 685, with a quarter of the products 662, with none of the three 361.
+// Equal runs of blocks for each CTA, whatever the sequences; cut groups are joined by k_join.
 #include "nvfp4_attend.cuh"
 
 namespace nvfp4 {

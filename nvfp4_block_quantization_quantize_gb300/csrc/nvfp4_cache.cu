@@ -118,7 +118,9 @@ __device__ __forceinline__ void quantize_into(uint8_t* part, int row, int D, int
 // L threads a head.  A token's heads (q, k, then v when they go to the cache) are cut into
 // `chunks` of `per` heads, one a warp.  TURN: norms and rotation, of pairs half the rotated elements apart (HALF) or of
 // neighbours; CACHE: k and v go to the cache.
-// Registers for as many warps as keep memory busy: 64 a thread without a cache (bf16), 80 with.
+// Registers for as many warps as keep memory busy: 64 a thread without a cache or a turn (bf16), 80 with both.
+// Measured, 16384 bf16 tokens: 32 + 8 heads of 128 turned 65 us, 5.2 TB/s (201 us with the layout read at run time); 8 + 8 heads
+// quantized and read back 40 us for the two kernels (a thread a block in k_cache_read, its place found for each: 67 us).
 enum Turn { kNoTurn, kHalf, kNeighbours };
 
 template <int DT, int L, Turn TURN, bool CACHE>
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kHeadsThreads, DT == NVFP4_BF16 && !(TURN != k
 }
 
 // A warp takes part of a slot's blocks of 16 elements, keys first, then values, a thread a block: 8 bytes of codes and a
-// scale to 16 values (zeros where there is no such slot).  LG: log2 of the blocks of a head.
+// scale to 16 values (zeros where there is no such slot): bound by memory.  LG: log2 of the blocks of a head.
 template <int ODT, int LG>
 __global__ void __launch_bounds__(256) k_cache_read(const CacheReadArgs a, int chunks) {
     pdl_trigger();

@@ -169,7 +169,7 @@ struct AttendArgs {
     int out_dtype;
     float* lse;
     uint8_t* workspace;
-    int rows_above, rows_upto;                              // a kernel's sequences: of that many rows (queries times heads a KV head)
+    int take;                                               // which sequences a kernel takes: all, or those of few or of many rows
 };
 
 // launchers (each returns cudaGetLastError() after its launches)

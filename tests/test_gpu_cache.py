@@ -240,6 +240,14 @@ CASES = [
     ([400 + 37 * i for i in range(30)], [65 + 7 * i for i in range(30)], 6, 3, 64, 16, "bf16", "none", {}),
     ([900], [450], 12, 4, 128, 64, "bf16", "head", {"window": 1}),
     ([900], [450], 12, 4, 128, 64, "bf16", "head", {"scale": -0.05}),
+    # many heads a KV head without offsets; sequences on both sides of what the tensor-memory kernel takes
+    ([9000, 300, 5000], None, 80, 1, 128, 64, "bf16", "head", {}),
+    ([5461, 5462, 2000, 4096, 4095], [6, 6, 17, 8, 8], 8, 1, 128, 32, "bf16", "none", {"causal": False}),
+    ([5461, 5462, 2000, 4096, 4095], [6, 6, 17, 8, 8], 8, 1, 64, 32, "bf16", "tensor", {"sinks": True, "window": 3000}),
+    ([3000, 2500], [300, 257], 8, 2, 128, 64, "bf16", "none", {"window": 1000}),
+    ([2048, 4096], [2048, 130], 4, 2, 64, 64, "bf16", "none", {}),
+    ([1024, 1023, 1], None, 24, 1, 128, 64, "bf16", "none", {}),
+    ([1500, 1025, 1], None, 24, 1, 64, 64, "bf16", "none", {"sinks": True}),
 ]
 
 
