@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
         if (lane == 0) {
             uint8_t* const dst = my_ring + stage * 2 * kRecord<D>;
             uint64_t* const bar = my_bars + stage;
-            const uint8_t* const src = ahead_head + page_a * page_bytes + ahead_tile * kRecord<D>;
+            const uint8_t* const src = ahead_head + page_a * page_bytes + static_cast<int64_t>(ahead_tile) * kRecord<D>;
             if (is_a && is_b && ahead_tile + 1 < per_page) {      // one piece of memory
                 mbar_expect_tx(bar, 2 * kRecord<D>);
                 bulk_copy(dst, src, 2 * kRecord<D>, bar);

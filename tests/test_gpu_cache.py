@@ -245,6 +245,9 @@ CASES = [
     ([5461, 5462, 2000, 4096, 4095], [6, 6, 17, 8, 8], 8, 1, 128, 32, "bf16", "none", {"causal": False}),
     ([5461, 5462, 2000, 4096, 4095], [6, 6, 17, 8, 8], 8, 1, 64, 32, "bf16", "tensor", {"sinks": True, "window": 3000}),
     ([3000, 2500], [300, 257], 8, 2, 128, 64, "bf16", "none", {"window": 1000}),
+    ([300, 600, 513, 0, 1], [1000, 900, 700, 80, 700], 5, 1, 128, 48, "bf16", "none", {}),
+    ([300, 600, 513, 0, 1], [1000, 900, 700, 80, 700], 5, 1, 64, 48, "bf16", "head", {"sinks": True, "window": 20}),
+    ([1100 + 37 * i for i in range(30)], [129 + 7 * i for i in range(30)], 6, 3, 64, 16, "bf16", "none", {}),
     ([2048, 4096], [2048, 130], 4, 2, 64, 64, "bf16", "none", {}),
     ([1024, 1023, 1], None, 24, 1, 128, 64, "bf16", "none", {}),
     ([1500, 1025, 1], None, 24, 1, 64, 64, "bf16", "none", {"sinks": True}),

@@ -208,30 +208,36 @@ def test_wrong_lengths_offsets_and_pages():
         assert ((got[:1].double() - out).abs() <= tolerance(out, mass, most, v.abs().max().item(), 64, 128, q.dtype, got.dtype)).all()
 
 
-def test_many_rows_of_wrong_pages():
-    c, q, kw = small(6, lens=(300, 200), n=1, P=16, H=1, Hq=1)
+@pytest.mark.parametrize("L", [300, 2000])                # the second by the tensor-memory kernel
+def test_many_rows_of_wrong_pages(L):
+    c, q, kw = small(6, lens=(L, 200), n=1, P=16, H=1, Hq=1)
     q = (2 * normal(gen(3), 300, 1, 128)).to(torch.bfloat16)
     off = torch.tensor([0, 150, 300], device="cuda")
     pages = c.pages.clone()
     pages[0, 5] = -1
     got = nv.nvfp4_cache_attention(q, c.cache, pages, c.lengths, offsets=off, causal=False, out_dtype="f32", **kw)
     k, v = c.values(0)
-    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep = torch.ones(L, dtype=torch.bool, device="cuda")
     keep[80:96] = False
     out, _, mass, most = attention(q[:150], k[keep], v[keep], 150, scale=128 ** -0.5, causal=False)
-    assert ((got[:150].double() - out).abs() <= tolerance(out, mass, most, v.abs().max().item(), 300, 128, q.dtype, got.dtype)).all()
+    assert ((got[:150].double() - out).abs() <= tolerance(out, mass, most, v.abs().max().item(), L, 128, q.dtype, got.dtype)).all()
 
 
-@pytest.mark.parametrize("n", [1, 100])
-def test_a_shared_page_and_infinities_stay_in_their_rows(n):
-    c, q, kw = small(7, lens=(50, 50), n=1, Hq=2, H=1)
+@pytest.mark.parametrize("n,L", [(1, 50), (100, 50), (100, 1500)])
+def test_a_shared_page_and_infinities_stay_in_their_rows(n, L):
+    c, q, kw = small(7, lens=(L, L), n=1, Hq=2, H=1)
     q = (2 * normal(gen(4), 2 * n, 2, 128)).to(torch.bfloat16)
     off = None if n == 1 else torch.tensor([0, n, 2 * n], device="cuda")
     pages = c.pages.clone()
     pages[1] = pages[0]                                    # both sequences are the same keys
     q[n:] = q[:n]
     a = nv.nvfp4_cache_attention(q, c.cache, pages, c.lengths, offsets=off, **kw)
-    assert torch.equal(a[:n], a[n:])
+    if L == 50:                                            # (longer groups may be cut between CTAs, each elsewhere)
+        assert torch.equal(a[:n], a[n:])
+    k, v = c.values(0)
+    out, _, mass, most = attention(q[:n], k, v, n, scale=128 ** -0.5)
+    tol = tolerance(out, mass, most, v.abs().max().item(), L, 128, q.dtype, a.dtype)
+    assert ((a[:n].double() - out).abs() <= tol).all() and ((a[n:].double() - out).abs() <= tol).all()
     q[0, 0, 3], q[n, 1, 5] = math.inf, math.nan
     b = nv.nvfp4_cache_attention(q, c.cache, pages, c.lengths, offsets=off, causal=False, **kw)
     q[0, 0, 3], q[n, 1, 5] = 0.0, 0.0
@@ -245,11 +251,34 @@ def test_a_shared_page_and_infinities_stay_in_their_rows(n):
 def test_large_and_small_queries(scale):
     """Logits far apart: one key takes all weight, in both kernels; f16 holds the queries by their power of two."""
     for n, Hq in ((1, 4), (70, 4)):
-        c = Paged(8, [900, 300], 2, 128, 16, "none")
+        c = Paged(8, [2000, 300], 2, 128, 16, "none")
         q = (scale * normal(gen(5), 2 * n, Hq, 128)).to(torch.bfloat16)
         off = torch.tensor([0, n, 2 * n], device="cuda")
         got, lse = nv.nvfp4_cache_attention(q, c.cache, c.pages, c.lengths, offsets=off, out_dtype="f32", want_lse=True)
         c.check(q, [n, n], got, lse)
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_one_page_past_32_bits(n):
+    """A page of over 2^31 bytes, its last tokens used, by a few rows and by many."""
+    D, L = 128, 1100
+    P = ((1 << 31) // (18 * D) + 200) * 16
+    cache = torch.empty(2, 1, P // 16, 18 * D, dtype=torch.uint8, device="cuda")
+    g = gen(5)
+    k, v = normal(g, L, 1, D), normal(g, L, 1, D)
+    slots = 2 * P - L + torch.arange(L, device="cuda")
+    nv.nvfp4_cache_write(cache, k, v, slots)
+    tiny = nv.nvfp4_cache_empty(1, 1104, 1, D)
+    nv.nvfp4_cache_write(tiny, k, v, torch.arange(L, device="cuda") + 4)      # (as far into a tile: P - L is 4 more than tiles)
+    for x, y in zip(nv.nvfp4_cache_read(cache, slots), nv.nvfp4_cache_read(tiny, torch.arange(L, device="cuda") + 4)):
+        assert torch.equal(x, y)
+    q = normal(g, n, 4, D).to(torch.bfloat16)
+    kw = dict(offsets=torch.tensor([0, n], device="cuda"), window=L - n, out_dtype="f32")
+    got = nv.nvfp4_cache_attention(q, cache, torch.tensor([[1]], dtype=torch.int32, device="cuda"), torch.tensor([P], device="cuda"), **kw)
+    kc, ks, vc, vs = (take(x, torch.arange(L, device="cuda") + 4) for x in parts(tiny))
+    k, v = values(kc, ks, None), values(vc, vs, None)
+    out, _, mass, most = attention(q, k, v, n, scale=D ** -0.5, window=L - n)
+    assert ((got.double() - out).abs() <= tolerance(out, mass, most, v.abs().max().item(), L, D, q.dtype, got.dtype)).all()
 
 
 def test_slots_past_32_bits():
@@ -281,12 +310,12 @@ def test_many_queries_in_a_cache_past_32_bits():
     cache = torch.empty(pages, H, P // 16, 18 * D, dtype=torch.uint8, device="cuda")
     g = gen(3)
     table = torch.tensor([[pages - 1, pages - 7]], dtype=torch.int32, device="cuda")
-    j = torch.arange(200, device="cuda")
-    k, v = normal(g, 200, H, D), normal(g, 200, H, D)
+    j = torch.arange(256, device="cuda")
+    k, v = normal(g, 256, H, D), normal(g, 256, H, D)
     nv.nvfp4_cache_write(cache, k, v, table[0].long()[j // P] * P + j % P)
     tiny = nv.nvfp4_cache_empty(2, P, H, D)
     nv.nvfp4_cache_write(tiny, k, v, j)
-    q, ln, off = normal(g, 130, 8, D).to(torch.bfloat16), torch.tensor([200], device="cuda"), torch.tensor([0, 130], device="cuda")
+    q, ln, off = normal(g, 130, 64, D).to(torch.bfloat16), torch.tensor([256], device="cuda"), torch.tensor([0, 130], device="cuda")
     want = nv.nvfp4_cache_attention(q, tiny, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), ln, offsets=off)
     assert torch.equal(nv.nvfp4_cache_attention(q, cache, table, ln, offsets=off), want)
 
