@@ -1160,6 +1160,8 @@ def nvfp4_rope_phases(rotary_dim: int, base: float = 10000.0, *, factor: float =
         freq = [float(f) for f in inv_freq]
         if len(freq) != half:
             raise ValueError(f"nvfp4_rope_phases: inv_freq must hold {half} values")
+        if method == "ntk":
+            raise ValueError("nvfp4_rope_phases: ntk takes a base, not inv_freq")
     elif not base > 0.0:
         raise ValueError("nvfp4_rope_phases: base must be positive")
     else:
@@ -1169,8 +1171,8 @@ def nvfp4_rope_phases(rotary_dim: int, base: float = 10000.0, *, factor: float =
     if method == "linear":
         freq = [f / factor for f in freq]
     elif method == "yarn":
-        if not original or original <= 0 or not beta_fast > beta_slow > 0:
-            raise ValueError("nvfp4_rope_phases: yarn needs original > 0 and beta_fast > beta_slow > 0")
+        if not original or original <= 0 or not beta_fast > beta_slow > 0 or not base > 1.0:
+            raise ValueError("nvfp4_rope_phases: yarn needs original > 0, beta_fast > beta_slow > 0 and a base above 1")
 
         def pair(turns):                        # the pair that makes so many turns in `original` positions
             return half * math.log(original / (turns * 2 * math.pi)) / math.log(base)

@@ -243,7 +243,8 @@ def test_longer_contexts():
 @pytest.mark.parametrize("kw", [dict(rotary_dim=0), dict(rotary_dim=3), dict(factor=0.5), dict(factor=NAN), dict(factor=INF),
                                 dict(base=0.0), dict(base=-1.0), dict(method="other"), dict(method="yarn"),
                                 dict(method="yarn", original=0), dict(method="yarn", original=4096, beta_fast=1.0),
-                                dict(inv_freq=[1.0]), dict(inv_freq=[1.0, INF])])
+                                dict(inv_freq=[1.0]), dict(inv_freq=[1.0, INF]), dict(inv_freq=[1.0, 0.5], method="ntk", factor=2.0),
+                                dict(method="yarn", original=4096, base=1.0)])
 def test_frequencies_refused(kw):
     with pytest.raises(ValueError, match="nvfp4_rope_phases"):
         nv.nvfp4_rope_phases(**{"rotary_dim": 4, **kw})
