@@ -686,8 +686,10 @@ bool two_tiles(const AttendArgs& a) {
 }
 
 // Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1000 keys of one sequence 10.7 us,
-// cut 11.2, of 32 sequences 14.5 and 20.5; 200 keys of one 7.0 and 11.1.
-constexpr int kSmall = 1024;
+// cut 11.2, of 32 sequences 14.5 and 20.5; 200 keys of one 7.0 and 11.1.  Not where there are more groups than kWaves
+// times the CTAs that run at once: equal runs then keep all busy (8 KV heads of 128: 64 sequences of 1024 keys 28.3 us uncut,
+// 29.8 cut, 256 of them 114 and 82; 1000 of 100 keys 499 and 89).
+constexpr int kSmall = 1024, kWaves = 2;
 
 int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
     const int64_t G = a.Hq / a.cache.Hkv;
@@ -699,8 +701,9 @@ int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
 int64_t grid_of(const AttendArgs& a, int R, int* split) {
     const int64_t cap = a.width * a.cache.page_size;
     const int64_t runs = runs_bound(a, R);
-    *split = cap > kSmall || runs > (int64_t{1} << 20);
-    return *split ? static_cast<int64_t>(sm_count()) * (a.cache.D <= 128 && R == 8 ? 2 : 1) : runs;      // as many as run at once
+    const int64_t at_once = static_cast<int64_t>(sm_count()) * (a.cache.D <= 128 && R == 8 ? 2 : 1);
+    *split = cap > kSmall || runs > kWaves * at_once;
+    return *split ? at_once : runs;
 }
 
 template <int D, int NT, bool F32>

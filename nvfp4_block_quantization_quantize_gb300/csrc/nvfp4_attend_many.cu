@@ -14,11 +14,12 @@
 //     2^15 each of them fits f16, and no maximum is looked for.  Else it is raised to the block's, O, in tensor
 //     memory too, is rescaled and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
-// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 712 us, 1.45 PFLOP/s (of 1.92 of a large
+// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 703 us, 1.47 PFLOP/s (of 1.92 of a large
 // product; the warp-level kernel's way took 4.9 ms).  A maximum looked for in each block took 1.78 ms, one warpgroup
 // decoding keys and values 0.81 ms.  What is left is shared: without the softmax's arithmetic 713 of then 771 us, without the
 // decoding 685, with a quarter of the products 662, with none of the three 361.
-// Equal runs of blocks for each CTA, whatever the sequences; cut groups are joined by k_join.
+// Equal runs of blocks for each CTA, whatever the sequences; cut groups are joined by k_join.  A group costs 9 us besides
+// its blocks (1.5 us each): queries, first copies and the end are not all behind another's products.
 #include "nvfp4_attend.cuh"
 
 namespace nvfp4 {
@@ -187,9 +188,10 @@ __device__ __forceinline__ void unrolled(F f) {           // f(0) .. f(N - 1), e
 }
 
 // The work of a sequence, in keys that its groups of 256 rows are to look at: w0 + rt * step a group of row tile rt (the
-// first kGroupKeys for what it costs besides).  With a causal mask the row tiles look at more and more; that they look at whole
+// first kGroupKeys for what it costs besides: a prompt of 8192 queries, 32 heads of 128 over 8, takes 804 us with 256, 589 with
+// 512, 478 with 768, 465 with 1024; of 2048 91, 85, 83, 85).  With a causal mask the row tiles look at more and more; that they look at whole
 // blocks, and a window cuts off the first keys, is not counted.
-constexpr int kGroupKeys = 256;
+constexpr int kGroupKeys = 768;
 constexpr int kMinKeys = 512;                             // a CTA's run is not made shorter
 
 struct Load {
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     if (threadIdx.x == 32) {
         for (int i = 0; i < kBars; ++i) {
             const bool threads = (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) || (i >= kPFull && i < kOFull) || i >= kRaw;
-            mbar_init(bars + i, i == kQFull ? 256 : threads ? 128 : i == kQEmpty ? 9 : 1);       // (the products' end and 8 softmax warps)
+            mbar_init(bars + i, i == kQFull ? 256 : threads ? 128 : i == kQEmpty ? 9 : 1);       // (the last S, and 8 softmax warps)
         }
         *lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -505,6 +507,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 }
             };
             int at = place_of(page_of());
+            load(at);
             // ---- this item's queries: copied as they are, a row a thread, then made f16 where they lie (its pieces in their
             // swizzled order), D / 8 threads a row
             if (items > 0) ok = wait(bars + kQEmpty, (items - 1) & 1, lost);
@@ -525,30 +528,31 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 ok = wait(bars + kRaw + tile, raws++ & 1, lost);
                 constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
                 const int q = lane % kLanes;
-#pragma unroll 1
-                for (int i = 0; ok && i < 32; i += kAtOnce) {
-                    const int in_tile = (warp & 3) * 32 + i + lane / kLanes, r = tile * 128 + in_tile;
-                    uint8_t* const at = dst + q / 8 * M::half + in_tile * 128;
-                    const uint4 u = *reinterpret_cast<const uint4*>(at + (q & 7) * 16);
-                    uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y), u.z), u.w);
-                    top = max(top << 16, top & 0xFFFF0000u);
+                if (ok) {
+#pragma unroll 2
+                    for (int i = 0; i < 32; i += kAtOnce) {
+                        const int in_tile = (warp & 3) * 32 + i + lane / kLanes, r = tile * 128 + in_tile;
+                        uint8_t* const at = dst + q / 8 * M::half + in_tile * 128;
+                        const uint4 u = *reinterpret_cast<const uint4*>(at + (q & 7) * 16);
+                        uint32_t top = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, u.x), u.y), u.z), u.w);
+                        top = max(top << 16, top & 0xFFFF0000u);
 #pragma unroll
-                    for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));      // all have read
-                    const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
-                    const float down = copysignf(power_of_two(-ex), a.scale);
-                    if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
-                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t o[4];
+                        for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));      // all have read
+                        const int ex = min(max(static_cast<int>(top >> 23) - 127, -112), 126) - 14;
+                        const float down = copysignf(power_of_two(-ex), a.scale);
+                        if (q == 0) factors[r] = mul_rn(power_of_two(ex), all);
+                        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)           // rows past the group's last are zeros
-                        o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
-                    *reinterpret_cast<uint4*>(at + (((q & 7) ^ (in_tile & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int k = 0; k < 4; ++k)           // rows past the group's last are zeros
+                            o[k] = r < it.rows ? pack_f16(mul_rn(__uint_as_float(v[k] << 16), down), mul_rn(__uint_as_float(v[k] & 0xFFFF0000u), down)) : 0u;
+                        *reinterpret_cast<uint4*>(at + (((q & 7) ^ (in_tile & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
                 }
             }
             if (!ok) break;
             fence_async();
             arrive(bars + kQFull);
-            load(at);
             // ---- its blocks
             for (int blk = from; blk < to; ++blk, ++n) {
                 const int st = n & 1, j0 = it.j0 + blk * kKeys;
@@ -621,6 +625,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 qk(0, st);
                 if (two) qk(1, st);
                 commit_warp<1>(el, bars + kKEmpty + st);
+                if (from + 1 == to) commit_warp<1>(el, bars + kQEmpty);
             };
             if (n & 1) start(Constant<1>());
             else start(Constant<0>());
@@ -648,13 +653,13 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 if (more) {
                     if (two) qk(1, st1);
                     commit_warp<1>(el, bars + kKEmpty + st1);
+                    if (blk + 2 == to) commit_warp<1>(el, bars + kQEmpty);      // the next item's queries may come
                 }
                 ++n;
                 return true;
             };
             for (int blk = from; ok && blk < to; ++blk) ok = n & 1 ? turn(Constant<1>(), blk) : turn(Constant<0>(), blk);
             if (!ok) break;
-            commit_warp<1>(el, bars + kQEmpty);
             ++items;
         }
         }
@@ -691,6 +696,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     const uint32_t have = there[block & 3];
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
                     const Seen seen{lo - j0, hi - j0, have};
+                    const bool fresh = blk == from;       // the maximum is this block's
+                    if (fresh) m = raised<D>(m, l, true, c, seen, s_at, o_at, false).x;
                     if (whole) {
                         uint32_t p16[kKeys / 2];
                         for (int again = 0;; ++again) {
@@ -718,15 +725,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                                 l = add_rn(l, more);
                                 break;
                             }
-                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, blk > from);
+                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, true);
                             m = x.x, l = x.y;
                         }
                         tmem_store32(s_at, p16);
                         tmem_store32(s_at + 32, p16 + 32);
                     } else {
-                        const bool need = masked_weights(m, c, seen, s_at, false) > kMostSum;
+                        const bool need = !fresh && masked_weights(m, c, seen, s_at, false) > kMostSum;
                         if (__any_sync(kFullMask, need)) {
-                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, blk > from);
+                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, true);
                             m = x.x, l = x.y;
                         }
                         l = add_rn(l, masked_weights(m, c, seen, s_at, true));
