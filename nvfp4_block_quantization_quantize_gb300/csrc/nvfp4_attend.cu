@@ -25,6 +25,8 @@
 // 630 instructions of a warp (half of them the decoding: a word of eight codes is 4 conversions), and with the registers for
 // 16 warps an SM the slots are 61 % full, the ALUs 55 to 65 %.  Tiles alone instead of pairs took 228 us, divisions to
 // find a tile's place 258, masks on every tile 187, runs shared by a CTA's warps 157.
+#include <algorithm>
+
 #include "nvfp4_attend.cuh"
 
 namespace nvfp4 {
@@ -191,11 +193,23 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                 end = i + 1 < warps ? run_start<R>(a, shares, quotient(units * (i + 1), warps)).u : units;
             }
         } else {                                          // one group a CTA
-            const Shares<Groups<R>> shares(a);
-            if (blockIdx.x < shares.total) {
-                shares.find(a, blockIdx.x, &t.b, &t.before);
+            bool some;
+            if (a.offsets) {
+                const Shares<Groups<R>> shares(a);
+                some = blockIdx.x < shares.total;
+                if (some) {
+                    shares.find(a, blockIdx.x, &t.b, &t.before);
+                    t.s = sequence<R>(a, t.b);
+                    t.group = blockIdx.x - t.before;
+                }
+            } else {                                      // every sequence has as many
+                const uint32_t groups = (a.Hq / a.cache.Hkv + R - 1) / R * a.cache.Hkv;
+                t.b = blockIdx.x / groups, t.group = blockIdx.x % groups;
                 t.s = sequence<R>(a, t.b);
-                t.group = blockIdx.x - t.before, t.before = 0;
+                some = t.s.n > 0;
+            }
+            if (some) {
+                t.before = 0;
                 const int64_t first = t.group * (kGroupCost + t.s.tiles);
                 auto at = [&](int w) {                    // the first warp of those without a tile has the group's start
                     const int x = t.s.tiles * w / kWarps;
@@ -685,11 +699,11 @@ bool two_tiles(const AttendArgs& a) {
     return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && (rows + 15) / 16 * 8 < (rows + 7) / 8 * 5;
 }
 
-// Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1000 keys of one sequence 10.7 us,
-// cut 11.2, of 32 sequences 14.5 and 20.5; 200 keys of one 7.0 and 11.1.  Not where there are more groups than kWaves
-// times the CTAs that run at once: equal runs then keep all busy (8 KV heads of 128: 64 sequences of 1024 keys 28.3 us uncut,
-// 29.8 cut, 256 of them 114 and 82; 1000 of 100 keys 499 and 89).
-constexpr int kSmall = 1024, kWaves = 2;
+// Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1000 keys of one sequence 10.3 us,
+// cut 11.0, of 32 sequences 14.2 and 20.7; 1300 keys 12.7 and 11.2, 17.2 and 22.8.  Not where there are more groups than
+// kWaves times the CTAs that run at once: equal runs then keep all busy (8 KV heads of 128: 64 sequences of 1000 keys 26.7 us
+// uncut, 29.8 cut, 256 of 1024 114 and 82; 1000 of 100 keys 499 and 89).
+constexpr int kSmall = 1200, kWaves = 2;
 
 int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
     const int64_t G = a.Hq / a.cache.Hkv;
@@ -699,7 +713,8 @@ int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
 
 // CTAs of k_attend; *split: whether runs may cut groups
 int64_t grid_of(const AttendArgs& a, int R, int* split) {
-    const int64_t cap = a.width * a.cache.page_size;
+    int64_t cap = a.width * a.cache.page_size;            // keys of a group, at most
+    if (a.window > 0) cap = std::min<int64_t>(cap, a.window + (a.ragged ? a.T : 1));
     const int64_t runs = runs_bound(a, R);
     const int64_t at_once = static_cast<int64_t>(sm_count()) * (a.cache.D <= 128 && R == 8 ? 2 : 1);
     *split = cap > kSmall || runs > kWaves * at_once;

@@ -186,29 +186,6 @@ struct Finish {
         if (a.lse) lse = l == 0.0f ? __int_as_float(0xFF800000) : mul_rn(add_rn(m, log2f(l)), kLn2);
     }
 
-    // 16 elements from element d, as two or four 32-byte pieces where the output lies on 32 bytes
-    __device__ __forceinline__ void store16(const AttendArgs& a, int64_t token, int head, int d, const uint32_t* v) const {
-        const int64_t at = (token * a.Hq + head) * a.cache.D + d;
-        float y[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] = mul_rn(__uint_as_float(v[k]), by);
-        const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-        if (a.out_dtype == NVFP4_F32) {
-            float* const p = static_cast<float*>(a.out) + at;
-#pragma unroll
-            for (int k = 0; k < 16; k += 8) store32(p + k, reinterpret_cast<const uint32_t*>(y + k), wide);
-        } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            store32(static_cast<uint16_t*>(a.out) + at, w, wide);
-        }
-        if (a.lse && d == 0) a.lse[token * a.Hq + head] = lse;
-    }
-
     // 4 elements from element d
     __device__ __forceinline__ void store(const AttendArgs& a, int64_t token, int head, int d, float* v) const {
 #pragma unroll

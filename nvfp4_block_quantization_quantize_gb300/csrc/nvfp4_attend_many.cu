@@ -14,12 +14,12 @@
 //     2^15 each of them fits f16, and no maximum is looked for.  Else it is raised to the block's, O, in tensor
 //     memory too, is rescaled and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
-// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 703 us, 1.47 PFLOP/s (of 1.92 of a large
+// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 702 us, 1.47 PFLOP/s (of 1.92 of a large
 // product; the warp-level kernel's way took 4.9 ms).  A maximum looked for in each block took 1.78 ms, one warpgroup
 // decoding keys and values 0.81 ms.  What is left is shared: without the softmax's arithmetic 713 of then 771 us, without the
 // decoding 685, with a quarter of the products 662, with none of the three 361.
 // Equal runs of blocks for each CTA, whatever the sequences; cut groups are joined by k_join.  A group costs 9 us besides
-// its blocks (1.5 us each): queries, first copies and the end are not all behind another's products.
+// its blocks (1.5 us each, a masked one 4): queries, first copies and the end are not all behind another's products.
 #include "nvfp4_attend.cuh"
 
 namespace nvfp4 {
@@ -275,11 +275,11 @@ __device__ __forceinline__ int64_t runs_of(int64_t keys, int64_t ctas) {
 
 // A CTA's run of parts of groups, as a warp walks along it (in shared memory; one lane walks).
 struct Run {
-    Spot at, end;
+    Spot at;
     Seq s;
     bool known, first, more;          // s is at.b's; nothing was done yet; there is a part: blocks at.blk .. to of at's group
 
-    __device__ __forceinline__ void look(const AttendArgs& a) {
+    __device__ __forceinline__ void look(const AttendArgs& a, const Spot& end) {
         while (true) {
             // (a run that ends where it starts, amid a group, is an empty part of it)
             more = at.b < a.B && (!at.group_of(end) || (first ? end.blk > 0 : at.blk < end.blk));
@@ -290,20 +290,20 @@ struct Run {
             ++at.b, at.rt = at.h = at.blk = 0, known = first = false;
         }
     }
-    __device__ __forceinline__ void start(const AttendArgs& a, const Spot& from, const Spot& to) {
-        at = from, end = to, known = false, first = true;
-        look(a);
+    __device__ __forceinline__ void start(const AttendArgs& a, const Spot& from, const Spot& end) {
+        at = from, known = false, first = true;
+        look(a, end);
     }
-    __device__ __forceinline__ void step(const AttendArgs& a) {
+    __device__ __forceinline__ void step(const AttendArgs& a, const Spot& end) {
         first = false;
         at.blk = at.group_of(end) ? end.blk : 0;
         if (!at.group_of(end) && ++at.h == a.cache.Hkv) {
             at.h = 0;
             if (++at.rt == s.runs / a.cache.Hkv) at.rt = 0, ++at.b, known = false;
         }
-        look(a);
+        look(a, end);
     }
-    __device__ __forceinline__ int to(const Item& it) const { return at.group_of(end) ? end.blk : it.blocks; }
+    __device__ __forceinline__ int to(const Item& it, const Spot& end) const { return at.group_of(end) ? end.blk : it.blocks; }
 };
 
 template <int D>
@@ -312,12 +312,14 @@ struct Many {
     static constexpr int tile = D / 64 * half;            // Q of a tile, K or V of a block
     static constexpr int stages = 2;                      // blocks of K, and of V
     static constexpr int q = 0, k = 2 * tile, v = k + stages * tile;
-    static constexpr int factor = v + stages * tile;      // [256] fp32
+    static constexpr int stage = v + stages * tile;       // of rows on their way out: [8 softmax warps][32 rows][128 bytes]
+    static constexpr int factor = stage + 8 * 32 * 128;   // [256] fp32
     static constexpr int bars = factor + kRows * 4;
     static constexpr int spots = bars + 256;              // where the runs of the CTA before, of this and the next start
     static constexpr int runs = spots + 3 * sizeof(Spot); // of each warp
     static constexpr int bytes = runs + kThreadsMany / 32 * sizeof(Run);
     // tensor memory: S (and P over it) of A and B, O of A and B
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     static constexpr int s_col = 0, o_col = 2 * kKeys;
     static constexpr int cols = 512;
     static_assert(2 * kKeys + 2 * D <= cols, "O of two tiles fits");
@@ -356,7 +358,7 @@ __device__ __noinline__ float2 raised(float m, float l, bool need, float c, Seen
         const uint32_t see = seen.of(q);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (see >> i & 1) top = max_nd(top, __uint_as_float(v[i]));
+            top = max_nd(top, see >> i & 1 ? __uint_as_float(v[i]) : kNone);
     }
     need = need && top > kNone;
     const float to = need ? fmaxf(m, __fmul_ru(top, c)) : m, less = exp2_approx(sub_rn(m, to));
@@ -389,7 +391,7 @@ __device__ __noinline__ float masked_weights(float m, float c, Seen seen, uint32
         const uint32_t see = seen.of(q);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float y = see >> i & 1 ? exp2_approx(__fmaf_rn(__uint_as_float(v[i]), c, -m)) : 0.0f;
+            const float x = __fmaf_rn(__uint_as_float(v[i]), c, -m), y = exp2_approx(see >> i & 1 ? x : kNone);      // (no branch)
             sum = add_rn(sum, y);
             v[i] = __float_as_uint(y);
         }
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
     __syncwarp();
     auto step = [&]() {
         __syncwarp();
-        if (lane == 0) run.step(a);
+        if (lane == 0) run.step(a, spots[2]);
         __syncwarp();
     };
     uint32_t n = 0, items = 0;                            // blocks and parts with blocks so far
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         uint32_t raws = 0;                                // copies of queries so far
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
-            const int h = run.at.h, from = run.at.blk, to = run.to(it);
+            const int h = run.at.h, from = run.at.blk, to = run.to(it, spots[2]);
             if (from == to) continue;
             const int pos0 = it.s.len - it.s.n;
             const int seen_lo = a.window > 0 ? max(0, pos0 + it.first - a.window + 1) : 0;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         uint32_t turn_b = 0;                              // blocks that tile B took part in
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
-            const int from = run.at.blk, to = run.to(it);
+            const int from = run.at.blk, to = run.to(it, spots[2]);
             if (from == to) continue;
             const bool two = it.rows > 128;
             if (!(ok = wait(bars + kQFull, items & 1, lost))) break;
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
         uint32_t turn = 0, mine = 0;                      // blocks and items that this tile took part in
         for (; ok && run.more; step()) {
             const Item it(a, run.s, run.at.rt);
-            const int h = run.at.h, from = run.at.blk, to = run.to(it);
+            const int h = run.at.h, from = run.at.blk, to = run.to(it, spots[2]);
             const int r = tile * 128 + t;
             int query, head;
             split_row(it.s.n, G, min(run.at.rt * kRows + r, it.s.n * G - 1), &query, &head);
@@ -754,24 +756,56 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 float* const part = reinterpret_cast<float*>(a.workspace) +
                                     (static_cast<int64_t>(blockIdx.x) * 2 + (from > 0 ? 0 : 1)) * kPart<D, kRows>;
                 const Finish f(a, h * G + head, h, m, l);
+                const bool wide = !complete || a.out_dtype == NVFP4_F32;
+                const int64_t row = (it.s.row0 + query) * a.Hq + h * G + head;
+                const uint64_t base = r >= it.rows ? 0
+                                      : complete   ? reinterpret_cast<uint64_t>(a.out) + row * D * (wide ? 4 : 2)
+                                                   : reinterpret_cast<uint64_t>(part + r * D);
+                const float by = complete ? f.by : 1.0f;
+                if (complete && a.lse && r < it.rows) a.lse[row] = f.lse;
+                // 128 bytes of each of the warp's rows at a time, through shared memory, so that 8 lanes write a row's (a row
+                // a lane kept the stores of 256 rows busy for 3 to 5 us)
+                uint8_t* const out = smem + M::stage + (warp - 4) * 32 * 128;
+                uint8_t* const mine = out + lane * 128;
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t v[32];
+                for (int q = 0; q < (wide ? D / 32 : D / 64); ++q) {
+                    __syncwarp();                         // the rows before are read
+#pragma unroll 1
+                    for (int half = 0; half < (wide ? 1 : 2); ++half) {
+                        uint32_t v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    if (from < to) {
-                        __syncwarp();
-                        tmem_load32(o_at + 32 * q, v);
-                        tmem_wait_load(v);
-                    }
-                    if (r < it.rows) {
-                        if (complete) {
-                            f.store16(a, it.s.row0 + query, h * G + head, 32 * q, v);
-                            f.store16(a, it.s.row0 + query, h * G + head, 32 * q + 16, v + 16);
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                        if (from < to) {
+                            __syncwarp();
+                            tmem_load32(o_at + 32 * (wide ? q : 2 * q + half), v);
+                            tmem_wait_load(v);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), by));
+                        if (wide) {
+#pragma unroll
+                            for (int p = 0; p < 8; ++p)
+                                *reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)) = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) store32(part + r * D + 32 * q + i, v + i, reinterpret_cast<uintptr_t>(a.workspace) % 32 == 0);
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * p + 2 * i]), __uint_as_float(v[8 * p + 2 * i + 1]));
+                                    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+                                }
+                                *reinterpret_cast<uint4*>(mine + ((p + 4 * half ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
                         }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int x = 4 * i + (lane >> 3);
+                        const uint64_t to_row = __shfl_sync(kFullMask, base, x);
+                        const uint4 u = *reinterpret_cast<const uint4*>(out + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+                        if (to_row) *reinterpret_cast<uint4*>(to_row + q * 128 + (lane & 7) * 16) = u;
                     }
                 }
                 if (!complete && r < it.rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
@@ -789,7 +823,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                 if (r >= it.rows) continue;
                 int query, head;
                 split_row(it.s.n, G, run.at.rt * kRows + r, &query, &head);
-                if (from == 0 && run.to(it) == it.blocks) {
+                if (from == 0 && run.to(it, spots[2]) == it.blocks) {
                     const float nan = __int_as_float(0x7FC00000);
                     const Finish f(a, h * G + head, h, 0.0f, nan);
                     for (int d = 0; d < D; d += 4) {
