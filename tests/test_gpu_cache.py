@@ -250,6 +250,9 @@ CASES = [
     ([1100 + 37 * i for i in range(30)], [129 + 7 * i for i in range(30)], 6, 3, 64, 16, "bf16", "none", {}),
     ([2048, 4096], [2048, 130], 4, 2, 64, 64, "bf16", "none", {}),
     ([1024, 1023, 1], None, 24, 1, 128, 64, "bf16", "none", {}),
+    ([1100, 30, 0], None, 256, 1, 64, 16, "bf16", "head", {}),
+    ([30000, 5, 470], None, 8, 2, 128, 64, "bf16", "head", {"window": 500}),
+    ([30000, 5, 470], [3, 5, 2], 8, 2, 64, 64, "f32", "head", {"window": 1100, "sinks": True}),
     ([1500, 1025, 1], None, 24, 1, 64, 64, "bf16", "none", {"sinks": True}),
 ]
 
