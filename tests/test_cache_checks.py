@@ -168,10 +168,11 @@ def test_workspace_that_is_an_input_is_refused(lib):
 def test_workspace_sizes(lib):
     """None for what no call may cut, more where offsets allow a sequence many rows, 0 for sizes a call refuses."""
     ws = lib.nvfp4_cache_attention_workspace
-    assert ws(4, 4, 2, 64, 4, 32, 16, 1, 0) == 0
+    assert ws(1, 4, 2, 64, 1, 32, 16, 1, 0) == 0            # (two groups: no more than run at once anywhere)
     few = ws(4, 8, 1, 128, 4, 1000, 16, 1, 0)
     assert 0 < few < ws(100, 8, 1, 128, 4, 1000, 16, 1, 1)
-    assert ws(100, 8, 1, 128, 100, 32, 16, 1, 0) == 0 < ws(100, 8, 1, 128, 100, 32, 16, 1, 1)
+    assert ws(1, 8, 1, 128, 1, 32, 16, 1, 0) == 0 < ws(100, 8, 1, 128, 1, 32, 16, 1, 1)
+    assert ws(10000, 8, 1, 128, 10000, 32, 16, 1, 0) > 0    # more groups than run at once
     for bad in ((-1, 4, 2, 64, 4, 32, 16, 1, 0), (4, 3, 2, 64, 4, 32, 16, 1, 0), (4, 4, 2, 96, 4, 32, 16, 1, 0),
                 (4, 4, 2, 64, 4, 1 << 40, 16, 1, 0), (4, 4, 2, 64, 4, 32, 0, 1, 0)):
         assert ws(*bad) == 0
