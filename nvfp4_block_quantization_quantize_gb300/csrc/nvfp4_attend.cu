@@ -12,8 +12,9 @@
 //   - O^T = V^T P^T as m16n8k16 with 16 elements times 8 rows over 16 tokens.  Its A fragment pairs
 //     tokens; two tokens' codes are interleaved four bits at a time before they are decoded.  P^T's
 //     8 x 8 blocks are turned from S^T's layout by movmatrix.
-//   - Online softmax: a row's maximum is raised only when a weight would pass 2^8 (f16 holds
-//     2^15), which a vote finds without exchanging maxima.
+//   - Online softmax: weights are made by a reference kBase below a maximum, so that small ones keep
+//     their bits in f16; it is raised only when a weight would pass 2^15, which f16 holds, and
+//     which a vote finds without exchanging maxima.
 // Work is counted in tiles of 16 tokens of a group, over all groups of all sequences, and
 // each warp takes an equal run of them, whatever the lengths: a warp finishes the groups that
 // lie in its run by itself, those that are cut between the warps of a CTA are joined in shared memory at its
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                     }
                 }
                 const bool whole = have == 3u && j0 >= all_lo && j0 + 32 <= all_hi;
-                // logits less the maximum; that is raised where a weight would pass 2^kSlack
+                // logits less the reference; that is raised where a weight would pass 2^kMost
                 float w[2][NT][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) high |= w[e][nt][k] > kSlack;
+                        for (int k = 0; k < 4; ++k) high |= w[e][nt][k] > kMost;
                 if (__any_sync(kFullMask, high)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int i = k; i < 4; i += 2)
-                                    if (w[e][nt][i] > kNone) m = max_nd(m, __fmul_ru(sc[e][nt][i], factor[nt][k]));
+                                    if (w[e][nt][i] > kNone)
+                                        m = max_nd(m, __fsub_ru(__fmul_ru(sc[e][nt][i], factor[nt][k]), kBase));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 4));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 8));
                             m = max_nd(m, __shfl_xor_sync(kFullMask, m, 16));
