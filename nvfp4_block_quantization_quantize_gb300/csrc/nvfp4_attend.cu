@@ -131,11 +131,16 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
     return r;
 }
 
-// what f16 pair h leaves of lo and hi
-__device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi) {
+// what f16 pair h leaves of lo and hi, `times` as large
+__device__ __forceinline__ uint32_t rest_f16(uint32_t h, float lo, float hi, float times = 1.0f) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_f16(sub_rn(lo, v.x), sub_rn(hi, v.y));
+    return pack_f16(mul_rn(sub_rn(lo, v.x), times), mul_rn(sub_rn(hi, v.y), times));
 }
+
+// What the first f16 leaves of an fp32 query's weight (at most 2^3 of a weight up to 2^15, 2^-25 of one that is smaller than
+// f16 holds) is rounded this many times as large, and its product divided by it: half a step is then 2^-36, not the 2^-25 at
+// which f16 ends.
+constexpr float kRestScale = 2048.0f;
 
 // A part of a cut group, as a warp leaves it: the first part of its run lies in `sums`, the last in its ring.
 struct Left {
@@ -158,7 +163,8 @@ struct Shape {
     static constexpr int bytes = ring + sums + stats + bars + kWarps * 2 * (sizeof(Place) + sizeof(Left));
 };
 
-// F32: queries and weights enter the products as two f16, and a tile's sums are added in fp32
+// F32: queries and weights enter the products as two f16 (a weight's second one kRestScale times as large), and a tile's sums
+// are added in fp32
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_attend(const AttendArgs a, int split) {
     using S = Shape<D, NT>;
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t u = pack_f16(w[e][nt][2 * k], w[e][nt][2 * k + 1]);
                             pf[e][0][nt][k] = turn8x8(u);
-                            if (F32) pf[e][kParts - 1][nt][k] = turn8x8(rest_f16(u, w[e][nt][2 * k], w[e][nt][2 * k + 1]));
+                            if (F32) pf[e][kParts - 1][nt][k] = turn8x8(rest_f16(u, w[e][nt][2 * k], w[e][nt][2 * k + 1], kRestScale));
                         }
                     }
                 // O^T: this lane's tokens are c, c + 4, c + 8 and c + 12, its words of 8 elements r * kUnits ..
@@ -574,11 +580,12 @@ __global__ void __launch_bounds__(kWarps * 32, D <= 128 && NT == 1 ? 2 : 1) k_at
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 if (F32) {
-                                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                    mma_f16(part, f, pf[e][0][nt][0], pf[e][0][nt][1]);
+                                    mma_f16(rest, f, pf[e][kParts - 1][nt][0], pf[e][kParts - 1][nt][1]);
 #pragma unroll
-                                    for (int p = kParts - 1; p >= 0; --p) mma_f16(part, f, pf[e][p][nt][0], pf[e][p][nt][1]);
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) o[nt][4 * i + j][k] = add_rn(o[nt][4 * i + j][k], part[k]);
+                                    for (int k = 0; k < 4; ++k)
+                                        o[nt][4 * i + j][k] = add_rn(o[nt][4 * i + j][k], __fmaf_rn(rest[k], 1.0f / kRestScale, part[k]));
                                 } else {
                                     mma_f16(o[nt][4 * i + j], f, pf[e][0][nt][0], pf[e][0][nt][1]);
                                 }

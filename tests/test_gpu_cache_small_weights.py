@@ -49,3 +49,11 @@ def test_bf16_queries(shape, gap):
     """A weight as one f16, the largest at 2^11 or above when the reference is set: half a step of 2^-25 is 2^-36 of it."""
     n, Hq, H, D, L = shape
     check("bf16", n, Hq, H, D, L, gap, 2.0 ** -36)
+
+
+@pytest.mark.parametrize("gap", [9.0, 15.0, 18.0, 24.0])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_fp32_queries(shape, gap):
+    """Weights as two f16, the second scaled before it is rounded: half a step of 2^-47 of the largest weight."""
+    n, Hq, H, D, L = shape
+    check("f32", n, Hq, H, D, L, gap, 2.0 ** -47)
