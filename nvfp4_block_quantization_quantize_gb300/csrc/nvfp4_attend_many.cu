@@ -10,11 +10,12 @@
 //   - One warp issues the products: S of tile A, S of B, then for each block O of a tile and its next S.
 //     While one tile's softmax runs the other's products do.
 //   - A softmax warpgroup a tile, a thread a row: S out of tensor memory, weights back as f16 over S,
-//     which P V reads from there.  Weights are made by the maximum as it stands: while a block's sum is at most
-//     2^15 each of them fits f16, and no maximum is looked for.  Else it is raised to the block's, O, in tensor
-//     memory too, is rescaled and the block's weights are made again.
+//     which P V reads from there.  Weights are made by a reference as it stands: while a block's sum is at
+//     most 65504 each of them fits f16, and no maximum is looked for.  Else, or where so little is left of
+//     them that f16 would lose bits, the reference is moved to the block's maximum, O, in tensor memory
+//     too, is rescaled and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
-// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 702 us, 1.47 PFLOP/s (of 1.92 of a large
+// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 716 us, 1.44 PFLOP/s (of 1.92 of a large
 // product; the warp-level kernel's way took 4.9 ms).  A maximum looked for in each block took 1.78 ms, one warpgroup
 // decoding keys and values 0.81 ms.  What is left is shared: without the softmax's arithmetic 713 of then 771 us, without the
 // decoding 685, with a quarter of the products 662, with none of the three 361.
@@ -331,7 +332,18 @@ __device__ __forceinline__ uint32_t columns(int from, int to) {
     return from >= 32 ? 0u : from <= 0 ? below : below & ~((1u << from) - 1u);
 }
 
-constexpr float kMostSum = 32768.0f;                      // of a block's weights: each fits f16
+// A row's reference stands kBaseMany below the largest logit of the block that it is set by.  It is raised where a block's
+// weights add up to more than kMostSum (each of them fits f16), and lowered where they add up to less than kLeastSum: half a
+// step of f16's small values, 2^-25, of 128 weights is then at most 2^-9 of their sum, and 2^-27 of the largest weight of the
+// block that sets the reference.  It is lowered by at most kDrop and not past a denominator of kFar, so that sums stay
+// far inside fp32.  2 x 2048 queries on 16384 keys: 698 us with a base of 0 and never lowered, 712 with 4, 733 with 6, 757 with
+// 7 (more rows are raised); lowered below 2^-9, with 2, 716, with 3 729; below 2^-6, with 3, 725, with 4 749.
+constexpr float kBaseMany = 2.0f, kMostSum = 65504.0f, kLeastSum = 0.001953125f, kDrop = 40.0f, kFar = 16777216.0f;
+
+// whether a block's sum is outside [kLeastSum, kMostSum] (positive floats compare as their bits; a NaN or 0 is outside too)
+__device__ __forceinline__ bool misplaced(float sum) {
+    return __float_as_uint(sum) - __float_as_uint(kLeastSum) > __float_as_uint(kMostSum) - __float_as_uint(kLeastSum);
+}
 
 // The keys of a block that a row sees: from lo to hi, relative to the block, of tiles that have a page.
 struct Seen {
@@ -343,11 +355,11 @@ struct Seen {
     }
 };
 
-// The maximum of this thread's row raised to that of the block, l and the row of O rescaled, for the rows of a warp that
-// need it (the others keep theirs): (maximum, l).  The maximum is rounded up, so that no logit exceeds it.  Out of line: it
-// runs for the first blocks of a group.
+// The reference of this thread's row moved to kBaseMany below the block's largest logit, l and the row of O rescaled, for the
+// rows of a warp that need it (the others keep theirs): (reference, l).  It is rounded up, so that no weight exceeds 2^kBaseMany.
+// Out of line: it runs for the first blocks of a group, and where logits change by many orders.
 template <int D>
-__device__ __noinline__ float2 raised(float m, float l, bool need, float c, Seen seen, uint32_t s_at, uint32_t o_at, bool sums) {
+__device__ __noinline__ float2 moved(float m, float l, bool need, float c, Seen seen, uint32_t s_at, uint32_t o_at, bool sums) {
     float top = kNone;
 #pragma unroll 1
     for (int q = 0; q < kKeys / 32; ++q) {
@@ -361,7 +373,8 @@ __device__ __noinline__ float2 raised(float m, float l, bool need, float c, Seen
             top = max_nd(top, see >> i & 1 ? __uint_as_float(v[i]) : kNone);
     }
     need = need && top > kNone;
-    const float to = need ? fmaxf(m, __fmul_ru(top, c)) : m, less = exp2_approx(sub_rn(m, to));
+    const float least = l < kFar ? sub_rn(m, kDrop) : m;
+    const float to = need ? fmaxf(least, __fsub_ru(__fmul_ru(top, c), kBaseMany)) : m, less = exp2_approx(sub_rn(m, to));
     if (sums) {
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -698,8 +711,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     const uint32_t have = there[block & 3];
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
                     const Seen seen{lo - j0, hi - j0, have};
-                    const bool fresh = blk == from;       // the maximum is this block's
-                    if (fresh) m = raised<D>(m, l, true, c, seen, s_at, o_at, false).x;
+                    const bool fresh = blk == from;       // the reference is this block's
+                    if (fresh) m = moved<D>(m, l, true, c, seen, s_at, o_at, false).x;
                     if (whole) {
                         uint32_t p16[kKeys / 2];
                         for (int again = 0;; ++again) {
@@ -723,19 +736,20 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                             float a0, a1;
                             unpack2(sum, a0, a1);
                             const float more = add_rn(a0, a1);
-                            if (again || !__any_sync(kFullMask, more > kMostSum)) {
+                            if (again || !__any_sync(kFullMask, misplaced(more))) {
                                 l = add_rn(l, more);
                                 break;
                             }
-                            const float2 x = raised<D>(m, l, more > kMostSum, c, seen, s_at, o_at, true);
+                            const float2 x = moved<D>(m, l, misplaced(more), c, seen, s_at, o_at, true);
                             m = x.x, l = x.y;
                         }
                         tmem_store32(s_at, p16);
                         tmem_store32(s_at + 32, p16 + 32);
                     } else {
-                        const bool need = !fresh && masked_weights(m, c, seen, s_at, false) > kMostSum;
+                        const float some = fresh ? 0.0f : masked_weights(m, c, seen, s_at, false);
+                        const bool need = some != 0.0f && misplaced(some);      // (a row that sees nothing here has no weights)
                         if (__any_sync(kFullMask, need)) {
-                            const float2 x = raised<D>(m, l, need, c, seen, s_at, o_at, true);
+                            const float2 x = moved<D>(m, l, need, c, seen, s_at, o_at, true);
                             m = x.x, l = x.y;
                         }
                         l = add_rn(l, masked_weights(m, c, seen, s_at, true));
