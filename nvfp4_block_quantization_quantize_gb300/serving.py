@@ -80,7 +80,8 @@ class FP4Projection:
 class FP4Attention:
     """A layer's attention over a paged cache in NVFP4: queries, keys and values of norm(x + hidden) by one
     projection, norms of their heads and rotation with the keys' and values' way into the cache, attention, and the
-    projection back.
+    projection back.  Between the products all is held in x's type, float32 or bfloat16 (bf16 prompts take the tensor-memory
+    kernel, fp32 ones the warp-level one).
 
     qkv [(q_heads + 2 kv_heads) * head_dim, D] (queries, then keys, then values), out [D, q_heads * head_dim];
     head_dim 64, 128 or 256, D a multiple of 64.  q_norm, k_norm: weights [head_dim] of the heads' norms, or None;
@@ -107,13 +108,14 @@ class FP4Attention:
         slots, positions [M]: where each token goes in the cache, and where it stands; pages [B, width], lengths [B] (these
         tokens among them) and offsets as nvfp4_cache_attention takes them."""
         M, H, Hk = x.shape[0], self.q_heads, self.kv_heads
-        y, hidden = self.qkv(x, hidden, "bf16")
+        dt = "f32" if x.dtype == torch.float32 else "bf16"
+        y, hidden = self.qkv(x, hidden, dt)
         y = y.view(M, H + 2 * Hk, self.head_dim)
         q = nvfp4_qk_norm_rope(y[:, :H], y[:, H:H + Hk], positions, cache=cache, v=y[:, H + Hk:], slots=slots, **self.rope,
                                **self.gamax)["q"]
-        o = nvfp4_cache_attention(q, cache, pages, lengths, offsets=offsets, window=self.window, sinks=self.sinks, **self.gamax)
-        out = self.back.product(o.view(M, H * self.head_dim), "f32" if x.dtype == torch.float32 else "bf16")
-        return out, hidden
+        o = nvfp4_cache_attention(q, cache, pages, lengths, offsets=offsets, window=self.window, sinks=self.sinks, out_dtype=dt,
+                                  **self.gamax)
+        return self.back.product(o.view(M, H * self.head_dim), dt), hidden
 
 
 class FP4Experts:
