@@ -7,7 +7,8 @@
 // its first rotary_dim elements turn to m (a cos t - b sin t, b cos t + a sin t), t = 2 pi *
 // position * phase / 2^64.  The phase is a whole number of 2^-64 turns, so position * phase wraps
 // exactly where whole turns drop out: a far position loses nothing (the angle's error is the
-// phase's rounding times the position, 2^-64 turns each).  The turn left is rounded to 2^-32.
+// phase's rounding times the position, 2^-65 turns each).  Of the turn left whole quarters drop out exactly too, and
+// the rest is rounded to fp32: sines and cosines next to zero keep their relative accuracy.
 // Each element is read once and written once, ten to twenty operations each:
 // bound by memory, by latency for a few tokens.
 //   - A thread holds 16 elements of a head: 8 pairs.  With the pairs' halves apart (half layout) they
@@ -145,12 +146,18 @@ __global__ void __launch_bounds__(kHeadsThreads, DT == NVFP4_BF16 && !(TURN != k
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint64_t turn = pos * __ldg(reinterpret_cast<const unsigned long long*>(a.phases) + 8 * t + i);
-            // the nearest of 2^32 parts of a turn, in [-1/2, 1/2), as half turns
-            const int32_t part = static_cast<int32_t>((turn + 0x80000000ull) >> 32);
-            float sine, cosine;
-            sincospif(mul_rn(static_cast<float>(part), 4.656612873077393e-10f), &sine, &cosine);     // 2^-31
-            cs[i] = mul_rn(cosine, a.magnitude);
-            sn[i] = mul_rn(sine, a.magnitude);
+            // whole quarters of a turn drop out exactly; what is left, at most 1/8 turn, in fp32: its nearest whole number of 2^32
+            // and the rest of that, each rounded by 2^-24 at most (a conversion of 64 bits takes longer: a token 3.08 us)
+            const uint64_t quarter = (turn + (1ull << 61)) >> 62, left = turn - (quarter << 62);
+            const float high = static_cast<float>(static_cast<int32_t>((left + 0x80000000ull) >> 32));
+            const float low = static_cast<float>(static_cast<int32_t>(left));
+            float s0, c0;
+            sincospif(mul_rn(__fmaf_rn(high, 4294967296.0f, low), 1.0842021724855044e-19f), &s0, &c0);      // 2^-63: in half turns
+            const float sine = quarter & 1 ? c0 : s0, cosine = quarter & 1 ? s0 : c0;
+            const uint32_t q = static_cast<uint32_t>(quarter);
+            const uint32_t sine_down = q << 30 & 0x80000000u, cosine_down = (q + 1) << 30 & 0x80000000u;      // their sign bits
+            cs[i] = mul_rn(__uint_as_float(__float_as_uint(cosine) ^ cosine_down), a.magnitude);
+            sn[i] = mul_rn(__uint_as_float(__float_as_uint(sine) ^ sine_down), a.magnitude);
         }
     }
     Place place{nullptr, 0};
