@@ -31,11 +31,14 @@ that write.
 from __future__ import annotations
 
 import ctypes
+import decimal
+import functools
 import importlib
 import math
 import os
 import threading
 import warnings
+from decimal import Decimal
 
 import torch
 
@@ -1140,6 +1143,23 @@ def nvfp4_grouped_mm(codes_a: torch.Tensor, scales_a: torch.Tensor, offsets: tor
 
 # ---- a cache of keys and values ---------------------------------------------------------------
 # Serving operators as well: device tensors, a given stream, no gradient.
+@functools.lru_cache(maxsize=None)
+def _pi():
+    """pi to 400 digits: 16 arctan(1/5) - 4 arctan(1/239) (Machin)."""
+    one = 10 ** 420
+
+    def arctan(n):                              # of 1 / n, in units of 1 / one
+        power, total, k = one // n, 0, 0
+        while power:
+            total += (-power if k & 1 else power) // (2 * k + 1)
+            power //= n * n
+            k += 1
+        return total
+
+    with decimal.localcontext(decimal.Context(prec=400)):
+        return Decimal(16 * arctan(5) - 4 * arctan(239)) / one
+
+
 def nvfp4_rope_phases(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0, method: str = "linear",
                       original: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0, inv_freq=None,
                       device=None) -> torch.Tensor:
@@ -1150,41 +1170,50 @@ def nvfp4_rope_phases(rotary_dim: int, base: float = 10000.0, *, factor: float =
     that the slowest pair is divided by it and the fastest stays; "yarn" divides the pairs that turn fewer than
     beta_slow times in `original` positions, leaves those that turn more than beta_fast times, and goes from one to the
     other along the pairs in between (its magnitude, 0.1 ln(factor) + 1, is the caller's to pass).  Made once for a
-    model, in 64 bits."""
+    model, on the host unless `device` says otherwise; each is the nearest whole number of 2^-64 turns, since a far
+    position multiplies what it is off by."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("nvfp4_rope_phases: rotary_dim must be even and positive")
     if not factor >= 1.0 or not math.isfinite(factor):
         raise ValueError("nvfp4_rope_phases: factor must be at least 1")
     half = rotary_dim // 2
     if inv_freq is not None:
-        freq = [float(f) for f in inv_freq]
-        if len(freq) != half:
+        given = [float(f) for f in inv_freq]
+        if len(given) != half:
             raise ValueError(f"nvfp4_rope_phases: inv_freq must hold {half} values")
+        if not all(math.isfinite(f) for f in given):
+            raise ValueError("nvfp4_rope_phases: frequencies must be finite")
         if method == "ntk":
             raise ValueError("nvfp4_rope_phases: ntk takes a base, not inv_freq")
-    elif not base > 0.0:
-        raise ValueError("nvfp4_rope_phases: base must be positive")
-    else:
-        if method == "ntk" and half > 1:
-            base = base * factor ** (half / (half - 1))
-        freq = [base ** (-2 * i / rotary_dim) for i in range(half)]
-    if method == "linear":
-        freq = [f / factor for f in freq]
-    elif method == "yarn":
-        if not original or original <= 0 or not beta_fast > beta_slow > 0 or not base > 1.0:
-            raise ValueError("nvfp4_rope_phases: yarn needs original > 0, beta_fast > beta_slow > 0 and a base above 1")
-
-        def pair(turns):                        # the pair that makes so many turns in `original` positions
-            return half * math.log(original / (turns * 2 * math.pi)) / math.log(base)
-
-        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rotary_dim - 1)
-        keep = [1.0 - min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(half)]
-        freq = [f * k + f / factor * (1.0 - k) for f, k in zip(freq, keep)]
-    elif method != "ntk":
+    elif not 0.0 < base < math.inf:
+        raise ValueError("nvfp4_rope_phases: base must be positive and finite")
+    if method not in ("linear", "ntk", "yarn"):
         raise ValueError(f"nvfp4_rope_phases: method {method!r}; expected linear, ntk or yarn")
-    if not all(math.isfinite(f) for f in freq):
-        raise ValueError("nvfp4_rope_phases: frequencies must be finite")
-    turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) % (1 << 64) for f in freq]
+    if method == "yarn" and (not original or original <= 0 or not beta_fast > beta_slow > 0 or not base > 1.0):
+        raise ValueError("nvfp4_rope_phases: yarn needs original > 0, beta_fast > beta_slow > 0 and a base above 1")
+    # digits: 60, and those of the largest frequency, whose whole turns drop out
+    large = max([1.0] + [abs(f) for f in given]) if inv_freq is not None else max(1.0, 1.0 / base)
+    with decimal.localcontext(decimal.Context(prec=60 + math.ceil(math.log10(min(large, 1e308))) + 16)):
+        by, base = Decimal(float(factor)), float(base)
+        if inv_freq is not None:
+            freq = [Decimal(f) for f in given]
+        else:
+            step = -2 / Decimal(rotary_dim) * Decimal(base).ln()            # of one pair's logarithm to the next's
+            if method == "ntk" and half > 1:
+                step -= by.ln() / (half - 1)
+            freq = [(i * step).exp() for i in range(half)]
+        if method == "linear":
+            freq = [f / by for f in freq]
+        elif method == "yarn":
+            def pair(turns):                    # the pair that makes so many turns in `original` positions
+                return half * math.log(original / (turns * 2 * math.pi)) / math.log(base)
+
+            low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rotary_dim - 1)
+            wide = Decimal(high - low) if high > low else Decimal("0.001")
+            keep = [1 - min(max((i - low) / wide, 0), 1) for i in range(half)]
+            freq = [f * k + f / by * (1 - k) for f, k in zip(freq, keep)]
+        unit = Decimal(1 << 64) / (2 * _pi())
+        turns = [int((f * unit).to_integral_value()) % (1 << 64) for f in freq]
     return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
