@@ -514,7 +514,8 @@ int nvfp4_qk_norm_rope(const void* q, const void* k, const void* v, int64_t T, i
     if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16)
         return fail(NVFP4_EINVAL, "rotary_dim must be a multiple of 16 up to D (got %lld)", (long long)rotary_dim);
     if ((q_weight == nullptr) != (k_weight == nullptr)) return fail(NVFP4_EINVAL, "give both q_weight and k_weight, or neither");
-    if (cached != (cache != nullptr) || cached != (v != nullptr) || cached == (k_out != nullptr)) {
+    // (a cache without pages has no memory: every slot lies outside it)
+    if ((cached ? cache == nullptr && pages != 0 : cache != nullptr) || cached != (v != nullptr) || cached == (k_out != nullptr)) {
         if (T > 0 && Hkv > 0) return fail(NVFP4_EINVAL, "give v, cache and slots and no k_out, or k_out and none of them");
     }
     if (cached) {
