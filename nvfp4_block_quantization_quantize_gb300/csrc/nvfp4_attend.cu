@@ -708,11 +708,21 @@ bool two_tiles(const AttendArgs& a) {
     return a.dtype == NVFP4_BF16 && a.cache.D <= 128 && (rows + 15) / 16 * 8 < (rows + 7) / 8 * 5;
 }
 
-// Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1000 keys of one sequence 10.3 us,
-// cut 11.0, of 32 sequences 14.2 and 20.7; 1300 keys 12.7 and 11.2, 17.2 and 22.8.  Not where there are more groups than
-// kWaves times the CTAs that run at once: equal runs then keep all busy (8 KV heads of 128: 64 sequences of 1000 keys 26.7 us
-// uncut, 29.8 cut, 256 of 1024 114 and 82; 1000 of 100 keys 499 and 89).
+// Keys up to which a group is not cut, but has a CTA of its own and no k_join after it: 1020 keys of one sequence 10.3 us,
+// cut 11.7, of 32 sequences 13.9 and 20.5; 1200 keys 11.5 and 11.7, 16.0 and 22.5; 1300 keys 12.6 and 11.7 (8 KV heads of 128,
+// bf16).  Heads of 512 bytes and more take longer a tile, so that few groups (up to half of the CTAs that run at once with
+// heads of 256, an eighth of twice as many with 128) are cut earlier: of fp32 128, 1020 keys of one sequence take 13.4 and 13.4,
+// 1060 14.8 and 13.4, of 8 16.4 and 17.6, of 32 21.7 and 26.1; of bf16 256 1020 keys 14.0 and 14.0, 1060 14.6 and 14.1, of
+// 16 15.4 and 18.9; of fp32 256 760 keys 16.0 and 16.9, 900 18.4 and 17.0, of 16 19.1 and 23.1.  Not
+// where there are more groups than kWaves times the CTAs that run at once: equal runs then keep all busy (8 KV heads of 128: 64
+// sequences of 1020 keys 26.5 us uncut, 29.7 cut, 256 of 1024 114 and 82; 1000 of 100 keys 499 and 89).
 constexpr int kSmall = 1200, kWaves = 2;
+
+int small_keys(const AttendArgs& a, int64_t runs, int64_t at_once) {
+    const int bytes = a.cache.D * (a.dtype == NVFP4_F32 ? 4 : 2);
+    if (bytes <= 256 || runs > at_once / (a.cache.D <= 128 ? 8 : 2)) return kSmall;
+    return bytes <= 512 ? 1024 : 768;
+}
 
 int64_t runs_bound(const AttendArgs& a, int R) {          // groups, at most
     const int64_t G = a.Hq / a.cache.Hkv;
@@ -726,7 +736,7 @@ int64_t grid_of(const AttendArgs& a, int R, int* split) {
     if (a.window > 0) cap = std::min<int64_t>(cap, a.window + (a.ragged ? a.T : 1));
     const int64_t runs = runs_bound(a, R);
     const int64_t at_once = static_cast<int64_t>(sm_count()) * (a.cache.D <= 128 && R == 8 ? 2 : 1);
-    *split = cap > kSmall || runs > kWaves * at_once;
+    *split = cap > small_keys(a, runs, at_once) || runs > kWaves * at_once;
     return *split ? at_once : runs;
 }
 
