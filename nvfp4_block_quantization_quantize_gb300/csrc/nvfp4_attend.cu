@@ -21,9 +21,9 @@
 // end, and those cut between CTAs leave partial sums in the workspace, which k_join adds in
 // order.  A warp works on pairs of tiles; its own ring of shared memory is filled by bulk copies,
 // one or two a pair, that run ahead across groups.
-// Measured: 64 sequences of 512 to 32768 keys, 8 KV heads of 128 and 64 query heads (655 MB), 128 us, 5.1 TB/s of the 6.7 of a
-// copy; one sequence of 131072 keys (151 MB) 45 us, one of 200 6.8 us.  Bound by issue and latency: a pair of tiles takes some
-// 630 instructions of a warp (half of them the decoding: a word of eight codes is 4 conversions), and with the registers for
+// Measured: 64 sequences of 512 to 32768 keys, 8 KV heads of 128 and 64 query heads (655 MB), 131 us, 5.0 TB/s of the 6.7 of a
+// copy; one sequence of 131072 keys (151 MB) 46 us, one of 200 6.4 us.  Bound by issue and latency: a pair of tiles takes some
+// 650 instructions of a warp (half of them the decoding: a word of eight codes is 4 conversions), and with the registers for
 // 16 warps an SM the slots are 61 % full, the ALUs 55 to 65 %.  Tiles alone instead of pairs took 228 us, divisions to
 // find a tile's place 258, masks on every tile 187, runs shared by a CTA's warps 157.
 #include <algorithm>

@@ -12,10 +12,10 @@
 //   - A softmax warpgroup a tile, a thread a row: S out of tensor memory, weights back as f16 over S,
 //     which P V reads from there.  Weights are made by a reference as it stands: while a block's sum is at
 //     most 65504 each of them fits f16, and no maximum is looked for.  Else, or where so little is left of
-//     them that f16 would lose bits, the reference is moved to the block's maximum, O, in tensor memory
-//     too, is rescaled and the block's weights are made again.
+//     them that f16 would lose bits, the reference is moved by the sum, O, in tensor memory too, is rescaled
+//     and the block's weights are made again.
 // Queries enter as f16 scaled by a power of two for each row, as in the other kernel.
-// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 716 us, 1.44 PFLOP/s (of 1.92 of a large
+// Measured: the last 2048 queries of 2 sequences of 16384 keys, 32 heads of 128 over 8, causal: 702 us, 1.47 PFLOP/s (of 1.92 of a large
 // product; the warp-level kernel's way took 4.9 ms).  A maximum looked for in each block took 1.78 ms, one warpgroup
 // decoding keys and values 0.81 ms.  What is left is shared: without the softmax's arithmetic 713 of then 771 us, without the
 // decoding 685, with a quarter of the products 662, with none of the three 361.
@@ -189,7 +189,7 @@ __device__ __forceinline__ void unrolled(F f) {           // f(0) .. f(N - 1), e
 }
 
 // The work of a sequence, in keys that its groups of 256 rows are to look at: w0 + rt * step a group of row tile rt (the
-// first kGroupKeys for what it costs besides: a prompt of 8192 queries, 32 heads of 128 over 8, takes 804 us with 256, 589 with
+// first kGroupKeys for what it costs besides: a prompt of 8192 queries, 32 heads of 128 over 8, took 804 us with 256, 589 with
 // 512, 478 with 768, 465 with 1024; of 2048 91, 85, 83, 85).  With a causal mask the row tiles look at more and more; that they look at whole
 // blocks, and a window cuts off the first keys, is not counted.
 constexpr int kGroupKeys = 768;
@@ -332,17 +332,21 @@ __device__ __forceinline__ uint32_t columns(int from, int to) {
     return from >= 32 ? 0u : from <= 0 ? below : below & ~((1u << from) - 1u);
 }
 
-// A row's reference stands kBaseMany below the largest logit of the block that it is set by.  It is raised where a block's
-// weights add up to more than kMostSum (each of them fits f16), and lowered where they add up to less than kLeastSum: half a
-// step of f16's small values, 2^-25, of 128 weights is then at most 2^-9 of their sum, and 2^-27 of the largest weight of the
-// block that sets the reference.  It is lowered by at most kDrop and not past a denominator of kFar, so that sums stay
-// far inside fp32.  2 x 2048 queries on 16384 keys: 698 us with a base of 0 and never lowered, 712 with 4, 733 with 6, 757 with
-// 7 (more rows are raised); lowered below 2^-9, with 2, 716, with 3 729; below 2^-6, with 3, 725, with 4 749.
-constexpr float kBaseMany = 2.0f, kMostSum = 65504.0f, kLeastSum = 0.001953125f, kDrop = 40.0f, kFar = 16777216.0f;
+// A row's reference stands kBaseMany below the largest logit of its first block.  It is raised where a block's weights add up to
+// more than kMostSum (each of them fits f16), so that they add up to 2^kUpSum, and lowered where they add up to less than kLeastSum,
+// so that they add up to 2^kDownSum: half a step of f16's small values, 2^-25, of 128 weights is then at most 2^-9 of a
+// block's sum, and 2^-29 of the largest weight of a block that sets or raises the reference.  It is lowered by at most kDrop, and
+// where the denominator is below kFar, so that sums stay far inside fp32.  A call of 2 x 2048 queries on 16384 keys, logits spread by
+// 3 nats / by 6 / by 12: 717, 832 and 1040 us with a base of 0, raised to the largest logit and never lowered; 726, 1134 and 1406
+// lowered to it too; by sums 714, 932 and 1117 (a base of 2 716, 6 731, 8 778; lowered below 2^-12 709, 879 and 1109).
+constexpr float kBaseMany = 4.0f, kMostSum = 65504.0f, kLeastSum = 0.001953125f, kUpSum = 12.0f, kDownSum = -2.0f;
+constexpr float kDrop = 24.0f, kFar = 16777216.0f;
 
-// whether a block's sum is outside [kLeastSum, kMostSum] (positive floats compare as their bits; a NaN or 0 is outside too)
-__device__ __forceinline__ bool misplaced(float sum) {
-    return __float_as_uint(sum) - __float_as_uint(kLeastSum) > __float_as_uint(kMostSum) - __float_as_uint(kLeastSum);
+// Whether the reference is to be moved for a block's sum: the sum is outside [kLeastSum, kMostSum], and l, where the sum is low, below
+// kFar.  (Positive floats compare as their bits; l stays below 2^49, since it is below kFar when it is scaled up by 2^kDrop.)
+__device__ __forceinline__ bool misplaced(float sum, float l) {
+    const uint32_t x = __float_as_uint(fmaxf(sum, mul_rn(l, kLeastSum / kFar)));
+    return x - __float_as_uint(kLeastSum) > __float_as_uint(kMostSum) - __float_as_uint(kLeastSum);
 }
 
 // The keys of a block that a row sees: from lo to hi, relative to the block, of tiles that have a page.
@@ -355,11 +359,8 @@ struct Seen {
     }
 };
 
-// The reference of this thread's row moved to kBaseMany below the block's largest logit, l and the row of O rescaled, for the
-// rows of a warp that need it (the others keep theirs): (reference, l).  It is rounded up, so that no weight exceeds 2^kBaseMany.
-// Out of line: it runs for the first blocks of a group, and where logits change by many orders.
-template <int D>
-__device__ __noinline__ float2 moved(float m, float l, bool need, float c, Seen seen, uint32_t s_at, uint32_t o_at, bool sums) {
+// The largest logit of a row's block (kNone if it sees none).
+__device__ __forceinline__ float largest(Seen seen, uint32_t s_at) {
     float top = kNone;
 #pragma unroll 1
     for (int q = 0; q < kKeys / 32; ++q) {
@@ -372,22 +373,39 @@ __device__ __noinline__ float2 moved(float m, float l, bool need, float c, Seen 
         for (int i = 0; i < 32; ++i)
             top = max_nd(top, see >> i & 1 ? __uint_as_float(v[i]) : kNone);
     }
-    need = need && top > kNone;
-    const float least = l < kFar ? sub_rn(m, kDrop) : m;
-    const float to = need ? fmaxf(least, __fsub_ru(__fmul_ru(top, c), kBaseMany)) : m, less = exp2_approx(sub_rn(m, to));
-    if (sums) {
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-            uint32_t v[32];
-            __syncwarp();
-            tmem_load32(o_at + 32 * q, v);
-            tmem_wait_load(v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
-            tmem_store32(o_at + 32 * q, v);
-        }
-        tmem_wait_store();
+    return top;
+}
+
+// The reference that a row's first block sets.  Rounded up, so that no weight exceeds 2^kBaseMany.
+__device__ __noinline__ float first_reference(float m, float c, Seen seen, uint32_t s_at) {
+    const float top = largest(seen, s_at);
+    return top > kNone ? __fsub_ru(__fmul_ru(top, c), kBaseMany) : m;
+}
+
+// The reference of this thread's row moved so that the block's weights, which add up to `sum`, will add up to 2^kUpSum or
+// 2^kDownSum, l and the row of O rescaled, for the rows of a warp that need it (the others keep theirs): (reference, l).
+// Out of line: it runs where logits change by many orders.
+template <int D>
+__device__ __noinline__ float2 moved(float m, float l, float sum, float c, Seen seen, uint32_t s_at, uint32_t o_at) {
+    const bool need = misplaced(sum, l), past = need && sum == -kNone;
+    float to = m;
+    if (need) to = fmaxf(sub_rn(m, kDrop), __fadd_ru(m, log2f(sum) - (sum > 1.0f ? kUpSum : kDownSum)));
+    if (__any_sync(kFullMask, past)) {                    // past fp32: by the largest
+        const float top = largest(seen, s_at);
+        if (past) to = fmaxf(m, __fsub_ru(__fmul_ru(top, c), kBaseMany));
     }
+    const float less = exp2_approx(sub_rn(m, to));
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_load32(o_at + 32 * q, v);
+        tmem_wait_load(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(mul_rn(__uint_as_float(v[i]), less));
+        tmem_store32(o_at + 32 * q, v);
+    }
+    tmem_wait_store();
     __syncwarp();
     return make_float2(to, mul_rn(l, less));
 }
@@ -712,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                     const bool whole = __all_sync(kFullMask, have == 0xFFu && j0 >= lo && j0 + kKeys <= hi);
                     const Seen seen{lo - j0, hi - j0, have};
                     const bool fresh = blk == from;       // the reference is this block's
-                    if (fresh) m = moved<D>(m, l, true, c, seen, s_at, o_at, false).x;
+                    if (fresh) m = first_reference(m, c, seen, s_at);
                     if (whole) {
                         uint32_t p16[kKeys / 2];
                         for (int again = 0;; ++again) {
@@ -736,20 +754,20 @@ __global__ void __launch_bounds__(kThreadsMany, 1) k_attend_many(const AttendArg
                             float a0, a1;
                             unpack2(sum, a0, a1);
                             const float more = add_rn(a0, a1);
-                            if (again || !__any_sync(kFullMask, misplaced(more))) {
+                            if (again || !__any_sync(kFullMask, misplaced(more, l))) {
                                 l = add_rn(l, more);
                                 break;
                             }
-                            const float2 x = moved<D>(m, l, misplaced(more), c, seen, s_at, o_at, true);
+                            const float2 x = moved<D>(m, l, more, c, seen, s_at, o_at);
                             m = x.x, l = x.y;
                         }
                         tmem_store32(s_at, p16);
                         tmem_store32(s_at + 32, p16 + 32);
                     } else {
-                        const float some = fresh ? 0.0f : masked_weights(m, c, seen, s_at, false);
-                        const bool need = some != 0.0f && misplaced(some);      // (a row that sees nothing here has no weights)
-                        if (__any_sync(kFullMask, need)) {
-                            const float2 x = moved<D>(m, l, need, c, seen, s_at, o_at, true);
+                        float some = fresh ? 1.0f : masked_weights(m, c, seen, s_at, false);
+                        if (some == 0.0f) some = 1.0f;        // a row that sees nothing here: its reference stays
+                        if (__any_sync(kFullMask, misplaced(some, l))) {
+                            const float2 x = moved<D>(m, l, some, c, seen, s_at, o_at);
                             m = x.x, l = x.y;
                         }
                         l = add_rn(l, masked_weights(m, c, seen, s_at, true));

@@ -65,10 +65,10 @@ def test_fp32_queries(shape, gap):
 @pytest.mark.parametrize("gap", [9.0, 15.0, 18.0])
 @pytest.mark.parametrize("shape", [(300, 2, 1, 128, 4000), (70, 8, 2, 64, 6000), (520, 4, 4, 128, 3333)])
 def test_many_bf16_queries(shape, gap):
-    """The tensor-memory kernel: half a step of 2^-25 is 2^-27 of the largest weight in its block of 128 keys, and 2^-9 of any other
+    """The tensor-memory kernel: half a step of 2^-25 is 2^-29 of the largest weight in its block of 128 keys, and 2^-9 of any other
     block's sum."""
     n, Hq, H, D, L = shape
-    check("bf16", n, Hq, H, D, L, gap, 2.0 ** -27, near=128, share=2.0 ** -9)
+    check("bf16", n, Hq, H, D, L, gap, 2.0 ** -29, near=128, share=2.0 ** -9)
 
 
 def test_many_bf16_queries_up_and_down():
