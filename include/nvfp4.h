@@ -352,8 +352,8 @@ enum nvfp4_rope_layout { NVFP4_ROPE_HALF = 0, NVFP4_ROPE_INTERLEAVED = 1 };
  *   rotary_dim  0 (no rotation; positions and phases NULL) .. D, a multiple of 16, of 32 with
  *               a cache and the half layout; layout: nvfp4_rope_layout
  *   q_out [T,Hq,D], k_out [T,Hkv,D] (NULL with a cache), of dtype
- *   slots       device int64 [T], with a cache: where each token goes; a slot outside
- *               [0, pages * page_size) is not written.  Slots are distinct: one that is given
+ *   slots       device int64 [T], with a cache (NULL if it has no pages): where each token goes; a slot
+ *               outside [0, pages * page_size) is not written.  Slots are distinct: one that is given
  *               twice holds bytes of both tokens (the others are right)
  * D: a multiple of 16 up to 512; with a cache 64, 128 or 256.  EINVAL on bad sizes, enums,
  * pointers, strides, eps or magnitude (not finite), an output that shares a byte with an input
@@ -406,8 +406,9 @@ int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int
  *              (ragged: 1 with offsets, 0 without), written and read by this call alone
  * Keys and values are exact in f16.  Queries enter as f16 after a power-of-two scaling per head, off
  * by at most 2^-39 of the head's largest magnitude (BF16), or as two f16, off by 2^-23 of themselves or
- * 2^-39 of that magnitude (F32); weights enter the second product as f16, or as two for F32
- * queries.  Sums, maxima and denominators are fp32, in an order that the lengths and sizes fix: the same
+ * 2^-39 of that magnitude (F32).  Weights enter the second product as f16, off by 2^-11 of themselves or
+ * 2^-36 of the row's largest weight (BF16; with many queries 2^-29 of the largest of its 128 keys, and the weights of
+ * 128 keys that are all smaller by 2^-9 of their sum), or as two f16, off by 2^-23 or 2^-47 (F32).  Sums, maxima and denominators are fp32, in an order that the lengths and sizes fix: the same
  * bits on every run.  EINVAL: Hq not a multiple of Hkv, bad sizes, enums, pointers, strides, bound or
  * scale (not finite), window < 0, a negative or too small workspace, T != B without offsets, an
  * output that shares a byte with an input or another output.  A CTA that stops waiting for its copies
