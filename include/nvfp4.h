@@ -407,8 +407,9 @@ int nvfp4_cache_read(const uint8_t* cache, int64_t pages, int64_t page_size, int
  * Keys and values are exact in f16.  Queries enter as f16 after a power-of-two scaling per head, off
  * by at most 2^-39 of the head's largest magnitude (BF16), or as two f16, off by 2^-23 of themselves or
  * 2^-39 of that magnitude (F32).  Weights enter the second product as f16, off by 2^-11 of themselves or
- * 2^-36 of the row's largest weight (BF16; with many queries 2^-29 of the largest of its 128 keys, and the weights of
- * 128 keys that are all smaller by 2^-9 of their sum), or as two f16, off by 2^-23 or 2^-47 (F32).  Sums, maxima and denominators are fp32, in an order that the lengths and sizes fix: the same
+ * 2^-36 of the row's largest weight (BF16; with many queries 2^-29 of the largest of its 128 keys, and the
+ * weights of 128 keys that are all smaller by 2^-9 of their sum), or as two f16, off by 2^-23 or 2^-47
+ * (F32).  Sums, maxima and denominators are fp32, in an order that the lengths and sizes fix: the same
  * bits on every run.  EINVAL: Hq not a multiple of Hkv, bad sizes, enums, pointers, strides, bound or
  * scale (not finite), window < 0, a negative or too small workspace, T != B without offsets, an
  * output that shares a byte with an input or another output.  A CTA that stops waiting for its copies
